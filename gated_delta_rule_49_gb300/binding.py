@@ -35,6 +35,13 @@ GDN_GATE_KDA = 1
 GDN_GATE_GDN2 = 2
 GATES = {"gdn": GDN_GATE_SCALAR, "kda": GDN_GATE_KDA, "gdn2": GDN_GATE_GDN2}
 
+GDN_NORM_RMS = 0
+GDN_NORM_L2 = 1
+NORMS = {"rms": GDN_NORM_RMS, "l2": GDN_NORM_L2}
+GDN_PAIR_HALF = 0
+GDN_PAIR_ADJACENT = 1
+PAIRINGS = {"half": GDN_PAIR_HALF, "adjacent": GDN_PAIR_ADJACENT}
+
 EXPORTS = (
     "gdn_prefill",
     "gdn_prefill_workspace_size",
@@ -62,6 +69,14 @@ EXPORTS = (
     "gdn_prefill_gathered_workspace_size",
     "gdn_prefill_gated_chunked",
     "gdn_prefill_gated_chunked_workspace_size",
+    "gdn_qk_norm_rotate",
+    "gdn_qk_norm_rotate_backward",
+    "gdn_qk_norm_rotate_backward_workspace_size",
+    "gdn_linear_prefill",
+    "gdn_linear_prefill_workspace_size",
+    "gdn_linear_backward",
+    "gdn_linear_backward_workspace_size",
+    "gdn_linear_decode_step",
 )
 
 _lock = threading.Lock()
@@ -138,6 +153,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gdn_prefill_gathered.restype = i
         lib.gdn_prefill_gathered_workspace_size.argtypes = [i] * 7
         lib.gdn_prefill_gathered_workspace_size.restype = sz
+        ll = ctypes.c_longlong
+        lib.gdn_qk_norm_rotate.argtypes = [vp] * 8 + [ll] + [i] * 4 + [ll] * 2 + [i, i, f, i, vp]
+        lib.gdn_qk_norm_rotate.restype = i
+        lib.gdn_qk_norm_rotate_backward.argtypes = (
+            [vp] * 12 + [ll] + [i] * 4 + [ll] * 2 + [i, i, f, i, vp, sz, vp])
+        lib.gdn_qk_norm_rotate_backward.restype = i
+        lib.gdn_qk_norm_rotate_backward_workspace_size.argtypes = [ll, i, i, i]
+        lib.gdn_qk_norm_rotate_backward_workspace_size.restype = sz
+        lib.gdn_linear_prefill.argtypes = [vp] * 8 + [i] * 6 + [ll] * 3 + [f, i, vp, sz, vp]
+        lib.gdn_linear_prefill.restype = i
+        lib.gdn_linear_prefill_workspace_size.argtypes = [i] * 7
+        lib.gdn_linear_prefill_workspace_size.restype = sz
+        lib.gdn_linear_backward.argtypes = [vp] * 12 + [i] * 6 + [ll] * 3 + [f, i, vp, sz, vp]
+        lib.gdn_linear_backward.restype = i
+        lib.gdn_linear_backward_workspace_size.argtypes = [i] * 8
+        lib.gdn_linear_backward_workspace_size.restype = sz
+        lib.gdn_linear_decode_step.argtypes = [vp] * 7 + [i] * 5 + [f, i, vp]
+        lib.gdn_linear_decode_step.restype = i
         _lib = lib
         return lib
 
@@ -440,6 +473,65 @@ def gather_normalize(x, idx, stream=None):
     return y
 
 
+def gdn_qk_norm_rotate(q, k, wq, wk, pos, inv_freq, yq, yk, N, Hq, Hk, D, R, q_stride, k_stride,
+                       norm, pairing, eps, dtype, stream=None) -> int:
+    st = load().gdn_qk_norm_rotate(_ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(pos),
+                                   _ptr(inv_freq), _ptr(yq), _ptr(yk), N, Hq, Hk, D, R, q_stride,
+                                   k_stride, norm, pairing, eps, dtype, _stream(stream))
+    return _check(st, "gdn_qk_norm_rotate")
+
+
+def gdn_qk_norm_rotate_backward(q, k, wq, wk, pos, inv_freq, dyq, dyk, dq, dk, dwq, dwk, N, Hq,
+                                Hk, D, R, q_stride, k_stride, norm, pairing, eps, dtype,
+                                workspace=None, workspace_bytes=0, stream=None) -> int:
+    st = load().gdn_qk_norm_rotate_backward(
+        _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq), _ptr(dyq), _ptr(dyk),
+        _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), N, Hq, Hk, D, R, q_stride, k_stride, norm,
+        pairing, eps, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "gdn_qk_norm_rotate_backward")
+
+
+def gdn_qk_norm_rotate_backward_workspace_size(N, Hq, Hk, D) -> int:
+    return int(load().gdn_qk_norm_rotate_backward_workspace_size(N, Hq, Hk, D))
+
+
+def gdn_linear_prefill(q, k, v, alpha, S0, o, S_T, offsets, B, T, Hq, H, K, V, q_stride, k_stride,
+                       v_stride, scale, dtype, workspace=None, workspace_bytes=0,
+                       stream=None) -> int:
+    st = load().gdn_linear_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(o),
+                                   _ptr(S_T), _ptr(offsets), B, T, Hq, H, K, V, q_stride,
+                                   k_stride, v_stride, scale, dtype, _ptr(workspace),
+                                   workspace_bytes, _stream(stream))
+    return _check(st, "gdn_linear_prefill")
+
+
+def gdn_linear_prefill_workspace_size(B, T, H, K, V, packed, dtype) -> int:
+    return int(load().gdn_linear_prefill_workspace_size(B, T, H, K, V, int(packed), dtype))
+
+
+def gdn_linear_backward(q, k, v, alpha, dO, S0, dS_T, dq, dk, dv, dS0, offsets, B, T, Hq, H, K, V,
+                        q_stride, k_stride, v_stride, scale, dtype, workspace=None,
+                        workspace_bytes=0, stream=None) -> int:
+    st = load().gdn_linear_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(dO), _ptr(S0),
+                                    _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dS0),
+                                    _ptr(offsets), B, T, Hq, H, K, V, q_stride, k_stride,
+                                    v_stride, scale, dtype, _ptr(workspace), workspace_bytes,
+                                    _stream(stream))
+    return _check(st, "gdn_linear_backward")
+
+
+def gdn_linear_backward_workspace_size(B, T, Hq, H, K, V, packed, dtype) -> int:
+    return int(load().gdn_linear_backward_workspace_size(B, T, Hq, H, K, V, int(packed), dtype))
+
+
+def gdn_linear_decode_step(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale, dtype,
+                           stream=None) -> int:
+    st = load().gdn_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S),
+                                       _ptr(S_out), _ptr(o), B, Hq, H, K, V, scale, dtype,
+                                       _stream(stream))
+    return _check(st, "gdn_linear_decode_step")
+
+
 def gdn_get_last_device_status(stream=None) -> int:
     return int(load().gdn_get_last_device_status(_stream(stream)))
 
@@ -505,3 +597,211 @@ def state_rank(S, max_iter=500, tol=1e-7, stream=None):
     outs = [torch.empty(lead, dtype=torch.float32, device=S.device) for _ in range(3)]
     gdn_state_rank(S, BH, V, K, *outs, max_iter=max_iter, tol=tol, stream=stream)
     return tuple(outs)
+
+
+def _reject(where, what):
+    e = GDNError(GDN_ERR_INVALID_ARG, where)
+    e.args = (f"{e.args[0]}: {what}",)
+    raise e
+
+
+def _token_stride(where, name, x, dtype=None, device=None):
+    """Elements between consecutive tokens of x [..., heads, channels]: a
+    token's heads and channels are dense, and the leading dimensions step
+    evenly, as in a part of a wider projection."""
+    heads, D = x.shape[-2:]
+    if dtype is not None and (x.dtype != dtype or x.device != device):
+        _reject(where, f"{name} is {x.dtype} on {x.device}, not {dtype} on {device}")
+    if x.is_contiguous():
+        return heads * D
+    st = x.stride()
+    if st[-1] != 1 or (st[-2] != D and heads > 1):
+        _reject(where, f"{name}'s heads and channels are not dense (strides {tuple(st)})")
+    step, span = 0, 1  # of the tokens seen so far, innermost first
+    for n, s in zip(reversed(x.shape[:-2]), reversed(st[:-2])):
+        if n == 1:
+            continue
+        if not step:
+            step = s
+        elif s != step * span:
+            _reject(where, f"{name}'s tokens do not lie evenly (strides {tuple(st)})")
+        span *= n
+    return step or heads * D
+
+
+def _dense(where, device, **named):
+    """Each tensor given: contiguous, on the device, of its type and shape."""
+    for name, (x, dtype, shape) in named.items():
+        if x is None:
+            continue
+        if x.dtype != dtype or x.device != device or tuple(x.shape) != tuple(shape) \
+                or not x.is_contiguous():
+            _reject(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                           f"on {device}")
+
+
+def _qk_norm_args(where, q, k, pos, inv_freq, wq, wk, norm, pairing):
+    import torch
+    if norm not in NORMS or pairing not in PAIRINGS:
+        _reject(where, f"norm {norm!r}, pairing {pairing!r}")
+    lead, (Hq, D) = q.shape[:-2], q.shape[-2:]
+    Hk = 0
+    ldq = _token_stride(where, "q", q)
+    ldk = 0
+    if k is not None:
+        Hk = k.shape[-2]
+        if k.shape[:-2] != lead or k.shape[-1] != D:
+            _reject(where, f"q {tuple(q.shape)} and k {tuple(k.shape)}")
+        ldk = _token_stride(where, "k", k, q.dtype, q.device)
+    R = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    _dense(where, q.device, pos=(pos, torch.int64, lead), wq=(wq, torch.float32, (D,)),
+           wk=(wk, torch.float32, (D,)), inv_freq=(inv_freq, torch.float32, (R // 2,)))
+    N = 1
+    for n in lead:
+        N *= n
+    return N, Hq, Hk, D, R, ldq, ldk, NORMS[norm], PAIRINGS[pairing]
+
+
+def qk_norm_rotate(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms", pairing="half",
+                   eps=1e-6, out=None, stream=None):
+    """Norms of q [..., Hq, D] and k [..., Hk, D] (or None) for each head, and
+    the rotation of their first 2 len(inv_freq) channels by pos * inv_freq, in
+    one pass (gdn_qk_norm_rotate).  pos [...] int64; wq, wk [D] float32 or None;
+    norm "rms" or "l2"; pairing "half" (i with i + R/2) or "adjacent".  q and k
+    may be slices of one projection.  Returns (yq, yk), new dense tensors or
+    `out` (which may hold dense q and k themselves)."""
+    import torch
+    where = "qk_norm_rotate"
+    N, Hq, Hk, D, R, ldq, ldk, nrm, pair = _qk_norm_args(where, q, k, pos, inv_freq, wq, wk, norm,
+                                                         pairing)
+    if out is None:
+        yq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        yk = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    else:
+        yq, yk = out
+        _dense(where, q.device, yq=(yq, q.dtype, q.shape))
+        if k is not None:
+            _dense(where, q.device, yk=(yk, k.dtype, k.shape))
+    gdn_qk_norm_rotate(q, k, wq, wk, pos, inv_freq, yq, yk, N, Hq, Hk, D, R, ldq, ldk, nrm, pair,
+                       eps, _dtype_code(q), stream)
+    return yq, yk
+
+
+def qk_norm_rotate_backward(q, k, pos, inv_freq, dyq, dyk, wq=None, wk=None, norm="rms",
+                            pairing="half", eps=1e-6, workspace=None, stream=None):
+    """Gradients of qk_norm_rotate from its inputs and dyq, dyk (dense).
+    Returns (dq, dk, dwq, dwk); a weight that was not given has None."""
+    import torch
+    where = "qk_norm_rotate_backward"
+    N, Hq, Hk, D, R, ldq, ldk, nrm, pair = _qk_norm_args(where, q, k, pos, inv_freq, wq, wk, norm,
+                                                         pairing)
+    _dense(where, q.device, dyq=(dyq, q.dtype, q.shape),
+           dyk=(dyk if k is not None else None, q.dtype, () if k is None else k.shape))
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+    need = 0
+    if wq is not None or wk is not None:
+        need = gdn_qk_norm_rotate_backward_workspace_size(N, Hq, Hk, D)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        need = workspace.numel() * workspace.element_size()
+    gdn_qk_norm_rotate_backward(q, k, wq, wk, pos, inv_freq, dyq, dyk, dq, dk, dwq, dwk, N, Hq, Hk,
+                                D, R, ldq, ldk, nrm, pair, eps, _dtype_code(q), workspace, need,
+                                stream)
+    return dq, dk, dwq, dwk
+
+
+def _linear_args(where, q, k, v, alpha, offsets, **states):
+    """Sizes and token strides of q, k [B, T, Hq, K], v [B, T, H, V]; with
+    offsets, of q, k [tokens, Hq, K], v [tokens, H, V]."""
+    import torch
+    dims = 4 if offsets is None else 3
+    if q.dim() != dims or k.shape != q.shape or v.dim() != dims or v.shape[:-2] != q.shape[:-2]:
+        _reject(where, f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}"
+                       + ("" if offsets is None else " with offsets"))
+    Hq, K = q.shape[-2:]
+    H, V = v.shape[-2:]
+    if offsets is None:
+        B, T = q.shape[:2]
+    else:
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            _reject(where, "offsets must be [sequences + 1]")
+        B, T = offsets.shape[0] - 1, q.shape[0]
+        _dense(where, v.device, offsets=(offsets, torch.int32, offsets.shape))
+    _dense(where, v.device, alpha=(alpha, torch.float32, (H,)),
+           **{n: (s, torch.float32, (B, H, V, K)) for n, s in states.items()})
+    ld = tuple(_token_stride(where, n, x, v.dtype, v.device)
+               for n, x in (("q", q), ("k", k), ("v", v)))
+    return (B, T, Hq, H, K, V), ld
+
+
+def linear_prefill(q, k, v, alpha, S0=None, scale=1.0, offsets=None, want_o=True, want_state=True,
+                   out_state=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head, S_t = alpha S_{t-1} + v_t k_t^T and
+    o_t = scale S_t q_t (gdn_linear_prefill): q, k [B, T, Hq, K], v [B, T, H, V] (bf16 or fp32;
+    H a multiple of Hq; slices of one projection will do), alpha [H] fp32, S0 [B, H, V, K] fp32 or
+    None.  With offsets [B + 1] int32 the sequences lie packed: q, k [tokens, Hq, K],
+    v [tokens, H, V].  Returns (o, S_T); out_state may be S0."""
+    import torch
+    (B, T, Hq, H, K, V), ld = _linear_args("linear_prefill", q, k, v, alpha, offsets, S0=S0,
+                                           out_state=out_state)
+    dt = _dtype_code(v)
+    o = torch.empty(v.shape, dtype=v.dtype, device=v.device) if want_o else None
+    ST = out_state
+    if want_state and ST is None:
+        ST = torch.empty((B, H, V, K), dtype=torch.float32, device=v.device)
+    need = gdn_linear_prefill_workspace_size(B, T, H, K, V, offsets is not None, dt)
+    if workspace is not None:
+        need = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+    gdn_linear_prefill(q, k, v, alpha, S0, o, ST, offsets, B, T, Hq, H, K, V, *ld, scale, dt,
+                       workspace, need, stream)
+    return o, ST
+
+
+def linear_backward(q, k, v, alpha, do, S0=None, dS_T=None, scale=1.0, offsets=None,
+                    want_dS0=None, workspace=None, stream=None):
+    """Gradients of linear_prefill from its inputs, do (dense, as v) and dS_T (fp32 or None).
+    Returns (dq, dk, dv, dS0); dS0 is formed if S0 is given or want_dS0 is true, else None.
+    alpha is a constant and has none."""
+    import torch
+    where = "linear_backward"
+    (B, T, Hq, H, K, V), ld = _linear_args(where, q, k, v, alpha, offsets, S0=S0, dS_T=dS_T)
+    _dense(where, v.device, do=(do, v.dtype, v.shape))
+    dt = _dtype_code(v)
+    dq, dk, dv = (torch.empty(x.shape, dtype=v.dtype, device=v.device) for x in (q, k, v))
+    dS0 = None
+    if want_dS0 or (want_dS0 is None and S0 is not None):
+        dS0 = torch.empty((B, H, V, K), dtype=torch.float32, device=v.device)
+    need = gdn_linear_backward_workspace_size(B, T, Hq, H, K, V, offsets is not None, dt)
+    if workspace is not None:
+        need = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+    gdn_linear_backward(q, k, v, alpha, do, S0, dS_T, dq, dk, dv, dS0, offsets, B, T, Hq, H, K, V,
+                        *ld, scale, dt, workspace, need, stream)
+    return dq, dk, dv, dS0
+
+
+def linear_decode_step(q, k, v, alpha, S, scale=1.0, S_out=None, o=None, stream=None):
+    """One token of linear_prefill: q, k [B, Hq, K]; v [B, H, V]; alpha [H]; S [B, H, V, K],
+    updated in place unless S_out is given.  Returns o [B, H, V]."""
+    import torch
+    where = "linear_decode_step"
+    if q.dim() != 3 or v.dim() != 3:
+        _reject(where, f"q {tuple(q.shape)}, v {tuple(v.shape)}")
+    B, Hq, K = q.shape
+    H, V = v.shape[1:]
+    if S_out is None:
+        S_out = S
+    if o is None:
+        o = torch.empty((B, H, V), dtype=v.dtype, device=v.device)
+    _dense(where, v.device, q=(q, v.dtype, (B, Hq, K)), k=(k, v.dtype, (B, Hq, K)),
+           v=(v, v.dtype, (B, H, V)), o=(o, v.dtype, (B, H, V)),
+           alpha=(alpha, torch.float32, (H,)), S=(S, torch.float32, (B, H, V, K)),
+           S_out=(S_out, torch.float32, (B, H, V, K)))
+    gdn_linear_decode_step(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale, _dtype_code(v),
+                           stream)
+    return o

@@ -88,6 +88,49 @@ int from_cuda(cudaError_t e) {
     return GDN_ERR_CUDA;
 }
 
+// The argument checks that the norm's forward and backward pass share.
+int check_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
+                  const long long *pos, const float *inv_freq, long long N, int Hq, int Hk, int D,
+                  int R, long long q_stride, long long k_stride, int norm, int pairing, float eps,
+                  int dtype) {
+    if (N < 0 || Hq < 0 || Hk < 0 || Hq > 65536 || Hk > 65536 || N > (1LL << 40))
+        return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
+    if (norm != GDN_NORM_RMS && norm != GDN_NORM_L2) return GDN_ERR_INVALID_ARG;
+    if (pairing != GDN_PAIR_HALF && pairing != GDN_PAIR_ADJACENT) return GDN_ERR_INVALID_ARG;
+    if (!(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    if (D != 32 && D != 64 && D != 128 && D != 256) return GDN_ERR_UNSUPPORTED;
+    if (R < 0 || R > D) return GDN_ERR_INVALID_ARG;
+    if (R % 16) return GDN_ERR_UNSUPPORTED;
+    const int unit = dtype == GDN_BF16 ? 8 : 4;  // elements of 16 bytes
+    if ((Hq && (q_stride < (long long)Hq * D || q_stride % unit)) ||
+        (Hk && (k_stride < (long long)Hk * D || k_stride % unit)))
+        return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, wq, wk, pos, inv_freq};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    if (N && ((Hq && !q) || (Hk && !k) || (R && Hq + Hk && (!pos || !inv_freq))))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+bool linear_kv(int K, int V) { return supported_kv(K, V) || (K == 64 && V == 64); }
+
+// The checks of sizes that the linear attention calls share.
+int check_linear(int B, int T, int Hq, int H, int K, int V, long long q_stride, long long k_stride,
+                 long long v_stride, int dtype) {
+    if (B < 0 || T < 0 || H < 0 || K <= 0 || V <= 0) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
+    if (!linear_kv(K, V)) return GDN_ERR_UNSUPPORTED;
+    if (H && (Hq < 1 || H % Hq)) return GDN_ERR_INVALID_ARG;
+    const int unit = dtype == GDN_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (H && (q_stride < (long long)Hq * K || k_stride < (long long)Hq * K ||
+              v_stride < (long long)H * V || q_stride % unit || k_stride % unit || v_stride % unit))
+        return GDN_ERR_INVALID_ARG;
+    if ((long long)B * H > (1 << 24) || (long long)B * T > (1LL << 40)) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -464,6 +507,196 @@ int gdn_state_rank(const float *S, int BH, int V, int K, float *fro2, float *sig
         if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
     return from_cuda(gdn::launch_state_rank(S, BH, V, K, fro2, sigma1, stable_rank, max_iter,
                                             tol, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_qk_norm_rotate(const void *q, const void *k, const float *wq, const float *wk,
+                       const long long *pos, const float *inv_freq, void *yq, void *yk,
+                       long long N, int Hq, int Hk, int D, int R, long long q_stride,
+                       long long k_stride, gdn_norm norm, gdn_pairing pairing, float eps,
+                       gdn_dtype dtype, void *stream) {
+    const int e = check_qk_norm(q, k, wq, wk, pos, inv_freq, N, Hq, Hk, D, R, q_stride, k_stride,
+                                norm, pairing, eps, dtype);
+    if (e != GDN_OK || N == 0 || Hq + Hk == 0) return e;
+    if ((Hq && !yq) || (Hk && !yk)) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(yq) || !aligned16(yk)) return GDN_ERR_ALIGNMENT;
+    // in place only where the rows lie as the outputs do
+    if ((yq == q && Hq && q_stride != (long long)Hq * D) ||
+        (yk == k && Hk && k_stride != (long long)Hk * D))
+        return GDN_ERR_INVALID_ARG;
+    return from_cuda(gdn::launch_qk_norm(q, k, wq, wk, pos, inv_freq, yq, yk, N, Hq, Hk, D, R,
+                                         q_stride, k_stride, norm == GDN_NORM_L2,
+                                         pairing == GDN_PAIR_HALF, eps, dtype,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_qk_norm_rotate_backward_workspace_size(long long N, int Hq, int Hk, int D) {
+    if (N <= 0 || Hq < 0 || Hk < 0 || Hq + Hk <= 0 || D <= 0) return 0;
+    return (size_t)gdn::qk_norm_backward_grid(N, Hq + Hk, D) * 2 * D * sizeof(float);
+}
+
+int gdn_qk_norm_rotate_backward(const void *q, const void *k, const float *wq, const float *wk,
+                                const long long *pos, const float *inv_freq, const void *dyq,
+                                const void *dyk, void *dq, void *dk, float *dwq, float *dwk,
+                                long long N, int Hq, int Hk, int D, int R, long long q_stride,
+                                long long k_stride, gdn_norm norm, gdn_pairing pairing, float eps,
+                                gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    const int e = check_qk_norm(q, k, wq, wk, pos, inv_freq, N, Hq, Hk, D, R, q_stride, k_stride,
+                                norm, pairing, eps, dtype);
+    if (e != GDN_OK) return e;
+    if ((dwq && !wq) || (dwk && !wk)) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {dyq, dyk, dq, dk, dwq, dwk, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N == 0 || Hq + Hk == 0) {  // sums over nothing
+        cudaError_t c = cudaSuccess;
+        if (dwq) c = cudaMemsetAsync(dwq, 0, sizeof(float) * D, st);
+        if (dwk && c == cudaSuccess) c = cudaMemsetAsync(dwk, 0, sizeof(float) * D, st);
+        return from_cuda(c);
+    }
+    if ((Hq && (!dyq || !dq)) || (Hk && (!dyk || !dk))) return GDN_ERR_INVALID_ARG;
+    if ((dwq || dwk) &&
+        (!workspace || workspace_bytes < gdn_qk_norm_rotate_backward_workspace_size(N, Hq, Hk, D)))
+        return GDN_ERR_WORKSPACE;
+    return from_cuda(gdn::launch_qk_norm_backward(
+        q, k, wq, wk, pos, inv_freq, dyq, dyk, dq, dk, dwq, dwk, N, Hq, Hk, D, R, q_stride,
+        k_stride, norm == GDN_NORM_L2, pairing == GDN_PAIR_HALF, eps, dtype,
+        static_cast<float *>(workspace), st));
+}
+
+size_t gdn_linear_prefill_workspace_size(int B, int T, int H, int K, int V, int packed,
+                                         gdn_dtype dtype) {
+    if (B <= 0 || T <= 0 || H <= 0 || !linear_kv(K, V)) return 0;
+    return gdn::linear_scan_workspace(B, T, H, K, V, packed != 0, dtype);
+}
+
+int gdn_linear_prefill(const void *q, const void *k, const void *v, const float *alpha,
+                       const float *S0, void *o, float *S_T, const int *offsets, int B, int T,
+                       int Hq, int H, int K, int V, long long q_stride, long long k_stride,
+                       long long v_stride, float scale, gdn_dtype dtype, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    const int e = check_linear(B, T, Hq, H, K, V, q_stride, k_stride, v_stride, dtype);
+    if (e != GDN_OK) return e;
+    if (!o && !S_T) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, v, alpha, S0, o, S_T, offsets, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    if (B == 0 || H == 0) return GDN_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return empty_prefill(S0, S_T, B, H, K, V, st);
+    if ((!q && o) || !k || !v || !alpha) return GDN_ERR_INVALID_ARG;
+    if (workspace_bytes < gdn_linear_prefill_workspace_size(B, T, H, K, V, offsets != nullptr, dtype) ||
+        (!workspace && workspace_bytes))
+        return GDN_ERR_WORKSPACE;
+    gdn::LinearScan a = {};
+    a.q = q; a.k = k; a.v = v;
+    a.alpha = alpha; a.S0 = S0; a.o = o; a.ST = S_T; a.offsets = offsets;
+    a.B = B; a.T = T; a.H = H; a.Hq = a.Hk = Hq; a.Hv = H; a.K = K; a.V = V;
+    a.ldq = q_stride; a.ldk = k_stride; a.ldv = v_stride;
+    a.write_scale = 1.f;
+    a.read_scale = scale;
+    return from_cuda(gdn::launch_linear_scan(a, dtype, workspace, st));
+}
+
+namespace {
+// The scans' slots, rounded up so that what follows is aligned.
+size_t linear_backward_slots(int B, int T, int H, int K, int V, bool packed, gdn_dtype dtype) {
+    const size_t a = gdn::linear_scan_workspace(B, T, H, K, V, packed, dtype);
+    const size_t b = gdn::linear_scan_workspace(B, T, H, V, K, packed, dtype);
+    return ((a > b ? a : b) + 255) & ~size_t(255);
+}
+}  // namespace
+
+size_t gdn_linear_backward_workspace_size(int B, int T, int Hq, int H, int K, int V, int packed,
+                                          gdn_dtype dtype) {
+    if (B <= 0 || T <= 0 || H <= 0 || Hq <= 0 || !linear_kv(K, V)) return 0;
+    size_t n = linear_backward_slots(B, T, H, K, V, packed != 0, dtype);
+    // one head's part of a gradient that a group of heads shares, in float32
+    if (Hq != H) n += (size_t)(packed ? 1 : B) * T * H * K * sizeof(float);
+    return n;
+}
+
+int gdn_linear_backward(const void *q, const void *k, const void *v, const float *alpha,
+                        const void *dO, const float *S0, const float *dS_T, void *dq, void *dk,
+                        void *dv, float *dS0, const int *offsets, int B, int T, int Hq, int H,
+                        int K, int V, long long q_stride, long long k_stride, long long v_stride,
+                        float scale, gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+    const int e = check_linear(B, T, Hq, H, K, V, q_stride, k_stride, v_stride, dtype);
+    if (e != GDN_OK) return e;
+    if (!dq && !dk && !dv && !dS0) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, v, alpha, dO, S0, dS_T, dq, dk, dv, dS0, offsets, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    if (B == 0 || H == 0) return GDN_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return empty_prefill(dS_T, dS0, B, H, K, V, st);
+    if (!q || !k || !v || !alpha || !dO) return GDN_ERR_INVALID_ARG;
+    const size_t need =
+        gdn_linear_backward_workspace_size(B, T, Hq, H, K, V, offsets != nullptr, dtype);
+    if (workspace_bytes < need || (!workspace && workspace_bytes)) return GDN_ERR_WORKSPACE;
+    const long long tokens = offsets ? T : (long long)B * T;
+    float *part = reinterpret_cast<float *>(
+        static_cast<char *>(workspace) +
+        linear_backward_slots(B, T, H, K, V, offsets != nullptr, dtype));
+    const int group = H / Hq;
+    const long long ldo = (long long)H * V;
+
+    gdn::LinearScan a = {};
+    a.alpha = alpha; a.offsets = offsets;
+    a.B = B; a.T = T; a.H = H;
+    cudaError_t c = cudaSuccess;
+    auto shared = [&](void *grad) {  // dq and dk: summed over the heads that share them
+        a.o = group > 1 ? part : grad;
+        a.o_float = group > 1 || dtype == GDN_FP32;
+        c = gdn::launch_linear_scan(a, dtype, workspace, st);
+        if (c == cudaSuccess && group > 1)
+            c = gdn::launch_group_sum(part, grad, tokens, Hq, group, K, dtype, st);
+    };
+    if (dq) {
+        a.q = dO; a.ldq = ldo; a.Hq = H;
+        a.k = v; a.ldk = v_stride; a.Hk = H;
+        a.v = k; a.ldv = k_stride; a.Hv = Hq;
+        a.K = V; a.V = K;
+        a.S0 = S0; a.s0_transposed = true; a.reverse = false;
+        a.write_scale = 1.f; a.read_scale = scale;
+        shared(dq);
+    }
+    if (c == cudaSuccess && dk) {
+        a.q = v; a.ldq = v_stride; a.Hq = H;
+        a.k = dO; a.ldk = ldo; a.Hk = H;
+        a.v = q; a.ldv = q_stride; a.Hv = Hq;
+        a.K = V; a.V = K;
+        a.S0 = dS_T; a.s0_transposed = true; a.reverse = true;
+        a.write_scale = scale; a.read_scale = 1.f;
+        shared(dk);
+    }
+    if (c == cudaSuccess && (dv || dS0)) {
+        a.q = k; a.ldq = k_stride; a.Hq = Hq;
+        a.k = q; a.ldk = q_stride; a.Hk = Hq;
+        a.v = dO; a.ldv = ldo; a.Hv = H;
+        a.K = K; a.V = V;
+        a.S0 = dS_T; a.s0_transposed = false; a.reverse = true;
+        a.write_scale = scale; a.read_scale = 1.f;
+        a.o = dv; a.ST = dS0; a.o_float = dtype == GDN_FP32;
+        c = gdn::launch_linear_scan(a, dtype, workspace, st);
+    }
+    return from_cuda(c);
+}
+
+int gdn_linear_decode_step(const void *q, const void *k, const void *v, const float *alpha,
+                           const float *S, float *S_out, void *o, int B, int Hq, int H, int K,
+                           int V, float scale, gdn_dtype dtype, void *stream) {
+    const int e = check_linear(B, 1, Hq, H, K, V, (long long)Hq * K, (long long)Hq * K,
+                               (long long)H * V, dtype);
+    if (e != GDN_OK || B == 0 || H == 0) return e;
+    if (!q || !k || !v || !alpha || !S || !S_out || !o) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, v, alpha, S, S_out, o};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    return from_cuda(gdn::launch_linear_decode(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale,
+                                               dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_get_last_device_status(void *stream) {

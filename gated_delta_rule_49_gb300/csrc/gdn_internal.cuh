@@ -164,6 +164,47 @@ cudaError_t launch_prefill_host(const void *q, const void *k, const void *v, con
                                 int T, int H, int K, int V, gdn_dtype dt, int window,
                                 void *workspace, cudaStream_t stream);
 
+// Norms of queries and keys for each head with the position rotation; the
+// backward pass needs qk_norm_backward_grid * 2 * D floats for the weights'
+// gradients.
+int qk_norm_backward_grid(long long N, int heads, int D);
+cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
+                           const long long *pos, const float *inv_freq, void *yq, void *yk,
+                           long long N, int Hq, int Hk, int D, int R, long long ldq, long long ldk,
+                           bool l2, bool half, float eps, gdn_dtype dt, cudaStream_t stream);
+cudaError_t launch_qk_norm_backward(const void *q, const void *k, const float *wq,
+                                    const float *wk, const long long *pos, const float *inv_freq,
+                                    const void *dyq, const void *dyk, void *dq, void *dk,
+                                    float *dwq, float *dwk, long long N, int Hq, int Hk, int D,
+                                    int R, long long ldq, long long ldk, bool l2, bool half,
+                                    float eps, gdn_dtype dt, float *partial, cudaStream_t stream);
+
+// Linear attention with a decay for each head, one scan of it (gdn_linear.cuh
+// holds what it means): the prompt's outputs, or one of the three gradients.
+struct LinearScan {
+    const void *q, *k, *v;   // [tokens, Hq | Hk | Hv, K | K | V], token strides ldq | ldk | ldv
+    const float *alpha;      // [H]
+    const float *S0;         // [B, H, V, K] or, with s0_transposed, [B, H, K, V]; or NULL
+    void *o;                 // [tokens, H, V] or NULL
+    float *ST;               // [B, H, V, K] or NULL
+    const int *offsets;      // [B + 1] token offsets of packed sequences, or NULL: B x T tokens
+    int B, T;                // packed: T tokens in all
+    int H, Hq, Hk, Hv, K, V;
+    long long ldq, ldk, ldv;
+    float write_scale, read_scale;
+    bool reverse, s0_transposed, o_float;
+};
+// Bytes of workspace of one scan; launches it.
+size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt);
+cudaError_t launch_linear_scan(const LinearScan &a, gdn_dtype dt, void *workspace,
+                               cudaStream_t stream);
+// y [rows, Hq, D] (dtype) = sums of x [rows, H, D] (float32) over groups of H / Hq heads.
+cudaError_t launch_group_sum(const float *x, void *y, long long rows, int Hq, int group, int D,
+                             gdn_dtype dt, cudaStream_t stream);
+cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *alpha,
+                                 const float *S, float *S_out, void *o, int B, int Hq, int H,
+                                 int K, int V, float scale, gdn_dtype dt, cudaStream_t stream);
+
 // Programmatic dependent launch: a kernel launched this way may be scheduled
 // while the previous kernel on the stream finishes; it must execute
 // pdl_wait() before its first global-memory access (which then sees all of

@@ -1,0 +1,373 @@
+// Linear attention with a decay for each head on the CUDA cores: the token by
+// token scan (float32 runs and the (32, 32) variant), the single-token step,
+// and the dispatch of a scan.
+#include "gdn_linear.cuh"
+#include "gdn_vec8.cuh"
+
+namespace gdn {
+namespace {
+
+// ------------------------------------------------------------------ scan
+//
+// Value channels are independent: row v of the state is S_v <- a S_v +
+// (write_scale v_t) k_t, o_v = read_scale S_v . q_t.  A warp keeps 8 rows in
+// registers (a lane holds K / 32 columns of each), so a token costs 2 fused
+// multiply-adds and a product for each element and 9 shuffles for the 8 dot
+// products; a CTA of 4 warps covers 32 rows.  Tiles of 16 tokens go through
+// shared memory as float32, the next tile's loads in flight during this
+// one's arithmetic.  Bound by the float32 pipes: 3 K V instructions-lanes a
+// token and head, as many as a chunk form without tensor cores would need.
+constexpr int kScanThreads = 128;
+constexpr int kTile = 16;      // tokens
+constexpr int kRows = 8;       // rows of a warp
+constexpr int kCtaRows = 32;
+
+template <int C> struct Cols;  // C consecutive floats of a row
+template <> struct Cols<1> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[1]) { x[0] = p[0]; }
+};
+template <> struct Cols<2> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[2]) {
+        const float2 y = *reinterpret_cast<const float2 *>(p);
+        x[0] = y.x; x[1] = y.y;
+    }
+};
+template <> struct Cols<4> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[4]) {
+        const float4 y = *reinterpret_cast<const float4 *>(p);
+        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+    }
+};
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kScanThreads)
+    linear_token_kernel(const LinearScan p, SegPlan plan, const float *slots_in, float *slots_out,
+                        int *status) {
+    constexpr int C = K / 32;             // columns of a lane
+    constexpr int QV = kTile * K / 8;     // 8-element pieces of a q or k tile
+    constexpr int QN = (QV + kScanThreads - 1) / kScanThreads;
+    __shared__ __align__(16) float qs[kTile][K], ks[kTile][K], vs[kTile][kCtaRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int blocks = p.V / kCtaRows;
+    const int blk = blockIdx.x % blocks;
+    const int h = blockIdx.x / blocks % p.H;
+    const int item = blockIdx.x / blocks / p.H;
+    const LinearItem it = linear_item(p.offsets, p.B, p.T, plan.seg_len, item, status);
+    if (it.seq < 0) return;
+    const bool last = p.reverse ? it.j == 0 : it.j == it.n - 1;  // in scan order
+    if (slots_out && last && !p.S0) return;  // nothing starts from its end
+    const bool want_o = p.o && !slots_out;
+    const int f0 = it.j * plan.seg_len;
+    // tokens; the last segment's slot only takes a copy of S0
+    const int n = slots_out && last ? 0 : min(it.len - f0, plan.seg_len);
+    const float a = p.alpha[h], lg = decay_log2(a);
+    const size_t VK = (size_t)p.V * K;
+    const int row0 = blk * kCtaRows + warp * kRows;
+    const int hq = h / (p.H / p.Hq), hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
+
+    float S[kRows][C];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            S[r][c] = !slots_out ? linear_start(it, p.S0, p.s0_transposed, slots_in, h, p.H, p.V,
+                                                K, row0 + r, lane * C + c, plan.seg_len, lg,
+                                                p.reverse)
+                      : last ? given_start(p.S0, p.s0_transposed, (size_t)it.seq * p.H + h, p.V, K,
+                                           row0 + r, lane * C + c)
+                             : 0.f;
+    const T *qp = static_cast<const T *>(p.q) + (long long)hq * K;
+    const T *kp = static_cast<const T *>(p.k) + (long long)hk * K;
+    const T *vp = static_cast<const T *>(p.v) + (long long)hv * p.V + blk * kCtaRows;
+    // token of scan position i
+    auto token = [&](int i) { return it.first + f0 + (p.reverse ? n - 1 - i : i); };
+
+    Vec8<T> rq[QN], rk[QN], rv;
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int x = 0; x < QN; ++x) {
+            const int piece = threadIdx.x + x * kScanThreads;
+            const int t = piece / (K / 8), c = piece % (K / 8);
+            if (piece < QV && i0 + t < n) {
+                const long long tok = token(i0 + t);
+                if (want_o) rq[x].load_cached(qp + tok * p.ldq + 8 * c);
+                rk[x].load_cached(kp + tok * p.ldk + 8 * c);
+            }
+        }
+        const int t = threadIdx.x / 4, c = threadIdx.x % 4;
+        if (threadIdx.x < kTile * 4 && i0 + t < n)
+            rv.load_cached(vp + token(i0 + t) * p.ldv + 8 * c);
+    };
+    auto put = [&](int i0) {
+        float x8[8];
+#pragma unroll
+        for (int x = 0; x < QN; ++x) {
+            const int piece = threadIdx.x + x * kScanThreads;
+            const int t = piece / (K / 8), c = piece % (K / 8);
+            if (piece < QV && i0 + t < n) {
+                if (want_o) {
+                    rq[x].get(x8);
+                    Vec8<float>::store(&qs[t][8 * c], x8);
+                }
+                rk[x].get(x8);
+                Vec8<float>::store(&ks[t][8 * c], x8);
+            }
+        }
+        const int t = threadIdx.x / 4, c = threadIdx.x % 4;
+        if (threadIdx.x < kTile * 4 && i0 + t < n) {
+            rv.get(x8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x8[e] *= p.write_scale;
+            Vec8<float>::store(&vs[t][8 * c], x8);
+        }
+    };
+
+    // the row whose dot product this lane holds after the transposing sums
+    const int my_row = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+    // a reversed scan takes its start state up undecayed
+    bool lead = !(p.reverse && it.j == it.n - 1);
+    if (n > 0) fetch(0);
+    for (int i0 = 0; i0 < n; i0 += kTile) {
+        __syncthreads();
+        put(i0);
+        __syncthreads();
+        if (i0 + kTile < n) fetch(i0 + kTile);
+        const int m = min(kTile, n - i0);
+#pragma unroll 4
+        for (int t = 0; t < m; ++t) {
+            float kk[C], qq[C], w[kRows], acc[kRows];
+            Cols<C>::load(&ks[t][lane * C], kk);
+            Cols<4>::load(&vs[t][warp * kRows], *reinterpret_cast<float(*)[4]>(&w[0]));
+            Cols<4>::load(&vs[t][warp * kRows + 4], *reinterpret_cast<float(*)[4]>(&w[4]));
+            const float at = lead ? a : 1.f;
+            lead = true;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int c = 0; c < C; ++c) S[r][c] = fmaf(w[r], kk[c], at * S[r][c]);
+            if (!want_o) continue;
+            Cols<C>::load(&qs[t][lane * C], qq);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                acc[r] = S[r][0] * qq[0];
+#pragma unroll
+                for (int c = 1; c < C; ++c) acc[r] = fmaf(S[r][c], qq[c], acc[r]);
+            }
+            // sums over the warp, halving the rows a lane holds at each step
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+                const int half = 4 >> s, bit = 16 >> s;
+                const bool up = lane & bit;
+#pragma unroll
+                for (int r = 0; r < half; ++r) {
+                    const float give = up ? acc[r] : acc[r + half];
+                    const float keep = up ? acc[r + half] : acc[r];
+                    acc[r] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+                }
+            }
+            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 2);
+            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
+            if ((lane & 3) == 0) {
+                const float o = p.read_scale * acc[0];
+                const long long at_o = (token(i0 + t) * p.H + h) * p.V + row0 + my_row;
+                if (p.o_float) static_cast<float *>(p.o)[at_o] = o;
+                else static_cast<T *>(p.o)[at_o] = from_f32<T>(o);
+            }
+        }
+    }
+    float *end = slots_out ? slots_out + ((size_t)(it.slot0 + it.j) * p.H + h) * VK
+                 : p.ST && last ? p.ST + ((size_t)it.seq * p.H + h) * VK : nullptr;
+    if (!end) return;
+    // the state that a reversed scan returns has decayed once more
+    const float f = !slots_out && p.reverse && it.len > 0 ? a : 1.f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) end[(size_t)(row0 + r) * K + lane * C + c] = f * S[r][c];
+}
+
+SegPlan token_plan(int B, int T, int H, int V, bool packed) {
+    // a CTA needs some hundred nanoseconds a token, whatever else runs: cut
+    // few long sequences until about six CTAs an SM run, segments of 256
+    // tokens at least (each costs a second pass over k and v)
+    const int nsm = sm_count() > 0 ? sm_count() : 152;
+    const long long per_token_range = (long long)H * (V / kCtaRows);
+    const long long have = per_token_range * B;
+    if (have >= 3LL * nsm || T <= 512) return {T > 0 ? T : 1, B};
+    const long long want = (6LL * nsm + per_token_range - 1) / per_token_range;  // segments in all
+    long long len = (packed ? T : (long long)T * B) / want;
+    len = len < 256 ? 256 : (len + 15) / 16 * 16;
+    if (len * 2 > T) return {T, B};
+    const long long n = (T + len - 1) / len;
+    return {(int)len, (int)(packed ? n + B : n * B)};
+}
+
+template <typename T>
+cudaError_t launch_token(const LinearScan &p, float *slots, cudaStream_t st) {
+    const SegPlan plan = token_plan(p.B, p.T, p.H, p.V, p.offsets != nullptr);
+    const bool cut = plan.items > p.B;
+    const long long grid = (long long)plan.items * p.H * (p.V / kCtaRows);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    int *status = device_status_ptr();
+    auto run = [&](const float *in, float *out) {
+        switch (p.K) {
+            case 32: linear_token_kernel<T, 32><<<(unsigned)grid, kScanThreads, 0, st>>>(p, plan, in, out, status); break;
+            case 64: linear_token_kernel<T, 64><<<(unsigned)grid, kScanThreads, 0, st>>>(p, plan, in, out, status); break;
+            case 128: linear_token_kernel<T, 128><<<(unsigned)grid, kScanThreads, 0, st>>>(p, plan, in, out, status); break;
+            default: return cudaErrorInvalidValue;
+        }
+        return cudaGetLastError();
+    };
+    if (cut) {
+        const cudaError_t e = run(nullptr, slots);
+        if (e != cudaSuccess) return e;
+    }
+    return run(cut ? slots : nullptr, nullptr);
+}
+
+// ------------------------------------------------------------------ step
+//
+// S <- a S + v k^T, o = scale S q, one read and one write of the state: 8 V K
+// bytes a head, bound by memory.  K / 4 lanes own a row as float4 pieces; a
+// lane's row loads are all issued before any arithmetic.
+constexpr int kStepThreads = 128;
+constexpr int kStepRows = 4;  // rows of a lane
+
+__device__ __forceinline__ float4 load4(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kStepThreads)
+    linear_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                       const float *__restrict__ alpha, const float *S, float *S_out,
+                       T *__restrict__ o, int H, int group, int V, int blocks, float scale) {
+    constexpr int LPR = K / 4, RPW = 32 / LPR;
+    const int bh = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cl = lane % LPR;
+    const int row0 = (blk * (kStepThreads / 32) + warp) * RPW * kStepRows + lane / LPR;
+    const size_t head = (size_t)bh * V;
+    // the previous step's states are complete before the first read
+    pdl_wait();
+    float4 s[kStepRows];
+    float w[kStepRows];
+#pragma unroll
+    for (int r = 0; r < kStepRows; ++r) {
+        const int row = row0 + r * RPW;
+        if (row < V) {
+            s[r] = load4(S + (head + row) * K + 4 * cl);
+            w[r] = to_f32(v[head + row]);
+        } else {
+            s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            w[r] = 0.f;
+        }
+    }
+    const int hq = bh / group;  // [B, H] -> [B, Hq], H = group Hq
+    const float4 kf = load4(k + (size_t)hq * K + 4 * cl), qf = load4(q + (size_t)hq * K + 4 * cl);
+    const float a = alpha[bh % H];
+    pdl_trigger();
+#pragma unroll
+    for (int r = 0; r < kStepRows; ++r) {
+        const int row = row0 + r * RPW;
+        float4 x = s[r];
+        x.x = fmaf(w[r], kf.x, a * x.x);
+        x.y = fmaf(w[r], kf.y, a * x.y);
+        x.z = fmaf(w[r], kf.z, a * x.z);
+        x.w = fmaf(w[r], kf.w, a * x.w);
+        float d = x.x * qf.x + x.y * qf.y + x.z * qf.z + x.w * qf.w;
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+        if (row < V) {
+            *reinterpret_cast<float4 *>(S_out + (head + row) * K + 4 * cl) = x;
+            if (cl == 0) o[head + row] = from_f32<T>(scale * d);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_step(const void *q, const void *k, const void *v, const float *alpha,
+                        const float *S, float *S_out, void *o, int B, int Hq, int H, int K, int V,
+                        float scale, cudaStream_t st) {
+    const int rows = (kStepThreads / 32) * (32 / (K / 4)) * kStepRows;
+    const int blocks = (V + rows - 1) / rows;
+    const long long grid = (long long)B * H * blocks;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, (unsigned)grid, kStepThreads, 0, st, static_cast<const T *>(q),
+                          static_cast<const T *>(k), static_cast<const T *>(v), alpha, S, S_out,
+                          static_cast<T *>(o), H, H / Hq, V, blocks, scale);
+    };
+    switch (K) {
+        case 32: return go(linear_step_kernel<T, 32>);
+        case 64: return go(linear_step_kernel<T, 64>);
+        case 128: return go(linear_step_kernel<T, 128>);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// Sums over the heads of a group, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) group_sum_kernel(const float *x, T *y, long long pieces,
+                                                        int group, int D) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= pieces) return;
+    const int per = D / 8;
+    const long long row = i / per;
+    const float *src = x + row * group * D + (i - row * per) * 8;
+    float s[8] = {};
+    for (int g = 0; g < group; ++g) {
+        Vec8<float> v;
+        v.load(src + (long long)g * D);
+        float u[8];
+        v.get(u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += u[e];
+    }
+    Vec8<T>::store(y + i * 8, s);
+}
+
+}  // namespace
+
+size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt) {
+    (void)dt;
+    const SegPlan plan = token_plan(B, T, H, V, packed);
+    return plan.items > B ? (size_t)plan.items * H * V * K * sizeof(float) : 0;
+}
+
+cudaError_t launch_linear_scan(const LinearScan &a, gdn_dtype dt, void *workspace,
+                               cudaStream_t stream) {
+    float *slots = static_cast<float *>(workspace);
+    return dt == GDN_BF16 ? launch_token<__nv_bfloat16>(a, slots, stream)
+                          : launch_token<float>(a, slots, stream);
+}
+
+cudaError_t launch_group_sum(const float *x, void *y, long long rows, int Hq, int group, int D,
+                             gdn_dtype dt, cudaStream_t stream) {
+    const long long pieces = rows * Hq * (D / 8), grid = (pieces + 255) / 256;
+    if (grid == 0) return cudaSuccess;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (dt == GDN_BF16)
+        group_sum_kernel<<<(unsigned)grid, 256, 0, stream>>>(x, static_cast<__nv_bfloat16 *>(y),
+                                                             pieces, group, D);
+    else
+        group_sum_kernel<<<(unsigned)grid, 256, 0, stream>>>(x, static_cast<float *>(y), pieces,
+                                                             group, D);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *alpha,
+                                 const float *S, float *S_out, void *o, int B, int Hq, int H,
+                                 int K, int V, float scale, gdn_dtype dt, cudaStream_t stream) {
+    return dt == GDN_BF16 ? launch_step<__nv_bfloat16>(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V,
+                                                       scale, stream)
+                          : launch_step<float>(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale,
+                                               stream);
+}
+
+}  // namespace gdn

@@ -1,0 +1,157 @@
+// One scan of linear attention with a decay a = alpha[h] for each head, as
+// both the prompt pass and each of the three gradients need it:
+//
+//     S <- a S + write_scale v_t k_t^T
+//     o_t = read_scale S q_t
+//
+// over the tokens of a sequence, first to last, or last to first (`reverse`).
+// The gradients of o_t = scale S_t q_t are scans of the same form:
+//
+//     dq_t = scale S_t^T do_t            first to last on (q, k, v) = (do, v, k)
+//     dk_t = R_t^T v_t,  dv_t = R_t k_t  last to first on (v, do, q) and (k, q, do)
+//     R_t  = a R_{t+1} + scale do_t q_t^T,  dS0 = a R_1
+//
+// with the states transposed where k and v change places (s0_transposed: the
+// start state is given as [K, V]).  What differs in a reversed scan: R takes
+// dS_T up before the last token without a decay, and the state that is
+// returned has decayed once more (dS0 = a R_1).
+//
+// Sequences are cut into segments of seg_len tokens when there are few of
+// them: the end state is linear in what was written, so a first pass finds
+// each segment's end state from a zero start, and the second starts each
+// segment from the decayed sum of the others'.
+#pragma once
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+
+struct SegPlan {
+    int seg_len;  // tokens of a segment
+    int items;    // upper bound of the segments of all sequences (dense: the number)
+};
+
+// One segment of one sequence.
+struct LinearItem {
+    int seq;           // -1: nothing to do
+    int base;          // the sequence's first token (packed), or its number x T
+    long long first;   // base in tokens from the start of the tensors
+    int len;           // tokens of the sequence
+    int j, n;          // this segment and the number of them (>= 1)
+    int slot0;         // slot of segment 0 in the workspace
+};
+
+// The item-th segment, found by the calling warp (every lane returns it).
+// Bad offsets give an empty sequence and the bounds bit of the status.
+__device__ __forceinline__ LinearItem linear_item(const int *offsets, int B, int T, int seg_len,
+                                                  int item, int *status) {
+    LinearItem r;
+    if (!offsets) {
+        const int n = T > seg_len ? (T + seg_len - 1) / seg_len : 1;
+        r.seq = item / n;
+        r.j = item - r.seq * n;
+        r.n = n;
+        r.slot0 = r.seq * n;
+        r.len = T;
+        r.first = (long long)r.seq * T;
+        r.base = 0;
+        if (r.seq >= B) r.seq = -1;
+        return r;
+    }
+    const int lane = threadIdx.x & 31;
+    int before = 0;  // segments of the sequences before this warp-wide piece
+    r.seq = -1;
+    for (int s0 = 0; s0 < B; s0 += 32) {
+        const int s = s0 + lane;
+        int a = 0, len = 0, n = 0;
+        if (s < B) {
+            a = offsets[s];
+            const int b = offsets[s + 1];
+            if (a < 0 || b < a || b > T) {
+                if (status) atomicOr(status, kStatusBounds);
+                a = 0;
+            } else {
+                len = b - a;
+            }
+            n = len > seg_len ? (len + seg_len - 1) / seg_len : 1;
+        }
+        int incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        const int excl = before + incl - n;
+        const bool mine = n > 0 && item >= excl && item < excl + n;
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        if (who) {
+            const int l = __ffs(who) - 1;
+            r.seq = s0 + l;
+            r.base = __shfl_sync(0xffffffffu, a, l);
+            r.len = __shfl_sync(0xffffffffu, len, l);
+            r.n = __shfl_sync(0xffffffffu, n, l);
+            r.slot0 = __shfl_sync(0xffffffffu, excl, l);
+            r.j = item - r.slot0;
+            r.first = r.base;
+            return r;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return r;
+}
+
+// log2 of a decay; 0 becomes a number whose multiples exp2 takes to 0 while
+// 0 times it stays 0 (a^0 = 1).
+__device__ __forceinline__ float decay_log2(float a) { return fmaxf(log2f(a), -1e30f); }
+
+// Tokens between the end of segment i and the start (in scan order) of
+// segment j of a sequence, i before j in scan order.
+__device__ __forceinline__ int tokens_between(int i, int j, int len, int seg_len, bool reverse) {
+    if (!reverse) return (j - i - 1) * seg_len;
+    const int end = (j + 1) * seg_len < len ? (j + 1) * seg_len : len;
+    return i * seg_len - end;
+}
+
+// One element of the start state that the caller gives.
+__device__ __forceinline__ float given_start(const float *S0, bool transposed, size_t head, int V,
+                                             int K, int v, int k) {
+    const float *p = S0 + head * V * K;
+    return transposed ? p[(size_t)k * V + v] : p[(size_t)v * K + k];
+}
+
+// One element of a segment's start state: S0 and the segments before it in
+// scan order, from their end states in `slots` ([slot][H][V][K]).  The slot of
+// a sequence's last segment in scan order, whose end nothing starts from, holds
+// a copy of S0: the end states may be written over S0 while segments start.
+__device__ __forceinline__ float linear_start(const LinearItem &it, const float *S0,
+                                              bool s0_transposed, const float *slots, int h, int H,
+                                              int V, int K, int v, int k, int seg_len, float lg,
+                                              bool reverse) {
+    float s = 0.f;
+    const size_t VK = (size_t)V * K;
+    if (S0) {
+        s = slots ? slots[((size_t)(it.slot0 + (reverse ? 0 : it.n - 1)) * H + h) * VK +
+                          (size_t)v * K + k]
+                  : given_start(S0, s0_transposed, (size_t)it.seq * H + h, V, K, v, k);
+        const int past = reverse ? (it.j == it.n - 1 ? 0 : it.len - (it.j + 1) * seg_len)
+                                 : it.j * seg_len;
+        // a reversed scan takes its start state up undecayed
+        const int steps = reverse && past > 0 ? past - 1 : past;
+        if (steps > 0) s *= exp2f((float)steps * lg);
+    }
+    if (slots) {
+        for (int i = 0; i < it.n; ++i) {
+            if (reverse ? i <= it.j : i >= it.j) continue;
+            const int gap = tokens_between(i, it.j, it.len, seg_len, reverse);
+            s = fmaf(exp2f((float)gap * lg), slots[((size_t)(it.slot0 + i) * H + h) * VK + (size_t)v * K + k], s);
+        }
+    }
+    return s;
+}
+
+// The scan on the tensor cores (bf16, K and V of 64 or 128); the segments it
+// takes.
+SegPlan linear_tc_plan(int B, int T, int H, int K, int V, bool packed);
+cudaError_t launch_linear_tc(const LinearScan &a, float *slots, cudaStream_t stream);
+
+}  // namespace gdn

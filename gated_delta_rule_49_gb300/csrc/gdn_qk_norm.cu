@@ -1,0 +1,281 @@
+// Norms of queries and keys for each head with the position rotation in the
+// same pass, and its backward pass.
+//
+// For one head's channels x of one token (D channels, R <= D of them rotated):
+//
+//     r = (c sum_i x_i^2 + eps)^(-1/2),  c = 1/D (RMS) or 1 (L2)
+//     n = w .* x r
+//     y = rotate(n): pairs (i, i + R/2) or (2i, 2i + 1), i < R/2, turned by
+//         the angle pos * inv_freq[i]; channels >= R pass unchanged
+//
+// Backward, g = rotate^T(dy) and h = w .* g:
+//
+//     dw_i = sum over tokens and heads of g_i x_i r
+//     dx   = r (h - c r^2 x (x . h))
+//
+// Bound by memory: x read once and y written once (backward: x and dy read,
+// dx written).  A row of D channels is held by D / 8 lanes, 8 channels each,
+// so that a lane's load is one 16-byte piece in bf16 and two in float32, and
+// norms and the pairs of the half layout are exchanged by shuffles.  The
+// angles of a tile of tokens are formed once, in shared memory, and serve all
+// of their heads: float64 product and reduction to a fraction of a turn (an
+// angle of 1e6 has lost 4 of its digits in float32), then a float32 sincospi
+// of that fraction.
+#include "gdn_vec8.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct QkNormArgs {
+    const void *q, *k, *dyq, *dyk;
+    const float *wq, *wk;
+    const long long *pos;
+    const float *inv_freq;
+    void *yq, *yk;  // backward: dq, dk
+    float *partial;  // backward: [grid][2][D]
+    long long N, ldq, ldk;
+    int Hq, Hk, R;
+    float eps;
+};
+
+template <int LPR> __device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// x of the lane's channels [8 c, 8 c + 8) turned by the token's angles; `sign`
+// -1 turns back.  R is a multiple of 16, so R / 2 is a whole number of lanes.
+template <int LPR, bool HALF>
+__device__ __forceinline__ void rotate8(float (&x)[8], const float2 *cs, int R, int c, int lane,
+                                        float sign) {
+    if constexpr (HALF) {
+        const int half = R >> 4;  // lanes of one half of the rotated channels
+        const int row0 = lane - c;
+        const bool turned = c < 2 * half;
+        const bool low = c < half;
+        const int other = turned ? row0 + (low ? c + half : c - half) : lane;
+        const float2 *t = cs + 8 * (low ? c : c - half);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = __shfl_sync(0xffffffffu, x[i], other);
+            if (turned) {
+                const float2 u = t[i];
+                const float s = low ? -sign * u.y : sign * u.y;
+                x[i] = fmaf(x[i], u.x, y * s);
+            }
+        }
+    } else {
+        if (8 * c < R) {
+            const float2 *t = cs + 4 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 u = t[i];
+                const float s = sign * u.y, a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = fmaf(a, u.x, -b * s);
+                x[2 * i + 1] = fmaf(a, s, b * u.x);
+            }
+        }
+    }
+}
+
+// cos and sin of every angle of tokens [t0, t0 + nt).
+__device__ __forceinline__ void fill_angles(float2 *cs, const QkNormArgs &p, long long t0, int nt) {
+    const int half = p.R >> 1;
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+        const int t = i / half, f = i - t * half;
+        double turns = (double)p.pos[t0 + t] * (double)p.inv_freq[f] * 0.15915494309189533577;
+        turns -= rint(turns);
+        float s, c;
+        sincospif(2.f * (float)turns, &s, &c);
+        cs[i] = make_float2(c, s);
+    }
+}
+
+// One CTA takes tiles of TT tokens with all of their heads.
+template <typename T, int D, bool HALF, bool BACK>
+__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs p, int TT, float c_norm) {
+    constexpr int LPR = D / 8;             // lanes of a row
+    constexpr int ROWS = kThreads / LPR;   // rows in flight
+    extern __shared__ __align__(16) float2 cs[];
+    const int lane = threadIdx.x & 31;
+    const int c = threadIdx.x % LPR;
+    const int heads = p.Hq + p.Hk;
+    float wq[8], wk[8], dwq[8], dwk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        wq[i] = p.wq ? p.wq[8 * c + i] : 1.f;
+        wk[i] = p.wk ? p.wk[8 * c + i] : 1.f;
+        dwq[i] = dwk[i] = 0.f;
+    }
+    for (long long t0 = (long long)blockIdx.x * TT; t0 < p.N; t0 += (long long)gridDim.x * TT) {
+        const int nt = (int)min((long long)TT, p.N - t0);
+        __syncthreads();  // the previous tile's angles are read
+        fill_angles(cs, p, t0, nt);
+        __syncthreads();
+        const int rows = nt * heads;
+        for (int r0 = 0; r0 < rows; r0 += ROWS) {
+            const int r = r0 + threadIdx.x / LPR;
+            const bool live = r < rows;
+            const int t = live ? r / heads : 0;
+            const int h = live ? r - t * heads : 0;
+            const bool isq = h < p.Hq;
+            const long long tok = t0 + t;
+            const T *src = isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
+                               : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D;
+            const long long dst = (isq ? (tok * p.Hq + h) : (tok * p.Hk + h - p.Hq)) * D + 8 * c;
+            float x[8] = {}, g[8];
+            if (live) {
+                Vec8<T> raw;
+                raw.load(src + 8 * c);
+                raw.get(x);
+            }
+            if constexpr (BACK) {
+                Vec8<T> raw;
+                if (live) {
+                    raw.load(static_cast<const T *>(isq ? p.dyq : p.dyk) + dst);
+                    raw.get(g);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = 0.f;
+                }
+            }
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            ss = row_sum<LPR>(ss);
+            const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
+            const float2 *ct = cs + t * (p.R >> 1);
+            if constexpr (!BACK) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= rn * (isq ? wq[i] : wk[i]);
+                rotate8<LPR, HALF>(x, ct, p.R, c, lane, 1.f);
+            } else {
+                rotate8<LPR, HALF>(g, ct, p.R, c, lane, -1.f);
+                float dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = g[i] * (x[i] * rn);
+                    if (isq) dwq[i] += live ? d : 0.f;
+                    else dwk[i] += live ? d : 0.f;
+                    g[i] *= isq ? wq[i] : wk[i];
+                    dot = fmaf(x[i], g[i], dot);
+                }
+                dot = row_sum<LPR>(dot) * c_norm * rn * rn;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = rn * fmaf(-dot, x[i], g[i]);
+            }
+            if (live) Vec8<T>::store(static_cast<T *>(isq ? p.yq : p.yk) + dst, x);
+        }
+    }
+    if constexpr (BACK) {
+        if (!p.partial) return;
+        // sums over this CTA's rows, in the fixed order of its threads
+        float *red = reinterpret_cast<float *>(cs);
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                red[(threadIdx.x / LPR) * D + 8 * c + i] = which ? dwk[i] : dwq[i];
+            __syncthreads();
+            for (int d = threadIdx.x; d < D; d += kThreads) {
+                float s = 0.f;
+                for (int r = 0; r < ROWS; ++r) s += red[r * D + d];
+                p.partial[((long long)blockIdx.x * 2 + which) * D + d] = s;
+            }
+        }
+    }
+}
+
+// dw[which][d] = sum over the CTAs of their partial sums, in a fixed order.
+__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float *partial, int n, int D,
+                                                         float *dwq, float *dwk) {
+    __shared__ float red[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;  // of 2 D
+    float s = 0.f;
+    for (int i = w; i < n; i += 8) s += partial[(long long)i * 2 * D + col];
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0) {
+        float t = 0.f;
+        for (int i = 0; i < 8; ++i) t += red[i][lane];
+        float *dst = col < D ? dwq : dwk;
+        if (dst) dst[col < D ? col : col - D] = t;
+    }
+}
+
+int tile_tokens(int heads, int D) {
+    // about 8 rows a lane group: the angles of a tile then cost one sincospi
+    // a thread next to 8 rows of work
+    // (at most 32 KB of angles)
+    const int tokens = 8 * kThreads / (D / 8) / heads, most = 8192 / D;
+    return tokens < 1 ? 1 : (tokens > most ? most : tokens);
+}
+
+template <typename T, bool HALF, bool BACK>
+cudaError_t launch_d(const QkNormArgs &p, int D, float c, int grid, int TT, size_t smem,
+                     cudaStream_t st) {
+    switch (D) {
+        case 32: qk_norm_kernel<T, 32, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
+        case 64: qk_norm_kernel<T, 64, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
+        case 128: qk_norm_kernel<T, 128, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
+        case 256: qk_norm_kernel<T, 256, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
+        default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+template <bool BACK>
+cudaError_t launch_any(const QkNormArgs &p, int D, float c, bool half, gdn_dtype dt, int grid,
+                       int TT, cudaStream_t st) {
+    size_t smem = (size_t)TT * (p.R / 2) * sizeof(float2);
+    if (BACK && smem < kThreads * 8 * sizeof(float)) smem = kThreads * 8 * sizeof(float);
+    if (dt == GDN_BF16)
+        return half ? launch_d<__nv_bfloat16, true, BACK>(p, D, c, grid, TT, smem, st)
+                    : launch_d<__nv_bfloat16, false, BACK>(p, D, c, grid, TT, smem, st);
+    return half ? launch_d<float, true, BACK>(p, D, c, grid, TT, smem, st)
+                : launch_d<float, false, BACK>(p, D, c, grid, TT, smem, st);
+}
+
+}  // namespace
+
+int qk_norm_backward_grid(long long N, int heads, int D) {
+    const long long tiles = (N + tile_tokens(heads, D) - 1) / tile_tokens(heads, D);
+    const long long most = 4LL * (sm_count() > 0 ? sm_count() : 152);
+    return (int)(tiles < most ? tiles : most);
+}
+
+cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
+                           const long long *pos, const float *inv_freq, void *yq, void *yk,
+                           long long N, int Hq, int Hk, int D, int R, long long ldq, long long ldk,
+                           bool l2, bool half, float eps, gdn_dtype dt, cudaStream_t st) {
+    QkNormArgs p = {q, k, nullptr, nullptr, wq, wk, pos, inv_freq, yq, yk, nullptr,
+                    N, ldq, ldk, Hq, Hk, R, eps};
+    const int TT = tile_tokens(Hq + Hk, D);
+    const long long tiles = (N + TT - 1) / TT;
+    const int grid = (int)(tiles < 0x7fffffff ? tiles : 0x7fffffff);
+    return launch_any<false>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid, TT, st);
+}
+
+cudaError_t launch_qk_norm_backward(const void *q, const void *k, const float *wq,
+                                    const float *wk, const long long *pos, const float *inv_freq,
+                                    const void *dyq, const void *dyk, void *dq, void *dk,
+                                    float *dwq, float *dwk, long long N, int Hq, int Hk, int D,
+                                    int R, long long ldq, long long ldk, bool l2, bool half,
+                                    float eps, gdn_dtype dt, float *partial, cudaStream_t st) {
+    const bool want = dwq || dwk;
+    QkNormArgs p = {q, k, dyq, dyk, wq, wk, pos, inv_freq, dq, dk, want ? partial : nullptr,
+                    N, ldq, ldk, Hq, Hk, R, eps};
+    const int grid = qk_norm_backward_grid(N, Hq + Hk, D);
+    const cudaError_t e = launch_any<true>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid,
+                                           tile_tokens(Hq + Hk, D), st);
+    if (e != cudaSuccess || !want) return e;
+    qk_norm_dw_kernel<<<2 * D / 32, 256, 0, st>>>(partial, grid, D, dwq, dwk);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

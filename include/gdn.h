@@ -454,6 +454,126 @@ GDN_API int gdn_drrqr_select(const float *G, int H, int n, int k, float f, int m
                              int *idx, float *rho_max, int *swaps, void *stream);
 
 /*
+ * gdn_qk_norm_rotate -- norms of queries and keys for each head and the
+ * position rotation, in one pass.  For the D channels x of one token and head:
+ *
+ *     r = (c sum_i x_i^2 + eps)^(-1/2),  c = 1/D (GDN_NORM_RMS) or 1 (GDN_NORM_L2)
+ *     n = w .* x r
+ *     y = n with the pairs (i, i + R/2) (GDN_PAIR_HALF) or (2i, 2i + 1)
+ *         (GDN_PAIR_ADJACENT), i < R/2, turned by pos * inv_freq[i]:
+ *         (a, b) -> (a cos - b sin, a sin + b cos); channels >= R pass
+ *
+ *   q [N, Hq, D], k [N, Hk, D] (dtype): consecutive tokens q_stride / k_stride
+ *          elements apart (>= Hq D / Hk D, a multiple of 16 bytes), so that they
+ *          may be parts of one projection; Hq or Hk may be 0 (pointer ignored)
+ *   wq, wk [D] float32, or NULL for ones
+ *   pos    [N] int64, any value: angles are formed in float64
+ *   inv_freq [R/2] float32       (pos and inv_freq may be NULL when R = 0)
+ *   yq, yk (dtype), dense; may be q / k themselves where those are dense
+ *
+ * D in {32, 64, 128, 256} and R a multiple of 16 up to D (else
+ * GDN_ERR_UNSUPPORTED).  Everything is float32 from the load to the one
+ * rounding of y.
+ */
+typedef enum { GDN_NORM_RMS = 0, GDN_NORM_L2 = 1 } gdn_norm;
+typedef enum { GDN_PAIR_HALF = 0, GDN_PAIR_ADJACENT = 1 } gdn_pairing;
+GDN_API int gdn_qk_norm_rotate(const void *q, const void *k, const float *wq, const float *wk,
+                               const long long *pos, const float *inv_freq, void *yq, void *yk,
+                               long long N, int Hq, int Hk, int D, int R, long long q_stride,
+                               long long k_stride, gdn_norm norm, gdn_pairing pairing, float eps,
+                               gdn_dtype dtype, void *stream);
+
+/*
+ * gdn_qk_norm_rotate_backward -- gradients of gdn_qk_norm_rotate from its
+ * inputs and dyq, dyk (dense, dtype): dq, dk (dense, dtype), and dwq, dwk [D]
+ * float32 (each may be NULL; needs its weight).  With g = y's gradient turned
+ * back and h = w .* g: dw = sum g .* x r, dx = r (h - c r^2 x (x . h)).
+ * dq / dk may be dyq / dyk.  The weights' gradients need a workspace of
+ * gdn_qk_norm_rotate_backward_workspace_size bytes and are summed in a fixed
+ * order: equal inputs give equal bits.
+ */
+GDN_API size_t gdn_qk_norm_rotate_backward_workspace_size(long long N, int Hq, int Hk, int D);
+GDN_API int gdn_qk_norm_rotate_backward(const void *q, const void *k, const float *wq,
+                                        const float *wk, const long long *pos,
+                                        const float *inv_freq, const void *dyq, const void *dyk,
+                                        void *dq, void *dk, float *dwq, float *dwk, long long N,
+                                        int Hq, int Hk, int D, int R, long long q_stride,
+                                        long long k_stride, gdn_norm norm, gdn_pairing pairing,
+                                        float eps, gdn_dtype dtype, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_linear_prefill -- linear attention with a fixed decay for each head,
+ * over the tokens of B sequences:
+ *
+ *     S_t = alpha[h] S_{t-1} + v_t k_t^T,     o_t = scale S_t q_t
+ *
+ * (the delta rule above without its erasing term; the pages' "linear
+ * attention" with a decay).
+ *
+ *   q, k  [B, T, Hq, K], v [B, T, H, V] (dtype); H a multiple of Hq, and heads
+ *         [g H/Hq, (g + 1) H/Hq) of v share head g of q and k.  Consecutive
+ *         tokens lie q_stride / k_stride / v_stride elements apart (at least
+ *         a dense token, a multiple of 16 bytes)
+ *   alpha [H] float32 in [0, 1] (not checked; 0^0 = 1)
+ *   S0    [B, H, V, K] float32, or NULL = zero
+ *   o     [B, T, H, V] (dtype), dense, or NULL
+ *   S_T   [B, H, V, K] float32, or NULL; may be S0
+ *   offsets  NULL, or [B + 1] int32 on the device: the B sequences lie packed
+ *         in T tokens, sequence b in [offsets[b], offsets[b + 1]) (an empty one
+ *         has S_T = S0).  Offsets that do not rise, or pass T, make that
+ *         sequence empty and set GDN_ERR_DEVICE_BOUNDS; tokens of no sequence
+ *         keep what o held.
+ *
+ * (K, V) in (32, 32), (64, 64), (64, 128), (128, 128).  A value that is not a
+ * number reaches the outputs of its own sequence only; among those it may reach
+ * tokens up to 127 before it, which are computed in one block with it.
+ * workspace: gdn_linear_prefill_workspace_size bytes (0 where the sequences
+ * alone fill the device), 256-byte aligned.
+ */
+GDN_API size_t gdn_linear_prefill_workspace_size(int B, int T, int H, int K, int V, int packed,
+                                                 gdn_dtype dtype);
+GDN_API int gdn_linear_prefill(const void *q, const void *k, const void *v, const float *alpha,
+                               const float *S0, void *o, float *S_T, const int *offsets, int B,
+                               int T, int Hq, int H, int K, int V, long long q_stride,
+                               long long k_stride, long long v_stride, float scale,
+                               gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * gdn_linear_backward -- gradients of gdn_linear_prefill from its inputs and
+ * dO [B, T, H, V] (dtype, dense) and dS_T [B, H, V, K] float32 (NULL = zero):
+ *
+ *     dq_t = scale S_t^T dO_t,   dk_t = R_t^T v_t,   dv_t = R_t k_t,   dS0 = alpha R_1,
+ *     R_t = alpha R_{t+1} + scale dO_t q_t^T   (R_T takes dS_T up undecayed)
+ *
+ * dq, dk [B, T, Hq, K] (summed over the heads that share them, in float32 and
+ * in a fixed order) and dv [B, T, H, V] (dtype, dense), dS0 [B, H, V, K]
+ * float32; each may be NULL, one at least is wanted.  S0 as given to the
+ * forward pass (NULL = zero; the states are recomputed, none is kept from it).
+ * The decays are constants of the model and have no gradient.  dS0 may be dS_T.
+ */
+GDN_API size_t gdn_linear_backward_workspace_size(int B, int T, int Hq, int H, int K, int V,
+                                                  int packed, gdn_dtype dtype);
+GDN_API int gdn_linear_backward(const void *q, const void *k, const void *v, const float *alpha,
+                                const void *dO, const float *S0, const float *dS_T, void *dq,
+                                void *dk, void *dv, float *dS0, const int *offsets, int B, int T,
+                                int Hq, int H, int K, int V, long long q_stride,
+                                long long k_stride, long long v_stride, float scale,
+                                gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
+ * gdn_linear_decode_step -- one token of gdn_linear_prefill: q, k [B, Hq, K],
+ * v, o [B, H, V] (dtype, dense), alpha [H]; reads S [B, H, V, K] float32 and
+ * writes S_out, which may be S.
+ */
+GDN_API int gdn_linear_decode_step(const void *q, const void *k, const void *v,
+                                   const float *alpha, const float *S, float *S_out, void *o,
+                                   int B, int Hq, int H, int K, int V, float scale,
+                                   gdn_dtype dtype, void *stream);
+
+/*
  * gdn_get_last_device_status -- synchronise `stream`, then read and clear the
  * current device's status word.  Returns GDN_OK, GDN_ERR_TIMEOUT,
  * GDN_ERR_DEVICE_BOUNDS, GDN_WARN_NOT_CONVERGED, GDN_WARN_RANK_DEFICIENT or
