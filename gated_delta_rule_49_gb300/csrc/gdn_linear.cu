@@ -334,15 +334,21 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float *x, T *y, lo
 
 }  // namespace
 
+// bf16 runs on the tensor cores where a tile fills them
+static bool on_tensor_cores(int K, int V, gdn_dtype dt) {
+    return dt == GDN_BF16 && K >= 64 && V >= 64;
+}
+
 size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt) {
-    (void)dt;
-    const SegPlan plan = token_plan(B, T, H, V, packed);
+    const SegPlan plan = on_tensor_cores(K, V, dt) ? linear_tc_plan(B, T, H, K, V, packed)
+                                                   : token_plan(B, T, H, V, packed);
     return plan.items > B ? (size_t)plan.items * H * V * K * sizeof(float) : 0;
 }
 
 cudaError_t launch_linear_scan(const LinearScan &a, gdn_dtype dt, void *workspace,
                                cudaStream_t stream) {
     float *slots = static_cast<float *>(workspace);
+    if (on_tensor_cores(a.K, a.V, dt)) return launch_linear_tc(a, slots, stream);
     return dt == GDN_BF16 ? launch_token<__nv_bfloat16>(a, slots, stream)
                           : launch_token<float>(a, slots, stream);
 }

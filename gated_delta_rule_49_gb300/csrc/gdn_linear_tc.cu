@@ -1,0 +1,626 @@
+// Linear attention with a decay for each head on the tensor cores (bf16 q, k,
+// v; K and V of 64 or 128), in chunks of C = 128 tokens.  With p the place of
+// a token in scan order within its chunk and S the state at the chunk's start:
+//
+//     O = diag(read a^(p_t + 1)) [Q S^T + P V],
+//         P_ts = write a^(-(p_s + 1)) (q_t . k_s) where p_s <= p_t, else 0
+//     S <- a^C S + D,   D = (diag(write a^(C - 1 - p_s)) V)^T K
+//
+// The row factor stands outside of both products, so that they share one
+// accumulator.  Where a^128 would leave 2^-64 .. 1 the row factor is held at
+// 2^-64 and P takes the exact remaining power; what that mis-weights is S's
+// part of rows that have decayed by more than 2^-64.
+//
+// Precision: P and S are rounded to bf16 as operands (a step of the bf16
+// output each).  The state itself has to be a float32 result, so the weighted
+// V goes in as hi + lo bf16 pieces, D is formed chunk by chunk from zero in
+// the float32 accumulator, and S is kept in float32 registers, added to with
+// rounding (an accumulator carried through all chunks would be cut, not
+// rounded, at every product).
+//
+// One CTA runs one segment of one (sequence, head), 20 warps in groups of 4:
+//   0-3   P: row t of Q K^T from TMEM, weighted, back to TMEM as bf16 (over
+//         the columns that it came from) for the product with V
+//   4-7   O: row t from TMEM, scaled, to shared memory in Q's place and out by
+//         TMA (ragged chunks: plain stores)
+//   8-15  state: two groups of 128 threads (value channel v each); the first
+//         takes tokens 0-63 and state columns [0, K/2), the second the rest:
+//         column v of V from shared memory, weighted, split and written to
+//         TMEM as an A operand; then S's row piece: S = a^C S + D, and as bf16
+//         to shared memory for the next chunk's Q S^T
+//   16    TMA loads of Q, K, V, two chunks ahead
+//   17    issues the MMAs (18 and 19 only fill the group)
+// Launched with 96 registers a thread (5 groups x 128 threads x 96 = 61440);
+// the groups then share the same 480 registers a lane of the five as
+// 88 + 80 + 2 x 136 + 40, so that S, a row piece of 64 floats, needs no spill.
+// TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64.
+#include <cstring>
+
+#include "gdn_chunk.cuh"
+#include "gdn_internal.cuh"
+#include "gdn_linear.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kC = 128;             // tokens of a chunk
+constexpr int kStages = 2;
+constexpr int kWarps = 20;
+constexpr int kBarP = 1, kBarO = 2, kBarS = 3;  // named barriers
+constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColLo = 448;
+
+template <int K, int V>
+struct LinLayout {
+    static constexpr uint32_t QSLOT = kC * 2 * (K > V ? K : V);  // also takes O
+    static constexpr uint32_t KSLOT = kC * 2 * K;
+    static constexpr uint32_t VSLOT = kC * 2 * V;
+    static constexpr uint32_t Q = 0;
+    static constexpr uint32_t KK = Q + kStages * QSLOT;
+    static constexpr uint32_t VV = KK + kStages * KSLOT;
+    static constexpr uint32_t S = VV + kStages * VSLOT;
+    static constexpr uint32_t TABLE = S + 2 * K * V;  // column factors of P, weights of V
+    static constexpr uint32_t SMEM = TABLE + 2 * kC * 4 + 1024;  // + alignment
+};
+
+template <int N> __device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct LinBars {
+    uint64_t full[kStages], kvfree[kStages], qfree[kStages];
+    uint64_t scores, p, vw, d, s, o, ofree, tail;
+};
+
+struct LinTcArgs {
+    LinearScan a;
+    SegPlan plan;
+    const float *slots_in;
+    float *slots_out;
+    int *status;
+};
+
+template <int K, int V>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                     const LinTcArgs arg) {
+    using L = LinLayout<K, V>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ LinBars bar;
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    volatile int *abort_v = &abort_flag;
+
+    const LinearScan &p = arg.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % p.H;
+    const LinearItem it =
+        linear_item(p.offsets, p.B, p.T, arg.plan.seg_len, blockIdx.x / p.H, arg.status);
+    if (it.seq < 0) return;
+    const bool rev = p.reverse;
+    const bool last = rev ? it.j == 0 : it.j == it.n - 1;  // segment, in scan order
+    const bool first = rev ? it.j == it.n - 1 : it.j == 0;
+    float *const slot = arg.slots_out
+                            ? arg.slots_out + ((size_t)(it.slot0 + it.j) * p.H + h) * V * K
+                            : nullptr;
+    if (slot && last) {  // nothing starts from its end: the slot takes a copy of S0
+        if (p.S0)
+            for (int i = tid; i < V * K; i += kWarps * 32)
+                slot[i] = given_start(p.S0, p.s0_transposed, (size_t)it.seq * p.H + h, V, K, i / K,
+                                      i % K);
+        return;
+    }
+    const bool want_o = p.o && !slot;
+    float *const end = slot ? slot
+                       : p.ST && last ? p.ST + ((size_t)it.seq * p.H + h) * V * K : nullptr;
+    const int f0 = it.j * arg.plan.seg_len;
+    const int tokens = min(it.len - f0, arg.plan.seg_len);
+    const int nc = (tokens + kC - 1) / kC;
+    // i-th chunk in scan order: first token (from the segment's first) and number
+    auto chunk_at = [&](int i) { return (rev ? nc - 1 - i : i) * kC; };
+    auto chunk_n = [&](int i) { return min(kC, tokens - chunk_at(i)); };
+    // a reversed scan takes its start state up undecayed
+    auto chunk_lead = [&](int i) { return rev && first && i == 0 ? 0 : 1; };
+    const float lg = decay_log2(p.alpha[h]);
+
+    if (warp == 17) {
+        tmem_alloc(&tmem_at, 512);
+        tmem_relinquish();
+        if (lane == 0) {
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(&bar.full[s], 1);
+                mbar_init(&bar.kvfree[s], 1);
+                mbar_init(&bar.qfree[s], 1);
+            }
+            mbar_init(&bar.scores, 1);
+            mbar_init(&bar.p, 4);
+            mbar_init(&bar.vw, 8);
+            mbar_init(&bar.d, 1);
+            mbar_init(&bar.s, 8);
+            mbar_init(&bar.o, 1);
+            mbar_init(&bar.ofree, 4);
+            mbar_init(&bar.tail, 8);
+            abort_flag = 0;
+            fence_mbar_init();
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    const uint32_t quad = (uint32_t)(warp & 3) << 21;  // 32 TMEM lanes of this warp
+    float *const colfac = reinterpret_cast<float *>(smem + L::TABLE);
+    float *const vweight = colfac + kC;
+
+    // After a wait has run out every later wait returns at once and nothing is
+    // written any more, but the loops keep their barriers and end.
+    bool dead = false;
+    auto wait = [&](uint64_t *b, uint32_t parity) {
+        if (dead) return;
+        if (!mbar_wait_or_abort(b, parity & 1, kSpinLimit, abort_v)) {
+            *abort_v = 1;
+            dead = true;
+        }
+    };
+    auto wait_warp = [&](uint64_t *b, uint32_t parity) {
+        wait(b, parity);
+        __syncwarp();
+    };
+    auto arrive_warp = [&](uint64_t *b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+    };
+
+    if (warp < 4) {
+        // ---------------------------------------------------------------- P
+        reg_dec<88>();
+        if (want_o) {
+            const int t = warp * 32 + lane;
+            const bool mild = lg * kC >= -64.f;
+            for (int i = 0; i < nc; ++i) {
+                const int n = chunk_n(i), lead = chunk_lead(i);
+                if (i == 0 || (rev && i == 1)) {  // the last tables' readers are done
+                    named_sync(kBarP, 128);
+                    const int ps = (rev ? n - 1 - t : t) + lead;  // of column t
+                    colfac[t] = ps < 0 || (rev && t >= n) ? 0.f
+                                : mild ? p.write_scale * exp2f(-(float)ps * lg) : p.write_scale;
+                    named_sync(kBarP, 128);
+                }
+                const int pt = (rev ? n - 1 - t : t) + lead;
+                const float lrho = fmaxf((float)pt * lg, -64.f);
+                wait_warp(&bar.scores, i);
+                tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {  // 32 columns
+                    uint32_t w[16];
+                    if (rev ? b < warp : b > warp) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = 0;
+                    } else {
+                        float x[32];
+                        tmem_ld32(tmem + quad + kColP + 32 * b, x);
+                        tmem_ld_wait();
+                        const float4 *f4 = reinterpret_cast<const float4 *>(colfac + 32 * b);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 f = f4[e];
+                            x[4 * e] *= f.x;
+                            x[4 * e + 1] *= f.y;
+                            x[4 * e + 2] *= f.z;
+                            x[4 * e + 3] *= f.w;
+                        }
+                        if (!mild) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int lag = rev ? 32 * b + e - t : t - 32 * b - e;
+                                x[e] *= lag < 0 ? 0.f : exp2f((float)lag * lg - lrho);
+                            }
+                        }
+                        if (b == warp) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (rev ? e < lane : e > lane) x[e] = 0.f;
+                        }
+                        pack_row(x, w);
+                    }
+                    tmem_st16(tmem + quad + kColP + 16 * b, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                arrive_warp(&bar.p);
+            }
+        }
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- O
+        reg_dec<80>();
+        if (want_o) {
+            const int t = (warp & 3) * 32 + lane;
+            for (int i = 0; i < nc; ++i) {
+                const int n = chunk_n(i), at = f0 + chunk_at(i);
+                const int pt = (rev ? n - 1 - t : t) + chunk_lead(i);
+                const float rho = p.read_scale * exp2f(fmaxf((float)pt * lg, -64.f));
+                uint8_t *const stage = smem + L::Q + (i % kStages) * L::QSLOT;
+                const bool whole = n == kC && !p.o_float;
+                const size_t row = ((size_t)(it.first + at + t) * p.H + h) * V;
+                wait_warp(&bar.o, i);
+                tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < V / 32; ++b) {
+                    float x[32];
+                    tmem_ld32(tmem + quad + kColO + 32 * b, x);
+                    tmem_ld_wait();
+                    if (p.o_float) {
+                        if (t < n && !dead) {
+                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row + 32 * b);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = make_float4(rho * x[4 * e], rho * x[4 * e + 1],
+                                                     rho * x[4 * e + 2], rho * x[4 * e + 3]);
+                        }
+                        continue;
+                    }
+                    if (whole) {
+                        store_row<4>(stage + (b / 2) * (kC * 128), t, (b % 2) * 4, x, rho);
+                    } else if (t < n && !dead) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] *= rho;
+                        pack_row(x, w);
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + row + 32 * b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    }
+                }
+                tc_fence_before();
+                arrive_warp(&bar.ofree);
+                if (whole) fence_proxy_async_smem();
+                named_sync(kBarO, 128);
+                if (warp == 4 && lane == 0) {
+                    if (whole && !dead) {
+                        const int c2 = p.offsets ? it.base + at : at, c3 = p.offsets ? 0 : it.seq;
+#pragma unroll
+                        for (int b = 0; b < V / 64; ++b)
+                            tma_store_4d(&mo, stage + b * (kC * 128), 64 * b, h, c2, c3);
+                        bulk_commit_group();
+                        bulk_wait_read_all();
+                    }
+                    mbar_arrive(&bar.qfree[i % kStages]);
+                }
+            }
+            if (warp == 4 && lane == 0) bulk_wait_all();
+        }
+    } else if (warp < 16) {
+        // ---------------------------------------------------------------- state
+        reg_inc<136>();
+        constexpr int NS = K / 2;
+        const int g = (warp - 8) >> 2;
+        const int v = (warp & 3) * 32 + lane;
+        const bool mine = (warp & 3) * 32 < V;  // V = 64: lanes 64.. carry nothing
+        const int k0 = g * NS;
+        float S[NS];
+        if (!slot && mine) {
+#pragma unroll
+            for (int e = 0; e < NS; ++e) S[e] = 0.f;
+            if (p.S0) {
+                const int past = first ? 0
+                                 : rev ? it.len - (it.j + 1) * arg.plan.seg_len - 1 : f0;
+                const float f = exp2f((float)past * lg);
+                if (arg.slots_in) {
+                    const float4 *src = reinterpret_cast<const float4 *>(
+                        arg.slots_in + (((size_t)(it.slot0 + (rev ? 0 : it.n - 1)) * p.H + h) * V + v) * K + k0);
+#pragma unroll
+                    for (int e = 0; e < NS / 4; ++e) {
+                        const float4 x = src[e];
+                        S[4 * e] = f * x.x; S[4 * e + 1] = f * x.y;
+                        S[4 * e + 2] = f * x.z; S[4 * e + 3] = f * x.w;
+                    }
+                } else {
+                    const size_t head = (size_t)it.seq * p.H + h;
+#pragma unroll
+                    for (int e = 0; e < NS; ++e)
+                        S[e] = f * given_start(p.S0, p.s0_transposed, head, V, K, v, k0 + e);
+                }
+            }
+            if (arg.slots_in) {
+                for (int j = rev ? it.j + 1 : 0; j < (rev ? it.n : it.j); ++j) {
+                    const int gap = tokens_between(j, it.j, it.len, arg.plan.seg_len, rev);
+                    const float f = exp2f((float)gap * lg);
+                    const float4 *src = reinterpret_cast<const float4 *>(
+                        arg.slots_in + (((size_t)(it.slot0 + j) * p.H + h) * V + v) * K + k0);
+#pragma unroll
+                    for (int e = 0; e < NS / 4; ++e) {
+                        const float4 x = src[e];
+                        S[4 * e] = fmaf(f, x.x, S[4 * e]);
+                        S[4 * e + 1] = fmaf(f, x.y, S[4 * e + 1]);
+                        S[4 * e + 2] = fmaf(f, x.z, S[4 * e + 2]);
+                        S[4 * e + 3] = fmaf(f, x.w, S[4 * e + 3]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < NS; ++e) S[e] = 0.f;
+        }
+        const int st = tid - 256;  // 0..255 of both groups
+        int n_table = -1;
+        for (int i = 0; i < nc; ++i) {
+            const int n = chunk_n(i);
+            if (want_o) {
+                if (mine) {
+                    // rows of 128 bytes hold 64 columns; K = 64: the groups share one row
+#pragma unroll
+                    for (int e = 0; e < NS / 32; ++e) {
+                        float x[32];
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) x[y] = S[32 * e + y];
+                        const int col = k0 + 32 * e;
+                        store_row<4>(smem + L::S + (col / 64) * (V * 128), v, (col % 64) / 8, x);
+                    }
+                }
+                fence_proxy_async_smem();
+                arrive_warp(&bar.s);
+            }
+            const bool update = i + 1 < nc || end;
+            if (!update && n == kC) continue;
+            const uint32_t vbase = L::VV + (i % kStages) * L::VSLOT;
+            wait_warp(&bar.full[i % kStages], i / kStages);
+            if (n < kC) {
+                // the rows behind the sequence's last token are another's, or none
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                uint8_t *kt = smem + L::KK + (i % kStages) * L::KSLOT, *vt = smem + vbase;
+                for (int x = st; x < (kC - n) * 8; x += 256) {
+                    const int at = (n + x / 8) * 128 + (x % 8) * 16;
+#pragma unroll
+                    for (int b = 0; b < K / 64; ++b) *reinterpret_cast<uint4 *>(kt + b * (kC * 128) + at) = zero;
+#pragma unroll
+                    for (int b = 0; b < V / 64; ++b) *reinterpret_cast<uint4 *>(vt + b * (kC * 128) + at) = zero;
+                }
+                fence_proxy_async_smem();
+                named_sync(kBarS, 256);
+                arrive_warp(&bar.tail);
+            }
+            if (!update) continue;
+            if (n != n_table) {  // both groups come here together
+                named_sync(kBarS, 256);
+                if (st < kC)
+                    vweight[st] = st < n ? p.write_scale * exp2f((float)(rev ? st : n - 1 - st) * lg) : 0.f;
+                named_sync(kBarS, 256);
+                n_table = n;
+            }
+            if (mine) {
+                const uint8_t *col = smem + vbase + (v >> 6) * (kC * 128) + (v & 7) * 2;
+                const uint32_t chunk = (v & 63) >> 3;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {  // 32 tokens
+                    uint32_t hi[16], lo[16];
+                    const int s0 = g * 64 + q * 32;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int s = s0 + 2 * e;
+                        const float2 w = *reinterpret_cast<const float2 *>(vweight + s);
+                        const uint16_t ra = *reinterpret_cast<const uint16_t *>(
+                            col + s * 128 + ((chunk ^ ((2 * e) & 7)) << 4));
+                        const uint16_t rb = *reinterpret_cast<const uint16_t *>(
+                            col + (s + 1) * 128 + ((chunk ^ ((2 * e + 1) & 7)) << 4));
+                        const float x = w.x * __uint_as_float((uint32_t)ra << 16);
+                        const float y = w.y * __uint_as_float((uint32_t)rb << 16);
+                        hi[e] = pack_bf16(x, y);
+                        lo[e] = pack_bf16(x - __uint_as_float(hi[e] << 16),
+                                          y - __uint_as_float(hi[e] & 0xffff0000u));
+                    }
+                    tmem_st16(tmem + quad + kColHi + s0 / 2, hi);
+                    tmem_st16(tmem + quad + kColLo + s0 / 2, lo);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            arrive_warp(&bar.vw);
+            const float ac = exp2f((float)(n + chunk_lead(i) - 1) * lg);
+            wait_warp(&bar.d, i);
+            tc_fence_after();
+            if (mine) {
+#pragma unroll
+                for (int e = 0; e < NS / 32; ++e) {
+                    float x[32];
+                    tmem_ld32(tmem + quad + kColD + k0 + 32 * e, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) S[32 * e + y] = fmaf(ac, S[32 * e + y], x[y]);
+                }
+            }
+            tc_fence_before();
+            if (!want_o) arrive_warp(&bar.s);  // D is read
+        }
+        if (end && mine && !dead) {
+            // the state that a reversed scan returns has decayed once more
+            const float f = !slot && rev && it.len > 0 ? exp2f(lg) : 1.f;
+            float4 *dst = reinterpret_cast<float4 *>(end + (size_t)v * K + k0);
+#pragma unroll
+            for (int e = 0; e < NS / 4; ++e)
+                dst[e] = make_float4(f * S[4 * e], f * S[4 * e + 1], f * S[4 * e + 2], f * S[4 * e + 3]);
+        }
+    } else {
+        reg_dec<40>();
+        // ---------------------------------------------------------------- loads
+        if (warp == 16 && lane == 0) {
+            tma_prefetch_desc(&mk);
+            tma_prefetch_desc(&mv);
+            if (want_o) tma_prefetch_desc(&mq);
+            const int hq = h / (p.H / p.Hq), hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
+            const uint32_t bytes = kC * 2 * (K + V + (want_o ? K : 0));
+            int issued = 0;
+            for (int i = 0; i < nc; ++i) {
+                const int s = i % kStages;
+                if (i >= kStages) {
+                    wait(&bar.kvfree[s], i / kStages - 1);
+                    if (want_o) wait(&bar.qfree[s], i / kStages - 1);
+                }
+                if (dead) break;
+                const int at = f0 + chunk_at(i);
+                const int c2 = p.offsets ? it.base + at : at, c3 = p.offsets ? 0 : it.seq;
+                mbar_arrive_expect_tx(&bar.full[s], bytes);
+                issued = i + 1;
+#pragma unroll
+                for (int b = 0; b < K / 64; ++b) {
+                    if (want_o)
+                        tma_load_4d(smem + L::Q + s * L::QSLOT + b * (kC * 128), &mq, &bar.full[s],
+                                    64 * b, hq, c2, c3);
+                    tma_load_4d(smem + L::KK + s * L::KSLOT + b * (kC * 128), &mk, &bar.full[s],
+                                64 * b, hk, c2, c3);
+                }
+#pragma unroll
+                for (int b = 0; b < V / 64; ++b)
+                    tma_load_4d(smem + L::VV + s * L::VSLOT + b * (kC * 128), &mv, &bar.full[s],
+                                64 * b, hv, c2, c3);
+            }
+            // copies in flight land before the CTA ends (again with a limit)
+            for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                mbar_wait(&bar.full[i % kStages], (i / kStages) & 1, kSpinLimit);
+        }
+        // ---------------------------------------------------------------- MMAs
+        if (warp == 17 && lane == 0) {
+            const uint32_t base = smem_u32(smem);
+            constexpr uint32_t id_scores = idesc_bf16(128, 128, false, false);
+            constexpr uint32_t id_qs = idesc_bf16(128, V, false, false);
+            constexpr uint32_t id_pv = idesc_bf16(128, V, false, true);
+            constexpr uint32_t id_d = idesc_bf16(128, K, false, true);
+            int nd = 0;  // chunks whose D is formed
+            for (int i = 0; i < nc; ++i) {
+                const int s = i % kStages;
+                const uint32_t q = base + L::Q + s * L::QSLOT, k = base + L::KK + s * L::KSLOT,
+                               v = base + L::VV + s * L::VSLOT, sm = base + L::S;
+                wait(&bar.full[s], i / kStages);
+                if (chunk_n(i) < kC) wait(&bar.tail, 0);  // one ragged chunk a segment
+                if (want_o) {
+                    if (i > 0) wait(&bar.o, i - 1);  // P is read
+                    tc_fence_after();
+                    if (dead) continue;
+#pragma unroll
+                    for (int x = 0; x < K / 16; ++x)
+                        mma_bf16(tmem + kColP, sdesc(q + (x / 4) * (kC * 128) + (x % 4) * 32, 16, 1024),
+                                 sdesc(k + (x / 4) * (kC * 128) + (x % 4) * 32, 16, 1024), id_scores,
+                                 x > 0);
+                    mma_commit(&bar.scores);
+                    wait(&bar.s, i);
+                    if (i > 0) wait(&bar.ofree, i - 1);
+                    tc_fence_after();
+                    if (dead) continue;
+#pragma unroll
+                    for (int x = 0; x < K / 16; ++x)
+                        mma_bf16(tmem + kColO, sdesc(q + (x / 4) * (kC * 128) + (x % 4) * 32, 16, 1024),
+                                 sdesc(sm + (x / 4) * (V * 128) + (x % 4) * 32, 16, 1024), id_qs, x > 0);
+                } else if (i > 0) {
+                    wait(&bar.s, i - 1);
+                }
+                if (i + 1 < nc || end) {
+                    wait(&bar.vw, nd++);
+                    tc_fence_after();
+                    if (dead) continue;
+#pragma unroll
+                    for (int x = 0; x < 2 * kC / 16; ++x)
+                        mma_bf16_ta(tmem + kColD, tmem + (x < 8 ? kColHi : kColLo) + 8 * (x % 8),
+                                    sdesc(k + (x % 8) * 2048, kC * 128, 1024), id_d, x > 0);
+                    mma_commit(&bar.d);
+                }
+                if (want_o) {
+                    wait(&bar.p, i);
+                    tc_fence_after();
+                    if (dead) continue;
+#pragma unroll
+                    for (int x = 0; x < kC / 16; ++x)
+                        mma_bf16_ta(tmem + kColO, tmem + kColP + 8 * x,
+                                    sdesc(v + x * 2048, kC * 128, 1024), id_pv, 1);
+                    mma_commit(&bar.o);
+                }
+                mma_commit(&bar.kvfree[s]);
+            }
+            // every product is done before the tensor memory is given back
+            if (nc > 0) mbar_wait(&bar.kvfree[(nc - 1) % kStages], ((nc - 1) / kStages) & 1, dead ? 1000000 : kSpinLimit);
+        }
+    }
+    if (dead) *abort_v = 1;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_v && tid == 0 && arg.status) atomicOr(arg.status, kStatusTimeout);
+    if (warp == 17) tmem_dealloc(tmem, 512);
+}
+
+template <int K, int V>
+cudaError_t launch_kv(const LinearScan &a, float *slots, cudaStream_t st) {
+    using L = LinLayout<K, V>;
+    static uintptr_t attr_set[64] = {};  // context the attribute was set in
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    auto kern = linear_tc_kernel<K, V>;
+    if (attr_set[dev] != context_key()) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = context_key();
+    }
+    const bool packed = a.offsets != nullptr;
+    const int B = packed ? 1 : a.B;
+    CUtensorMap mq, mk, mv, mo;
+    if (!make_strided_token_map(&mk, a.k, B, a.T, a.ldk, a.ldk * a.T, a.Hk, K, kC) ||
+        !make_strided_token_map(&mv, a.v, B, a.T, a.ldv, a.ldv * a.T, a.Hv, V, kC))
+        return cudaErrorInvalidValue;
+    mq = mk;
+    mo = mv;
+    if (a.o) {
+        if (!make_strided_token_map(&mq, a.q, B, a.T, a.ldq, a.ldq * a.T, a.Hq, K, kC))
+            return cudaErrorInvalidValue;
+        const long long ldo = (long long)a.H * V;
+        if (!a.o_float && !make_strided_token_map(&mo, a.o, B, a.T, ldo, ldo * a.T, a.H, V, kC))
+            return cudaErrorInvalidValue;
+    }
+    LinTcArgs arg = {a, linear_tc_plan(a.B, a.T, a.H, K, V, packed), nullptr, nullptr,
+                     device_status_ptr()};
+    const long long grid = (long long)arg.plan.items * a.H;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (arg.plan.items > a.B) {
+        arg.slots_out = slots;
+        kern<<<(unsigned)grid, kWarps * 32, L::SMEM, st>>>(mq, mk, mv, mo, arg);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        arg.slots_out = nullptr;
+        arg.slots_in = slots;
+    }
+    kern<<<(unsigned)grid, kWarps * 32, L::SMEM, st>>>(mq, mk, mv, mo, arg);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+SegPlan linear_tc_plan(int B, int T, int H, int K, int V, bool packed) {
+    (void)K;
+    (void)V;
+    // One CTA an SM.  A CTA alone takes about 1 us a chunk, and about 50 of
+    // them together are bound by memory: more segments than for some 64 CTAs
+    // only add the first pass's reading of k and v.  Segments of 4 chunks at
+    // least.
+    const long long have = (long long)B * H;
+    if (have >= 64 || T <= 8 * kC) return {T > 0 ? T : 1, B};
+    const long long want = (64 + H - 1) / H;  // segments in all
+    long long len = (packed ? T : (long long)T * B) / want;
+    len = len < 4 * kC ? 4 * kC : (len + kC - 1) / kC * kC;
+    if (len * 2 > T) return {T, B};
+    const long long n = (T + len - 1) / len;
+    return {(int)len, (int)(packed ? n + B : n * B)};
+}
+
+cudaError_t launch_linear_tc(const LinearScan &a, float *slots, cudaStream_t stream) {
+    if (a.K == 128 && a.V == 128) return launch_kv<128, 128>(a, slots, stream);
+    if (a.K == 64 && a.V == 128) return launch_kv<64, 128>(a, slots, stream);
+    if (a.K == 128 && a.V == 64) return launch_kv<128, 64>(a, slots, stream);
+    if (a.K == 64 && a.V == 64) return launch_kv<64, 64>(a, slots, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn

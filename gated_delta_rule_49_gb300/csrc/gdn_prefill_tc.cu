@@ -1768,12 +1768,17 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // [B, Ts, H, C] bf16 tensor whose first T tokens per batch entry are used,
 // viewed as 4-D (C, H, T, B) with 64 x 1 x 64 x 1 boxes.
 bool make_token_map(CUtensorMap *m, const void *ptr, int B, int T, int Ts, int H, int C) {
+    return make_strided_token_map(m, ptr, B, T, (long long)H * C, (long long)Ts * H * C, H, C, 64);
+}
+
+bool make_strided_token_map(CUtensorMap *m, const void *ptr, int B, int T, long long token_stride,
+                            long long batch_stride, int H, int C, int box_tokens) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {(cuuint64_t)C, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
-    cuuint64_t strides[3] = {(cuuint64_t)C * 2, (cuuint64_t)C * 2 * H,
-                             (cuuint64_t)C * 2 * H * Ts};
-    cuuint32_t box[4] = {64, 1, 64, 1};
+    cuuint64_t strides[3] = {(cuuint64_t)C * 2, (cuuint64_t)token_stride * 2,
+                             (cuuint64_t)batch_stride * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_tokens, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides,
                box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -278,5 +278,9 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 // 128-byte swizzle.  Returns false if the driver entry point is missing or
 // the encoder rejects the arguments.
 bool make_token_map(CUtensorMap *m, const void *ptr, int B, int T, int Ts, int H, int C);
+// The same with any distance (in elements, multiples of 8) between tokens and
+// between batch entries, and boxes of 64 channels x box_tokens tokens.
+bool make_strided_token_map(CUtensorMap *m, const void *ptr, int B, int T, long long token_stride,
+                            long long batch_stride, int H, int C, int box_tokens);
 
 }  // namespace gdn
