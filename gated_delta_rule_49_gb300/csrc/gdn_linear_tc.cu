@@ -13,7 +13,7 @@
 //
 // Precision: P and S are rounded to bf16 as operands (a step of the bf16
 // output each).  The state itself has to be a float32 result, so the weighted
-// V goes in as hi + lo bf16 pieces, D is formed chunk by chunk from zero in
+// V goes in as three bf16 pieces that add up to it, D is formed chunk by chunk from zero in
 // the float32 accumulator, and S is kept in float32 registers, added to with
 // rounding (an accumulator carried through all chunks would be cut, not
 // rounded, at every product).
@@ -32,8 +32,9 @@
 //   17    issues the MMAs (18 and 19 only fill the group)
 // Launched with 96 registers a thread (5 groups x 128 threads x 96 = 61440);
 // the groups then share the same 480 registers a lane of the five as
-// 88 + 80 + 2 x 136 + 40, so that S, a row piece of 64 floats, needs no spill.
-// TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64.
+// 80 + 80 + 2 x 136 + 48, so that S, a row piece of 64 floats, needs no spill.
+// TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64
+// (and 64 of the scores' columns).
 #include <cstring>
 
 #include "gdn_chunk.cuh"
@@ -47,7 +48,8 @@ constexpr int kC = 128;             // tokens of a chunk
 constexpr int kStages = 2;
 constexpr int kWarps = 20;
 constexpr int kBarP = 1, kBarO = 2, kBarS = 3;  // named barriers
-constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColLo = 448;
+constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColMid = 448,
+                   kColLow = 64;
 
 template <int K, int V>
 struct LinLayout {
@@ -67,6 +69,90 @@ template <int N> __device__ __forceinline__ void reg_dec() {
 }
 template <int N> __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One lane of a warp whose lanes are all here.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
+}
+
+// Products with descriptors given by their low words: the high word (stride
+// 1024, version, swizzle) is the same for every tile here, and steps within a
+// tile are additions to the address field.
+constexpr uint32_t kDescHi = 0x40004040u;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values, transposed: a lane gets rows lane / 4
+// (of the transposed blocks), columns 2 (lane % 4) and the next, of each.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 TMEM lanes x 16 columns: register 4 c + 2 m + r of a lane goes to TMEM
+// lane 8 r + lane / 4, column 8 c + 4 m + lane % 4.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+// The upper halves of two words, x's below y's.
+__device__ __forceinline__ uint32_t upper_halves(float x, float y) {
+    return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+}
+__device__ __forceinline__ float upper_half(float x) {
+    return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+// a *= f, b *= g as one packed product.
+__device__ __forceinline__ void mul2(float &a, float &b, float f, float g) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f), "f"(g));
+}
+// a = f a + c, b = f b + d as one packed operation.
+__device__ __forceinline__ void fma2(float &a, float &b, float f, float c, float d) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %4};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f), "f"(c), "f"(d));
+}
+// x -= upper_half(x), y -= upper_half(y) as one packed operation (exact).
+__device__ __forceinline__ void drop_upper_halves(float &x, float &y) {
+    const float u = upper_half(x), w = upper_half(y);
+    asm("{\n\t.reg .b64 a, b, m;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "mov.b64 m, {%4, %4};\n\tfma.rn.f32x2 a, b, m, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(u), "f"(w), "f"(-1.f));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 struct LinBars {
@@ -161,11 +247,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     // written any more, but the loops keep their barriers and end.
     bool dead = false;
     auto wait = [&](uint64_t *b, uint32_t parity) {
-        if (dead) return;
-        if (!mbar_wait_or_abort(b, parity & 1, kSpinLimit, abort_v)) {
-            *abort_v = 1;
-            dead = true;
-        }
+        if (dead || mbar_try_wait(b, parity & 1)) return;
+        const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+        while (!mbar_try_wait(b, parity & 1))
+            if (*abort_v || (uint32_t)clock() - t0 > (uint32_t)kSpinLimit) {
+                *abort_v = 1;
+                dead = true;
+                return;
+            }
     };
     auto wait_warp = [&](uint64_t *b, uint32_t parity) {
         wait(b, parity);
@@ -178,7 +268,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
     if (warp < 4) {
         // ---------------------------------------------------------------- P
-        reg_dec<88>();
+        reg_dec<80>();
         if (want_o) {
             const int t = warp * 32 + lane;
             const bool mild = lg * kC >= -64.f;
@@ -195,7 +285,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const float lrho = fmaxf((float)pt * lg, -64.f);
                 wait_warp(&bar.scores, i);
                 tc_fence_after();
-#pragma unroll
+                // Rolled: twenty warps in five roles, unrolled, missed the
+                // instruction cache at every chunk (a quarter of all stalls).
+#pragma unroll 1
                 for (int b = 0; b < 4; ++b) {  // 32 columns
                     uint32_t w[16];
                     if (rev ? b < warp : b > warp) {
@@ -205,28 +297,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         float x[32];
                         tmem_ld32(tmem + quad + kColP + 32 * b, x);
                         tmem_ld_wait();
-                        const float4 *f4 = reinterpret_cast<const float4 *>(colfac + 32 * b);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float4 f = f4[e];
-                            x[4 * e] *= f.x;
-                            x[4 * e + 1] *= f.y;
-                            x[4 * e + 2] *= f.z;
-                            x[4 * e + 3] *= f.w;
-                        }
                         if (!mild) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 const int lag = rev ? 32 * b + e - t : t - 32 * b - e;
-                                x[e] *= lag < 0 ? 0.f : exp2f((float)lag * lg - lrho);
+                                x[e] *= ex2((float)max(lag, 0) * lg - lrho);
                             }
                         }
-                        if (b == warp) {
+                        const float4 *f4 = reinterpret_cast<const float4 *>(colfac + 32 * b);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (rev ? e < lane : e > lane) x[e] = 0.f;
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 f = f4[e];
+                            mul2(x[4 * e], x[4 * e + 1], f.x, f.y);
+                            mul2(x[4 * e + 2], x[4 * e + 3], f.z, f.w);
                         }
                         pack_row(x, w);
+                        if (b == warp) {  // the columns at or before this row, in scan order
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                // 16 bits of a pair for each of its columns that counts
+                                const int bits = 16 * (rev ? 2 * e + 2 - lane : lane + 1 - 2 * e);
+                                const uint32_t ones = __funnelshift_lc(0xffffffffu, 0u, max(bits, 0));
+                                w[e] &= rev ? __brev(ones) : ones;
+                            }
+                        }
                     }
                     tmem_st16(tmem + quad + kColP + 16 * b, w);
                 }
@@ -249,7 +343,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const size_t row = ((size_t)(it.first + at + t) * p.H + h) * V;
                 wait_warp(&bar.o, i);
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < V / 32; ++b) {
                     float x[32];
                     tmem_ld32(tmem + quad + kColO + 32 * b, x);
@@ -393,29 +487,45 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 named_sync(kBarS, 256);
                 n_table = n;
             }
+            if (want_o) {
+                wait_warp(&bar.p, i);  // the scores are read
+                tc_fence_after();
+            }
+            // Rows [32 (warp % 4), + 32) of V^T, this group's 64 tokens, as three
+            // bf16 pieces whose sum is the float32 product: each takes the upper
+            // half of what is left.  The lowest goes over the scores' columns,
+            // of which P needs only the first half.
             if (mine) {
-                const uint8_t *col = smem + vbase + (v >> 6) * (kC * 128) + (v & 7) * 2;
-                const uint32_t chunk = (v & 63) >> 3;
+                // lanes 8 j .. address block j: tokens + 8 (j / 2), channels + 8 (j % 2)
+                const uint32_t row = g * 64 + (lane & 7) + ((lane >> 4) << 3);
+                const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
+#pragma unroll 1
+                for (int rc = 0; rc < 4; ++rc) {  // 16 channels x 32 tokens
+                    const uint32_t col = (uint32_t)(warp & 3) * 32 + 16 * (rc >> 1) + (lane & 8);
+                    const uint32_t src = smem_u32(smem) + vbase + (col >> 6) * (kC * 128) +
+                                         swz128(row, (col & 63) >> 3) + (rc & 1) * 4096;
+                    uint32_t hi[8], mid[8], low[8];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {  // 32 tokens
-                    uint32_t hi[16], lo[16];
-                    const int s0 = g * 64 + q * 32;
+                    for (int m = 0; m < 2; ++m) {  // 16 tokens
+                        uint32_t x[4];
+                        ldmatrix4_trans(x, src + m * 2048);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int s = s0 + 2 * e;
-                        const float2 w = *reinterpret_cast<const float2 *>(vweight + s);
-                        const uint16_t ra = *reinterpret_cast<const uint16_t *>(
-                            col + s * 128 + ((chunk ^ ((2 * e) & 7)) << 4));
-                        const uint16_t rb = *reinterpret_cast<const uint16_t *>(
-                            col + (s + 1) * 128 + ((chunk ^ ((2 * e + 1) & 7)) << 4));
-                        const float x = w.x * __uint_as_float((uint32_t)ra << 16);
-                        const float y = w.y * __uint_as_float((uint32_t)rb << 16);
-                        hi[e] = pack_bf16(x, y);
-                        lo[e] = pack_bf16(x - __uint_as_float(hi[e] << 16),
-                                          y - __uint_as_float(hi[e] & 0xffff0000u));
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 w = w2[16 * (rc & 1) + 8 * m + 4 * (e >> 1)];
+                            float u = __uint_as_float(x[e] << 16);
+                            float y = __uint_as_float(x[e] & 0xffff0000u);
+                            mul2(u, y, w.x, w.y);
+                            hi[4 * m + e] = upper_halves(u, y);
+                            drop_upper_halves(u, y);
+                            mid[4 * m + e] = upper_halves(u, y);
+                            drop_upper_halves(u, y);
+                            low[4 * m + e] = upper_halves(u, y);
+                        }
                     }
-                    tmem_st16(tmem + quad + kColHi + s0 / 2, hi);
-                    tmem_st16(tmem + quad + kColLo + s0 / 2, lo);
+                    const uint32_t at = tmem + quad + ((uint32_t)(rc >> 1) << 20) + g * 32 + 16 * (rc & 1);
+                    tmem_st_16x128(at + kColHi, hi);
+                    tmem_st_16x128(at + kColMid, mid);
+                    tmem_st_16x128(at + kColLow, low);
                 }
                 tmem_st_wait();
             }
@@ -446,9 +556,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 dst[e] = make_float4(f * S[4 * e], f * S[4 * e + 1], f * S[4 * e + 2], f * S[4 * e + 3]);
         }
     } else {
-        reg_dec<40>();
+        reg_dec<48>();
         // ---------------------------------------------------------------- loads
-        if (warp == 16 && lane == 0) {
+        if (warp == 16 && elect_one()) {
             tma_prefetch_desc(&mk);
             tma_prefetch_desc(&mv);
             if (want_o) tma_prefetch_desc(&mq);
@@ -484,59 +594,70 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 mbar_wait(&bar.full[i % kStages], (i / kStages) & 1, kSpinLimit);
         }
         // ---------------------------------------------------------------- MMAs
-        if (warp == 17 && lane == 0) {
+        if (warp == 17 && elect_one()) {
             const uint32_t base = smem_u32(smem);
             constexpr uint32_t id_scores = idesc_bf16(128, 128, false, false);
             constexpr uint32_t id_qs = idesc_bf16(128, V, false, false);
             constexpr uint32_t id_pv = idesc_bf16(128, V, false, true);
             constexpr uint32_t id_d = idesc_bf16(128, K, false, true);
-            int nd = 0;  // chunks whose D is formed
+            const uint32_t q_0 = desc_lo(base + L::Q, 16), k_0 = desc_lo(base + L::KK, 16),
+                           s_0 = desc_lo(base + L::S, 16), kt_0 = desc_lo(base + L::KK, kC * 128),
+                           v_0 = desc_lo(base + L::VV, kC * 128);
+#pragma unroll 1
             for (int i = 0; i < nc; ++i) {
                 const int s = i % kStages;
-                const uint32_t q = base + L::Q + s * L::QSLOT, k = base + L::KK + s * L::KSLOT,
-                               v = base + L::VV + s * L::VSLOT, sm = base + L::S;
+                const uint32_t q = q_0 + s * (L::QSLOT >> 4), k = k_0 + s * (L::KSLOT >> 4),
+                               kt = kt_0 + s * (L::KSLOT >> 4), v = v_0 + s * (L::VSLOT >> 4);
                 wait(&bar.full[s], i / kStages);
                 if (chunk_n(i) < kC) wait(&bar.tail, 0);  // one ragged chunk a segment
                 if (want_o) {
-                    if (i > 0) wait(&bar.o, i - 1);  // P is read
+                    if (i > 0) {  // P and the lowest pieces of V, in the scores' columns, are read
+                        wait(&bar.o, i - 1);
+                        wait(&bar.d, i - 1);
+                    }
                     tc_fence_after();
                     if (dead) continue;
+#pragma unroll 1
+                    for (int y = 0; y < K / 64; ++y)
 #pragma unroll
-                    for (int x = 0; x < K / 16; ++x)
-                        mma_bf16(tmem + kColP, sdesc(q + (x / 4) * (kC * 128) + (x % 4) * 32, 16, 1024),
-                                 sdesc(k + (x / 4) * (kC * 128) + (x % 4) * 32, 16, 1024), id_scores,
-                                 x > 0);
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t off = y * (kC * 8) + 2 * x;
+                            mma_ss(tmem + kColP, q + off, k + off, id_scores, y + x > 0);
+                        }
                     mma_commit(&bar.scores);
                     wait(&bar.s, i);
                     if (i > 0) wait(&bar.ofree, i - 1);
                     tc_fence_after();
                     if (dead) continue;
+#pragma unroll 1
+                    for (int y = 0; y < K / 64; ++y)
 #pragma unroll
-                    for (int x = 0; x < K / 16; ++x)
-                        mma_bf16(tmem + kColO, sdesc(q + (x / 4) * (kC * 128) + (x % 4) * 32, 16, 1024),
-                                 sdesc(sm + (x / 4) * (V * 128) + (x % 4) * 32, 16, 1024), id_qs, x > 0);
+                        for (int x = 0; x < 4; ++x)
+                            mma_ss(tmem + kColO, q + y * (kC * 8) + 2 * x, s_0 + y * (V * 8) + 2 * x,
+                                   id_qs, y + x > 0);
+                    wait(&bar.p, i);
+                    tc_fence_after();
+                    if (dead) continue;
+#pragma unroll 4
+                    for (int x = 0; x < kC / 16; ++x)
+                        mma_ts(tmem + kColO, tmem + kColP + 8 * x, v + x * (2048 >> 4), id_pv, 1);
+                    mma_commit(&bar.o);
                 } else if (i > 0) {
                     wait(&bar.s, i - 1);
                 }
                 if (i + 1 < nc || end) {
-                    wait(&bar.vw, nd++);
+                    wait(&bar.vw, i);
                     tc_fence_after();
                     if (dead) continue;
-#pragma unroll
-                    for (int x = 0; x < 2 * kC / 16; ++x)
-                        mma_bf16_ta(tmem + kColD, tmem + (x < 8 ? kColHi : kColLo) + 8 * (x % 8),
-                                    sdesc(k + (x % 8) * 2048, kC * 128, 1024), id_d, x > 0);
+                    // the small pieces first: the sum is cut to its size at each product
+#pragma unroll 1
+                    for (int y = 0; y < 3; ++y) {
+                        const uint32_t a = tmem + (y == 0 ? kColLow : y == 1 ? kColMid : kColHi);
+#pragma unroll 4
+                        for (int x = 0; x < kC / 16; ++x)
+                            mma_ts(tmem + kColD, a + 8 * x, kt + x * (2048 >> 4), id_d, y + x > 0);
+                    }
                     mma_commit(&bar.d);
-                }
-                if (want_o) {
-                    wait(&bar.p, i);
-                    tc_fence_after();
-                    if (dead) continue;
-#pragma unroll
-                    for (int x = 0; x < kC / 16; ++x)
-                        mma_bf16_ta(tmem + kColO, tmem + kColP + 8 * x,
-                                    sdesc(v + x * 2048, kC * 128, 1024), id_pv, 1);
-                    mma_commit(&bar.o);
                 }
                 mma_commit(&bar.kvfree[s]);
             }
