@@ -19,10 +19,10 @@
 // rounded, at every product).
 //
 // One CTA runs one segment of one (sequence, head), 20 warps in groups of 4:
-//   0-3   P: row t of Q K^T from TMEM, weighted, back to TMEM as bf16 (over
-//         the columns that it came from) for the product with V
-//   4-7   O: row t from TMEM, scaled, to shared memory in Q's place and out by
-//         TMA (ragged chunks: plain stores)
+//   0-7   rows (two warps share 32 of them): P, from Q K^T in TMEM, weighted,
+//         back to TMEM as bf16 (over the columns that it came from) for the
+//         product with V; then O from TMEM, scaled, to shared memory in Q's
+//         place and out by TMA (ragged chunks: plain stores)
 //   8-15  state: two groups of 128 threads (value channel v each); the first
 //         takes tokens 0-63 and state columns [0, K/2), the second the rest:
 //         column v of V from shared memory, weighted, split and written to
@@ -32,7 +32,7 @@
 //   17    issues the MMAs (18 and 19 only fill the group)
 // Launched with 96 registers a thread (5 groups x 128 threads x 96 = 61440);
 // the groups then share the same 480 registers a lane of the five as
-// 80 + 80 + 2 x 136 + 48, so that S, a row piece of 64 floats, needs no spill.
+// 2 x 88 + 2 x 128 + 48, so that S, a row piece of 64 floats, needs no spill.
 // TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64
 // (and 64 of the scores' columns).
 #include <cstring>
@@ -47,7 +47,7 @@ namespace {
 constexpr int kC = 128;             // tokens of a chunk
 constexpr int kStages = 2;
 constexpr int kWarps = 20;
-constexpr int kBarP = 1, kBarO = 2, kBarS = 3;  // named barriers
+constexpr int kBarRows = 1, kBarS = 2, kBarPair = 3;  // named barriers (kBarPair + 0 .. 3)
 constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColMid = 448,
                    kColLow = 64;
 
@@ -155,9 +155,46 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A row's 32 scores in TMEM times a^lag / rho (the way of strong decays): `lag0`
+// is the first column's lag, which rises along the row (up) or falls.
+__device__ __forceinline__ void weigh_each(uint32_t taddr, int lag0, bool up, float lg, float lrho) {
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 8) {
+        uint32_t r[8];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr + c));
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int lag = up ? lag0 + c + e : lag0 - c - e;
+            r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2((float)max(lag, 0) * lg - lrho));
+        }
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr + c),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    }
+    tmem_st_wait();
+}
+
+// mbar_try_wait that leaves the thread asleep until the phase completes, or
+// for up to a millisecond: waits that spun took two fifths of all issued
+// instructions.
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+
 struct LinBars {
     uint64_t full[kStages], kvfree[kStages], qfree[kStages];
-    uint64_t scores, p, vw, d, s, o, ofree, tail;
+    uint64_t vw[2], scores, p, d, s, o, ofree, tail;
 };
 
 struct LinTcArgs {
@@ -224,12 +261,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 mbar_init(&bar.qfree[s], 1);
             }
             mbar_init(&bar.scores, 1);
-            mbar_init(&bar.p, 4);
-            mbar_init(&bar.vw, 8);
+            mbar_init(&bar.p, 8);
+            mbar_init(&bar.vw[0], 8);
+            mbar_init(&bar.vw[1], 8);
             mbar_init(&bar.d, 1);
             mbar_init(&bar.s, 8);
             mbar_init(&bar.o, 1);
-            mbar_init(&bar.ofree, 4);
+            mbar_init(&bar.ofree, 8);
             mbar_init(&bar.tail, 8);
             abort_flag = 0;
             fence_mbar_init();
@@ -247,10 +285,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     // written any more, but the loops keep their barriers and end.
     bool dead = false;
     auto wait = [&](uint64_t *b, uint32_t parity) {
-        if (dead || mbar_try_wait(b, parity & 1)) return;
+        if (dead || mbar_sleep_wait(b, parity & 1)) return;
         const uint32_t t0 = (uint32_t)clock();
 #pragma unroll 1
-        while (!mbar_try_wait(b, parity & 1))
+        while (!mbar_sleep_wait(b, parity & 1))
             if (*abort_v || (uint32_t)clock() - t0 > (uint32_t)kSpinLimit) {
                 *abort_v = 1;
                 dead = true;
@@ -266,44 +304,47 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (lane == 0) mbar_arrive(b);
     };
 
-    if (warp < 4) {
-        // ---------------------------------------------------------------- P
-        reg_dec<80>();
+    if (warp < 8) {
+        // ---------------------------------------------------------------- rows
+        reg_dec<88>();
         if (want_o) {
-            const int t = warp * 32 + lane;
+            const int t = (warp & 3) * 32 + lane, part = warp >> 2;
             const bool mild = lg * kC >= -64.f;
+#pragma unroll 1
             for (int i = 0; i < nc; ++i) {
                 const int n = chunk_n(i), lead = chunk_lead(i);
                 if (i == 0 || (rev && i == 1)) {  // the last tables' readers are done
-                    named_sync(kBarP, 128);
+                    named_sync(kBarRows, 256);
                     const int ps = (rev ? n - 1 - t : t) + lead;  // of column t
-                    colfac[t] = ps < 0 || (rev && t >= n) ? 0.f
-                                : mild ? p.write_scale * exp2f(-(float)ps * lg) : p.write_scale;
-                    named_sync(kBarP, 128);
+                    if (part == 0)
+                        colfac[t] = ps < 0 || (rev && t >= n) ? 0.f
+                                    : mild ? p.write_scale * exp2f(-(float)ps * lg) : p.write_scale;
+                    named_sync(kBarRows, 256);
                 }
                 const int pt = (rev ? n - 1 - t : t) + lead;
                 const float lrho = fmaxf((float)pt * lg, -64.f);
                 wait_warp(&bar.scores, i);
                 tc_fence_after();
-                // Rolled: twenty warps in five roles, unrolled, missed the
+                // P: this warp takes two blocks of 32 columns of its 32 rows.
+                // Rolled: twenty warps in their roles, unrolled, missed the
                 // instruction cache at every chunk (a quarter of all stalls).
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {  // 32 columns
+                for (int b = 2 * part; b < 2 * part + 2; ++b) {
                     uint32_t w[16];
-                    if (rev ? b < warp : b > warp) {
+                    const int q = warp & 3;
+                    const bool blank = rev ? b < q : b > q;
+                    float x[32];
+                    if (!blank) {
+                        if (!mild) weigh_each(tmem + quad + kColP + 32 * b, rev ? 32 * b - t : t - 32 * b, rev, lg, lrho);
+                        tmem_ld32(tmem + quad + kColP + 32 * b, x);
+                        tmem_ld_wait();
+                    }
+                    // blocks 2 and 3 of P go over the scores' block 1
+                    if (b == 1 || b == 2) named_sync(kBarPair + q, 64);
+                    if (blank) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) w[e] = 0;
                     } else {
-                        float x[32];
-                        tmem_ld32(tmem + quad + kColP + 32 * b, x);
-                        tmem_ld_wait();
-                        if (!mild) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int lag = rev ? 32 * b + e - t : t - 32 * b - e;
-                                x[e] *= ex2((float)max(lag, 0) * lg - lrho);
-                            }
-                        }
                         const float4 *f4 = reinterpret_cast<const float4 *>(colfac + 32 * b);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -312,7 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                             mul2(x[4 * e + 2], x[4 * e + 3], f.z, f.w);
                         }
                         pack_row(x, w);
-                        if (b == warp) {  // the columns at or before this row, in scan order
+                        if (b == q) {  // the columns at or before this row, in scan order
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 // 16 bits of a pair for each of its columns that counts
@@ -327,56 +368,46 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_warp(&bar.p);
-            }
-        }
-    } else if (warp < 8) {
-        // ---------------------------------------------------------------- O
-        reg_dec<80>();
-        if (want_o) {
-            const int t = (warp & 3) * 32 + lane;
-            for (int i = 0; i < nc; ++i) {
-                const int n = chunk_n(i), at = f0 + chunk_at(i);
-                const int pt = (rev ? n - 1 - t : t) + chunk_lead(i);
-                const float rho = p.read_scale * exp2f(fmaxf((float)pt * lg, -64.f));
+
+                // O: half of this row's columns
+                const float rho = p.read_scale * exp2f(lrho);
                 uint8_t *const stage = smem + L::Q + (i % kStages) * L::QSLOT;
                 const bool whole = n == kC && !p.o_float;
-                const size_t row = ((size_t)(it.first + at + t) * p.H + h) * V;
                 wait_warp(&bar.o, i);
                 tc_fence_after();
 #pragma unroll 1
-                for (int b = 0; b < V / 32; ++b) {
+                for (int b = part * (V / 64); b < (part + 1) * (V / 64); ++b) {
                     float x[32];
                     tmem_ld32(tmem + quad + kColO + 32 * b, x);
                     tmem_ld_wait();
-                    if (p.o_float) {
-                        if (t < n && !dead) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) mul2(x[2 * e], x[2 * e + 1], rho, rho);
+                    if (whole) {
+                        store_row<4>(stage + (b / 2) * (kC * 128), t, (b % 2) * 4, x);
+                    } else if (t < n && !dead) {
+                        const size_t row = ((size_t)(it.first + f0 + chunk_at(i) + t) * p.H + h) * V;
+                        if (p.o_float) {
                             float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row + 32 * b);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                dst[e] = make_float4(rho * x[4 * e], rho * x[4 * e + 1],
-                                                     rho * x[4 * e + 2], rho * x[4 * e + 3]);
+                                dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                        } else {
+                            uint32_t w[16];
+                            pack_row(x, w);
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + row + 32 * b);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         }
-                        continue;
-                    }
-                    if (whole) {
-                        store_row<4>(stage + (b / 2) * (kC * 128), t, (b % 2) * 4, x, rho);
-                    } else if (t < n && !dead) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] *= rho;
-                        pack_row(x, w);
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + row + 32 * b);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                     }
                 }
                 tc_fence_before();
                 arrive_warp(&bar.ofree);
                 if (whole) fence_proxy_async_smem();
-                named_sync(kBarO, 128);
-                if (warp == 4 && lane == 0) {
+                named_sync(kBarRows, 256);
+                if (warp == 0 && lane == 0) {
                     if (whole && !dead) {
+                        const int at = f0 + chunk_at(i);
                         const int c2 = p.offsets ? it.base + at : at, c3 = p.offsets ? 0 : it.seq;
 #pragma unroll
                         for (int b = 0; b < V / 64; ++b)
@@ -386,12 +417,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
                     mbar_arrive(&bar.qfree[i % kStages]);
                 }
+                __syncwarp();
             }
-            if (warp == 4 && lane == 0) bulk_wait_all();
+            if (warp == 0 && lane == 0) bulk_wait_all();
         }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- state
-        reg_inc<136>();
+        reg_inc<128>();
         constexpr int NS = K / 2;
         const int g = (warp - 8) >> 2;
         const int v = (warp & 3) * 32 + lane;
@@ -495,42 +527,44 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             // bf16 pieces whose sum is the float32 product: each takes the upper
             // half of what is left.  The lowest goes over the scores' columns,
             // of which P needs only the first half.
-            if (mine) {
-                // lanes 8 j .. address block j: tokens + 8 (j / 2), channels + 8 (j % 2)
-                const uint32_t row = g * 64 + (lane & 7) + ((lane >> 4) << 3);
-                const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
+            // lanes 8 j .. address block j: tokens + 8 (j / 2), channels + 8 (j % 2)
+            const uint32_t tok = g * 64 + (lane & 7) + ((lane >> 4) << 3);
+            const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
 #pragma unroll 1
-                for (int rc = 0; rc < 4; ++rc) {  // 16 channels x 32 tokens
-                    const uint32_t col = (uint32_t)(warp & 3) * 32 + 16 * (rc >> 1) + (lane & 8);
-                    const uint32_t src = smem_u32(smem) + vbase + (col >> 6) * (kC * 128) +
-                                         swz128(row, (col & 63) >> 3) + (rc & 1) * 4096;
-                    uint32_t hi[8], mid[8], low[8];
+            for (int c = 0; c < 2; ++c) {  // 32 tokens; the products with the first go ahead
+                if (mine) {
+                    float2 w[4];
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {  // 16 tokens
-                        uint32_t x[4];
-                        ldmatrix4_trans(x, src + m * 2048);
+                    for (int e = 0; e < 4; ++e) w[e] = w2[16 * c + 4 * e];
+#pragma unroll 1
+                    for (int r = 0; r < 2; ++r) {  // 16 channels
+                        const uint32_t col = (uint32_t)(warp & 3) * 32 + 16 * r + (lane & 8);
+                        const uint32_t src = smem_u32(smem) + vbase + (col >> 6) * (kC * 128) +
+                                             swz128(tok, (col & 63) >> 3) + c * 4096;
+                        uint32_t hi[8], mid[8], low[8], x[2][4];
+                        ldmatrix4_trans(x[0], src);
+                        ldmatrix4_trans(x[1], src + 2048);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 w = w2[16 * (rc & 1) + 8 * m + 4 * (e >> 1)];
-                            float u = __uint_as_float(x[e] << 16);
-                            float y = __uint_as_float(x[e] & 0xffff0000u);
-                            mul2(u, y, w.x, w.y);
-                            hi[4 * m + e] = upper_halves(u, y);
+                        for (int e = 0; e < 8; ++e) {
+                            float u = __uint_as_float(x[e >> 2][e & 3] << 16);
+                            float y = __uint_as_float(x[e >> 2][e & 3] & 0xffff0000u);
+                            mul2(u, y, w[e >> 1].x, w[e >> 1].y);
+                            hi[e] = upper_halves(u, y);
                             drop_upper_halves(u, y);
-                            mid[4 * m + e] = upper_halves(u, y);
+                            mid[e] = upper_halves(u, y);
                             drop_upper_halves(u, y);
-                            low[4 * m + e] = upper_halves(u, y);
+                            low[e] = upper_halves(u, y);
                         }
+                        const uint32_t at = tmem + quad + ((uint32_t)r << 20) + g * 32 + 16 * c;
+                        tmem_st_16x128(at + kColHi, hi);
+                        tmem_st_16x128(at + kColMid, mid);
+                        tmem_st_16x128(at + kColLow, low);
                     }
-                    const uint32_t at = tmem + quad + ((uint32_t)(rc >> 1) << 20) + g * 32 + 16 * (rc & 1);
-                    tmem_st_16x128(at + kColHi, hi);
-                    tmem_st_16x128(at + kColMid, mid);
-                    tmem_st_16x128(at + kColLow, low);
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
+                tc_fence_before();
+                arrive_warp(&bar.vw[c]);
             }
-            tc_fence_before();
-            arrive_warp(&bar.vw);
             const float ac = exp2f((float)(n + chunk_lead(i) - 1) * lg);
             wait_warp(&bar.d, i);
             tc_fence_after();
@@ -646,17 +680,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     wait(&bar.s, i - 1);
                 }
                 if (i + 1 < nc || end) {
-                    wait(&bar.vw, i);
-                    tc_fence_after();
-                    if (dead) continue;
-                    // the small pieces first: the sum is cut to its size at each product
 #pragma unroll 1
-                    for (int y = 0; y < 3; ++y) {
-                        const uint32_t a = tmem + (y == 0 ? kColLow : y == 1 ? kColMid : kColHi);
-#pragma unroll 4
-                        for (int x = 0; x < kC / 16; ++x)
-                            mma_ts(tmem + kColD, a + 8 * x, kt + x * (2048 >> 4), id_d, y + x > 0);
+                    for (int c = 0; c < 2; ++c) {
+                        wait(&bar.vw[c], i);
+                        tc_fence_after();
+                        if (dead) break;
+                        // the small pieces first: the sum is cut to its size at each product
+#pragma unroll 1
+                        for (int y = 0; y < 3; ++y) {
+                            const uint32_t a = tmem + (y == 0 ? kColLow : y == 1 ? kColMid : kColHi);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {  // tokens 32 c .. and 64 + 32 c ..
+                                const int z = 2 * c + (x & 1) + 4 * (x >> 1);
+                                mma_ts(tmem + kColD, a + 8 * z, kt + z * (2048 >> 4), id_d,
+                                       c + y + x > 0);
+                            }
+                        }
                     }
+                    if (dead) continue;
                     mma_commit(&bar.d);
                 }
                 mma_commit(&bar.kvfree[s]);
