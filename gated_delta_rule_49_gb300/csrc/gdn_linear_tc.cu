@@ -21,20 +21,21 @@
 // One CTA runs one segment of one (sequence, head), 20 warps in groups of 4:
 //   0-7   rows (two warps share 32 of them): P, from Q K^T in TMEM, weighted,
 //         back to TMEM as bf16 (over the columns that it came from) for the
-//         product with V; then O from TMEM, scaled, to shared memory in Q's
+//         product with V; then O from TMEM, scaled, to shared memory in V's
 //         place and out by TMA (ragged chunks: plain stores)
-//   8-15  state: two groups of 128 threads (value channel v each); the first
-//         takes tokens 0-63 and state columns [0, K/2), the second the rest:
-//         column v of V from shared memory, weighted, split and written to
-//         TMEM as an A operand; then S's row piece: S = a^C S + D, and as bf16
-//         to shared memory for the next chunk's Q S^T
-//   16    TMA loads of Q, K, V, two chunks ahead
-//   17    issues the MMAs (18 and 19 only fill the group)
+//   8-15  state: two groups of 128 threads; each chunk's V in two halves of
+//         tokens, transposed, weighted and split: two pieces to TMEM, the
+//         lowest back to shared memory, all as operands of D; and S = a^C S + D
+//         (thread v holds half of row v), as bf16 to shared memory for the next
+//         chunk's Q S^T.  The first half of the next chunk's V goes before the
+//         wait for D, so that D is formed while it runs.
+//   16    loads K and V, two chunks ahead; 18 loads Q (free as soon as Q S^T
+//         is done; the next is on its way to the L2 cache by then)
+//   17    issues the MMAs (19 only fills its group)
 // Launched with 96 registers a thread (5 groups x 128 threads x 96 = 61440);
 // the groups then share the same 480 registers a lane of the five as
 // 2 x 88 + 2 x 128 + 48, so that S, a row piece of 64 floats, needs no spill.
-// TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64
-// (and 64 of the scores' columns).
+// TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64.
 #include <cstring>
 
 #include "gdn_chunk.cuh"
@@ -48,16 +49,18 @@ constexpr int kC = 128;             // tokens of a chunk
 constexpr int kStages = 2;
 constexpr int kWarps = 20;
 constexpr int kBarRows = 1, kBarS = 2, kBarPair = 3;  // named barriers (kBarPair + 0 .. 3)
-constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColMid = 448,
-                   kColLow = 64;
+constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColMid = 448;
 
 template <int K, int V>
 struct LinLayout {
-    static constexpr uint32_t QSLOT = kC * 2 * (K > V ? K : V);  // also takes O
+    static constexpr uint32_t QSLOT = kC * 2 * K;
     static constexpr uint32_t KSLOT = kC * 2 * K;
-    static constexpr uint32_t VSLOT = kC * 2 * V;
-    static constexpr uint32_t Q = 0;
-    static constexpr uint32_t KK = Q + kStages * QSLOT;
+    static constexpr uint32_t VSLOT = kC * 2 * V;  // then takes O
+    // as an operand of 128 rows the lowest pieces reach past V = 64 columns,
+    // into what follows (rows that nothing reads)
+    static constexpr uint32_t LOW = 0;
+    static constexpr uint32_t Q = LOW + kC * 2 * V;
+    static constexpr uint32_t KK = Q + QSLOT;
     static constexpr uint32_t VV = KK + kStages * KSLOT;
     static constexpr uint32_t S = VV + kStages * VSLOT;
     static constexpr uint32_t TABLE = S + 2 * K * V;  // column factors of P, weights of V
@@ -110,6 +113,13 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
+                 : "memory");
+}
+// The way back.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
 // 16 TMEM lanes x 16 columns: register 4 c + 2 m + r of a lane goes to TMEM
@@ -193,7 +203,7 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t *b, uint32_t parity) {
 }
 
 struct LinBars {
-    uint64_t full[kStages], kvfree[kStages], qfree[kStages];
+    uint64_t full[kStages], kfree[kStages], vfree[kStages], qfull, qs, d0;
     uint64_t vw[2], scores, p, d, s, o, ofree, tail;
 };
 
@@ -257,9 +267,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (lane == 0) {
             for (int s = 0; s < kStages; ++s) {
                 mbar_init(&bar.full[s], 1);
-                mbar_init(&bar.kvfree[s], 1);
-                mbar_init(&bar.qfree[s], 1);
+                mbar_init(&bar.kfree[s], 1);
+                mbar_init(&bar.vfree[s], 1);
             }
+            mbar_init(&bar.qfull, 1);
+            mbar_init(&bar.qs, 1);
+            mbar_init(&bar.d0, 1);
             mbar_init(&bar.scores, 1);
             mbar_init(&bar.p, 8);
             mbar_init(&bar.vw[0], 8);
@@ -295,6 +308,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 return;
             }
     };
+    // chunks whose D is formed: all but a last one whose end nobody wants
+    auto updates = [&](int i) { return i + 1 < nc || end; };
     auto wait_warp = [&](uint64_t *b, uint32_t parity) {
         wait(b, parity);
         __syncwarp();
@@ -371,7 +386,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
                 // O: half of this row's columns
                 const float rho = p.read_scale * exp2f(lrho);
-                uint8_t *const stage = smem + L::Q + (i % kStages) * L::QSLOT;
+                uint8_t *const stage = smem + L::VV + (i % kStages) * L::VSLOT;
                 const bool whole = n == kC && !p.o_float;
                 wait_warp(&bar.o, i);
                 tc_fence_after();
@@ -415,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         bulk_commit_group();
                         bulk_wait_read_all();
                     }
-                    mbar_arrive(&bar.qfree[i % kStages]);
+                    mbar_arrive(&bar.vfree[i % kStages]);
                 }
                 __syncwarp();
             }
@@ -475,8 +490,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
         const int st = tid - 256;  // 0..255 of both groups
         int n_table = -1;
-        for (int i = 0; i < nc; ++i) {
-            const int n = chunk_n(i);
+        auto store_state = [&] {
             if (want_o) {
                 if (mine) {
                     // rows of 128 bytes hold 64 columns; K = 64: the groups share one row
@@ -490,48 +504,51 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
                 }
                 fence_proxy_async_smem();
-                arrive_warp(&bar.s);
             }
-            const bool update = i + 1 < nc || end;
-            if (!update && n == kC) continue;
-            const uint32_t vbase = L::VV + (i % kStages) * L::VSLOT;
-            wait_warp(&bar.full[i % kStages], i / kStages);
-            if (n < kC) {
-                // the rows behind the sequence's last token are another's, or none
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                uint8_t *kt = smem + L::KK + (i % kStages) * L::KSLOT, *vt = smem + vbase;
-                for (int x = st; x < (kC - n) * 8; x += 256) {
-                    const int at = (n + x / 8) * 128 + (x % 8) * 16;
-#pragma unroll
-                    for (int b = 0; b < K / 64; ++b) *reinterpret_cast<uint4 *>(kt + b * (kC * 128) + at) = zero;
-#pragma unroll
-                    for (int b = 0; b < V / 64; ++b) *reinterpret_cast<uint4 *>(vt + b * (kC * 128) + at) = zero;
-                }
-                fence_proxy_async_smem();
-                named_sync(kBarS, 256);
-                arrive_warp(&bar.tail);
-            }
-            if (!update) continue;
-            if (n != n_table) {  // both groups come here together
-                named_sync(kBarS, 256);
-                if (st < kC)
-                    vweight[st] = st < n ? p.write_scale * exp2f((float)(rev ? st : n - 1 - st) * lg) : 0.f;
-                named_sync(kBarS, 256);
-                n_table = n;
-            }
-            if (want_o) {
-                wait_warp(&bar.p, i);  // the scores are read
-                tc_fence_after();
-            }
-            // Rows [32 (warp % 4), + 32) of V^T, this group's 64 tokens, as three
-            // bf16 pieces whose sum is the float32 product: each takes the upper
-            // half of what is left.  The lowest goes over the scores' columns,
-            // of which P needs only the first half.
-            // lanes 8 j .. address block j: tokens + 8 (j / 2), channels + 8 (j % 2)
-            const uint32_t tok = g * 64 + (lane & 7) + ((lane >> 4) << 3);
-            const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
+            arrive_warp(&bar.s);
+        };
+        // lanes 8 j .. address block j: tokens + 8 (j / 2), channels + 8 (j % 2)
+        const uint32_t tok = g * 64 + (lane & 7) + ((lane >> 4) << 3);
+        const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
+        if (nc > 0) store_state();
+        // step 2 i + c: half c of chunk i's V; S takes chunk i - 1 up after the
+        // first half of chunk i is on its way
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {  // 32 tokens; the products with the first go ahead
+        for (int step = 0; step <= 2 * nc; ++step) {
+            const int i = step >> 1, c = step & 1;
+            if (c == 0 && i < nc) {
+                const int n = chunk_n(i);
+                wait_warp(&bar.full[i % kStages], i / kStages);
+                if (n < kC) {
+                    // the rows behind the sequence's last token are another's, or none
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    uint8_t *kt = smem + L::KK + (i % kStages) * L::KSLOT,
+                            *vt = smem + L::VV + (i % kStages) * L::VSLOT;
+                    for (int x = st; x < (kC - n) * 8; x += 256) {
+                        const int at = (n + x / 8) * 128 + (x % 8) * 16;
+#pragma unroll
+                        for (int b = 0; b < K / 64; ++b)
+                            *reinterpret_cast<uint4 *>(kt + b * (kC * 128) + at) = zero;
+#pragma unroll
+                        for (int b = 0; b < V / 64; ++b)
+                            *reinterpret_cast<uint4 *>(vt + b * (kC * 128) + at) = zero;
+                    }
+                    fence_proxy_async_smem();
+                    named_sync(kBarS, 256);
+                    arrive_warp(&bar.tail);
+                }
+                if (n != n_table && updates(i)) {  // both groups come here together
+                    named_sync(kBarS, 256);
+                    if (st < kC)
+                        vweight[st] = st < n ? p.write_scale * exp2f((float)(rev ? st : n - 1 - st) * lg) : 0.f;
+                    named_sync(kBarS, 256);
+                    n_table = n;
+                }
+                if (i > 0 && updates(i)) wait_warp(&bar.d0, i - 1);  // the pieces' places are free
+            }
+            if (i < nc && updates(i)) {
+                // 32 tokens of this group's 64 as three bf16 pieces whose sum is
+                // the float32 product: each takes the upper half of what is left
                 if (mine) {
                     float2 w[4];
 #pragma unroll
@@ -539,47 +556,54 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll 1
                     for (int r = 0; r < 2; ++r) {  // 16 channels
                         const uint32_t col = (uint32_t)(warp & 3) * 32 + 16 * r + (lane & 8);
-                        const uint32_t src = smem_u32(smem) + vbase + (col >> 6) * (kC * 128) +
-                                             swz128(tok, (col & 63) >> 3) + c * 4096;
-                        uint32_t hi[8], mid[8], low[8], x[2][4];
+                        const uint32_t off = (col >> 6) * (kC * 128) + swz128(tok, (col & 63) >> 3) + c * 4096;
+                        const uint32_t src = smem_u32(smem) + L::VV + (i % kStages) * L::VSLOT + off;
+                        uint32_t hi[8], mid[8], x[2][4];
                         ldmatrix4_trans(x[0], src);
                         ldmatrix4_trans(x[1], src + 2048);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            float u = __uint_as_float(x[e >> 2][e & 3] << 16);
-                            float y = __uint_as_float(x[e >> 2][e & 3] & 0xffff0000u);
+                            uint32_t &z = x[e >> 2][e & 3];
+                            float u = __uint_as_float(z << 16);
+                            float y = __uint_as_float(z & 0xffff0000u);
                             mul2(u, y, w[e >> 1].x, w[e >> 1].y);
                             hi[e] = upper_halves(u, y);
                             drop_upper_halves(u, y);
                             mid[e] = upper_halves(u, y);
                             drop_upper_halves(u, y);
-                            low[e] = upper_halves(u, y);
+                            z = upper_halves(u, y);
                         }
                         const uint32_t at = tmem + quad + ((uint32_t)r << 20) + g * 32 + 16 * c;
                         tmem_st_16x128(at + kColHi, hi);
                         tmem_st_16x128(at + kColMid, mid);
-                        tmem_st_16x128(at + kColLow, low);
+                        const uint32_t low = smem_u32(smem) + L::LOW + off;
+                        stmatrix4_trans(low, x[0][0], x[0][1], x[0][2], x[0][3]);
+                        stmatrix4_trans(low + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
                     }
                     tmem_st_wait();
+                    fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 arrive_warp(&bar.vw[c]);
             }
-            const float ac = exp2f((float)(n + chunk_lead(i) - 1) * lg);
-            wait_warp(&bar.d, i);
-            tc_fence_after();
-            if (mine) {
+            if (c == 0 && i > 0 && updates(i - 1)) {
+                const float ac = exp2f((float)(chunk_n(i - 1) + chunk_lead(i - 1) - 1) * lg);
+                wait_warp(&bar.d, i - 1);
+                tc_fence_after();
+                if (mine) {
 #pragma unroll
-                for (int e = 0; e < NS / 32; ++e) {
-                    float x[32];
-                    tmem_ld32(tmem + quad + kColD + k0 + 32 * e, x);
-                    tmem_ld_wait();
+                    for (int e = 0; e < NS / 32; ++e) {
+                        float x[32];
+                        tmem_ld32(tmem + quad + kColD + k0 + 32 * e, x);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) S[32 * e + y] = fmaf(ac, S[32 * e + y], x[y]);
+                        for (int y = 0; y < 32; y += 2)
+                            fma2(S[32 * e + y], S[32 * e + y + 1], ac, x[y], x[y + 1]);
+                    }
                 }
+                tc_fence_before();
+                if (i < nc) store_state();
             }
-            tc_fence_before();
-            if (!want_o) arrive_warp(&bar.s);  // D is read
         }
         if (end && mine && !dead) {
             // the state that a reversed scan returns has decayed once more
@@ -592,40 +616,54 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     } else {
         reg_dec<48>();
         // ---------------------------------------------------------------- loads
+        auto token_at = [&](int i) { return (p.offsets ? it.base : 0) + f0 + chunk_at(i); };
+        const int c3 = p.offsets ? 0 : it.seq;
         if (warp == 16 && elect_one()) {
             tma_prefetch_desc(&mk);
             tma_prefetch_desc(&mv);
-            if (want_o) tma_prefetch_desc(&mq);
-            const int hq = h / (p.H / p.Hq), hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
-            const uint32_t bytes = kC * 2 * (K + V + (want_o ? K : 0));
+            const int hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
             int issued = 0;
+#pragma unroll 1
             for (int i = 0; i < nc; ++i) {
                 const int s = i % kStages;
                 if (i >= kStages) {
-                    wait(&bar.kvfree[s], i / kStages - 1);
-                    if (want_o) wait(&bar.qfree[s], i / kStages - 1);
+                    wait(&bar.kfree[s], i / kStages - 1);
+                    if (want_o) wait(&bar.vfree[s], i / kStages - 1);
                 }
                 if (dead) break;
-                const int at = f0 + chunk_at(i);
-                const int c2 = p.offsets ? it.base + at : at, c3 = p.offsets ? 0 : it.seq;
-                mbar_arrive_expect_tx(&bar.full[s], bytes);
+                mbar_arrive_expect_tx(&bar.full[s], kC * 2 * (K + V));
                 issued = i + 1;
 #pragma unroll
-                for (int b = 0; b < K / 64; ++b) {
-                    if (want_o)
-                        tma_load_4d(smem + L::Q + s * L::QSLOT + b * (kC * 128), &mq, &bar.full[s],
-                                    64 * b, hq, c2, c3);
+                for (int b = 0; b < K / 64; ++b)
                     tma_load_4d(smem + L::KK + s * L::KSLOT + b * (kC * 128), &mk, &bar.full[s],
-                                64 * b, hk, c2, c3);
-                }
+                                64 * b, hk, token_at(i), c3);
 #pragma unroll
                 for (int b = 0; b < V / 64; ++b)
                     tma_load_4d(smem + L::VV + s * L::VSLOT + b * (kC * 128), &mv, &bar.full[s],
-                                64 * b, hv, c2, c3);
+                                64 * b, hv, token_at(i), c3);
             }
             // copies in flight land before the CTA ends (again with a limit)
             for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
                 mbar_wait(&bar.full[i % kStages], (i / kStages) & 1, kSpinLimit);
+        }
+        if (warp == 18 && want_o && elect_one()) {
+            tma_prefetch_desc(&mq);
+            const int hq = h / (p.H / p.Hq);
+            int issued = 0;
+#pragma unroll 1
+            for (int i = 0; i < nc; ++i) {
+                if (i > 0) wait(&bar.qs, i - 1);
+                if (dead) break;
+                mbar_arrive_expect_tx(&bar.qfull, kC * 2 * K);
+                issued = i + 1;
+#pragma unroll
+                for (int b = 0; b < K / 64; ++b) {
+                    tma_load_4d(smem + L::Q + b * (kC * 128), &mq, &bar.qfull, 64 * b, hq,
+                                token_at(i), c3);
+                    if (i + 1 < nc) tma_prefetch_l2_4d(&mq, 64 * b, hq, token_at(i + 1), c3);
+                }
+            }
+            if (issued) mbar_wait(&bar.qfull, (issued - 1) & 1, kSpinLimit);
         }
         // ---------------------------------------------------------------- MMAs
         if (warp == 17 && elect_one()) {
@@ -634,21 +672,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             constexpr uint32_t id_qs = idesc_bf16(128, V, false, false);
             constexpr uint32_t id_pv = idesc_bf16(128, V, false, true);
             constexpr uint32_t id_d = idesc_bf16(128, K, false, true);
-            const uint32_t q_0 = desc_lo(base + L::Q, 16), k_0 = desc_lo(base + L::KK, 16),
+            constexpr uint32_t id_low = idesc_bf16(128, K, true, true);
+            const uint32_t q = desc_lo(base + L::Q, 16), k_0 = desc_lo(base + L::KK, 16),
                            s_0 = desc_lo(base + L::S, 16), kt_0 = desc_lo(base + L::KK, kC * 128),
-                           v_0 = desc_lo(base + L::VV, kC * 128);
+                           v_0 = desc_lo(base + L::VV, kC * 128), low = desc_lo(base + L::LOW, kC * 128);
 #pragma unroll 1
             for (int i = 0; i < nc; ++i) {
                 const int s = i % kStages;
-                const uint32_t q = q_0 + s * (L::QSLOT >> 4), k = k_0 + s * (L::KSLOT >> 4),
-                               kt = kt_0 + s * (L::KSLOT >> 4), v = v_0 + s * (L::VSLOT >> 4);
+                const uint32_t kt = kt_0 + s * (L::KSLOT >> 4);
                 wait(&bar.full[s], i / kStages);
                 if (chunk_n(i) < kC) wait(&bar.tail, 0);  // one ragged chunk a segment
                 if (want_o) {
-                    if (i > 0) {  // P and the lowest pieces of V, in the scores' columns, are read
-                        wait(&bar.o, i - 1);
-                        wait(&bar.d, i - 1);
-                    }
+                    const uint32_t k = k_0 + s * (L::KSLOT >> 4);
+                    wait(&bar.qfull, i);
+                    if (i > 0) wait(&bar.o, i - 1);  // P, in the scores' columns, is read
                     tc_fence_after();
                     if (dead) continue;
 #pragma unroll 1
@@ -659,7 +696,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                             mma_ss(tmem + kColP, q + off, k + off, id_scores, y + x > 0);
                         }
                     mma_commit(&bar.scores);
-                    wait(&bar.s, i);
+                }
+                wait(&bar.s, i);
+                if (want_o) {
                     if (i > 0) wait(&bar.ofree, i - 1);
                     tc_fence_after();
                     if (dead) continue;
@@ -669,41 +708,48 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         for (int x = 0; x < 4; ++x)
                             mma_ss(tmem + kColO, q + y * (kC * 8) + 2 * x, s_0 + y * (V * 8) + 2 * x,
                                    id_qs, y + x > 0);
+                    mma_commit(&bar.qs);
+                }
+#pragma unroll 1
+                for (int c = 0; c < 2 && updates(i); ++c) {
+                    wait(&bar.vw[c], i);
+                    tc_fence_after();
+                    if (dead) break;
+                    // the small pieces first: the sum is cut to its size at each product
+#pragma unroll 1
+                    for (int y = 0; y < 3; ++y) {
+                        const uint32_t a = tmem + (y == 1 ? kColMid : kColHi);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {  // tokens 32 c .. and 64 + 32 c ..
+                            const int z = 2 * c + (x & 1) + 4 * (x >> 1);
+                            if (y == 0)
+                                mma_ss(tmem + kColD, low + z * (2048 >> 4), kt + z * (2048 >> 4),
+                                       id_low, c + x > 0);
+                            else
+                                mma_ts(tmem + kColD, a + 8 * z, kt + z * (2048 >> 4), id_d, 1);
+                        }
+                    }
+                    mma_commit(c ? &bar.d : &bar.d0);
+                }
+                if (want_o) {
+                    // after both halves of V: O, which goes to V's place, then
+                    // finds it read by the state threads too
                     wait(&bar.p, i);
                     tc_fence_after();
                     if (dead) continue;
+                    const uint32_t v = v_0 + s * (L::VSLOT >> 4);
 #pragma unroll 4
                     for (int x = 0; x < kC / 16; ++x)
                         mma_ts(tmem + kColO, tmem + kColP + 8 * x, v + x * (2048 >> 4), id_pv, 1);
                     mma_commit(&bar.o);
-                } else if (i > 0) {
-                    wait(&bar.s, i - 1);
                 }
-                if (i + 1 < nc || end) {
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        wait(&bar.vw[c], i);
-                        tc_fence_after();
-                        if (dead) break;
-                        // the small pieces first: the sum is cut to its size at each product
-#pragma unroll 1
-                        for (int y = 0; y < 3; ++y) {
-                            const uint32_t a = tmem + (y == 0 ? kColLow : y == 1 ? kColMid : kColHi);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {  // tokens 32 c .. and 64 + 32 c ..
-                                const int z = 2 * c + (x & 1) + 4 * (x >> 1);
-                                mma_ts(tmem + kColD, a + 8 * z, kt + z * (2048 >> 4), id_d,
-                                       c + y + x > 0);
-                            }
-                        }
-                    }
-                    if (dead) continue;
-                    mma_commit(&bar.d);
-                }
-                mma_commit(&bar.kvfree[s]);
+                if (dead) continue;
+                mma_commit(&bar.kfree[s]);
             }
             // every product is done before the tensor memory is given back
-            if (nc > 0) mbar_wait(&bar.kvfree[(nc - 1) % kStages], ((nc - 1) / kStages) & 1, dead ? 1000000 : kSpinLimit);
+            if (nc > 0)
+                mbar_wait(&bar.kfree[(nc - 1) % kStages], ((nc - 1) / kStages) & 1,
+                          dead ? 1000000 : kSpinLimit);
         }
     }
     if (dead) *abort_v = 1;
