@@ -48,7 +48,7 @@ namespace {
 constexpr int kC = 128;             // tokens of a chunk
 constexpr int kStages = 2;
 constexpr int kWarps = 20;
-constexpr int kBarRows = 1, kBarS = 2, kBarPair = 3;  // named barriers (kBarPair + 0 .. 3)
+constexpr int kBarRows = 1, kBarS = 2, kBarPair = 3;  // named barriers (kBarPair + 0 .. 3), 8, 9: halves of the rows
 constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColMid = 448;
 
 template <int K, int V>
@@ -203,7 +203,7 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t *b, uint32_t parity) {
 }
 
 struct LinBars {
-    uint64_t full[kStages], kfree[kStages], vfree[kStages], qfull, qs, d0;
+    uint64_t full[kStages], kvfree[kStages], vfree[kStages], qfull, qs, d0, dfree;
     uint64_t vw[2], scores, p, d, s, o, ofree, tail;
 };
 
@@ -267,12 +267,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (lane == 0) {
             for (int s = 0; s < kStages; ++s) {
                 mbar_init(&bar.full[s], 1);
-                mbar_init(&bar.kfree[s], 1);
-                mbar_init(&bar.vfree[s], 1);
+                mbar_init(&bar.kvfree[s], 1);
+                mbar_init(&bar.vfree[s], 2);
             }
             mbar_init(&bar.qfull, 1);
             mbar_init(&bar.qs, 1);
             mbar_init(&bar.d0, 1);
+            mbar_init(&bar.dfree, 8);
             mbar_init(&bar.scores, 1);
             mbar_init(&bar.p, 8);
             mbar_init(&bar.vw[0], 8);
@@ -386,47 +387,51 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
                 // O: half of this row's columns
                 const float rho = p.read_scale * exp2f(lrho);
-                uint8_t *const stage = smem + L::VV + (i % kStages) * L::VSLOT;
                 const bool whole = n == kC && !p.o_float;
                 wait_warp(&bar.o, i);
                 tc_fence_after();
 #pragma unroll 1
-                for (int b = part * (V / 64); b < (part + 1) * (V / 64); ++b) {
+                for (int b = 0; b < V / 64; ++b) {
                     float x[32];
-                    tmem_ld32(tmem + quad + kColO + 32 * b, x);
+                    tmem_ld32(tmem + quad + kColO + 32 * (b + part * (V / 64)), x);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) mul2(x[2 * e], x[2 * e + 1], rho, rho);
                     if (whole) {
-                        store_row<4>(stage + (b / 2) * (kC * 128), t, (b % 2) * 4, x);
+                        store_row<4>(smem + L::VV + (i % kStages) * L::VSLOT +
+                                         (V == 128 ? part * (kC * 128) : 0), t,
+                                     V == 128 ? 4 * b : 4 * part, x);
                     } else if (t < n && !dead) {
-                        const size_t row = ((size_t)(it.first + f0 + chunk_at(i) + t) * p.H + h) * V;
+                        const size_t at = ((size_t)(it.first + f0 + chunk_at(i) + t) * p.H + h) * V +
+                                          32 * (b + part * (V / 64));
                         if (p.o_float) {
-                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row + 32 * b);
+                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                         } else {
                             uint32_t w[16];
                             pack_row(x, w);
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + row + 32 * b);
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         }
                     }
+                    __syncwarp();
                 }
                 tc_fence_before();
                 arrive_warp(&bar.ofree);
+                // V = 128: each half of the warps sends its 64 columns; V = 64: all send one box
                 if (whole) fence_proxy_async_smem();
-                named_sync(kBarRows, 256);
-                if (warp == 0 && lane == 0) {
-                    if (whole && !dead) {
+                if (V == 128) named_sync(kBarRows + 7 + part, 128);
+                else named_sync(kBarRows, 256);
+                if ((warp & 3) == 0 && lane == 0) {
+                    if (whole && !dead && (V == 128 || part == 0)) {
                         const int at = f0 + chunk_at(i);
-                        const int c2 = p.offsets ? it.base + at : at, c3 = p.offsets ? 0 : it.seq;
-#pragma unroll
-                        for (int b = 0; b < V / 64; ++b)
-                            tma_store_4d(&mo, stage + b * (kC * 128), 64 * b, h, c2, c3);
+                        tma_store_4d(&mo, smem + L::VV + (i % kStages) * L::VSLOT + part * (kC * 128),
+                                     64 * part, h, p.offsets ? it.base + at : at,
+                                     p.offsets ? 0 : it.seq);
                         bulk_commit_group();
                         bulk_wait_read_all();
                     }
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
                 __syncwarp();
             }
-            if (warp == 0 && lane == 0) bulk_wait_all();
+            if ((warp & 3) == 0 && lane == 0) bulk_wait_all();
         }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- state
@@ -491,26 +496,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const int st = tid - 256;  // 0..255 of both groups
         int n_table = -1;
         auto store_state = [&] {
-            if (want_o) {
-                if (mine) {
-                    // rows of 128 bytes hold 64 columns; K = 64: the groups share one row
+            if (mine) {
+                // rows of 128 bytes hold 64 columns; K = 64: the groups share one row
 #pragma unroll
-                    for (int e = 0; e < NS / 32; ++e) {
-                        float x[32];
+                for (int e = 0; e < NS / 32; ++e) {
+                    float x[32];
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) x[y] = S[32 * e + y];
-                        const int col = k0 + 32 * e;
-                        store_row<4>(smem + L::S + (col / 64) * (V * 128), v, (col % 64) / 8, x);
-                    }
+                    for (int y = 0; y < 32; ++y) x[y] = S[32 * e + y];
+                    const int col = k0 + 32 * e;
+                    store_row<4>(smem + L::S + (col / 64) * (V * 128), v, (col % 64) / 8, x);
                 }
-                fence_proxy_async_smem();
             }
+            fence_proxy_async_smem();
             arrive_warp(&bar.s);
         };
         // lanes 8 j .. address block j: tokens + 8 (j / 2), channels + 8 (j % 2)
         const uint32_t tok = g * 64 + (lane & 7) + ((lane >> 4) << 3);
         const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
-        if (nc > 0) store_state();
+        if (want_o && nc > 0) store_state();
         // step 2 i + c: half c of chunk i's V; S takes chunk i - 1 up after the
         // first half of chunk i is on its way
 #pragma unroll 1
@@ -602,7 +605,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
                 }
                 tc_fence_before();
-                if (i < nc) store_state();
+                arrive_warp(&bar.dfree);
+                if (want_o && i < nc) store_state();
             }
         }
         if (end && mine && !dead) {
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int i = 0; i < nc; ++i) {
                 const int s = i % kStages;
                 if (i >= kStages) {
-                    wait(&bar.kfree[s], i / kStages - 1);
+                    wait(&bar.kvfree[s], i / kStages - 1);
                     if (want_o) wait(&bar.vfree[s], i / kStages - 1);
                 }
                 if (dead) break;
@@ -641,6 +645,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int b = 0; b < V / 64; ++b)
                     tma_load_4d(smem + L::VV + s * L::VSLOT + b * (kC * 128), &mv, &bar.full[s],
                                 64 * b, hv, token_at(i), c3);
+                // two chunks on, to the L2 cache
+                if (i + kStages < nc) {
+#pragma unroll
+                    for (int b = 0; b < K / 64; ++b)
+                        tma_prefetch_l2_4d(&mk, 64 * b, hk, token_at(i + kStages), c3);
+#pragma unroll
+                    for (int b = 0; b < V / 64; ++b)
+                        tma_prefetch_l2_4d(&mv, 64 * b, hv, token_at(i + kStages), c3);
+                }
             }
             // copies in flight land before the CTA ends (again with a limit)
             for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
@@ -660,7 +673,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int b = 0; b < K / 64; ++b) {
                     tma_load_4d(smem + L::Q + b * (kC * 128), &mq, &bar.qfull, 64 * b, hq,
                                 token_at(i), c3);
-                    if (i + 1 < nc) tma_prefetch_l2_4d(&mq, 64 * b, hq, token_at(i + 1), c3);
+                    if (i + 2 < nc) tma_prefetch_l2_4d(&mq, 64 * b, hq, token_at(i + 2), c3);
                 }
             }
             if (issued) mbar_wait(&bar.qfull, (issued - 1) & 1, kSpinLimit);
@@ -697,43 +710,45 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         }
                     mma_commit(&bar.scores);
                 }
-                wait(&bar.s, i);
-                if (want_o) {
-                    if (i > 0) wait(&bar.ofree, i - 1);
-                    tc_fence_after();
-                    if (dead) continue;
+                // D's first half goes ahead of the state's way through shared memory
 #pragma unroll 1
-                    for (int y = 0; y < K / 64; ++y)
+                for (int c = 0; c < 2; ++c) {
+                    if (updates(i)) {
+                        wait(&bar.vw[c], i);
+                        if (c == 0 && i > 0) wait(&bar.dfree, i - 1);
+                        tc_fence_after();
+                        if (dead) break;
+                        // the small pieces first: the sum is cut to its size at each product
+#pragma unroll 1
+                        for (int y = 0; y < 3; ++y) {
+                            const uint32_t a = tmem + (y == 1 ? kColMid : kColHi);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mma_ss(tmem + kColO, q + y * (kC * 8) + 2 * x, s_0 + y * (V * 8) + 2 * x,
-                                   id_qs, y + x > 0);
-                    mma_commit(&bar.qs);
-                }
-#pragma unroll 1
-                for (int c = 0; c < 2 && updates(i); ++c) {
-                    wait(&bar.vw[c], i);
-                    tc_fence_after();
-                    if (dead) break;
-                    // the small pieces first: the sum is cut to its size at each product
-#pragma unroll 1
-                    for (int y = 0; y < 3; ++y) {
-                        const uint32_t a = tmem + (y == 1 ? kColMid : kColHi);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {  // tokens 32 c .. and 64 + 32 c ..
-                            const int z = 2 * c + (x & 1) + 4 * (x >> 1);
-                            if (y == 0)
-                                mma_ss(tmem + kColD, low + z * (2048 >> 4), kt + z * (2048 >> 4),
-                                       id_low, c + x > 0);
-                            else
-                                mma_ts(tmem + kColD, a + 8 * z, kt + z * (2048 >> 4), id_d, 1);
+                            for (int x = 0; x < 4; ++x) {  // tokens 32 c .. and 64 + 32 c ..
+                                const int z = 2 * c + (x & 1) + 4 * (x >> 1);
+                                if (y == 0)
+                                    mma_ss(tmem + kColD, low + z * (2048 >> 4), kt + z * (2048 >> 4),
+                                           id_low, c + x > 0);
+                                else
+                                    mma_ts(tmem + kColD, a + 8 * z, kt + z * (2048 >> 4), id_d, 1);
+                            }
                         }
+                        mma_commit(c ? &bar.d : &bar.d0);
                     }
-                    mma_commit(c ? &bar.d : &bar.d0);
+                    if (c == 0 && want_o) {
+                        wait(&bar.s, i);
+                        if (i > 0) wait(&bar.ofree, i - 1);
+                        tc_fence_after();
+                        if (dead) break;
+#pragma unroll 1
+                        for (int y = 0; y < K / 64; ++y)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                mma_ss(tmem + kColO, q + y * (kC * 8) + 2 * x,
+                                       s_0 + y * (V * 8) + 2 * x, id_qs, y + x > 0);
+                        mma_commit(&bar.qs);
+                    }
                 }
                 if (want_o) {
-                    // after both halves of V: O, which goes to V's place, then
-                    // finds it read by the state threads too
                     wait(&bar.p, i);
                     tc_fence_after();
                     if (dead) continue;
@@ -744,11 +759,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     mma_commit(&bar.o);
                 }
                 if (dead) continue;
-                mma_commit(&bar.kfree[s]);
+                mma_commit(&bar.kvfree[s]);
             }
             // every product is done before the tensor memory is given back
             if (nc > 0)
-                mbar_wait(&bar.kfree[(nc - 1) % kStages], ((nc - 1) / kStages) & 1,
+                mbar_wait(&bar.kvfree[(nc - 1) % kStages], ((nc - 1) / kStages) & 1,
                           dead ? 1000000 : kSpinLimit);
         }
     }
@@ -781,13 +796,11 @@ cudaError_t launch_kv(const LinearScan &a, float *slots, cudaStream_t st) {
         return cudaErrorInvalidValue;
     mq = mk;
     mo = mv;
-    if (a.o) {
-        if (!make_strided_token_map(&mq, a.q, B, a.T, a.ldq, a.ldq * a.T, a.Hq, K, kC))
-            return cudaErrorInvalidValue;
-        const long long ldo = (long long)a.H * V;
-        if (!a.o_float && !make_strided_token_map(&mo, a.o, B, a.T, ldo, ldo * a.T, a.H, V, kC))
-            return cudaErrorInvalidValue;
-    }
+    if (a.o && !make_strided_token_map(&mq, a.q, B, a.T, a.ldq, a.ldq * a.T, a.Hq, K, kC))
+        return cudaErrorInvalidValue;
+    const long long ldo = (long long)a.H * V;
+    if (a.o && !a.o_float && !make_strided_token_map(&mo, a.o, B, a.T, ldo, ldo * a.T, a.H, V, kC))
+        return cudaErrorInvalidValue;
     LinTcArgs arg = {a, linear_tc_plan(a.B, a.T, a.H, K, V, packed), nullptr, nullptr,
                      device_status_ptr()};
     const long long grid = (long long)arg.plan.items * a.H;
