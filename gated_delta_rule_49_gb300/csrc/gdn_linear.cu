@@ -186,20 +186,28 @@ __global__ void __launch_bounds__(kScanThreads)
         for (int c = 0; c < C; ++c) end[(size_t)(row0 + r) * K + lane * C + c] = f * S[r][c];
 }
 
+// Cuts as in linear_tc_plan, counted in token times: about six CTAs run on an
+// SM, one needs its segment's tokens and about 32 more to start and end, and a
+// first pass as long again.
 SegPlan token_plan(int B, int T, int H, int V, bool packed) {
-    // a CTA needs some hundred nanoseconds a token, whatever else runs: cut
-    // few long sequences until about six CTAs an SM run, segments of 256
-    // tokens at least (each costs a second pass over k and v)
     const int nsm = sm_count() > 0 ? sm_count() : 152;
-    const long long per_token_range = (long long)H * (V / kCtaRows);
-    const long long have = per_token_range * B;
-    if (have >= 3LL * nsm || T <= 512) return {T > 0 ? T : 1, B};
-    const long long want = (6LL * nsm + per_token_range - 1) / per_token_range;  // segments in all
-    long long len = (packed ? T : (long long)T * B) / want;
-    len = len < 256 ? 256 : (len + 15) / 16 * 16;
-    if (len * 2 > T) return {T, B};
-    const long long n = (T + len - 1) / len;
-    return {(int)len, (int)(packed ? n + B : n * B)};
+    const long long longest = packed && 4LL * T / B < T ? 4LL * T / B : T;
+    auto waves = [&](long long items) {
+        return (double)((items * H * (V / kCtaRows) + 6 * nsm - 1) / (6 * nsm));
+    };
+    SegPlan best{T > 0 ? T : 1, B};
+    double least = waves(B) * (longest + 32);
+    for (int n = 2; n <= 64 && longest / n >= 2 * kTile; ++n) {
+        const long long len = (longest + (long long)n * kTile - 1) / ((long long)n * kTile) * kTile;
+        const long long per = ((packed ? T : longest) + len - 1) / len;
+        const long long items = packed ? per + B : per * B;
+        const double cost = waves(items) * (len + 32) * 2;
+        if (cost < least) {
+            least = cost;
+            best = {(int)len, (int)items};
+        }
+    }
+    return best;
 }
 
 template <typename T>

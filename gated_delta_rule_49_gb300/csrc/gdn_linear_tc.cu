@@ -3,13 +3,12 @@
 // a token in scan order within its chunk and S the state at the chunk's start:
 //
 //     O = diag(read a^(p_t + 1)) [Q S^T + P V],
-//         P_ts = write a^(-(p_s + 1)) (q_t . k_s) where p_s <= p_t, else 0
+//         P_ts = write a^(p_t - p_s) / a^(p_t + 1) (q_t . k_s) where p_s <= p_t, else 0
 //     S <- a^C S + D,   D = (diag(write a^(C - 1 - p_s)) V)^T K
 //
 // The row factor stands outside of both products, so that they share one
-// accumulator.  Where a^128 would leave 2^-64 .. 1 the row factor is held at
-// 2^-64 and P takes the exact remaining power; what that mis-weights is S's
-// part of rows that have decayed by more than 2^-64.
+// accumulator.  It is held at 2^-64 and P takes the exact remaining power: what
+// that mis-weights is S's part of rows that have decayed by more than 2^-64.
 //
 // Precision: P and S are rounded to bf16 as operands (a step of the bf16
 // output each).  The state itself has to be a float32 result, so the weighted
@@ -21,17 +20,17 @@
 // One CTA runs one segment of one (sequence, head), 20 warps in groups of 4:
 //   0-7   rows (two warps share 32 of them): P, from Q K^T in TMEM, weighted,
 //         back to TMEM as bf16 (over the columns that it came from) for the
-//         product with V; then O from TMEM, scaled, to shared memory in V's
-//         place and out by TMA (ragged chunks: plain stores)
+//         product with V; then O from TMEM, scaled, to shared memory (in K's
+//         place) and out by TMA (ragged chunks: plain stores)
 //   8-15  state: two groups of 128 threads; each chunk's V in two halves of
 //         tokens, transposed, weighted and split: two pieces to TMEM, the
 //         lowest back to shared memory, all as operands of D; and S = a^C S + D
 //         (thread v holds half of row v), as bf16 to shared memory for the next
 //         chunk's Q S^T.  The first half of the next chunk's V goes before the
 //         wait for D, so that D is formed while it runs.
-//   16    loads K and V, two chunks ahead; 18 loads Q (free as soon as Q S^T
-//         is done; the next is on its way to the L2 cache by then)
-//   17    issues the MMAs (19 only fills its group)
+//   16    loads K and V, two chunks ahead; 18 loads Q (as soon as the last
+//         chunk's Q S^T is done)
+//   17    issues the MMAs; 19 sends O
 // Launched with 96 registers a thread (5 groups x 128 threads x 96 = 61440);
 // the groups then share the same 480 registers a lane of the five as
 // 2 x 88 + 2 x 128 + 48, so that S, a row piece of 64 floats, needs no spill.
@@ -48,14 +47,14 @@ namespace {
 constexpr int kC = 128;             // tokens of a chunk
 constexpr int kStages = 2;
 constexpr int kWarps = 20;
-constexpr int kBarRows = 1, kBarS = 2, kBarPair = 3;  // named barriers (kBarPair + 0 .. 3), 8, 9: halves of the rows
+constexpr int kBarRows = 1, kBarS = 2, kBarPair = 3;  // named barriers (kBarPair + 0 .. 3)
 constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColMid = 448;
 
 template <int K, int V>
 struct LinLayout {
     static constexpr uint32_t QSLOT = kC * 2 * K;
     static constexpr uint32_t KSLOT = kC * 2 * K;
-    static constexpr uint32_t VSLOT = kC * 2 * V;  // then takes O
+    static constexpr uint32_t VSLOT = kC * 2 * V;
     // as an operand of 128 rows the lowest pieces reach past V = 64 columns,
     // into what follows (rows that nothing reads)
     static constexpr uint32_t LOW = 0;
@@ -63,7 +62,11 @@ struct LinLayout {
     static constexpr uint32_t KK = Q + QSLOT;
     static constexpr uint32_t VV = KK + kStages * KSLOT;
     static constexpr uint32_t S = VV + kStages * VSLOT;
-    static constexpr uint32_t TABLE = S + 2 * K * V;  // column factors of P, weights of V
+    // O on its way out: K's slot of the chunk where all of the memory is taken
+    // (K is read before O is complete), else a place of its own
+    static constexpr bool O_IN_K = K == 128 && V == 128;
+    static constexpr uint32_t OUT = S + 2 * K * V;
+    static constexpr uint32_t TABLE = OUT + (O_IN_K ? 0 : kC * 2 * V);  // column factors of P, weights of V
     static constexpr uint32_t SMEM = TABLE + 2 * kC * 4 + 1024;  // + alignment
 };
 
@@ -188,6 +191,21 @@ __device__ __forceinline__ void weigh_each(uint32_t taddr, int lag0, bool up, fl
     tmem_st_wait();
 }
 
+// Block b of 32 columns of row t of a tile of kCols (64 or 32) columns, in the
+// swizzle of its row length (128 or 64 bytes).
+template <int kCols>
+__device__ __forceinline__ void store_row_out(uint8_t *tile, int t, int b, const float (&x)[32]) {
+    if constexpr (kCols == 64) {
+        store_row<4>(tile, t, 4 * b, x);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(tile + t * 64 + ((c ^ ((t >> 1) & 3)) << 4)) =
+                make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
+                           pack_bf16(x[8 * c + 4], x[8 * c + 5]), pack_bf16(x[8 * c + 6], x[8 * c + 7]));
+    }
+}
+
 // mbar_try_wait that leaves the thread asleep until the phase completes, or
 // for up to a millisecond: waits that spun took two fifths of all issued
 // instructions.
@@ -203,7 +221,7 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t *b, uint32_t parity) {
 }
 
 struct LinBars {
-    uint64_t full[kStages], kvfree[kStages], vfree[kStages], qfull, qs, d0, dfree;
+    uint64_t kfull[kStages], vfull[kStages], used[kStages], sent[kStages], staged, qfull, qs, d0, dfree;
     uint64_t vw[2], scores, p, d, s, o, ofree, tail;
 };
 
@@ -266,10 +284,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         tmem_relinquish();
         if (lane == 0) {
             for (int s = 0; s < kStages; ++s) {
-                mbar_init(&bar.full[s], 1);
-                mbar_init(&bar.kvfree[s], 1);
-                mbar_init(&bar.vfree[s], 2);
+                mbar_init(&bar.kfull[s], 1);
+                mbar_init(&bar.vfull[s], 1);
+                mbar_init(&bar.used[s], 1);
+                mbar_init(&bar.sent[s], 1);
             }
+            mbar_init(&bar.staged, 8);
             mbar_init(&bar.qfull, 1);
             mbar_init(&bar.qs, 1);
             mbar_init(&bar.d0, 1);
@@ -325,18 +345,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         reg_dec<88>();
         if (want_o) {
             const int t = (warp & 3) * 32 + lane, part = warp >> 2;
-            const bool mild = lg * kC >= -64.f;
+            // the powers within a block of 32 columns; a row's factor of the block
+            // takes the rest of the lag
+            if (part == 0 && t < 32) colfac[t] = p.write_scale * exp2f((float)(rev ? t : 31 - t) * lg);
+            named_sync(kBarRows, 256);
 #pragma unroll 1
             for (int i = 0; i < nc; ++i) {
                 const int n = chunk_n(i), lead = chunk_lead(i);
-                if (i == 0 || (rev && i == 1)) {  // the last tables' readers are done
-                    named_sync(kBarRows, 256);
-                    const int ps = (rev ? n - 1 - t : t) + lead;  // of column t
-                    if (part == 0)
-                        colfac[t] = ps < 0 || (rev && t >= n) ? 0.f
-                                    : mild ? p.write_scale * exp2f(-(float)ps * lg) : p.write_scale;
-                    named_sync(kBarRows, 256);
-                }
                 const int pt = (rev ? n - 1 - t : t) + lead;
                 const float lrho = fmaxf((float)pt * lg, -64.f);
                 wait_warp(&bar.scores, i);
@@ -350,8 +365,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     const int q = warp & 3;
                     const bool blank = rev ? b < q : b > q;
                     float x[32];
+                    // one power for the row and block: within the diagonal block
+                    // it reaches a^-31, so that where a < 1/4 its scores are
+                    // weighted one by one instead
+                    const bool each = b == q && lg < -2.f;
+                    const int far = rev ? 32 * b - t : t - 32 * b - 31;
                     if (!blank) {
-                        if (!mild) weigh_each(tmem + quad + kColP + 32 * b, rev ? 32 * b - t : t - 32 * b, rev, lg, lrho);
+                        if (each) weigh_each(tmem + quad + kColP + 32 * b, rev ? far : far + 31, rev, lg, lrho);
                         tmem_ld32(tmem + quad + kColP + 32 * b, x);
                         tmem_ld_wait();
                     }
@@ -361,12 +381,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) w[e] = 0;
                     } else {
-                        const float4 *f4 = reinterpret_cast<const float4 *>(colfac + 32 * b);
+                        const float rf = each ? p.write_scale : ex2((float)far * lg - lrho);
+                        const float4 *f4 = reinterpret_cast<const float4 *>(colfac);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const float4 f = f4[e];
+                            const float4 f = each ? make_float4(1.f, 1.f, 1.f, 1.f) : f4[e];
                             mul2(x[4 * e], x[4 * e + 1], f.x, f.y);
                             mul2(x[4 * e + 2], x[4 * e + 3], f.z, f.w);
+                            mul2(x[4 * e], x[4 * e + 1], rf, rf);
+                            mul2(x[4 * e + 2], x[4 * e + 3], rf, rf);
                         }
                         pack_row(x, w);
                         if (b == q) {  // the columns at or before this row, in scan order
@@ -388,22 +411,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 // O: half of this row's columns
                 const float rho = p.read_scale * exp2f(lrho);
                 const bool whole = n == kC && !p.o_float;
+                constexpr int kCols = V / 2;  // of a warp
+                uint8_t *const stage = smem + (L::O_IN_K ? L::KK + (i % kStages) * L::KSLOT : L::OUT) +
+                                       part * (kC * 2 * kCols);
+                if (!L::O_IN_K && i > 0) wait_warp(&bar.sent[(i - 1) % kStages], (i - 1) / kStages);
                 wait_warp(&bar.o, i);
                 tc_fence_after();
 #pragma unroll 1
-                for (int b = 0; b < V / 64; ++b) {
+                for (int b = 0; b < kCols / 32; ++b) {
                     float x[32];
-                    tmem_ld32(tmem + quad + kColO + 32 * (b + part * (V / 64)), x);
+                    tmem_ld32(tmem + quad + kColO + part * kCols + 32 * b, x);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) mul2(x[2 * e], x[2 * e + 1], rho, rho);
                     if (whole) {
-                        store_row<4>(smem + L::VV + (i % kStages) * L::VSLOT +
-                                         (V == 128 ? part * (kC * 128) : 0), t,
-                                     V == 128 ? 4 * b : 4 * part, x);
+                        store_row_out<kCols>(stage, t, b, x);
                     } else if (t < n && !dead) {
                         const size_t at = ((size_t)(it.first + f0 + chunk_at(i) + t) * p.H + h) * V +
-                                          32 * (b + part * (V / 64));
+                                          part * kCols + 32 * b;
                         if (p.o_float) {
                             float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at);
 #pragma unroll
@@ -422,24 +447,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
                 tc_fence_before();
                 arrive_warp(&bar.ofree);
-                // V = 128: each half of the warps sends its 64 columns; V = 64: all send one box
-                if (whole) fence_proxy_async_smem();
-                if (V == 128) named_sync(kBarRows + 7 + part, 128);
-                else named_sync(kBarRows, 256);
-                if ((warp & 3) == 0 && lane == 0) {
-                    if (whole && !dead && (V == 128 || part == 0)) {
-                        const int at = f0 + chunk_at(i);
-                        tma_store_4d(&mo, smem + L::VV + (i % kStages) * L::VSLOT + part * (kC * 128),
-                                     64 * part, h, p.offsets ? it.base + at : at,
-                                     p.offsets ? 0 : it.seq);
-                        bulk_commit_group();
-                        bulk_wait_read_all();
-                    }
-                    mbar_arrive(&bar.vfree[i % kStages]);
-                }
-                __syncwarp();
+                fence_proxy_async_smem();
+                arrive_warp(&bar.staged);
             }
-            if ((warp & 3) == 0 && lane == 0) bulk_wait_all();
         }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- state
@@ -521,8 +531,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const int i = step >> 1, c = step & 1;
             if (c == 0 && i < nc) {
                 const int n = chunk_n(i);
-                wait_warp(&bar.full[i % kStages], i / kStages);
+                wait_warp(&bar.vfull[i % kStages], i / kStages);
                 if (n < kC) {
+                    wait_warp(&bar.kfull[i % kStages], i / kStages);
                     // the rows behind the sequence's last token are another's, or none
                     const uint4 zero = make_uint4(0, 0, 0, 0);
                     uint8_t *kt = smem + L::KK + (i % kStages) * L::KSLOT,
@@ -626,38 +637,32 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             tma_prefetch_desc(&mk);
             tma_prefetch_desc(&mv);
             const int hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
-            int issued = 0;
+            int vs = 0, ks = 0;  // loads issued
 #pragma unroll 1
             for (int i = 0; i < nc; ++i) {
                 const int s = i % kStages;
-                if (i >= kStages) {
-                    wait(&bar.kvfree[s], i / kStages - 1);
-                    if (want_o) wait(&bar.vfree[s], i / kStages - 1);
-                }
+                if (i >= kStages) wait(&bar.used[s], i / kStages - 1);
                 if (dead) break;
-                mbar_arrive_expect_tx(&bar.full[s], kC * 2 * (K + V));
-                issued = i + 1;
-#pragma unroll
-                for (int b = 0; b < K / 64; ++b)
-                    tma_load_4d(smem + L::KK + s * L::KSLOT + b * (kC * 128), &mk, &bar.full[s],
-                                64 * b, hk, token_at(i), c3);
+                mbar_arrive_expect_tx(&bar.vfull[s], kC * 2 * V);
+                vs = i + 1;
 #pragma unroll
                 for (int b = 0; b < V / 64; ++b)
-                    tma_load_4d(smem + L::VV + s * L::VSLOT + b * (kC * 128), &mv, &bar.full[s],
+                    tma_load_4d(smem + L::VV + s * L::VSLOT + b * (kC * 128), &mv, &bar.vfull[s],
                                 64 * b, hv, token_at(i), c3);
-                // two chunks on, to the L2 cache
-                if (i + kStages < nc) {
+                if (L::O_IN_K && want_o && i >= kStages) wait(&bar.sent[s], i / kStages - 1);
+                if (dead) break;
+                mbar_arrive_expect_tx(&bar.kfull[s], kC * 2 * K);
+                ks = i + 1;
 #pragma unroll
-                    for (int b = 0; b < K / 64; ++b)
-                        tma_prefetch_l2_4d(&mk, 64 * b, hk, token_at(i + kStages), c3);
-#pragma unroll
-                    for (int b = 0; b < V / 64; ++b)
-                        tma_prefetch_l2_4d(&mv, 64 * b, hv, token_at(i + kStages), c3);
-                }
+                for (int b = 0; b < K / 64; ++b)
+                    tma_load_4d(smem + L::KK + s * L::KSLOT + b * (kC * 128), &mk, &bar.kfull[s],
+                                64 * b, hk, token_at(i), c3);
             }
             // copies in flight land before the CTA ends (again with a limit)
-            for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                mbar_wait(&bar.full[i % kStages], (i / kStages) & 1, kSpinLimit);
+            for (int i = vs > kStages ? vs - kStages : 0; i < vs; ++i)
+                mbar_wait(&bar.vfull[i % kStages], (i / kStages) & 1, kSpinLimit);
+            for (int i = ks > kStages ? ks - kStages : 0; i < ks; ++i)
+                mbar_wait(&bar.kfull[i % kStages], (i / kStages) & 1, kSpinLimit);
         }
         if (warp == 18 && want_o && elect_one()) {
             tma_prefetch_desc(&mq);
@@ -670,13 +675,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 mbar_arrive_expect_tx(&bar.qfull, kC * 2 * K);
                 issued = i + 1;
 #pragma unroll
-                for (int b = 0; b < K / 64; ++b) {
+                for (int b = 0; b < K / 64; ++b)
                     tma_load_4d(smem + L::Q + b * (kC * 128), &mq, &bar.qfull, 64 * b, hq,
                                 token_at(i), c3);
-                    if (i + 2 < nc) tma_prefetch_l2_4d(&mq, 64 * b, hq, token_at(i + 2), c3);
-                }
             }
             if (issued) mbar_wait(&bar.qfull, (issued - 1) & 1, kSpinLimit);
+        }
+        // ---------------------------------------------------------------- O out
+        if (warp == 19 && want_o && elect_one()) {
+#pragma unroll 1
+            for (int i = 0; i < nc; ++i) {
+                wait(&bar.staged, i);
+                if (chunk_n(i) == kC && !p.o_float && !dead) {
+                    const uint8_t *stage = smem + (L::O_IN_K ? L::KK + (i % kStages) * L::KSLOT : L::OUT);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        tma_store_4d(&mo, stage + b * (kC * V), b * (V / 2), h, token_at(i), c3);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                }
+                mbar_arrive(&bar.sent[i % kStages]);
+            }
+            bulk_wait_all();
         }
         // ---------------------------------------------------------------- MMAs
         if (warp == 17 && elect_one()) {
@@ -693,7 +713,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int i = 0; i < nc; ++i) {
                 const int s = i % kStages;
                 const uint32_t kt = kt_0 + s * (L::KSLOT >> 4);
-                wait(&bar.full[s], i / kStages);
+                wait(&bar.kfull[s], i / kStages);
+                wait(&bar.vfull[s], i / kStages);
                 if (chunk_n(i) < kC) wait(&bar.tail, 0);  // one ragged chunk a segment
                 if (want_o) {
                     const uint32_t k = k_0 + s * (L::KSLOT >> 4);
@@ -759,11 +780,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     mma_commit(&bar.o);
                 }
                 if (dead) continue;
-                mma_commit(&bar.kvfree[s]);
+                mma_commit(&bar.used[s]);
             }
             // every product is done before the tensor memory is given back
             if (nc > 0)
-                mbar_wait(&bar.kvfree[(nc - 1) % kStages], ((nc - 1) / kStages) & 1,
+                mbar_wait(&bar.used[(nc - 1) % kStages], ((nc - 1) / kStages) & 1,
                           dead ? 1000000 : kSpinLimit);
         }
     }
@@ -799,7 +820,7 @@ cudaError_t launch_kv(const LinearScan &a, float *slots, cudaStream_t st) {
     if (a.o && !make_strided_token_map(&mq, a.q, B, a.T, a.ldq, a.ldq * a.T, a.Hq, K, kC))
         return cudaErrorInvalidValue;
     const long long ldo = (long long)a.H * V;
-    if (a.o && !a.o_float && !make_strided_token_map(&mo, a.o, B, a.T, ldo, ldo * a.T, a.H, V, kC))
+    if (a.o && !a.o_float && !make_strided_token_map(&mo, a.o, B, a.T, ldo, ldo * a.T, a.H, V, kC, V / 2))
         return cudaErrorInvalidValue;
     LinTcArgs arg = {a, linear_tc_plan(a.B, a.T, a.H, K, V, packed), nullptr, nullptr,
                      device_status_ptr()};
@@ -819,21 +840,31 @@ cudaError_t launch_kv(const LinearScan &a, float *slots, cudaStream_t st) {
 
 }  // namespace
 
+// The cost of a cut is counted in chunk times: a wave of CTAs (one an SM) takes
+// its segment's chunks and about two more to start and end, and a first pass
+// over all but the last segments takes 0.6 of that.  (B = 1, T = 65536, H = 16,
+// 128 x 128: 4 segments a sequence 616 us, 9 286 us.)  How long the longest of
+// packed sequences is, the host does not know: four times the mean is assumed.
 SegPlan linear_tc_plan(int B, int T, int H, int K, int V, bool packed) {
     (void)K;
     (void)V;
-    // One CTA an SM.  A CTA alone takes about 1 us a chunk, and about 50 of
-    // them together are bound by memory: more segments than for some 64 CTAs
-    // only add the first pass's reading of k and v.  Segments of 4 chunks at
-    // least.
-    const long long have = (long long)B * H;
-    if (have >= 64 || T <= 8 * kC) return {T > 0 ? T : 1, B};
-    const long long want = (64 + H - 1) / H;  // segments in all
-    long long len = (packed ? T : (long long)T * B) / want;
-    len = len < 4 * kC ? 4 * kC : (len + kC - 1) / kC * kC;
-    if (len * 2 > T) return {T, B};
-    const long long n = (T + len - 1) / len;
-    return {(int)len, (int)(packed ? n + B : n * B)};
+    const int nsm = sm_count() > 0 ? sm_count() : 152;
+    const long long longest = packed && 4LL * T / B < T ? 4LL * T / B : T;
+    auto waves = [&](long long items) { return (double)((items * H + nsm - 1) / nsm); };
+    auto chunks = [](long long len) { return (double)((len + kC - 1) / kC); };
+    SegPlan best{T > 0 ? T : 1, B};
+    double least = waves(B) * (chunks(longest) + 2);
+    for (int n = 2; n <= 64 && longest / n >= 2 * kC; ++n) {
+        const long long len = (longest + (long long)n * kC - 1) / ((long long)n * kC) * kC;
+        const long long per = ((packed ? T : longest) + len - 1) / len;
+        const long long items = packed ? per + B : per * B;
+        const double cost = waves(items) * (chunks(len) + 2) * 1.6;
+        if (cost < least) {
+            least = cost;
+            best = {(int)len, (int)items};
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_linear_tc(const LinearScan &a, float *slots, cudaStream_t stream) {

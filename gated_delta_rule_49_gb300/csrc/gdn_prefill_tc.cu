@@ -1772,16 +1772,18 @@ bool make_token_map(CUtensorMap *m, const void *ptr, int B, int T, int Ts, int H
 }
 
 bool make_strided_token_map(CUtensorMap *m, const void *ptr, int B, int T, long long token_stride,
-                            long long batch_stride, int H, int C, int box_tokens) {
+                            long long batch_stride, int H, int C, int box_tokens,
+                            int box_channels) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {(cuuint64_t)C, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
     cuuint64_t strides[3] = {(cuuint64_t)C * 2, (cuuint64_t)token_stride * 2,
                              (cuuint64_t)batch_stride * 2};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_tokens, 1};
+    cuuint32_t box[4] = {(cuuint32_t)box_channels, 1, (cuuint32_t)box_tokens, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides,
-               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_channels == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }

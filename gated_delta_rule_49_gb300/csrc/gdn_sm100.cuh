@@ -279,8 +279,10 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 // the encoder rejects the arguments.
 bool make_token_map(CUtensorMap *m, const void *ptr, int B, int T, int Ts, int H, int C);
 // The same with any distance (in elements, multiples of 8) between tokens and
-// between batch entries, and boxes of 64 channels x box_tokens tokens.
+// between batch entries, and boxes of box_channels (64, or 32 with the 64-byte
+// swizzle) x box_tokens tokens.
 bool make_strided_token_map(CUtensorMap *m, const void *ptr, int B, int T, long long token_stride,
-                            long long batch_stride, int H, int C, int box_tokens);
+                            long long batch_stride, int H, int C, int box_tokens,
+                            int box_channels = 64);
 
 }  // namespace gdn
