@@ -93,7 +93,7 @@ int check_qk_norm(const void *q, const void *k, const float *wq, const float *wk
                   const long long *pos, const float *inv_freq, long long N, int Hq, int Hk, int D,
                   int R, long long q_stride, long long k_stride, int norm, int pairing, float eps,
                   int dtype) {
-    if (N < 0 || Hq < 0 || Hk < 0 || Hq > 65536 || Hk > 65536 || N > (1LL << 40))
+    if (N < 0 || Hq < 0 || Hk < 0 || Hq > 16384 || Hk > 16384 || N > (1LL << 40))
         return GDN_ERR_INVALID_ARG;
     if (dtype != GDN_BF16 && dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
     if (norm != GDN_NORM_RMS && norm != GDN_NORM_L2) return GDN_ERR_INVALID_ARG;

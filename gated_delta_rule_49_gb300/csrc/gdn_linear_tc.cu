@@ -840,25 +840,30 @@ cudaError_t launch_kv(const LinearScan &a, float *slots, cudaStream_t st) {
 
 }  // namespace
 
-// The cost of a cut is counted in chunk times: a wave of CTAs (one an SM) takes
-// its segment's chunks and about two more to start and end, and a first pass
-// over all but the last segments takes 0.6 of that.  (B = 1, T = 65536, H = 16,
-// 128 x 128: 4 segments a sequence 616 us, 9 286 us.)  How long the longest of
-// packed sequences is, the host does not know: four times the mean is assumed.
+// The cost of a cut is counted in chunk times: a CTA (one an SM) takes its
+// segment's chunks and about four more to start and end; a first pass over all
+// but the last segments takes 0.6 of that, and its launch three.  (B = 1,
+// T = 65536, H = 16, 128 x 128: 4 segments a sequence 616 us, 9 371 us.)  Packed
+// sequences' lengths are not known here: the longest is taken for four times the
+// mean, and the work for evenly spread.
 SegPlan linear_tc_plan(int B, int T, int H, int K, int V, bool packed) {
     (void)K;
     (void)V;
     const int nsm = sm_count() > 0 ? sm_count() : 152;
     const long long longest = packed && 4LL * T / B < T ? 4LL * T / B : T;
-    auto waves = [&](long long items) { return (double)((items * H + nsm - 1) / nsm); };
-    auto chunks = [](long long len) { return (double)((len + kC - 1) / kC); };
+    auto time = [&](long long items, long long len) {
+        const double one = (double)((len + kC - 1) / kC) + 4;
+        if (!packed) return one * (double)((items * H + nsm - 1) / nsm);
+        const double all = ((double)T / kC + 4.0 * items) * H / nsm;
+        return one > all ? one : all;
+    };
     SegPlan best{T > 0 ? T : 1, B};
-    double least = waves(B) * (chunks(longest) + 2);
+    double least = time(B, longest);
     for (int n = 2; n <= 64 && longest / n >= 2 * kC; ++n) {
         const long long len = (longest + (long long)n * kC - 1) / ((long long)n * kC) * kC;
         const long long per = ((packed ? T : longest) + len - 1) / len;
         const long long items = packed ? per + B : per * B;
-        const double cost = waves(items) * (chunks(len) + 2) * 1.6;
+        const double cost = time(items, len) * 1.6 + 3;
         if (cost < least) {
             least = cost;
             best = {(int)len, (int)items};

@@ -16,11 +16,16 @@
 // Bound by memory: x read once and y written once (backward: x and dy read,
 // dx written).  A row of D channels is held by D / 8 lanes, 8 channels each,
 // so that a lane's load is one 16-byte piece in bf16 and two in float32, and
-// norms and the pairs of the half layout are exchanged by shuffles.  The
-// angles of a tile of tokens are formed once, in shared memory, and serve all
-// of their heads: float64 product and reduction to a fraction of a turn (an
-// angle of 1e6 has lost 4 of its digits in float32), then a float32 sincospi
-// of that fraction.
+// norms and the pairs of the half layout are exchanged by shuffles.  A thread
+// has the loads of several rows in flight before it works on the first.
+//
+// The angles of a tile of tokens are formed once, in shared memory, and serve
+// all of their heads.  Only the fraction of a turn counts, and positions are
+// whole: a frequency is kept as inv_freq / 2 pi in 64-bit fixed point, whole
+// turns dropped (formed in float64, once a CTA), and the product with the
+// position in wrapping integers is that fraction to pos 2^-56 turns.  (In
+// float32 an angle of 1e6 has lost 4 of its digits; in float64, at the 2 lanes
+// a clock of an SM here, the products took a third of the pass.)
 #include "gdn_vec8.cuh"
 
 namespace gdn {
@@ -81,27 +86,41 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const float2 *cs, int R, 
     }
 }
 
+// The frequencies in turns, 2^64 a turn.
+__device__ __forceinline__ void fill_turns(unsigned long long *turns, const QkNormArgs &p) {
+    for (int f = threadIdx.x; f < (p.R >> 1); f += kThreads) {
+        double x = (double)p.inv_freq[f] * 0.15915494309189533577;
+        x -= floor(x);  // [0, 1)
+        turns[f] = (unsigned long long)(x * 9223372036854775808.0) << 1;
+    }
+}
+
 // cos and sin of every angle of tokens [t0, t0 + nt).
-__device__ __forceinline__ void fill_angles(float2 *cs, const QkNormArgs &p, long long t0, int nt) {
+__device__ __forceinline__ void fill_angles(float2 *cs, const unsigned long long *turns,
+                                            const QkNormArgs &p, long long t0, int nt) {
     const int half = p.R >> 1;
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = i / half, f = i - t * half;
-        double turns = (double)p.pos[t0 + t] * (double)p.inv_freq[f] * 0.15915494309189533577;
-        turns -= rint(turns);
+        const unsigned long long x = (unsigned long long)p.pos[t0 + t] * turns[f];
         float s, c;
-        sincospif(2.f * (float)turns, &s, &c);
+        sincospif((float)(int)(x >> 32) * 0x1p-31f, &s, &c);
         cs[i] = make_float2(c, s);
     }
 }
 
-// One CTA takes tiles of TT tokens with all of their heads.
+// A CTA takes tiles of TT tokens with all of their heads, a lane group of
+// D / 8 lanes U rows at a time.  `magic` = ceil(2^32 / heads) divides a row of
+// a tile by the number of heads (rows * heads < 2^32; 0: one head).
 template <typename T, int D, bool HALF, bool BACK>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs p, int TT, float c_norm) {
+__global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
+    qk_norm_kernel(const QkNormArgs p, int TT, float c_norm, unsigned magic) {
     constexpr int LPR = D / 8;             // lanes of a row
-    constexpr int ROWS = kThreads / LPR;   // rows in flight
-    extern __shared__ __align__(16) float2 cs[];
+    constexpr int ROWS = kThreads / LPR;   // rows at a time
+    constexpr int U = BACK && sizeof(T) == 4 ? 2 : 4;
+    extern __shared__ __align__(16) unsigned long long turns[];
+    float2 *const cs2 = reinterpret_cast<float2 *>(turns + (p.R >> 1));  // two tiles
     const int lane = threadIdx.x & 31;
-    const int c = threadIdx.x % LPR;
+    const int c = threadIdx.x % LPR, gi = threadIdx.x / LPR;
     const int heads = p.Hq + p.Hk;
     float wq[8], wk[8], dwq[8], dwk[8];
 #pragma unroll
@@ -110,76 +129,90 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs p, i
         wk[i] = p.wk ? p.wk[8 * c + i] : 1.f;
         dwq[i] = dwk[i] = 0.f;
     }
+    auto token_of = [&](int r) { return magic ? (int)__umulhi((unsigned)r, magic) : r; };
+    fill_turns(turns, p);
+    __syncthreads();
+    int buf = 0;
     for (long long t0 = (long long)blockIdx.x * TT; t0 < p.N; t0 += (long long)gridDim.x * TT) {
         const int nt = (int)min((long long)TT, p.N - t0);
-        __syncthreads();  // the previous tile's angles are read
-        fill_angles(cs, p, t0, nt);
-        __syncthreads();
         const int rows = nt * heads;
-        for (int r0 = 0; r0 < rows; r0 += ROWS) {
-            const int r = r0 + threadIdx.x / LPR;
-            const bool live = r < rows;
-            const int t = live ? r / heads : 0;
-            const int h = live ? r - t * heads : 0;
-            const bool isq = h < p.Hq;
-            const long long tok = t0 + t;
-            const T *src = isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
-                               : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D;
-            const long long dst = (isq ? (tok * p.Hq + h) : (tok * p.Hk + h - p.Hq)) * D + 8 * c;
-            float x[8] = {}, g[8];
-            if (live) {
-                Vec8<T> raw;
-                raw.load(src + 8 * c);
-                raw.get(x);
+        float2 *const cs = cs2 + buf * TT * (p.R >> 1);
+        buf ^= 1;
+        Vec8<T> rx[U], rg[BACK ? U : 1];
+        auto fetch = [&](int r0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * ROWS + gi;
+                if (r >= rows) continue;
+                const int t = token_of(r), h = r - t * heads;
+                const bool isq = h < p.Hq;
+                const long long tok = t0 + t;
+                rx[u].load((isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
+                                : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D) + 8 * c);
+                if constexpr (BACK)
+                    rg[u].load((isq ? static_cast<const T *>(p.dyq) + (tok * p.Hq + h) * D
+                                    : static_cast<const T *>(p.dyk) + (tok * p.Hk + h - p.Hq) * D) + 8 * c);
             }
-            if constexpr (BACK) {
-                Vec8<T> raw;
+        };
+        fetch(0);
+        fill_angles(cs, turns, p, t0, nt);
+        __syncthreads();  // two tiles of angles: the other is not read any more
+        for (int r0 = 0; r0 < rows; r0 += U * ROWS) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * ROWS + gi;
+                const bool live = r < rows;
+                const int t = live ? token_of(r) : 0;
+                const int h = live ? r - t * heads : 0;
+                const bool isq = h < p.Hq;
+                float x[8] = {}, g[8] = {};
                 if (live) {
-                    raw.load(static_cast<const T *>(isq ? p.dyq : p.dyk) + dst);
-                    raw.get(g);
+                    rx[u].get(x);
+                    if constexpr (BACK) rg[u].get(g);
+                }
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+                ss = row_sum<LPR>(ss);
+                const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
+                const float2 *ct = cs + t * (p.R >> 1);
+                if constexpr (!BACK) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] *= rn * (isq ? wq[i] : wk[i]);
+                    rotate8<LPR, HALF>(x, ct, p.R, c, lane, 1.f);
                 } else {
+                    rotate8<LPR, HALF>(g, ct, p.R, c, lane, -1.f);
+                    float dot = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] = 0.f;
+                    for (int i = 0; i < 8; ++i) {
+                        const float d = g[i] * (x[i] * rn);
+                        if (isq) dwq[i] += d;
+                        else dwk[i] += d;
+                        g[i] *= isq ? wq[i] : wk[i];
+                        dot = fmaf(x[i], g[i], dot);
+                    }
+                    dot = row_sum<LPR>(dot) * c_norm * rn * rn;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = rn * fmaf(-dot, x[i], g[i]);
+                }
+                if (live) {
+                    const long long tok = t0 + t;
+                    Vec8<T>::store((isq ? static_cast<T *>(p.yq) + (tok * p.Hq + h) * D
+                                        : static_cast<T *>(p.yk) + (tok * p.Hk + h - p.Hq) * D) + 8 * c, x);
                 }
             }
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            ss = row_sum<LPR>(ss);
-            const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
-            const float2 *ct = cs + t * (p.R >> 1);
-            if constexpr (!BACK) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= rn * (isq ? wq[i] : wk[i]);
-                rotate8<LPR, HALF>(x, ct, p.R, c, lane, 1.f);
-            } else {
-                rotate8<LPR, HALF>(g, ct, p.R, c, lane, -1.f);
-                float dot = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = g[i] * (x[i] * rn);
-                    if (isq) dwq[i] += live ? d : 0.f;
-                    else dwk[i] += live ? d : 0.f;
-                    g[i] *= isq ? wq[i] : wk[i];
-                    dot = fmaf(x[i], g[i], dot);
-                }
-                dot = row_sum<LPR>(dot) * c_norm * rn * rn;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = rn * fmaf(-dot, x[i], g[i]);
-            }
-            if (live) Vec8<T>::store(static_cast<T *>(isq ? p.yq : p.yk) + dst, x);
+            if (r0 + U * ROWS < rows) fetch(r0 + U * ROWS);
         }
     }
     if constexpr (BACK) {
         if (!p.partial) return;
         // sums over this CTA's rows, in the fixed order of its threads
-        float *red = reinterpret_cast<float *>(cs);
+        float *red = reinterpret_cast<float *>(cs2);
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                red[(threadIdx.x / LPR) * D + 8 * c + i] = which ? dwk[i] : dwq[i];
+            for (int i = 0; i < 8; ++i) red[gi * D + 8 * c + i] = which ? dwk[i] : dwq[i];
             __syncthreads();
             for (int d = threadIdx.x; d < D; d += kThreads) {
                 float s = 0.f;
@@ -210,20 +243,27 @@ __global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float *partial, i
 
 int tile_tokens(int heads, int D) {
     // about 8 rows a lane group: the angles of a tile then cost one sincospi
-    // a thread next to 8 rows of work
-    // (at most 32 KB of angles)
-    const int tokens = 8 * kThreads / (D / 8) / heads, most = 8192 / D;
+    // a thread next to 8 rows of work (at most 2 x 16 KB of angles)
+    const int tokens = 8 * kThreads / (D / 8) / heads, most = 4096 / D;
     return tokens < 1 ? 1 : (tokens > most ? most : tokens);
+}
+
+int norm_grid(long long N, int heads, int D, int per_sm) {
+    const long long tiles = (N + tile_tokens(heads, D) - 1) / tile_tokens(heads, D);
+    const long long most = (long long)per_sm * (sm_count() > 0 ? sm_count() : 152);
+    return (int)(tiles < most ? tiles : most);
 }
 
 template <typename T, bool HALF, bool BACK>
 cudaError_t launch_d(const QkNormArgs &p, int D, float c, int grid, int TT, size_t smem,
                      cudaStream_t st) {
+    const unsigned heads = p.Hq + p.Hk;
+    const unsigned magic = heads == 1 ? 0 : (unsigned)((0x100000000ull + heads - 1) / heads);
     switch (D) {
-        case 32: qk_norm_kernel<T, 32, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
-        case 64: qk_norm_kernel<T, 64, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
-        case 128: qk_norm_kernel<T, 128, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
-        case 256: qk_norm_kernel<T, 256, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c); break;
+        case 32: qk_norm_kernel<T, 32, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
+        case 64: qk_norm_kernel<T, 64, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
+        case 128: qk_norm_kernel<T, 128, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
+        case 256: qk_norm_kernel<T, 256, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
@@ -232,8 +272,9 @@ cudaError_t launch_d(const QkNormArgs &p, int D, float c, int grid, int TT, size
 template <bool BACK>
 cudaError_t launch_any(const QkNormArgs &p, int D, float c, bool half, gdn_dtype dt, int grid,
                        int TT, cudaStream_t st) {
-    size_t smem = (size_t)TT * (p.R / 2) * sizeof(float2);
+    size_t smem = (size_t)2 * TT * (p.R / 2) * sizeof(float2);
     if (BACK && smem < kThreads * 8 * sizeof(float)) smem = kThreads * 8 * sizeof(float);
+    smem += (p.R / 2) * sizeof(unsigned long long);
     if (dt == GDN_BF16)
         return half ? launch_d<__nv_bfloat16, true, BACK>(p, D, c, grid, TT, smem, st)
                     : launch_d<__nv_bfloat16, false, BACK>(p, D, c, grid, TT, smem, st);
@@ -243,11 +284,7 @@ cudaError_t launch_any(const QkNormArgs &p, int D, float c, bool half, gdn_dtype
 
 }  // namespace
 
-int qk_norm_backward_grid(long long N, int heads, int D) {
-    const long long tiles = (N + tile_tokens(heads, D) - 1) / tile_tokens(heads, D);
-    const long long most = 4LL * (sm_count() > 0 ? sm_count() : 152);
-    return (int)(tiles < most ? tiles : most);
-}
+int qk_norm_backward_grid(long long N, int heads, int D) { return norm_grid(N, heads, D, 2); }
 
 cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
                            const long long *pos, const float *inv_freq, void *yq, void *yk,
@@ -255,10 +292,8 @@ cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const 
                            bool l2, bool half, float eps, gdn_dtype dt, cudaStream_t st) {
     QkNormArgs p = {q, k, nullptr, nullptr, wq, wk, pos, inv_freq, yq, yk, nullptr,
                     N, ldq, ldk, Hq, Hk, R, eps};
-    const int TT = tile_tokens(Hq + Hk, D);
-    const long long tiles = (N + TT - 1) / TT;
-    const int grid = (int)(tiles < 0x7fffffff ? tiles : 0x7fffffff);
-    return launch_any<false>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid, TT, st);
+    const int grid = norm_grid(N, Hq + Hk, D, dt == GDN_BF16 ? 4 : 2);
+    return launch_any<false>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid, tile_tokens(Hq + Hk, D), st);
 }
 
 cudaError_t launch_qk_norm_backward(const void *q, const void *k, const float *wq,
