@@ -14,10 +14,13 @@
 //     dx   = r (h - c r^2 x (x . h))
 //
 // Bound by memory: x read once and y written once (backward: x and dy read,
-// dx written).  A row of D channels is held by D / 8 lanes, 8 channels each,
-// so that a lane's load is one 16-byte piece in bf16 and two in float32, and
-// norms and the pairs of the half layout are exchanged by shuffles.  A thread
-// has the loads of several rows in flight before it works on the first.
+// dx written).  A row of D channels is held by D / 8 lanes, two pieces of 4
+// channels each, chosen so that a lane holds both channels of its pairs: only
+// the sums over a row are exchanged by shuffles.  (With 8 consecutive channels a
+// lane the half layout took 8 more shuffles a row, and the angles' reads met 8 a
+// bank: 160 us where this takes 111 for B = 8, T = 4096, 16 + 16 heads of
+// 128 channels in bf16.)  A thread has the loads of several rows in flight
+// before it works on the first.
 //
 // The angles of a tile of tokens are formed once, in shared memory, and serve
 // all of their heads.  Only the fraction of a turn counts, and positions are
@@ -26,7 +29,7 @@
 // position in wrapping integers is that fraction to pos 2^-56 turns.  (In
 // float32 an angle of 1e6 has lost 4 of its digits; in float64, at the 2 lanes
 // a clock of an SM here, the products took a third of the pass.)
-#include "gdn_vec8.cuh"
+#include "gdn_internal.cuh"
 
 namespace gdn {
 namespace {
@@ -51,38 +54,59 @@ template <int LPR> __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// x of the lane's channels [8 c, 8 c + 8) turned by the token's angles; `sign`
-// -1 turns back.  R is a multiple of 16, so R / 2 is a whole number of lanes.
-template <int LPR, bool HALF>
-__device__ __forceinline__ void rotate8(float (&x)[8], const float2 *cs, int R, int c, int lane,
-                                        float sign) {
-    if constexpr (HALF) {
-        const int half = R >> 4;  // lanes of one half of the rotated channels
-        const int row0 = lane - c;
-        const bool turned = c < 2 * half;
-        const bool low = c < half;
-        const int other = turned ? row0 + (low ? c + half : c - half) : lane;
-        const float2 *t = cs + 8 * (low ? c : c - half);
+// Four consecutive values of the run dtype.
+template <typename T> struct Vec4;
+template <> struct Vec4<__nv_bfloat16> {
+    uint2 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        a = __ldcs(reinterpret_cast<const uint2 *>(p));
+    }
+    __device__ __forceinline__ void get(float *x) const {
+        x[0] = __uint_as_float(a.x << 16);
+        x[1] = __uint_as_float(a.x & 0xffff0000u);
+        x[2] = __uint_as_float(a.y << 16);
+        x[3] = __uint_as_float(a.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[0], x[1]), c = __floats2bfloat162_rn(x[2], x[3]);
+        __stcs(reinterpret_cast<uint2 *>(p), make_uint2(*reinterpret_cast<const uint32_t *>(&b),
+                                                        *reinterpret_cast<const uint32_t *>(&c)));
+    }
+};
+template <> struct Vec4<float> {
+    float4 a;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldcs(reinterpret_cast<const float4 *>(p));
+    }
+    __device__ __forceinline__ void get(float *x) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float *x) {
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+    }
+};
+
+// First channels of lane c's two pieces: of a half layout's rotated lanes 4 c
+// and R/2 + 4 c, else 8 c and 8 c + 4.
+template <bool HALF> __device__ __forceinline__ int piece_a(int c, int R) {
+    return HALF && 8 * c < R ? 4 * c : 8 * c;
+}
+template <bool HALF> __device__ __forceinline__ int piece_b(int c, int R) {
+    return HALF && 8 * c < R ? (R >> 1) + 4 * c : 8 * c + 4;
+}
+
+// The lane's pairs turned by frequencies 4 c .. 4 c + 3 of `cs` (a token's
+// angles, those of one place in each lane's four side by side); BACK: turned back.
+template <bool HALF, bool BACK>
+__device__ __forceinline__ void rotate8(float (&x)[8], const float2 *cs, int R, int c) {
+    if (8 * c >= R) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float y = __shfl_sync(0xffffffffu, x[i], other);
-            if (turned) {
-                const float2 u = t[i];
-                const float s = low ? -sign * u.y : sign * u.y;
-                x[i] = fmaf(x[i], u.x, y * s);
-            }
-        }
-    } else {
-        if (8 * c < R) {
-            const float2 *t = cs + 4 * c;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 u = t[i];
-                const float s = sign * u.y, a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = fmaf(a, u.x, -b * s);
-                x[2 * i + 1] = fmaf(a, s, b * u.x);
-            }
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = cs[i * (R >> 3) + c];
+        float &a = x[HALF ? i : 2 * i], &b = x[HALF ? 4 + i : 2 * i + 1];
+        const float s = BACK ? -u.y : u.y, y = a;
+        a = fmaf(y, u.x, -b * s);
+        b = fmaf(y, s, b * u.x);
     }
 }
 
@@ -104,7 +128,7 @@ __device__ __forceinline__ void fill_angles(float2 *cs, const unsigned long long
         const unsigned long long x = (unsigned long long)p.pos[t0 + t] * turns[f];
         float s, c;
         sincospif((float)(int)(x >> 32) * 0x1p-31f, &s, &c);
-        cs[i] = make_float2(c, s);
+        cs[t * half + (f & 3) * (half >> 2) + (f >> 2)] = make_float2(c, s);
     }
 }
 
@@ -117,17 +141,18 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
     constexpr int LPR = D / 8;             // lanes of a row
     constexpr int ROWS = kThreads / LPR;   // rows at a time
     constexpr int U = BACK && sizeof(T) == 4 ? 2 : 4;
-    extern __shared__ __align__(16) unsigned long long turns[];
+    extern __shared__ __align__(16) float weights[];  // wq, wk
+    unsigned long long *const turns = reinterpret_cast<unsigned long long *>(weights + 2 * D);
     float2 *const cs2 = reinterpret_cast<float2 *>(turns + (p.R >> 1));  // two tiles
-    const int lane = threadIdx.x & 31;
     const int c = threadIdx.x % LPR, gi = threadIdx.x / LPR;
+    const int pa = piece_a<HALF>(c, p.R), pb = piece_b<HALF>(c, p.R);
     const int heads = p.Hq + p.Hk;
-    float wq[8], wk[8], dwq[8], dwk[8];
+    float dwq[8], dwk[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        wq[i] = p.wq ? p.wq[8 * c + i] : 1.f;
-        wk[i] = p.wk ? p.wk[8 * c + i] : 1.f;
-        dwq[i] = dwk[i] = 0.f;
+    for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+    for (int d = threadIdx.x; d < 2 * D; d += kThreads) {
+        const float *w = d < D ? p.wq : p.wk;
+        weights[d] = w ? w[d % D] : 1.f;
     }
     auto token_of = [&](int r) { return magic ? (int)__umulhi((unsigned)r, magic) : r; };
     fill_turns(turns, p);
@@ -138,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
         const int rows = nt * heads;
         float2 *const cs = cs2 + buf * TT * (p.R >> 1);
         buf ^= 1;
-        Vec8<T> rx[U], rg[BACK ? U : 1];
+        Vec4<T> xa[U], xb[U], ga[BACK ? U : 1], gb[BACK ? U : 1];
         auto fetch = [&](int r0) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -147,11 +172,16 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
                 const int t = token_of(r), h = r - t * heads;
                 const bool isq = h < p.Hq;
                 const long long tok = t0 + t;
-                rx[u].load((isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
-                                : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D) + 8 * c);
-                if constexpr (BACK)
-                    rg[u].load((isq ? static_cast<const T *>(p.dyq) + (tok * p.Hq + h) * D
-                                    : static_cast<const T *>(p.dyk) + (tok * p.Hk + h - p.Hq) * D) + 8 * c);
+                const T *src = isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
+                                   : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D;
+                xa[u].load(src + pa);
+                xb[u].load(src + pb);
+                if constexpr (BACK) {
+                    src = isq ? static_cast<const T *>(p.dyq) + (tok * p.Hq + h) * D
+                              : static_cast<const T *>(p.dyk) + (tok * p.Hk + h - p.Hq) * D;
+                    ga[u].load(src + pa);
+                    gb[u].load(src + pb);
+                }
             }
         };
         fetch(0);
@@ -167,8 +197,12 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
                 const bool isq = h < p.Hq;
                 float x[8] = {}, g[8] = {};
                 if (live) {
-                    rx[u].get(x);
-                    if constexpr (BACK) rg[u].get(g);
+                    xa[u].get(x);
+                    xb[u].get(x + 4);
+                    if constexpr (BACK) {
+                        ga[u].get(g);
+                        gb[u].get(g + 4);
+                    }
                 }
                 float ss = 0.f;
 #pragma unroll
@@ -176,19 +210,22 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
                 ss = row_sum<LPR>(ss);
                 const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
                 const float2 *ct = cs + t * (p.R >> 1);
+                float w[8];
+                *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(weights + (isq ? 0 : D) + pa);
+                *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(weights + (isq ? 0 : D) + pb);
                 if constexpr (!BACK) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= rn * (isq ? wq[i] : wk[i]);
-                    rotate8<LPR, HALF>(x, ct, p.R, c, lane, 1.f);
+                    for (int i = 0; i < 8; ++i) x[i] *= rn * w[i];
+                    rotate8<HALF, false>(x, ct, p.R, c);
                 } else {
-                    rotate8<LPR, HALF>(g, ct, p.R, c, lane, -1.f);
+                    rotate8<HALF, true>(g, ct, p.R, c);
                     float dot = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float d = g[i] * (x[i] * rn);
                         if (isq) dwq[i] += d;
                         else dwk[i] += d;
-                        g[i] *= isq ? wq[i] : wk[i];
+                        g[i] *= w[i];
                         dot = fmaf(x[i], g[i], dot);
                     }
                     dot = row_sum<LPR>(dot) * c_norm * rn * rn;
@@ -197,8 +234,10 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
                 }
                 if (live) {
                     const long long tok = t0 + t;
-                    Vec8<T>::store((isq ? static_cast<T *>(p.yq) + (tok * p.Hq + h) * D
-                                        : static_cast<T *>(p.yk) + (tok * p.Hk + h - p.Hq) * D) + 8 * c, x);
+                    T *dst = isq ? static_cast<T *>(p.yq) + (tok * p.Hq + h) * D
+                                 : static_cast<T *>(p.yk) + (tok * p.Hk + h - p.Hq) * D;
+                    Vec4<T>::store(dst + pa, x);
+                    Vec4<T>::store(dst + pb, x + 4);
                 }
             }
             if (r0 + U * ROWS < rows) fetch(r0 + U * ROWS);
@@ -212,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) red[gi * D + 8 * c + i] = which ? dwk[i] : dwq[i];
+            for (int i = 0; i < 8; ++i)
+                red[gi * D + (i < 4 ? pa + i : pb + i - 4)] = which ? dwk[i] : dwq[i];
             __syncthreads();
             for (int d = threadIdx.x; d < D; d += kThreads) {
                 float s = 0.f;
@@ -274,7 +314,7 @@ cudaError_t launch_any(const QkNormArgs &p, int D, float c, bool half, gdn_dtype
                        int TT, cudaStream_t st) {
     size_t smem = (size_t)2 * TT * (p.R / 2) * sizeof(float2);
     if (BACK && smem < kThreads * 8 * sizeof(float)) smem = kThreads * 8 * sizeof(float);
-    smem += (p.R / 2) * sizeof(unsigned long long);
+    smem += (p.R / 2) * sizeof(unsigned long long) + 2 * D * sizeof(float);
     if (dt == GDN_BF16)
         return half ? launch_d<__nv_bfloat16, true, BACK>(p, D, c, grid, TT, smem, st)
                     : launch_d<__nv_bfloat16, false, BACK>(p, D, c, grid, TT, smem, st);
