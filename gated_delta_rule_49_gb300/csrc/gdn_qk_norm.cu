@@ -18,7 +18,7 @@
 // channels each, chosen so that a lane holds both channels of its pairs: only
 // the sums over a row are exchanged by shuffles.  (With 8 consecutive channels a
 // lane the half layout took 8 more shuffles a row, and the angles' reads met 8 a
-// bank: 160 us where this takes 111 for B = 8, T = 4096, 16 + 16 heads of
+// bank: 160 us where this takes 103 for B = 8, T = 4096, 16 + 16 heads of
 // 128 channels in bf16.)  A thread has the loads of several rows in flight
 // before it works on the first.
 //
@@ -35,6 +35,11 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
+
+// CTAs of an SM.  Backward in bf16, with 2 rows in flight a thread, takes 206,
+// 178, 210 and 300 us (1 row) with 2, 3, 4 and 5 for B = 8, T = 4096, 16 + 16
+// heads of 128 channels; forward hardly changes from 3 to 8.
+constexpr int norm_ctas(bool back, bool wide) { return back ? (wide ? 2 : 3) : 4; }
 
 struct QkNormArgs {
     const void *q, *k, *dyq, *dyk;
@@ -86,6 +91,33 @@ template <> struct Vec4<float> {
     }
 };
 
+// Packed float32 operations: a *= f, b *= g, and a = a f + c, b = b g + d.
+__device__ __forceinline__ void mul2(float &a, float &b, float f, float g) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f), "f"(g));
+}
+__device__ __forceinline__ void fma2(float &a, float &b, float f, float g, float c, float d) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmov.b64 z, {%4, %5};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f), "f"(g), "f"(c), "f"(d));
+}
+// sum of x_i y_i
+__device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) {
+    float s0 = x[0], s1 = x[1];
+    mul2(s0, s1, y[0], y[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        float a = x[i], b = x[i + 1];
+        fma2(a, b, y[i], y[i + 1], s0, s1);
+        s0 = a;
+        s1 = b;
+    }
+    return s0 + s1;
+}
+
 // First channels of lane c's two pieces: of a half layout's rotated lanes 4 c
 // and R/2 + 4 c, else 8 c and 8 c + 4.
 template <bool HALF> __device__ __forceinline__ int piece_a(int c, int R) {
@@ -96,17 +128,34 @@ template <bool HALF> __device__ __forceinline__ int piece_b(int c, int R) {
 }
 
 // The lane's pairs turned by frequencies 4 c .. 4 c + 3 of `cs` (a token's
-// angles, those of one place in each lane's four side by side); BACK: turned back.
+// angles: 4 cosines and 4 sines a lane); BACK: turned back.
 template <bool HALF, bool BACK>
-__device__ __forceinline__ void rotate8(float (&x)[8], const float2 *cs, int R, int c) {
+__device__ __forceinline__ void rotate8(float (&x)[8], const float4 *cs, int R, int c) {
     if (8 * c >= R) return;
+    const float4 u = cs[c], v = cs[(R >> 3) + c];
+    const float co[4] = {u.x, u.y, u.z, u.w};
+    float si[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (BACK) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = cs[i * (R >> 3) + c];
-        float &a = x[HALF ? i : 2 * i], &b = x[HALF ? 4 + i : 2 * i + 1];
-        const float s = BACK ? -u.y : u.y, y = a;
-        a = fmaf(y, u.x, -b * s);
-        b = fmaf(y, s, b * u.x);
+        for (int i = 0; i < 4; ++i) si[i] = -si[i];
+    }
+    if constexpr (HALF) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            float a0 = x[i], a1 = x[i + 1];
+            float t0 = -x[4 + i], t1 = -x[5 + i];
+            mul2(t0, t1, si[i], si[i + 1]);
+            fma2(x[i], x[i + 1], co[i], co[i + 1], t0, t1);
+            mul2(a0, a1, si[i], si[i + 1]);
+            fma2(x[4 + i], x[5 + i], co[i], co[i + 1], a0, a1);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = fmaf(a, co[i], -b * si[i]);
+            x[2 * i + 1] = fmaf(a, si[i], b * co[i]);
+        }
     }
 }
 
@@ -120,7 +169,7 @@ __device__ __forceinline__ void fill_turns(unsigned long long *turns, const QkNo
 }
 
 // cos and sin of every angle of tokens [t0, t0 + nt).
-__device__ __forceinline__ void fill_angles(float2 *cs, const unsigned long long *turns,
+__device__ __forceinline__ void fill_angles(float *cs, const unsigned long long *turns,
                                             const QkNormArgs &p, long long t0, int nt) {
     const int half = p.R >> 1;
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
@@ -128,7 +177,8 @@ __device__ __forceinline__ void fill_angles(float2 *cs, const unsigned long long
         const unsigned long long x = (unsigned long long)p.pos[t0 + t] * turns[f];
         float s, c;
         sincospif((float)(int)(x >> 32) * 0x1p-31f, &s, &c);
-        cs[t * half + (f & 3) * (half >> 2) + (f >> 2)] = make_float2(c, s);
+        cs[2 * t * half + f] = c;
+        cs[(2 * t + 1) * half + f] = s;
     }
 }
 
@@ -136,14 +186,14 @@ __device__ __forceinline__ void fill_angles(float2 *cs, const unsigned long long
 // D / 8 lanes U rows at a time.  `magic` = ceil(2^32 / heads) divides a row of
 // a tile by the number of heads (rows * heads < 2^32; 0: one head).
 template <typename T, int D, bool HALF, bool BACK>
-__global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
     qk_norm_kernel(const QkNormArgs p, int TT, float c_norm, unsigned magic) {
     constexpr int LPR = D / 8;             // lanes of a row
     constexpr int ROWS = kThreads / LPR;   // rows at a time
-    constexpr int U = BACK && sizeof(T) == 4 ? 2 : 4;
+    constexpr int U = BACK || sizeof(T) == 4 ? 2 : 4;
     extern __shared__ __align__(16) float weights[];  // wq, wk
     unsigned long long *const turns = reinterpret_cast<unsigned long long *>(weights + 2 * D);
-    float2 *const cs2 = reinterpret_cast<float2 *>(turns + (p.R >> 1));  // two tiles
+    float *const cs2 = reinterpret_cast<float *>(turns + (p.R >> 1));  // two tiles
     const int c = threadIdx.x % LPR, gi = threadIdx.x / LPR;
     const int pa = piece_a<HALF>(c, p.R), pb = piece_b<HALF>(c, p.R);
     const int heads = p.Hq + p.Hk;
@@ -157,37 +207,38 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
     auto token_of = [&](int r) { return magic ? (int)__umulhi((unsigned)r, magic) : r; };
     fill_turns(turns, p);
     __syncthreads();
+    const long long step = (long long)gridDim.x * TT;
+    Vec4<T> xa[U], xb[U], ga[BACK ? U : 1], gb[BACK ? U : 1];
+    // row u of the batch from row r0 of the tile of tokens t0 ..
+    auto fetch = [&](int u, long long t0, int r0) {
+        const int r = r0 + u * ROWS + gi;
+        if (t0 >= p.N || r >= (int)min((long long)TT, p.N - t0) * heads) return;
+        const int t = token_of(r), h = r - t * heads;
+        const bool isq = h < p.Hq;
+        const long long tok = t0 + t;
+        const T *src = isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
+                           : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D;
+        xa[u].load(src + pa);
+        xb[u].load(src + pb);
+        if constexpr (BACK) {
+            src = isq ? static_cast<const T *>(p.dyq) + (tok * p.Hq + h) * D
+                      : static_cast<const T *>(p.dyk) + (tok * p.Hk + h - p.Hq) * D;
+            ga[u].load(src + pa);
+            gb[u].load(src + pb);
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(u, (long long)blockIdx.x * TT, 0);
     int buf = 0;
-    for (long long t0 = (long long)blockIdx.x * TT; t0 < p.N; t0 += (long long)gridDim.x * TT) {
+    for (long long t0 = (long long)blockIdx.x * TT; t0 < p.N; t0 += step) {
         const int nt = (int)min((long long)TT, p.N - t0);
         const int rows = nt * heads;
-        float2 *const cs = cs2 + buf * TT * (p.R >> 1);
+        float *const cs = cs2 + buf * TT * p.R;
         buf ^= 1;
-        Vec4<T> xa[U], xb[U], ga[BACK ? U : 1], gb[BACK ? U : 1];
-        auto fetch = [&](int r0) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = r0 + u * ROWS + gi;
-                if (r >= rows) continue;
-                const int t = token_of(r), h = r - t * heads;
-                const bool isq = h < p.Hq;
-                const long long tok = t0 + t;
-                const T *src = isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
-                                   : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D;
-                xa[u].load(src + pa);
-                xb[u].load(src + pb);
-                if constexpr (BACK) {
-                    src = isq ? static_cast<const T *>(p.dyq) + (tok * p.Hq + h) * D
-                              : static_cast<const T *>(p.dyk) + (tok * p.Hk + h - p.Hq) * D;
-                    ga[u].load(src + pa);
-                    gb[u].load(src + pb);
-                }
-            }
-        };
-        fetch(0);
         fill_angles(cs, turns, p, t0, nt);
         __syncthreads();  // two tiles of angles: the other is not read any more
         for (int r0 = 0; r0 < rows; r0 += U * ROWS) {
+            const bool more = r0 + U * ROWS < rows;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = r0 + u * ROWS + gi;
@@ -204,33 +255,45 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
                         gb[u].get(g + 4);
                     }
                 }
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-                ss = row_sum<LPR>(ss);
+                // its place is free: the next batch's row, of the next tile at the end
+                fetch(u, more ? t0 : t0 + step, more ? r0 + U * ROWS : 0);
+                const float ss = row_sum<LPR>(dot8(x, x));
                 const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
-                const float2 *ct = cs + t * (p.R >> 1);
+                const float4 *ct = reinterpret_cast<const float4 *>(cs + t * p.R);
                 float w[8];
                 *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(weights + (isq ? 0 : D) + pa);
                 *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(weights + (isq ? 0 : D) + pb);
                 if constexpr (!BACK) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= rn * w[i];
+                    for (int i = 0; i < 8; i += 2) {
+                        mul2(w[i], w[i + 1], rn, rn);
+                        mul2(x[i], x[i + 1], w[i], w[i + 1]);
+                    }
                     rotate8<HALF, false>(x, ct, p.R, c);
                 } else {
                     rotate8<HALF, true>(g, ct, p.R, c);
-                    float dot = 0.f;
+                    float d[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float d = g[i] * (x[i] * rn);
-                        if (isq) dwq[i] += d;
-                        else dwk[i] += d;
-                        g[i] *= w[i];
-                        dot = fmaf(x[i], g[i], dot);
+                    for (int i = 0; i < 8; i += 2) {
+                        d[i] = x[i];
+                        d[i + 1] = x[i + 1];
+                        mul2(d[i], d[i + 1], rn, rn);
+                        mul2(d[i], d[i + 1], g[i], g[i + 1]);
+                        mul2(g[i], g[i + 1], w[i], w[i + 1]);
                     }
-                    dot = row_sum<LPR>(dot) * c_norm * rn * rn;
+                    if (isq) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = rn * fmaf(-dot, x[i], g[i]);
+                        for (int i = 0; i < 8; ++i) dwq[i] += d[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dwk[i] += d[i];
+                    }
+                    const float f = -row_sum<LPR>(dot8(x, g)) * c_norm * rn * rn;
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        fma2(x[i], x[i + 1], f, f, g[i], g[i + 1]);
+                        mul2(x[i], x[i + 1], rn, rn);
+                    }
                 }
                 if (live) {
                     const long long tok = t0 + t;
@@ -240,13 +303,12 @@ __global__ void __launch_bounds__(kThreads, BACK || sizeof(T) == 4 ? 2 : 4)
                     Vec4<T>::store(dst + pb, x + 4);
                 }
             }
-            if (r0 + U * ROWS < rows) fetch(r0 + U * ROWS);
         }
     }
     if constexpr (BACK) {
         if (!p.partial) return;
         // sums over this CTA's rows, in the fixed order of its threads
-        float *red = reinterpret_cast<float *>(cs2);
+        float *red = cs2;
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
@@ -324,7 +386,7 @@ cudaError_t launch_any(const QkNormArgs &p, int D, float c, bool half, gdn_dtype
 
 }  // namespace
 
-int qk_norm_backward_grid(long long N, int heads, int D) { return norm_grid(N, heads, D, 2); }
+int qk_norm_backward_grid(long long N, int heads, int D) { return norm_grid(N, heads, D, norm_ctas(true, false)); }
 
 cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
                            const long long *pos, const float *inv_freq, void *yq, void *yk,
@@ -332,7 +394,7 @@ cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const 
                            bool l2, bool half, float eps, gdn_dtype dt, cudaStream_t st) {
     QkNormArgs p = {q, k, nullptr, nullptr, wq, wk, pos, inv_freq, yq, yk, nullptr,
                     N, ldq, ldk, Hq, Hk, R, eps};
-    const int grid = norm_grid(N, Hq + Hk, D, dt == GDN_BF16 ? 4 : 2);
+    const int grid = norm_grid(N, Hq + Hk, D, norm_ctas(false, dt != GDN_BF16));
     return launch_any<false>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid, tile_tokens(Hq + Hk, D), st);
 }
 
