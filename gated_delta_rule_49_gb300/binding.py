@@ -605,18 +605,18 @@ def _reject(where, what):
     raise e
 
 
-def _token_stride(where, name, x, dtype=None, device=None):
+def _token_stride(where, name, x, dtype, device):
     """Elements between consecutive tokens of x [..., heads, channels]: a
     token's heads and channels are dense, and the leading dimensions step
     evenly, as in a part of a wider projection."""
+    if x.dtype is not dtype or x.get_device() != device:
+        _reject(where, f"{name} is {x.dtype} on {x.device}")
     heads, D = x.shape[-2:]
-    if dtype is not None and (x.dtype != dtype or x.device != device):
-        _reject(where, f"{name} is {x.dtype} on {x.device}, not {dtype} on {device}")
     if x.is_contiguous():
         return heads * D
     st = x.stride()
     if st[-1] != 1 or (st[-2] != D and heads > 1):
-        _reject(where, f"{name}'s heads and channels are not dense (strides {tuple(st)})")
+        _reject(where, f"{name}'s heads and channels are not dense (strides {st})")
     step, span = 0, 1  # of the tokens seen so far, innermost first
     for n, s in zip(reversed(x.shape[:-2]), reversed(st[:-2])):
         if n == 1:
@@ -624,42 +624,56 @@ def _token_stride(where, name, x, dtype=None, device=None):
         if not step:
             step = s
         elif s != step * span:
-            _reject(where, f"{name}'s tokens do not lie evenly (strides {tuple(st)})")
+            _reject(where, f"{name}'s tokens do not lie evenly (strides {st})")
         span *= n
     return step or heads * D
 
 
-def _dense(where, device, **named):
-    """Each tensor given: contiguous, on the device, of its type and shape."""
-    for name, (x, dtype, shape) in named.items():
-        if x is None:
-            continue
-        if x.dtype != dtype or x.device != device or tuple(x.shape) != tuple(shape) \
-                or not x.is_contiguous():
-            _reject(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                           f"on {device}")
+def _dense(where, name, x, dtype, device, shape):
+    """x, if given, is contiguous, on the device (a number), of its type and shape."""
+    if x is not None and (x.dtype is not dtype or x.get_device() != device or x.shape != shape
+                          or not x.is_contiguous()):
+        _reject(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                       f"device {device}; it is {x.dtype}, {tuple(x.shape)} on {x.device}")
+
+
+def _workspace(given, need, like):
+    """(workspace, its bytes): the one given, or a new one where one is needed."""
+    if given is not None:
+        return given, given.numel() * given.element_size()
+    if not need:
+        return None, 0
+    import torch
+    return torch.empty(need, dtype=torch.uint8, device=like.device), need
 
 
 def _qk_norm_args(where, q, k, pos, inv_freq, wq, wk, norm, pairing):
     import torch
     if norm not in NORMS or pairing not in PAIRINGS:
         _reject(where, f"norm {norm!r}, pairing {pairing!r}")
-    lead, (Hq, D) = q.shape[:-2], q.shape[-2:]
-    Hk = 0
-    ldq = _token_stride(where, "q", q)
-    ldk = 0
+    dt, dev, lead = q.dtype, q.get_device(), q.shape[:-2]
+    Hq, D = q.shape[-2:]
+    Hk = ldk = 0
+    ldq = _token_stride(where, "q", q, dt, dev)
     if k is not None:
         Hk = k.shape[-2]
         if k.shape[:-2] != lead or k.shape[-1] != D:
             _reject(where, f"q {tuple(q.shape)} and k {tuple(k.shape)}")
-        ldk = _token_stride(where, "k", k, q.dtype, q.device)
-    R = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    _dense(where, q.device, pos=(pos, torch.int64, lead), wq=(wq, torch.float32, (D,)),
-           wk=(wk, torch.float32, (D,)), inv_freq=(inv_freq, torch.float32, (R // 2,)))
-    N = 1
-    for n in lead:
-        N *= n
-    return N, Hq, Hk, D, R, ldq, ldk, NORMS[norm], PAIRINGS[pairing]
+        ldk = _token_stride(where, "k", k, dt, dev)
+    R = 0
+    if inv_freq is not None:
+        R = 2 * inv_freq.shape[0]
+        _dense(where, "inv_freq", inv_freq, torch.float32, dev, (R // 2,))
+    _dense(where, "pos", pos, torch.int64, dev, lead)
+    _dense(where, "wq", wq, torch.float32, dev, (D,))
+    _dense(where, "wk", wk, torch.float32, dev, (D,))
+    return lead.numel(), Hq, Hk, D, R, ldq, ldk, NORMS[norm], PAIRINGS[pairing]
+
+
+def _new(x):
+    """A new dense tensor of x's shape and type."""
+    import torch
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rotate(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms", pairing="half",
@@ -670,18 +684,17 @@ def qk_norm_rotate(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms", 
     norm "rms" or "l2"; pairing "half" (i with i + R/2) or "adjacent".  q and k
     may be slices of one projection.  Returns (yq, yk), new dense tensors or
     `out` (which may hold dense q and k themselves)."""
-    import torch
     where = "qk_norm_rotate"
     N, Hq, Hk, D, R, ldq, ldk, nrm, pair = _qk_norm_args(where, q, k, pos, inv_freq, wq, wk, norm,
                                                          pairing)
     if out is None:
-        yq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        yk = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        yq = _new(q)
+        yk = None if k is None else _new(k)
     else:
         yq, yk = out
-        _dense(where, q.device, yq=(yq, q.dtype, q.shape))
+        _dense(where, "out[0]", yq, q.dtype, q.get_device(), q.shape)
         if k is not None:
-            _dense(where, q.device, yk=(yk, k.dtype, k.shape))
+            _dense(where, "out[1]", yk, q.dtype, q.get_device(), k.shape)
     gdn_qk_norm_rotate(q, k, wq, wk, pos, inv_freq, yq, yk, N, Hq, Hk, D, R, ldq, ldk, nrm, pair,
                        eps, _dtype_code(q), stream)
     return yq, yk
@@ -691,49 +704,50 @@ def qk_norm_rotate_backward(q, k, pos, inv_freq, dyq, dyk, wq=None, wk=None, nor
                             pairing="half", eps=1e-6, workspace=None, stream=None):
     """Gradients of qk_norm_rotate from its inputs and dyq, dyk (dense).
     Returns (dq, dk, dwq, dwk); a weight that was not given has None."""
-    import torch
     where = "qk_norm_rotate_backward"
     N, Hq, Hk, D, R, ldq, ldk, nrm, pair = _qk_norm_args(where, q, k, pos, inv_freq, wq, wk, norm,
                                                          pairing)
-    _dense(where, q.device, dyq=(dyq, q.dtype, q.shape),
-           dyk=(dyk if k is not None else None, q.dtype, () if k is None else k.shape))
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+    _dense(where, "dyq", dyq, q.dtype, q.get_device(), q.shape)
+    if k is not None:
+        _dense(where, "dyk", dyk, q.dtype, q.get_device(), k.shape)
+    dq = _new(q)
+    dk = None if k is None else _new(k)
+    dwq = None if wq is None else _new(wq)
+    dwk = None if wk is None else _new(wk)
     need = 0
     if wq is not None or wk is not None:
         need = gdn_qk_norm_rotate_backward_workspace_size(N, Hq, Hk, D)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        need = workspace.numel() * workspace.element_size()
+    workspace, need = _workspace(workspace, need, q)
     gdn_qk_norm_rotate_backward(q, k, wq, wk, pos, inv_freq, dyq, dyk, dq, dk, dwq, dwk, N, Hq, Hk,
                                 D, R, ldq, ldk, nrm, pair, eps, _dtype_code(q), workspace, need,
                                 stream)
     return dq, dk, dwq, dwk
 
 
-def _linear_args(where, q, k, v, alpha, offsets, **states):
-    """Sizes and token strides of q, k [B, T, Hq, K], v [B, T, H, V]; with
+def _linear_args(where, q, k, v, alpha, offsets):
+    """Sizes, token strides and (type, device) of q, k [B, T, Hq, K], v [B, T, H, V]; with
     offsets, of q, k [tokens, Hq, K], v [tokens, H, V]."""
     import torch
+    qs, vs = q.shape, v.shape
     dims = 4 if offsets is None else 3
-    if q.dim() != dims or k.shape != q.shape or v.dim() != dims or v.shape[:-2] != q.shape[:-2]:
-        _reject(where, f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}"
+    if len(qs) != dims or k.shape != qs or len(vs) != dims or vs[:-2] != qs[:-2]:
+        _reject(where, f"q {tuple(qs)}, k {tuple(k.shape)}, v {tuple(vs)}"
                        + ("" if offsets is None else " with offsets"))
-    Hq, K = q.shape[-2:]
-    H, V = v.shape[-2:]
+    dt, dev = v.dtype, v.get_device()
+    Hq, K = qs[-2:]
+    H, V = vs[-2:]
     if offsets is None:
-        B, T = q.shape[:2]
+        B, T = qs[:2]
     else:
         if offsets.dim() != 1 or offsets.shape[0] < 1:
             _reject(where, "offsets must be [sequences + 1]")
-        B, T = offsets.shape[0] - 1, q.shape[0]
-        _dense(where, v.device, offsets=(offsets, torch.int32, offsets.shape))
-    _dense(where, v.device, alpha=(alpha, torch.float32, (H,)),
-           **{n: (s, torch.float32, (B, H, V, K)) for n, s in states.items()})
-    ld = tuple(_token_stride(where, n, x, v.dtype, v.device)
-               for n, x in (("q", q), ("k", k), ("v", v)))
-    return (B, T, Hq, H, K, V), ld
+        B, T = offsets.shape[0] - 1, qs[0]
+        _dense(where, "offsets", offsets, torch.int32, dev, (B + 1,))
+    _dense(where, "alpha", alpha, torch.float32, dev, (H,))
+    ldq = _token_stride(where, "q", q, dt, dev)
+    ldk = _token_stride(where, "k", k, dt, dev)
+    ldv = _token_stride(where, "v", v, dt, dev)
+    return B, T, Hq, H, K, V, ldq, ldk, ldv
 
 
 def linear_prefill(q, k, v, alpha, S0=None, scale=1.0, offsets=None, want_o=True, want_state=True,
@@ -744,20 +758,20 @@ def linear_prefill(q, k, v, alpha, S0=None, scale=1.0, offsets=None, want_o=True
     None.  With offsets [B + 1] int32 the sequences lie packed: q, k [tokens, Hq, K],
     v [tokens, H, V].  Returns (o, S_T); out_state may be S0."""
     import torch
-    (B, T, Hq, H, K, V), ld = _linear_args("linear_prefill", q, k, v, alpha, offsets, S0=S0,
-                                           out_state=out_state)
+    where = "linear_prefill"
+    B, T, Hq, H, K, V, ldq, ldk, ldv = _linear_args(where, q, k, v, alpha, offsets)
+    dev, shape = v.get_device(), (B, H, V, K)
+    _dense(where, "S0", S0, torch.float32, dev, shape)
+    _dense(where, "out_state", out_state, torch.float32, dev, shape)
     dt = _dtype_code(v)
-    o = torch.empty(v.shape, dtype=v.dtype, device=v.device) if want_o else None
+    o = _new(v) if want_o else None
     ST = out_state
     if want_state and ST is None:
-        ST = torch.empty((B, H, V, K), dtype=torch.float32, device=v.device)
-    need = gdn_linear_prefill_workspace_size(B, T, H, K, V, offsets is not None, dt)
-    if workspace is not None:
-        need = workspace.numel() * workspace.element_size()
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
-    gdn_linear_prefill(q, k, v, alpha, S0, o, ST, offsets, B, T, Hq, H, K, V, *ld, scale, dt,
-                       workspace, need, stream)
+        ST = torch.empty(shape, dtype=torch.float32, device=v.device)
+    workspace, need = _workspace(workspace, gdn_linear_prefill_workspace_size(
+        B, T, H, K, V, offsets is not None, dt), v)
+    gdn_linear_prefill(q, k, v, alpha, S0, o, ST, offsets, B, T, Hq, H, K, V, ldq, ldk, ldv, scale,
+                       dt, workspace, need, stream)
     return o, ST
 
 
@@ -768,20 +782,20 @@ def linear_backward(q, k, v, alpha, do, S0=None, dS_T=None, scale=1.0, offsets=N
     alpha is a constant and has none."""
     import torch
     where = "linear_backward"
-    (B, T, Hq, H, K, V), ld = _linear_args(where, q, k, v, alpha, offsets, S0=S0, dS_T=dS_T)
-    _dense(where, v.device, do=(do, v.dtype, v.shape))
+    B, T, Hq, H, K, V, ldq, ldk, ldv = _linear_args(where, q, k, v, alpha, offsets)
+    dev, shape = v.get_device(), (B, H, V, K)
+    _dense(where, "S0", S0, torch.float32, dev, shape)
+    _dense(where, "dS_T", dS_T, torch.float32, dev, shape)
+    _dense(where, "do", do, v.dtype, dev, v.shape)
     dt = _dtype_code(v)
-    dq, dk, dv = (torch.empty(x.shape, dtype=v.dtype, device=v.device) for x in (q, k, v))
+    dq, dk, dv = _new(q), _new(k), _new(v)
     dS0 = None
     if want_dS0 or (want_dS0 is None and S0 is not None):
-        dS0 = torch.empty((B, H, V, K), dtype=torch.float32, device=v.device)
-    need = gdn_linear_backward_workspace_size(B, T, Hq, H, K, V, offsets is not None, dt)
-    if workspace is not None:
-        need = workspace.numel() * workspace.element_size()
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        dS0 = torch.empty(shape, dtype=torch.float32, device=v.device)
+    workspace, need = _workspace(workspace, gdn_linear_backward_workspace_size(
+        B, T, Hq, H, K, V, offsets is not None, dt), v)
     gdn_linear_backward(q, k, v, alpha, do, S0, dS_T, dq, dk, dv, dS0, offsets, B, T, Hq, H, K, V,
-                        *ld, scale, dt, workspace, need, stream)
+                        ldq, ldk, ldv, scale, dt, workspace, need, stream)
     return dq, dk, dv, dS0
 
 
@@ -790,18 +804,23 @@ def linear_decode_step(q, k, v, alpha, S, scale=1.0, S_out=None, o=None, stream=
     updated in place unless S_out is given.  Returns o [B, H, V]."""
     import torch
     where = "linear_decode_step"
-    if q.dim() != 3 or v.dim() != 3:
-        _reject(where, f"q {tuple(q.shape)}, v {tuple(v.shape)}")
-    B, Hq, K = q.shape
-    H, V = v.shape[1:]
+    qs, vs = q.shape, v.shape
+    if len(qs) != 3 or len(vs) != 3 or qs[0] != vs[0]:
+        _reject(where, f"q {tuple(qs)}, v {tuple(vs)}")
+    B, Hq, K = qs
+    H, V = vs[1:]
+    dt, dev, shape = v.dtype, v.get_device(), (B, H, V, K)
     if S_out is None:
         S_out = S
     if o is None:
-        o = torch.empty((B, H, V), dtype=v.dtype, device=v.device)
-    _dense(where, v.device, q=(q, v.dtype, (B, Hq, K)), k=(k, v.dtype, (B, Hq, K)),
-           v=(v, v.dtype, (B, H, V)), o=(o, v.dtype, (B, H, V)),
-           alpha=(alpha, torch.float32, (H,)), S=(S, torch.float32, (B, H, V, K)),
-           S_out=(S_out, torch.float32, (B, H, V, K)))
+        o = torch.empty_like(v)
+    _dense(where, "q", q, dt, dev, qs)
+    _dense(where, "k", k, dt, dev, qs)
+    _dense(where, "v", v, dt, dev, vs)
+    _dense(where, "o", o, dt, dev, vs)
+    _dense(where, "alpha", alpha, torch.float32, dev, (H,))
+    _dense(where, "S", S, torch.float32, dev, shape)
+    _dense(where, "S_out", S_out, torch.float32, dev, shape)
     gdn_linear_decode_step(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale, _dtype_code(v),
                            stream)
     return o
