@@ -596,6 +596,7 @@ int gdn_linear_prefill(const void *q, const void *k, const void *v, const float 
     a.ldq = q_stride; a.ldk = k_stride; a.ldv = v_stride;
     a.write_scale = 1.f;
     a.read_scale = scale;
+    a.exact = true;
     return from_cuda(gdn::launch_linear_scan(a, dtype, workspace, st));
 }
 
@@ -679,7 +680,7 @@ int gdn_linear_backward(const void *q, const void *k, const void *v, const float
         a.K = K; a.V = V;
         a.S0 = dS_T; a.s0_transposed = false; a.reverse = true;
         a.write_scale = scale; a.read_scale = 1.f;
-        a.o = dv; a.ST = dS0; a.o_float = dtype == GDN_FP32;
+        a.o = dv; a.ST = dS0; a.exact = dS0 != nullptr; a.o_float = dtype == GDN_FP32;
         c = gdn::launch_linear_scan(a, dtype, workspace, st);
     }
     return from_cuda(c);

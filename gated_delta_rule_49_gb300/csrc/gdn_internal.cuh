@@ -193,6 +193,7 @@ struct LinearScan {
     long long ldq, ldk, ldv;
     float write_scale, read_scale;
     bool reverse, s0_transposed, o_float;
+    bool exact;  // the state to float32 accuracy (else to that of bf16 operands)
 };
 // Bytes of workspace of one scan; launches it.
 size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt);

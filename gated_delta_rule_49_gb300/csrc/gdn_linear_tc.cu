@@ -11,11 +11,12 @@
 // that mis-weights is S's part of rows that have decayed by more than 2^-64.
 //
 // Precision: P and S are rounded to bf16 as operands (a step of the bf16
-// output each).  The state itself has to be a float32 result, so the weighted
-// V goes in as three bf16 pieces that add up to it, D is formed chunk by chunk from zero in
-// the float32 accumulator, and S is kept in float32 registers, added to with
-// rounding (an accumulator carried through all chunks would be cut, not
-// rounded, at every product).
+// output each).  Where the state is a float32 result (`exact`) the weighted V
+// goes in as three bf16 pieces that add up to it; gradients that return no state
+// round it once instead, a step of the bf16 gradient like P's and S's.  D is
+// formed chunk by chunk from zero in the float32 accumulator, and S is kept in
+// float32 registers, added to with rounding (an accumulator carried through all
+// chunks would be cut, not rounded, at every product).
 //
 // One CTA runs one segment of one (sequence, head), 20 warps in groups of 4:
 //   0-7   rows (two warps share 32 of them): P, from Q K^T in TMEM, weighted,
@@ -561,8 +562,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 if (i > 0 && updates(i)) wait_warp(&bar.d0, i - 1);  // the pieces' places are free
             }
             if (i < nc && updates(i)) {
-                // 32 tokens of this group's 64 as three bf16 pieces whose sum is
-                // the float32 product: each takes the upper half of what is left
+                // 32 tokens of this group's 64; exact: as three bf16 pieces whose
+                // sum is the float32 product, each the upper half of what is left
                 if (mine) {
                     float2 w[4];
 #pragma unroll
@@ -572,27 +573,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         const uint32_t col = (uint32_t)(warp & 3) * 32 + 16 * r + (lane & 8);
                         const uint32_t off = (col >> 6) * (kC * 128) + swz128(tok, (col & 63) >> 3) + c * 4096;
                         const uint32_t src = smem_u32(smem) + L::VV + (i % kStages) * L::VSLOT + off;
-                        uint32_t hi[8], mid[8], x[2][4];
+                        const uint32_t at = tmem + quad + ((uint32_t)r << 20) + g * 32 + 16 * c;
+                        uint32_t hi[8], x[2][4];
                         ldmatrix4_trans(x[0], src);
                         ldmatrix4_trans(x[1], src + 2048);
+                        if (p.exact) {
+                            uint32_t mid[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            uint32_t &z = x[e >> 2][e & 3];
-                            float u = __uint_as_float(z << 16);
-                            float y = __uint_as_float(z & 0xffff0000u);
-                            mul2(u, y, w[e >> 1].x, w[e >> 1].y);
-                            hi[e] = upper_halves(u, y);
-                            drop_upper_halves(u, y);
-                            mid[e] = upper_halves(u, y);
-                            drop_upper_halves(u, y);
-                            z = upper_halves(u, y);
+                            for (int e = 0; e < 8; ++e) {
+                                uint32_t &z = x[e >> 2][e & 3];
+                                float u = __uint_as_float(z << 16);
+                                float y = __uint_as_float(z & 0xffff0000u);
+                                mul2(u, y, w[e >> 1].x, w[e >> 1].y);
+                                hi[e] = upper_halves(u, y);
+                                drop_upper_halves(u, y);
+                                mid[e] = upper_halves(u, y);
+                                drop_upper_halves(u, y);
+                                z = upper_halves(u, y);
+                            }
+                            tmem_st_16x128(at + kColMid, mid);
+                            const uint32_t low = smem_u32(smem) + L::LOW + off;
+                            stmatrix4_trans(low, x[0][0], x[0][1], x[0][2], x[0][3]);
+                            stmatrix4_trans(low + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t z = x[e >> 2][e & 3];
+                                float u = __uint_as_float(z << 16);
+                                float y = __uint_as_float(z & 0xffff0000u);
+                                mul2(u, y, w[e >> 1].x, w[e >> 1].y);
+                                hi[e] = pack_bf16(u, y);
+                            }
                         }
-                        const uint32_t at = tmem + quad + ((uint32_t)r << 20) + g * 32 + 16 * c;
                         tmem_st_16x128(at + kColHi, hi);
-                        tmem_st_16x128(at + kColMid, mid);
-                        const uint32_t low = smem_u32(smem) + L::LOW + off;
-                        stmatrix4_trans(low, x[0][0], x[0][1], x[0][2], x[0][3]);
-                        stmatrix4_trans(low + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
                     }
                     tmem_st_wait();
                     fence_proxy_async_smem();
@@ -741,16 +754,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         if (dead) break;
                         // the small pieces first: the sum is cut to its size at each product
 #pragma unroll 1
-                        for (int y = 0; y < 3; ++y) {
+                        for (int y = p.exact ? 0 : 2; y < 3; ++y) {
                             const uint32_t a = tmem + (y == 1 ? kColMid : kColHi);
+                            const bool on = c > 0 || y == 1 || (y == 2 && p.exact);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {  // tokens 32 c .. and 64 + 32 c ..
                                 const int z = 2 * c + (x & 1) + 4 * (x >> 1);
                                 if (y == 0)
                                     mma_ss(tmem + kColD, low + z * (2048 >> 4), kt + z * (2048 >> 4),
-                                           id_low, c + x > 0);
+                                           id_low, on || x > 0);
                                 else
-                                    mma_ts(tmem + kColD, a + 8 * z, kt + z * (2048 >> 4), id_d, 1);
+                                    mma_ts(tmem + kColD, a + 8 * z, kt + z * (2048 >> 4), id_d, on || x > 0);
                             }
                         }
                         mma_commit(c ? &bar.d : &bar.d0);
