@@ -63,8 +63,9 @@ struct LinLayout {
     static constexpr uint32_t KK = Q + QSLOT;
     static constexpr uint32_t VV = KK + kStages * KSLOT;
     static constexpr uint32_t S = VV + kStages * VSLOT;
-    // O on its way out: K's slot of the chunk where all of the memory is taken
-    // (K is read before O is complete), else a place of its own
+    // O on its way out: the lowest pieces' place where there are none, K's slot
+    // of the chunk where all of the memory is taken (K is read before O is
+    // complete), else a place of its own
     static constexpr bool O_IN_K = K == 128 && V == 128;
     static constexpr uint32_t OUT = S + 2 * K * V;
     static constexpr uint32_t TABLE = OUT + (O_IN_K ? 0 : kC * 2 * V);  // column factors of P, weights of V
@@ -332,6 +333,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     };
     // chunks whose D is formed: all but a last one whose end nobody wants
     auto updates = [&](int i) { return i + 1 < nc || end; };
+    const bool o_in_k = L::O_IN_K && p.exact;
+    auto o_place = [&](int i) {
+        return smem + (o_in_k ? L::KK + (i % kStages) * L::KSLOT : L::O_IN_K ? L::LOW : L::OUT);
+    };
     auto wait_warp = [&](uint64_t *b, uint32_t parity) {
         wait(b, parity);
         __syncwarp();
@@ -413,9 +418,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const float rho = p.read_scale * exp2f(lrho);
                 const bool whole = n == kC && !p.o_float;
                 constexpr int kCols = V / 2;  // of a warp
-                uint8_t *const stage = smem + (L::O_IN_K ? L::KK + (i % kStages) * L::KSLOT : L::OUT) +
-                                       part * (kC * 2 * kCols);
-                if (!L::O_IN_K && i > 0) wait_warp(&bar.sent[(i - 1) % kStages], (i - 1) / kStages);
+                uint8_t *const stage = o_place(i) + part * (kC * 2 * kCols);
+                if (!o_in_k && i > 0) wait_warp(&bar.sent[(i - 1) % kStages], (i - 1) / kStages);
                 wait_warp(&bar.o, i);
                 tc_fence_after();
 #pragma unroll 1
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int b = 0; b < V / 64; ++b)
                     tma_load_4d(smem + L::VV + s * L::VSLOT + b * (kC * 128), &mv, &bar.vfull[s],
                                 64 * b, hv, token_at(i), c3);
-                if (L::O_IN_K && want_o && i >= kStages) wait(&bar.sent[s], i / kStages - 1);
+                if (o_in_k && want_o && i >= kStages) wait(&bar.sent[s], i / kStages - 1);
                 if (dead) break;
                 mbar_arrive_expect_tx(&bar.kfull[s], kC * 2 * K);
                 ks = i + 1;
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int i = 0; i < nc; ++i) {
                 wait(&bar.staged, i);
                 if (chunk_n(i) == kC && !p.o_float && !dead) {
-                    const uint8_t *stage = smem + (L::O_IN_K ? L::KK + (i % kStages) * L::KSLOT : L::OUT);
+                    const uint8_t *stage = o_place(i);
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
                         tma_store_4d(&mo, stage + b * (kC * V), b * (V / 2), h, token_at(i), c3);
