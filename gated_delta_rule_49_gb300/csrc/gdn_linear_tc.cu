@@ -674,6 +674,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int b = 0; b < K / 64; ++b)
                     tma_load_4d(smem + L::KK + s * L::KSLOT + b * (kC * 128), &mk, &bar.kfull[s],
                                 64 * b, hk, token_at(i), c3);
+                // the next, whose place is not free yet, to the L2 cache
+                if (i > 0 && i + 1 < nc) {
+#pragma unroll
+                    for (int b = 0; b < V / 64; ++b)
+                        tma_prefetch_l2_4d(&mv, 64 * b, hv, token_at(i + 1), c3);
+#pragma unroll
+                    for (int b = 0; b < K / 64; ++b)
+                        tma_prefetch_l2_4d(&mk, 64 * b, hk, token_at(i + 1), c3);
+                }
             }
             // copies in flight land before the CTA ends (again with a limit)
             for (int i = vs > kStages ? vs - kStages : 0; i < vs; ++i)
@@ -693,8 +702,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 issued = i + 1;
 #pragma unroll
                 for (int b = 0; b < K / 64; ++b)
+                {
                     tma_load_4d(smem + L::Q + b * (kC * 128), &mq, &bar.qfull, 64 * b, hq,
                                 token_at(i), c3);
+                    if (i + 1 < nc) tma_prefetch_l2_4d(&mq, 64 * b, hq, token_at(i + 1), c3);
+                }
             }
             if (issued) mbar_wait(&bar.qfull, (issued - 1) & 1, kSpinLimit);
         }
