@@ -34,7 +34,9 @@
 //   17    issues the MMAs; 19 sends O
 // Launched with 96 registers a thread (5 groups x 128 threads x 96 = 61440);
 // the groups then share the same 480 registers a lane of the five as
-// 2 x 88 + 2 x 128 + 48, so that S, a row piece of 64 floats, needs no spill.
+// 2 x 96 + 2 x 128 + 32 (K = 64: 2 x 96 + 2 x 112 + 64), with which nothing
+// spills: with some 20 registers of the rows spilled a chunk took half as long
+// again.
 // TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64.
 #include <cstring>
 
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
     if (warp < 8) {
         // ---------------------------------------------------------------- rows
-        reg_dec<88>();
+        // (keeps the 96 registers of the launch)
         if (want_o) {
             const int t = (warp & 3) * 32 + lane, part = warp >> 2;
             // the powers within a block of 32 columns; a row's factor of the block
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- state
-        reg_inc<128>();
+        reg_inc<K == 128 ? 128 : 112>();
         constexpr int NS = K / 2;
         const int g = (warp - 8) >> 2;
         const int v = (warp & 3) * 32 + lane;
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 dst[e] = make_float4(f * S[4 * e], f * S[4 * e + 1], f * S[4 * e + 2], f * S[4 * e + 3]);
         }
     } else {
-        reg_dec<48>();
+        reg_dec<K == 128 ? 32 : 64>();
         // ---------------------------------------------------------------- loads
         auto token_at = [&](int i) { return (p.offsets ? it.base : 0) + f0 + chunk_at(i); };
         const int c3 = p.offsets ? 0 : it.seq;
