@@ -65,17 +65,33 @@ __global__ void __launch_bounds__(kScanThreads)
     const int row0 = blk * kCtaRows + warp * kRows;
     const int hq = h / (p.H / p.Hq), hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
 
+    // the start state: the loads of a slot together, one slot after another
     float S[kRows][C];
+    auto add_slot = [&](int at, float f) {
+        const float *src = slots_in + ((size_t)at * p.H + h) * VK + (size_t)row0 * K + lane * C;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            float x[C];
+            Cols<C>::load(src + r * K, x);
+#pragma unroll
+            for (int c = 0; c < C; ++c) S[r][c] = fmaf(f, x[c], S[r][c]);
+        }
+    };
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            S[r][c] = !slots_out ? linear_start(it, p.S0, p.s0_transposed, slots_in, h, p.H, p.V,
-                                                K, row0 + r, lane * C + c, plan.seg_len, lg,
-                                                p.reverse)
-                      : last ? given_start(p.S0, p.s0_transposed, (size_t)it.seq * p.H + h, p.V, K,
-                                           row0 + r, lane * C + c)
-                             : 0.f;
+            S[r][c] = p.S0 && (slots_out ? last : !slots_in)
+                          ? given_start(p.S0, p.s0_transposed, (size_t)it.seq * p.H + h, p.V, K,
+                                        row0 + r, lane * C + c)
+                          : 0.f;
+    if (slots_in) {
+        if (p.S0) add_slot(it.slot0 + (p.reverse ? 0 : it.n - 1),
+                           exp2f((float)start_steps(it, plan.seg_len, p.reverse) * lg));
+        for (int i = p.reverse ? it.j + 1 : 0; i < (p.reverse ? it.n : it.j); ++i)
+            add_slot(it.slot0 + i,
+                     exp2f((float)tokens_between(i, it.j, it.len, plan.seg_len, p.reverse) * lg));
+    }
     const T *qp = static_cast<const T *>(p.q) + (long long)hq * K;
     const T *kp = static_cast<const T *>(p.k) + (long long)hk * K;
     const T *vp = static_cast<const T *>(p.v) + (long long)hv * p.V + blk * kCtaRows;

@@ -119,34 +119,15 @@ __device__ __forceinline__ float given_start(const float *S0, bool transposed, s
     return transposed ? p[(size_t)k * V + v] : p[(size_t)v * K + k];
 }
 
-// One element of a segment's start state: S0 and the segments before it in
-// scan order, from their end states in `slots` ([slot][H][V][K]).  The slot of
-// a sequence's last segment in scan order, whose end nothing starts from, holds
-// a copy of S0: the end states may be written over S0 while segments start.
-__device__ __forceinline__ float linear_start(const LinearItem &it, const float *S0,
-                                              bool s0_transposed, const float *slots, int h, int H,
-                                              int V, int K, int v, int k, int seg_len, float lg,
-                                              bool reverse) {
-    float s = 0.f;
-    const size_t VK = (size_t)V * K;
-    if (S0) {
-        s = slots ? slots[((size_t)(it.slot0 + (reverse ? 0 : it.n - 1)) * H + h) * VK +
-                          (size_t)v * K + k]
-                  : given_start(S0, s0_transposed, (size_t)it.seq * H + h, V, K, v, k);
-        const int past = reverse ? (it.j == it.n - 1 ? 0 : it.len - (it.j + 1) * seg_len)
-                                 : it.j * seg_len;
-        // a reversed scan takes its start state up undecayed
-        const int steps = reverse && past > 0 ? past - 1 : past;
-        if (steps > 0) s *= exp2f((float)steps * lg);
-    }
-    if (slots) {
-        for (int i = 0; i < it.n; ++i) {
-            if (reverse ? i <= it.j : i >= it.j) continue;
-            const int gap = tokens_between(i, it.j, it.len, seg_len, reverse);
-            s = fmaf(exp2f((float)gap * lg), slots[((size_t)(it.slot0 + i) * H + h) * VK + (size_t)v * K + k], s);
-        }
-    }
-    return s;
+// How often S0 has decayed before a segment: a segment starts from S0 and the
+// end states of the segments before it in scan order, in the workspace's slots
+// ([slot][H][V][K]).  The slot of a sequence's last segment in scan order, whose
+// end nothing starts from, holds a copy of S0: the end states may be written
+// over S0 while segments start.
+__device__ __forceinline__ int start_steps(const LinearItem &it, int seg_len, bool reverse) {
+    if (!reverse) return it.j * seg_len;
+    // a reversed scan takes its start state up undecayed
+    return it.j == it.n - 1 ? 0 : it.len - (it.j + 1) * seg_len - 1;
 }
 
 // The scan on the tensor cores (bf16, K and V of 64 or 128); the segments it

@@ -471,9 +471,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
             for (int e = 0; e < NS; ++e) S[e] = 0.f;
             if (p.S0) {
-                const int past = first ? 0
-                                 : rev ? it.len - (it.j + 1) * arg.plan.seg_len - 1 : f0;
-                const float f = exp2f((float)past * lg);
+                const float f = exp2f((float)start_steps(it, arg.plan.seg_len, rev) * lg);
                 if (arg.slots_in) {
                     const float4 *src = reinterpret_cast<const float4 *>(
                         arg.slots_in + (((size_t)(it.slot0 + (rev ? 0 : it.n - 1)) * p.H + h) * V + v) * K + k0);
