@@ -319,6 +319,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     float *const colfac = reinterpret_cast<float *>(smem + L::TABLE);
     float *const vweight = colfac + kC;
 
+    if (!want_o && tid < kC)
+        vweight[tid] = p.write_scale * exp2f((float)(rev ? tid : kC - 1 - tid) * lg);
+    __syncthreads();
+
     // After a wait has run out every later wait returns at once and nothing is
     // written any more, but the loops keep their barriers and end.
     bool dead = false;
@@ -348,9 +352,77 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (lane == 0) mbar_arrive(b);
     };
 
+    // Half c of chunk i's V, by 4 warps for each half g of its tokens: a warp's
+    // lanes of TMEM are 32 channels.  Lanes 8 j .. address block j: tokens
+    // + 8 (j / 2), channels + 8 (j % 2).
+    auto convert = [&](int i, int c, int g) {
+        const uint32_t tok = g * 64 + (lane & 7) + ((lane >> 4) << 3);
+        const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
+        // 32 tokens of this group's 64; exact: as three bf16 pieces whose
+        // sum is the float32 product, each the upper half of what is left
+        if ((warp & 3) * 32 < V) {
+            float2 w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = w2[16 * c + 4 * e];
+#pragma unroll 1
+            for (int r = 0; r < 2; ++r) {  // 16 channels
+                const uint32_t col = (uint32_t)(warp & 3) * 32 + 16 * r + (lane & 8);
+                const uint32_t off = (col >> 6) * (kC * 128) + swz128(tok, (col & 63) >> 3) + c * 4096;
+                const uint32_t src = smem_u32(smem) + L::VV + (i % kStages) * L::VSLOT + off;
+                const uint32_t at = tmem + quad + ((uint32_t)r << 20) + g * 32 + 16 * c;
+                uint32_t hi[8], x[2][4];
+                ldmatrix4_trans(x[0], src);
+                ldmatrix4_trans(x[1], src + 2048);
+                if (p.exact) {
+                    uint32_t mid[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t &z = x[e >> 2][e & 3];
+                        float u = __uint_as_float(z << 16);
+                        float y = __uint_as_float(z & 0xffff0000u);
+                        mul2(u, y, w[e >> 1].x, w[e >> 1].y);
+                        hi[e] = upper_halves(u, y);
+                        drop_upper_halves(u, y);
+                        mid[e] = upper_halves(u, y);
+                        drop_upper_halves(u, y);
+                        z = upper_halves(u, y);
+                    }
+                    tmem_st_16x128(at + kColMid, mid);
+                    const uint32_t low = smem_u32(smem) + L::LOW + off;
+                    stmatrix4_trans(low, x[0][0], x[0][1], x[0][2], x[0][3]);
+                    stmatrix4_trans(low + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t z = x[e >> 2][e & 3];
+                        float u = __uint_as_float(z << 16);
+                        float y = __uint_as_float(z & 0xffff0000u);
+                        mul2(u, y, w[e >> 1].x, w[e >> 1].y);
+                        hi[e] = pack_bf16(u, y);
+                    }
+                }
+                tmem_st_16x128(at + kColHi, hi);
+            }
+            tmem_st_wait();
+            fence_proxy_async_smem();
+        }
+    };
+    // without outputs the rows' warps take the second halves
+    const bool help = !want_o && tokens % kC == 0;
+
     if (warp < 8) {
         // ---------------------------------------------------------------- rows
         // (keeps the 96 registers of the launch)
+        if (help) {
+#pragma unroll 1
+            for (int i = 0; i < nc && updates(i); ++i) {
+                wait_warp(&bar.vfull[i % kStages], i / kStages);
+                if (i > 0) wait_warp(&bar.d, i - 1);  // the pieces' places are free
+                convert(i, 1, warp >> 2);
+                tc_fence_before();
+                arrive_warp(&bar.vw[1]);
+            }
+        }
         if (want_o) {
             const int t = (warp & 3) * 32 + lane, part = warp >> 2;
             // the powers within a block of 32 columns; a row's factor of the block
@@ -509,7 +581,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int e = 0; e < NS; ++e) S[e] = 0.f;
         }
         const int st = tid - 256;  // 0..255 of both groups
-        int n_table = -1;
+        int n_table = help ? kC : -1;
         auto store_state = [&] {
             if (mine) {
                 // rows of 128 bytes hold 64 columns; K = 64: the groups share one row
@@ -525,9 +597,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             fence_proxy_async_smem();
             arrive_warp(&bar.s);
         };
-        // lanes 8 j .. address block j: tokens + 8 (j / 2), channels + 8 (j % 2)
-        const uint32_t tok = g * 64 + (lane & 7) + ((lane >> 4) << 3);
-        const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
         if (want_o && nc > 0) store_state();
         // step 2 i + c: half c of chunk i's V; S takes chunk i - 1 up after the
         // first half of chunk i is on its way
@@ -565,55 +634,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
                 if (i > 0 && updates(i)) wait_warp(&bar.d0, i - 1);  // the pieces' places are free
             }
-            if (i < nc && updates(i)) {
-                // 32 tokens of this group's 64; exact: as three bf16 pieces whose
-                // sum is the float32 product, each the upper half of what is left
-                if (mine) {
-                    float2 w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = w2[16 * c + 4 * e];
-#pragma unroll 1
-                    for (int r = 0; r < 2; ++r) {  // 16 channels
-                        const uint32_t col = (uint32_t)(warp & 3) * 32 + 16 * r + (lane & 8);
-                        const uint32_t off = (col >> 6) * (kC * 128) + swz128(tok, (col & 63) >> 3) + c * 4096;
-                        const uint32_t src = smem_u32(smem) + L::VV + (i % kStages) * L::VSLOT + off;
-                        const uint32_t at = tmem + quad + ((uint32_t)r << 20) + g * 32 + 16 * c;
-                        uint32_t hi[8], x[2][4];
-                        ldmatrix4_trans(x[0], src);
-                        ldmatrix4_trans(x[1], src + 2048);
-                        if (p.exact) {
-                            uint32_t mid[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                uint32_t &z = x[e >> 2][e & 3];
-                                float u = __uint_as_float(z << 16);
-                                float y = __uint_as_float(z & 0xffff0000u);
-                                mul2(u, y, w[e >> 1].x, w[e >> 1].y);
-                                hi[e] = upper_halves(u, y);
-                                drop_upper_halves(u, y);
-                                mid[e] = upper_halves(u, y);
-                                drop_upper_halves(u, y);
-                                z = upper_halves(u, y);
-                            }
-                            tmem_st_16x128(at + kColMid, mid);
-                            const uint32_t low = smem_u32(smem) + L::LOW + off;
-                            stmatrix4_trans(low, x[0][0], x[0][1], x[0][2], x[0][3]);
-                            stmatrix4_trans(low + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t z = x[e >> 2][e & 3];
-                                float u = __uint_as_float(z << 16);
-                                float y = __uint_as_float(z & 0xffff0000u);
-                                mul2(u, y, w[e >> 1].x, w[e >> 1].y);
-                                hi[e] = pack_bf16(u, y);
-                            }
-                        }
-                        tmem_st_16x128(at + kColHi, hi);
-                    }
-                    tmem_st_wait();
-                    fence_proxy_async_smem();
-                }
+            if (i < nc && updates(i) && !(help && c)) {
+                convert(i, c, g);
                 tc_fence_before();
                 arrive_warp(&bar.vw[c]);
             }
