@@ -326,18 +326,22 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
 }
 
 // dw[which][d] = sum over the CTAs of their partial sums, in a fixed order.
-__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float *partial, int n, int D,
-                                                         float *dwq, float *dwk) {
-    __shared__ float red[8][32];
+// 32 warps a CTA: the sums are a chain of loads, which one warp alone would
+// make some 400 long.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float *partial, int n, int D,
+                                                          float *dwq, float *dwk) {
+    __shared__ float red[32][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;  // of 2 D
     float s = 0.f;
-    for (int i = w; i < n; i += 8) s += partial[(long long)i * 2 * D + col];
+#pragma unroll 8
+    for (int i = w; i < n; i += 32) s += partial[(long long)i * 2 * D + col];
     red[w][lane] = s;
     __syncthreads();
     if (w == 0) {
         float t = 0.f;
-        for (int i = 0; i < 8; ++i) t += red[i][lane];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t += red[i][lane];
         float *dst = col < D ? dwq : dwk;
         if (dst) dst[col < D ? col : col - D] = t;
     }
@@ -411,7 +415,7 @@ cudaError_t launch_qk_norm_backward(const void *q, const void *k, const float *w
     const cudaError_t e = launch_any<true>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid,
                                            tile_tokens(Hq + Hk, D), st);
     if (e != cudaSuccess || !want) return e;
-    qk_norm_dw_kernel<<<2 * D / 32, 256, 0, st>>>(partial, grid, D, dwq, dwk);
+    qk_norm_dw_kernel<<<2 * D / 32, 1024, 0, st>>>(partial, grid, D, dwq, dwk);
     return cudaGetLastError();
 }
 
