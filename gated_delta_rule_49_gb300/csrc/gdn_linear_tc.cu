@@ -13,8 +13,9 @@
 // Precision: P and S are rounded to bf16 as operands (a step of the bf16
 // output each).  Where the state is a float32 result (`exact`) the weighted V
 // goes in as three bf16 pieces that add up to it; gradients that return no state
-// round it once instead, a step of the bf16 gradient like P's and S's.  D is
-// formed chunk by chunk from zero in the float32 accumulator, and S is kept in
+// leave out the third (2^-16 of the value; with one piece alone their error was
+// 1.6 times that of float32 arithmetic, with two it is 1.35 times: P's and S's
+// rounding).  D is formed chunk by chunk from zero in the float32 accumulator, and S is kept in
 // float32 registers, added to with rounding (an accumulator carried through all
 // chunks would be cut, not rounded, at every product).
 //
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     auto convert = [&](int i, int c, int g) {
         const uint32_t tok = g * 64 + (lane & 7) + ((lane >> 4) << 3);
         const float2 *w2 = reinterpret_cast<const float2 *>(vweight) + g * 32 + (lane & 3);
-        // 32 tokens of this group's 64; exact: as three bf16 pieces whose
-        // sum is the float32 product, each the upper half of what is left
+        // 32 tokens of this group's 64, as bf16 pieces, each the upper half of
+        // what is left: three whose sum is the float32 product (exact), or two
         if ((warp & 3) * 32 < V) {
             float2 w[4];
 #pragma unroll
@@ -373,33 +374,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 uint32_t hi[8], x[2][4];
                 ldmatrix4_trans(x[0], src);
                 ldmatrix4_trans(x[1], src + 2048);
-                if (p.exact) {
-                    uint32_t mid[8];
+                uint32_t mid[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t &z = x[e >> 2][e & 3];
-                        float u = __uint_as_float(z << 16);
-                        float y = __uint_as_float(z & 0xffff0000u);
-                        mul2(u, y, w[e >> 1].x, w[e >> 1].y);
-                        hi[e] = upper_halves(u, y);
-                        drop_upper_halves(u, y);
+                for (int e = 0; e < 8; ++e) {
+                    uint32_t &z = x[e >> 2][e & 3];
+                    float u = __uint_as_float(z << 16);
+                    float y = __uint_as_float(z & 0xffff0000u);
+                    mul2(u, y, w[e >> 1].x, w[e >> 1].y);
+                    hi[e] = upper_halves(u, y);
+                    drop_upper_halves(u, y);
+                    if (p.exact) {
                         mid[e] = upper_halves(u, y);
                         drop_upper_halves(u, y);
                         z = upper_halves(u, y);
+                    } else {
+                        mid[e] = pack_bf16(u, y);
                     }
-                    tmem_st_16x128(at + kColMid, mid);
+                }
+                tmem_st_16x128(at + kColMid, mid);
+                if (p.exact) {
                     const uint32_t low = smem_u32(smem) + L::LOW + off;
                     stmatrix4_trans(low, x[0][0], x[0][1], x[0][2], x[0][3]);
                     stmatrix4_trans(low + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t z = x[e >> 2][e & 3];
-                        float u = __uint_as_float(z << 16);
-                        float y = __uint_as_float(z & 0xffff0000u);
-                        mul2(u, y, w[e >> 1].x, w[e >> 1].y);
-                        hi[e] = pack_bf16(u, y);
-                    }
                 }
                 tmem_st_16x128(at + kColHi, hi);
             }
@@ -792,9 +788,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         if (dead) break;
                         // the small pieces first: the sum is cut to its size at each product
 #pragma unroll 1
-                        for (int y = p.exact ? 0 : 2; y < 3; ++y) {
+                        for (int y = p.exact ? 0 : 1; y < 3; ++y) {
                             const uint32_t a = tmem + (y == 1 ? kColMid : kColHi);
-                            const bool on = c > 0 || y == 1 || (y == 2 && p.exact);
+                            const bool on = c > 0 || y == 2 || (y == 1 && p.exact);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {  // tokens 32 c .. and 64 + 32 c ..
                                 const int z = 2 * c + (x & 1) + 4 * (x >> 1);
