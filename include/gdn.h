@@ -19,7 +19,8 @@
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - All tensor pointers are DEVICE pointers owned by the caller, dense and
- *    row-major, each 16-byte aligned (else GDN_ERR_ALIGNMENT).  The library
+ *    row-major (where no token stride is given), each 16-byte aligned (else
+ *    GDN_ERR_ALIGNMENT).  The library
  *    never allocates device memory in these calls.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream) and never synchronise, except
@@ -28,7 +29,8 @@
  *    launches nothing.  A failed launch returns GDN_ERR_CUDA.  No entry point
  *    calls exit(), traps or asserts on the device.
  *  - Supported (K, V) pairs: (32, 32), (64, 128), (128, 128); others return
- *    GDN_ERR_UNSUPPORTED.  K is d_k (or a pruned d_k'), V is d_v.
+ *    GDN_ERR_UNSUPPORTED (linear attention also takes (64, 64)).  K is d_k (or
+ *    a pruned d_k'), V is d_v.
  *  - State tensors, alpha and beta are always float32; q, k, v and o are
  *    bf16 (GDN_BF16) or float32 (GDN_FP32).  Arithmetic is float32 with the
  *    state carried in float32; in GDN_BF16 mode at V = 128 the prefill runs
@@ -525,9 +527,10 @@ GDN_API int gdn_qk_norm_rotate_backward(const void *q, const void *k, const floa
  *         sequence empty and set GDN_ERR_DEVICE_BOUNDS; tokens of no sequence
  *         keep what o held.
  *
- * (K, V) in (32, 32), (64, 64), (64, 128), (128, 128).  A value that is not a
- * number reaches the outputs of its own sequence only; among those it may reach
- * tokens up to 127 before it, which are computed in one block with it.
+ * (K, V) in (32, 32), (64, 64), (64, 128), (128, 128).  A value that is not
+ * finite reaches the outputs of its own sequence only, where it gives infinities
+ * or NaN; it may reach tokens up to 127 before it, which are computed in one
+ * block with it.
  * workspace: gdn_linear_prefill_workspace_size bytes (0 where the sequences
  * alone fill the device), 256-byte aligned.
  */
@@ -552,6 +555,8 @@ GDN_API int gdn_linear_prefill(const void *q, const void *k, const void *v, cons
  * float32; each may be NULL, one at least is wanted.  S0 as given to the
  * forward pass (NULL = zero; the states are recomputed, none is kept from it).
  * The decays are constants of the model and have no gradient.  dS0 may be dS_T.
+ * Tokens of no sequence keep what the gradients held (with shared heads they are
+ * undefined).  workspace: gdn_linear_backward_workspace_size bytes.
  */
 GDN_API size_t gdn_linear_backward_workspace_size(int B, int T, int Hq, int H, int K, int V,
                                                   int packed, gdn_dtype dtype);
