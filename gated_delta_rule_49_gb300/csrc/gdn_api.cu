@@ -531,7 +531,7 @@ int gdn_qk_norm_rotate(const void *q, const void *k, const float *wq, const floa
 
 size_t gdn_qk_norm_rotate_backward_workspace_size(long long N, int Hq, int Hk, int D) {
     if (N <= 0 || Hq < 0 || Hk < 0 || Hq + Hk <= 0 || D <= 0) return 0;
-    return (size_t)gdn::qk_norm_backward_grid(N, Hq + Hk, D) * 2 * D * sizeof(float);
+    return (size_t)gdn::qk_norm_backward_grid(N, Hq, Hk, D) * D * sizeof(float);
 }
 
 int gdn_qk_norm_rotate_backward(const void *q, const void *k, const float *wq, const float *wk,

@@ -165,9 +165,9 @@ cudaError_t launch_prefill_host(const void *q, const void *k, const void *v, con
                                 void *workspace, cudaStream_t stream);
 
 // Norms of queries and keys for each head with the position rotation; the
-// backward pass needs qk_norm_backward_grid * 2 * D floats for the weights'
+// backward pass needs qk_norm_backward_grid * D floats for the weights'
 // gradients.
-int qk_norm_backward_grid(long long N, int heads, int D);
+int qk_norm_backward_grid(long long N, int Hq, int Hk, int D);
 cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
                            const long long *pos, const float *inv_freq, void *yq, void *yk,
                            long long N, int Hq, int Hk, int D, int R, long long ldq, long long ldk,

@@ -18,7 +18,7 @@
 // channels each, chosen so that a lane holds both channels of its pairs: only
 // the sums over a row are exchanged by shuffles.  (With 8 consecutive channels a
 // lane the half layout took 8 more shuffles a row, and the angles' reads met 8 a
-// bank: 160 us where this takes 103 for B = 8, T = 4096, 16 + 16 heads of
+// bank: 160 us where this takes 93 for B = 8, T = 4096, 16 + 16 heads of
 // 128 channels in bf16.)  A thread has the loads of several rows in flight
 // before it works on the first.
 //
@@ -36,20 +36,31 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// CTAs of an SM.  Backward in bf16, with 2 rows in flight a thread, takes 206,
-// 178, 210 and 300 us (1 row) with 2, 3, 4 and 5 for B = 8, T = 4096, 16 + 16
-// heads of 128 channels; forward hardly changes from 3 to 8.
-constexpr int norm_ctas(bool back, bool wide) { return back ? (wide ? 2 : 3) : 4; }
+// CTAs of an SM, and rows in flight of a thread.  For B = 8, T = 4096, 16 + 16
+// heads of 128 channels in bf16: forward, 4 rows, 3 CTAs 93 us, 4 CTAs 103, 5 118
+// (3 CTAs of 3 or 8 rows: 100); backward, 4 rows, 2 CTAs 170 us, 3 CTAs 179, 1
+// CTA 262 (2 rows, 3 CTAs: 178).
+constexpr int norm_ctas(bool back, bool wide) { return back || wide ? 2 : 3; }
+constexpr int norm_rows(bool wide) { return wide ? 2 : 4; }
 
+// One of q and k: its rows are taken by CTAs of its own, so that nothing is
+// chosen row by row (issue slots are what runs short beside memory).
+struct QkSide {
+    const void *x, *dy;
+    const float *w;
+    void *y;             // backward: dx
+    long long ld;
+    int heads, tokens;   // of a tile
+    unsigned magic;      // ceil(2^32 / heads): divides a row of a tile (0: one head)
+};
 struct QkNormArgs {
-    const void *q, *k, *dyq, *dyk;
-    const float *wq, *wk;
+    QkSide side[2];
+    int first;           // CTAs of q, the rest are k's
     const long long *pos;
     const float *inv_freq;
-    void *yq, *yk;  // backward: dq, dk
-    float *partial;  // backward: [grid][2][D]
-    long long N, ldq, ldk;
-    int Hq, Hk, R;
+    float *partial;      // backward: [grid][D]
+    long long N;
+    int R;
     float eps;
 };
 
@@ -182,55 +193,57 @@ __device__ __forceinline__ void fill_angles(float *cs, const unsigned long long 
     }
 }
 
-// A CTA takes tiles of TT tokens with all of their heads, a lane group of
-// D / 8 lanes U rows at a time.  `magic` = ceil(2^32 / heads) divides a row of
-// a tile by the number of heads (rows * heads < 2^32; 0: one head).
+// A CTA takes tiles of some tokens with all heads of q or of k, a lane group of
+// D / 8 lanes U rows at a time.
 template <typename T, int D, bool HALF, bool BACK>
 __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
-    qk_norm_kernel(const QkNormArgs p, int TT, float c_norm, unsigned magic) {
+    qk_norm_kernel(const QkNormArgs p, float c_norm) {
     constexpr int LPR = D / 8;             // lanes of a row
     constexpr int ROWS = kThreads / LPR;   // rows at a time
-    constexpr int U = BACK || sizeof(T) == 4 ? 2 : 4;
-    extern __shared__ __align__(16) float weights[];  // wq, wk
-    unsigned long long *const turns = reinterpret_cast<unsigned long long *>(weights + 2 * D);
+    constexpr int U = norm_rows(sizeof(T) == 4);
+    extern __shared__ __align__(16) unsigned long long turns[];
     float *const cs2 = reinterpret_cast<float *>(turns + (p.R >> 1));  // two tiles
+    const bool isk = (int)blockIdx.x >= p.first;
+    const QkSide &sd = p.side[isk];
+    const int heads = sd.heads, TT = sd.tokens;
+    const unsigned magic = sd.magic;
     const int c = threadIdx.x % LPR, gi = threadIdx.x / LPR;
     const int pa = piece_a<HALF>(c, p.R), pb = piece_b<HALF>(c, p.R);
-    const int heads = p.Hq + p.Hk;
-    float dwq[8], dwk[8];
+    const T *const src = static_cast<const T *>(sd.x) + pa, *const gsrc = static_cast<const T *>(sd.dy) + pa;
+    T *const dst = static_cast<T *>(sd.y) + pa;
+    const int ab = pb - pa;
+    const long long ld = sd.ld;
+    const int ldy = heads * D;
+    float w[8], dw[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
-    for (int d = threadIdx.x; d < 2 * D; d += kThreads) {
-        const float *w = d < D ? p.wq : p.wk;
-        weights[d] = w ? w[d % D] : 1.f;
+    for (int i = 0; i < 8; ++i) {
+        w[i] = sd.w ? sd.w[i < 4 ? pa + i : pb + i - 4] : 1.f;
+        dw[i] = 0.f;
     }
     auto token_of = [&](int r) { return magic ? (int)__umulhi((unsigned)r, magic) : r; };
     fill_turns(turns, p);
     __syncthreads();
-    const long long step = (long long)gridDim.x * TT;
+    const long long tile0 = (long long)(isk ? blockIdx.x - p.first : blockIdx.x) * TT;
+    const long long step = (long long)(isk ? gridDim.x - p.first : p.first) * TT;
     Vec4<T> xa[U], xb[U], ga[BACK ? U : 1], gb[BACK ? U : 1];
     // row u of the batch from row r0 of the tile of tokens t0 ..
     auto fetch = [&](int u, long long t0, int r0) {
         const int r = r0 + u * ROWS + gi;
         if (t0 >= p.N || r >= (int)min((long long)TT, p.N - t0) * heads) return;
         const int t = token_of(r), h = r - t * heads;
-        const bool isq = h < p.Hq;
-        const long long tok = t0 + t;
-        const T *src = isq ? static_cast<const T *>(p.q) + tok * p.ldq + (long long)h * D
-                           : static_cast<const T *>(p.k) + tok * p.ldk + (long long)(h - p.Hq) * D;
-        xa[u].load(src + pa);
-        xb[u].load(src + pb);
+        const T *x = src + ((t0 + t) * ld + h * D);
+        xa[u].load(x);
+        xb[u].load(x + ab);
         if constexpr (BACK) {
-            src = isq ? static_cast<const T *>(p.dyq) + (tok * p.Hq + h) * D
-                      : static_cast<const T *>(p.dyk) + (tok * p.Hk + h - p.Hq) * D;
-            ga[u].load(src + pa);
-            gb[u].load(src + pb);
+            x = gsrc + (t0 * ldy + r * D);
+            ga[u].load(x);
+            gb[u].load(x + ab);
         }
     };
 #pragma unroll
-    for (int u = 0; u < U; ++u) fetch(u, (long long)blockIdx.x * TT, 0);
+    for (int u = 0; u < U; ++u) fetch(u, tile0, 0);
     int buf = 0;
-    for (long long t0 = (long long)blockIdx.x * TT; t0 < p.N; t0 += step) {
+    for (long long t0 = tile0; t0 < p.N; t0 += step) {
         const int nt = (int)min((long long)TT, p.N - t0);
         const int rows = nt * heads;
         float *const cs = cs2 + buf * TT * p.R;
@@ -244,8 +257,6 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
                 const int r = r0 + u * ROWS + gi;
                 const bool live = r < rows;
                 const int t = live ? token_of(r) : 0;
-                const int h = live ? r - t * heads : 0;
-                const bool isq = h < p.Hq;
                 float x[8] = {}, g[8] = {};
                 if (live) {
                     xa[u].get(x);
@@ -260,33 +271,23 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
                 const float ss = row_sum<LPR>(dot8(x, x));
                 const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
                 const float4 *ct = reinterpret_cast<const float4 *>(cs + t * p.R);
-                float w[8];
-                *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(weights + (isq ? 0 : D) + pa);
-                *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(weights + (isq ? 0 : D) + pb);
                 if constexpr (!BACK) {
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        mul2(w[i], w[i + 1], rn, rn);
+                        mul2(x[i], x[i + 1], rn, rn);
                         mul2(x[i], x[i + 1], w[i], w[i + 1]);
                     }
                     rotate8<HALF, false>(x, ct, p.R, c);
                 } else {
                     rotate8<HALF, true>(g, ct, p.R, c);
-                    float d[8];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        d[i] = x[i];
-                        d[i + 1] = x[i + 1];
-                        mul2(d[i], d[i + 1], rn, rn);
-                        mul2(d[i], d[i + 1], g[i], g[i + 1]);
+                        float d0 = x[i], d1 = x[i + 1];
+                        mul2(d0, d1, rn, rn);
+                        fma2(d0, d1, g[i], g[i + 1], dw[i], dw[i + 1]);
+                        dw[i] = d0;
+                        dw[i + 1] = d1;
                         mul2(g[i], g[i + 1], w[i], w[i + 1]);
-                    }
-                    if (isq) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dwq[i] += d[i];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dwk[i] += d[i];
                     }
                     const float f = -row_sum<LPR>(dot8(x, g)) * c_norm * rn * rn;
 #pragma unroll
@@ -296,11 +297,9 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
                     }
                 }
                 if (live) {
-                    const long long tok = t0 + t;
-                    T *dst = isq ? static_cast<T *>(p.yq) + (tok * p.Hq + h) * D
-                                 : static_cast<T *>(p.yk) + (tok * p.Hk + h - p.Hq) * D;
-                    Vec4<T>::store(dst + pa, x);
-                    Vec4<T>::store(dst + pb, x + 4);
+                    T *y = dst + (t0 * ldy + r * D);
+                    Vec4<T>::store(y, x);
+                    Vec4<T>::store(y + ab, x + 4);
                 }
             }
         }
@@ -309,67 +308,72 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
         if (!p.partial) return;
         // sums over this CTA's rows, in the fixed order of its threads
         float *red = cs2;
-#pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                red[gi * D + (i < 4 ? pa + i : pb + i - 4)] = which ? dwk[i] : dwq[i];
-            __syncthreads();
-            for (int d = threadIdx.x; d < D; d += kThreads) {
-                float s = 0.f;
-                for (int r = 0; r < ROWS; ++r) s += red[r * D + d];
-                p.partial[((long long)blockIdx.x * 2 + which) * D + d] = s;
-            }
+        for (int i = 0; i < 8; ++i) red[gi * D + (i < 4 ? pa + i : pb + i - 4)] = dw[i];
+        __syncthreads();
+        for (int d = threadIdx.x; d < D; d += kThreads) {
+            float s = 0.f;
+            for (int r = 0; r < ROWS; ++r) s += red[r * D + d];
+            p.partial[(long long)blockIdx.x * D + d] = s;
         }
     }
 }
 
-// dw[which][d] = sum over the CTAs of their partial sums, in a fixed order.
-// 32 warps a CTA: the sums are a chain of loads, which one warp alone would
-// make some 400 long.
-__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float *partial, int n, int D,
-                                                          float *dwq, float *dwk) {
+// dw[d] = sum over the CTAs of q (blocks of the first D columns) or of k, in a
+// fixed order.  32 warps a CTA: the sums are a chain of loads, which one warp
+// alone would make some 200 long.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float *partial, int first, int n,
+                                                          int D, float *dwq, float *dwk) {
     __shared__ float red[32][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;  // of 2 D
+    const bool isk = (int)blockIdx.x * 32 >= D;
+    const int col = blockIdx.x * 32 + lane - (isk ? D : 0);
+    float *dst = isk ? dwk : dwq;
+    if (!dst) return;
     float s = 0.f;
 #pragma unroll 8
-    for (int i = w; i < n; i += 32) s += partial[(long long)i * 2 * D + col];
+    for (int i = (isk ? first : 0) + w; i < (isk ? n : first); i += 32) s += partial[(long long)i * D + col];
     red[w][lane] = s;
     __syncthreads();
     if (w == 0) {
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) t += red[i][lane];
-        float *dst = col < D ? dwq : dwk;
-        if (dst) dst[col < D ? col : col - D] = t;
+        dst[col] = t;
     }
 }
 
 int tile_tokens(int heads, int D) {
     // about 8 rows a lane group: the angles of a tile then cost one sincospi
-    // a thread next to 8 rows of work (at most 2 x 16 KB of angles)
-    const int tokens = 8 * kThreads / (D / 8) / heads, most = 4096 / D;
+    // or two a thread next to 8 rows of work (at most 2 x 16 KB of angles)
+    const int tokens = heads ? 8 * kThreads / (D / 8) / heads : 1, most = 4096 / D;
     return tokens < 1 ? 1 : (tokens > most ? most : tokens);
 }
 
-int norm_grid(long long N, int heads, int D, int per_sm) {
-    const long long tiles = (N + tile_tokens(heads, D) - 1) / tile_tokens(heads, D);
+// CTAs of q and of both: one a tile, and no more than fit, by their rows.
+struct NormGrid {
+    int first, all;
+};
+NormGrid norm_grid(long long N, int Hq, int Hk, int D, int per_sm) {
+    const long long tq = Hq ? (N + tile_tokens(Hq, D) - 1) / tile_tokens(Hq, D) : 0;
+    const long long tk = Hk ? (N + tile_tokens(Hk, D) - 1) / tile_tokens(Hk, D) : 0;
     const long long most = (long long)per_sm * (sm_count() > 0 ? sm_count() : 152);
-    return (int)(tiles < most ? tiles : most);
+    if (tq + tk <= most) return {(int)tq, (int)(tq + tk)};
+    long long q = (most * Hq + (Hq + Hk) / 2) / (Hq + Hk);
+    q = Hq && q < 1 ? 1 : Hk && q > most - 1 ? most - 1 : q;
+    q = q < tq ? q : tq;
+    const long long k = most - q < tk ? most - q : tk;
+    return {(int)q, (int)(q + k)};
 }
 
 template <typename T, bool HALF, bool BACK>
-cudaError_t launch_d(const QkNormArgs &p, int D, float c, int grid, int TT, size_t smem,
-                     cudaStream_t st) {
-    const unsigned heads = p.Hq + p.Hk;
-    const unsigned magic = heads == 1 ? 0 : (unsigned)((0x100000000ull + heads - 1) / heads);
+cudaError_t launch_d(const QkNormArgs &p, int D, float c, int grid, size_t smem, cudaStream_t st) {
     switch (D) {
-        case 32: qk_norm_kernel<T, 32, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
-        case 64: qk_norm_kernel<T, 64, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
-        case 128: qk_norm_kernel<T, 128, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
-        case 256: qk_norm_kernel<T, 256, HALF, BACK><<<grid, kThreads, smem, st>>>(p, TT, c, magic); break;
+        case 32: qk_norm_kernel<T, 32, HALF, BACK><<<grid, kThreads, smem, st>>>(p, c); break;
+        case 64: qk_norm_kernel<T, 64, HALF, BACK><<<grid, kThreads, smem, st>>>(p, c); break;
+        case 128: qk_norm_kernel<T, 128, HALF, BACK><<<grid, kThreads, smem, st>>>(p, c); break;
+        case 256: qk_norm_kernel<T, 256, HALF, BACK><<<grid, kThreads, smem, st>>>(p, c); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
@@ -377,29 +381,38 @@ cudaError_t launch_d(const QkNormArgs &p, int D, float c, int grid, int TT, size
 
 template <bool BACK>
 cudaError_t launch_any(const QkNormArgs &p, int D, float c, bool half, gdn_dtype dt, int grid,
-                       int TT, cudaStream_t st) {
-    size_t smem = (size_t)2 * TT * (p.R / 2) * sizeof(float2);
+                       cudaStream_t st) {
+    const int tokens = p.side[0].tokens > p.side[1].tokens ? p.side[0].tokens : p.side[1].tokens;
+    size_t smem = (size_t)2 * tokens * p.R * sizeof(float);
     if (BACK && smem < kThreads * 8 * sizeof(float)) smem = kThreads * 8 * sizeof(float);
-    smem += (p.R / 2) * sizeof(unsigned long long) + 2 * D * sizeof(float);
+    smem += (p.R / 2) * sizeof(unsigned long long);
     if (dt == GDN_BF16)
-        return half ? launch_d<__nv_bfloat16, true, BACK>(p, D, c, grid, TT, smem, st)
-                    : launch_d<__nv_bfloat16, false, BACK>(p, D, c, grid, TT, smem, st);
-    return half ? launch_d<float, true, BACK>(p, D, c, grid, TT, smem, st)
-                : launch_d<float, false, BACK>(p, D, c, grid, TT, smem, st);
+        return half ? launch_d<__nv_bfloat16, true, BACK>(p, D, c, grid, smem, st)
+                    : launch_d<__nv_bfloat16, false, BACK>(p, D, c, grid, smem, st);
+    return half ? launch_d<float, true, BACK>(p, D, c, grid, smem, st)
+                : launch_d<float, false, BACK>(p, D, c, grid, smem, st);
+}
+
+QkSide side(const void *x, const void *dy, const float *w, void *y, long long ld, int heads, int D) {
+    return {x, dy, w, y, ld, heads, tile_tokens(heads, D),
+            heads <= 1 ? 0 : (unsigned)((0x100000000ull + heads - 1) / heads)};
 }
 
 }  // namespace
 
-int qk_norm_backward_grid(long long N, int heads, int D) { return norm_grid(N, heads, D, norm_ctas(true, false)); }
+// (as many partial sums as the most CTAs that either type runs with)
+int qk_norm_backward_grid(long long N, int Hq, int Hk, int D) {
+    return norm_grid(N, Hq, Hk, D, norm_ctas(true, false)).all;
+}
 
 cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
                            const long long *pos, const float *inv_freq, void *yq, void *yk,
                            long long N, int Hq, int Hk, int D, int R, long long ldq, long long ldk,
                            bool l2, bool half, float eps, gdn_dtype dt, cudaStream_t st) {
-    QkNormArgs p = {q, k, nullptr, nullptr, wq, wk, pos, inv_freq, yq, yk, nullptr,
-                    N, ldq, ldk, Hq, Hk, R, eps};
-    const int grid = norm_grid(N, Hq + Hk, D, norm_ctas(false, dt != GDN_BF16));
-    return launch_any<false>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid, tile_tokens(Hq + Hk, D), st);
+    const NormGrid g = norm_grid(N, Hq, Hk, D, norm_ctas(false, dt != GDN_BF16));
+    const QkNormArgs p = {{side(q, nullptr, wq, yq, ldq, Hq, D), side(k, nullptr, wk, yk, ldk, Hk, D)},
+                          g.first, pos, inv_freq, nullptr, N, R, eps};
+    return launch_any<false>(p, D, l2 ? 1.f : 1.f / D, half, dt, g.all, st);
 }
 
 cudaError_t launch_qk_norm_backward(const void *q, const void *k, const float *wq,
@@ -409,13 +422,12 @@ cudaError_t launch_qk_norm_backward(const void *q, const void *k, const float *w
                                     int R, long long ldq, long long ldk, bool l2, bool half,
                                     float eps, gdn_dtype dt, float *partial, cudaStream_t st) {
     const bool want = dwq || dwk;
-    QkNormArgs p = {q, k, dyq, dyk, wq, wk, pos, inv_freq, dq, dk, want ? partial : nullptr,
-                    N, ldq, ldk, Hq, Hk, R, eps};
-    const int grid = qk_norm_backward_grid(N, Hq + Hk, D);
-    const cudaError_t e = launch_any<true>(p, D, l2 ? 1.f : 1.f / D, half, dt, grid,
-                                           tile_tokens(Hq + Hk, D), st);
+    const NormGrid g = norm_grid(N, Hq, Hk, D, norm_ctas(true, dt != GDN_BF16));
+    const QkNormArgs p = {{side(q, dyq, wq, dq, ldq, Hq, D), side(k, dyk, wk, dk, ldk, Hk, D)},
+                          g.first, pos, inv_freq, want ? partial : nullptr, N, R, eps};
+    const cudaError_t e = launch_any<true>(p, D, l2 ? 1.f : 1.f / D, half, dt, g.all, st);
     if (e != cudaSuccess || !want) return e;
-    qk_norm_dw_kernel<<<2 * D / 32, 1024, 0, st>>>(partial, grid, D, dwq, dwk);
+    qk_norm_dw_kernel<<<2 * D / 32, 1024, 0, st>>>(partial, g.first, g.all, D, dwq, dwk);
     return cudaGetLastError();
 }
 
