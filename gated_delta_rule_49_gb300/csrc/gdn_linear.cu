@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kScanThreads)
     if (slots_in) {
         if (p.S0) add_slot(it.slot0 + (p.reverse ? 0 : it.n - 1),
                            exp2f((float)start_steps(it, plan.seg_len, p.reverse) * lg));
+#pragma unroll 4
         for (int i = p.reverse ? it.j + 1 : 0; i < (p.reverse ? it.n : it.j); ++i)
             add_slot(it.slot0 + i,
                      exp2f((float)tokens_between(i, it.j, it.len, plan.seg_len, p.reverse) * lg));
@@ -213,7 +214,7 @@ SegPlan token_plan(int B, int T, int H, int V, bool packed) {
     };
     SegPlan best{T > 0 ? T : 1, B};
     double least = waves(B) * (longest + 32);
-    for (int n = 2; n <= 64 && longest / n >= 2 * kTile; ++n) {
+    for (int n = 2; n <= 64 && longest / n >= kTile; ++n) {
         const long long len = (longest + (long long)n * kTile - 1) / ((long long)n * kTile) * kTile;
         const long long per = ((packed ? T : longest) + len - 1) / len;
         const long long items = packed ? per + B : per * B;
