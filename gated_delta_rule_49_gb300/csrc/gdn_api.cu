@@ -597,25 +597,30 @@ int gdn_linear_prefill(const void *q, const void *k, const void *v, const float 
     a.write_scale = 1.f;
     a.read_scale = scale;
     a.exact = true;
-    return from_cuda(gdn::launch_linear_scan(a, dtype, workspace, st));
+    return from_cuda(gdn::launch_linear_scan(&a, 1, dtype, workspace, st));
 }
 
 namespace {
-// The scans' slots, rounded up so that what follows is aligned.
+// The scans' slots, rounded up so that what follows is aligned: on the tensor
+// cores one scan runs after another, on the CUDA cores all at once.
 size_t linear_backward_slots(int B, int T, int H, int K, int V, bool packed, gdn_dtype dtype) {
-    const size_t a = gdn::linear_scan_workspace(B, T, H, K, V, packed, dtype);
-    const size_t b = gdn::linear_scan_workspace(B, T, H, V, K, packed, dtype);
-    return ((a > b ? a : b) + 255) & ~size_t(255);
+    const size_t dv = gdn::linear_scan_workspace(B, T, H, K, V, packed, dtype);
+    const size_t dqk = gdn::linear_scan_workspace(B, T, H, V, K, packed, dtype);
+    const size_t n = !gdn::linear_on_tensor_cores(K, V, dtype) ? 2 * dqk + dv : dqk > dv ? dqk : dv;
+    return (n + 255) & ~size_t(255);
+}
+// One head's part of a gradient that a group of heads shares, in float32 (bytes).
+size_t linear_part(int B, int T, int H, int K, bool packed) {
+    return ((size_t)(packed ? 1 : B) * T * H * K * sizeof(float) + 255) & ~size_t(255);
 }
 }  // namespace
 
 size_t gdn_linear_backward_workspace_size(int B, int T, int Hq, int H, int K, int V, int packed,
                                           gdn_dtype dtype) {
     if (B <= 0 || T <= 0 || H <= 0 || Hq <= 0 || !linear_kv(K, V)) return 0;
-    size_t n = linear_backward_slots(B, T, H, K, V, packed != 0, dtype);
-    // one head's part of a gradient that a group of heads shares, in float32
-    if (Hq != H) n += (size_t)(packed ? 1 : B) * T * H * K * sizeof(float);
-    return n;
+    const size_t n = linear_backward_slots(B, T, H, K, V, packed != 0, dtype);
+    if (Hq == H) return n;
+    return n + (gdn::linear_on_tensor_cores(K, V, dtype) ? 1 : 2) * linear_part(B, T, H, K, packed != 0);
 }
 
 int gdn_linear_backward(const void *q, const void *k, const void *v, const float *alpha,
@@ -638,42 +643,47 @@ int gdn_linear_backward(const void *q, const void *k, const void *v, const float
         gdn_linear_backward_workspace_size(B, T, Hq, H, K, V, offsets != nullptr, dtype);
     if (workspace_bytes < need || (!workspace && workspace_bytes)) return GDN_ERR_WORKSPACE;
     const long long tokens = offsets ? T : (long long)B * T;
-    float *part = reinterpret_cast<float *>(
-        static_cast<char *>(workspace) +
-        linear_backward_slots(B, T, H, K, V, offsets != nullptr, dtype));
+    char *const parts = static_cast<char *>(workspace) +
+                        linear_backward_slots(B, T, H, K, V, offsets != nullptr, dtype);
+    const bool together = !gdn::linear_on_tensor_cores(K, V, dtype);
     const int group = H / Hq;
+    float *const part_q = reinterpret_cast<float *>(parts);
+    float *const part_k = together ? reinterpret_cast<float *>(
+                                         parts + linear_part(B, T, H, K, offsets != nullptr))
+                                   : part_q;
     const long long ldo = (long long)H * V;
 
-    gdn::LinearScan a = {};
-    a.alpha = alpha; a.offsets = offsets;
-    a.B = B; a.T = T; a.H = H;
-    cudaError_t c = cudaSuccess;
-    auto shared = [&](void *grad) {  // dq and dk: summed over the heads that share them
-        a.o = group > 1 ? part : grad;
-        a.o_float = group > 1 || dtype == GDN_FP32;
-        c = gdn::launch_linear_scan(a, dtype, workspace, st);
-        if (c == cudaSuccess && group > 1)
-            c = gdn::launch_group_sum(part, grad, tokens, Hq, group, K, dtype, st);
-    };
+    gdn::LinearScan base = {};
+    base.alpha = alpha; base.offsets = offsets;
+    base.B = B; base.T = T; base.H = H;
+    gdn::LinearScan scans[3];
+    int n = 0;
+    // dq and dk go out in float32, one part a head, where a group of heads shares them
     if (dq) {
+        gdn::LinearScan &a = scans[n++] = base;
         a.q = dO; a.ldq = ldo; a.Hq = H;
         a.k = v; a.ldk = v_stride; a.Hk = H;
         a.v = k; a.ldv = k_stride; a.Hv = Hq;
         a.K = V; a.V = K;
         a.S0 = S0; a.s0_transposed = true; a.reverse = false;
         a.write_scale = 1.f; a.read_scale = scale;
-        shared(dq);
+        a.o = group > 1 ? part_q : dq;
+        a.o_float = group > 1 || dtype == GDN_FP32;
     }
-    if (c == cudaSuccess && dk) {
+    if (dk) {
+        gdn::LinearScan &a = scans[n++] = base;
         a.q = v; a.ldq = v_stride; a.Hq = H;
         a.k = dO; a.ldk = ldo; a.Hk = H;
         a.v = q; a.ldv = q_stride; a.Hv = Hq;
         a.K = V; a.V = K;
         a.S0 = dS_T; a.s0_transposed = true; a.reverse = true;
         a.write_scale = scale; a.read_scale = 1.f;
-        shared(dk);
+        a.o = group > 1 ? part_k : dk;
+        a.o_float = group > 1 || dtype == GDN_FP32;
     }
-    if (c == cudaSuccess && (dv || dS0)) {
+    const int shared = n;
+    if (dv || dS0) {
+        gdn::LinearScan &a = scans[n++] = base;
         a.q = k; a.ldq = k_stride; a.Hq = Hq;
         a.k = q; a.ldk = q_stride; a.Hk = Hq;
         a.v = dO; a.ldv = ldo; a.Hv = H;
@@ -681,7 +691,22 @@ int gdn_linear_backward(const void *q, const void *k, const void *v, const float
         a.S0 = dS_T; a.s0_transposed = false; a.reverse = true;
         a.write_scale = scale; a.read_scale = 1.f;
         a.o = dv; a.ST = dS0; a.exact = dS0 != nullptr; a.o_float = dtype == GDN_FP32;
-        c = gdn::launch_linear_scan(a, dtype, workspace, st);
+    }
+    cudaError_t c = cudaSuccess;
+    // all at once where nothing keeps them apart: dS0 may take dS_T's place, which dk's scan
+    // reads, and the launch takes two scans of one width first
+    if (together && n == 3 && (!dS0 || (dS0 != dS_T && dS0 != S0))) {
+        c = gdn::launch_linear_scan(scans, 3, dtype, workspace, st);
+        if (c == cudaSuccess && group > 1)
+            c = gdn::launch_group_sum(part_q, part_k, dq, dk, tokens, Hq, group, K, dtype, st);
+        return from_cuda(c);
+    }
+    for (int i = 0; i < n && c == cudaSuccess; ++i) {
+        c = gdn::launch_linear_scan(&scans[i], 1, dtype, workspace, st);
+        if (c == cudaSuccess && i < shared && group > 1)
+            c = gdn::launch_group_sum(static_cast<const float *>(scans[i].o), nullptr,
+                                      i == 0 && dq ? dq : dk, nullptr, tokens, Hq, group, K, dtype,
+                                      st);
     }
     return from_cuda(c);
 }

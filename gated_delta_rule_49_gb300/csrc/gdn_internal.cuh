@@ -195,13 +195,17 @@ struct LinearScan {
     bool reverse, s0_transposed, o_float;
     bool exact;  // the state to float32 accuracy (else to that of bf16 operands)
 };
-// Bytes of workspace of one scan; launches it.
+// Whether a scan runs on the tensor cores; bytes of workspace of one scan.
+bool linear_on_tensor_cores(int K, int V, gdn_dtype dt);
 size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt);
-cudaError_t launch_linear_scan(const LinearScan &a, gdn_dtype dt, void *workspace,
+// One scan, or on the CUDA cores up to three independent ones (the first two of
+// one width K), each with its own workspace one after another.
+cudaError_t launch_linear_scan(const LinearScan *a, int count, gdn_dtype dt, void *workspace,
                                cudaStream_t stream);
-// y [rows, Hq, D] (dtype) = sums of x [rows, H, D] (float32) over groups of H / Hq heads.
-cudaError_t launch_group_sum(const float *x, void *y, long long rows, int Hq, int group, int D,
-                             gdn_dtype dt, cudaStream_t stream);
+// y [rows, Hq, D] (dtype) = sums of x [rows, H, D] (float32) over groups of H / Hq heads; for
+// one tensor, or two of the same sizes (x1 not NULL).
+cudaError_t launch_group_sum(const float *x0, const float *x1, void *y0, void *y1, long long rows,
+                             int Hq, int group, int D, gdn_dtype dt, cudaStream_t stream);
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *alpha,
                                  const float *S, float *S_out, void *o, int B, int Hq, int H,
                                  int K, int V, float scale, gdn_dtype dt, cudaStream_t stream);

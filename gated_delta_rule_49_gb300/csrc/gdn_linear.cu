@@ -39,14 +39,31 @@ template <> struct Cols<4> {
     }
 };
 
+//
+// Up to three scans run in one launch (a backward pass: they do not depend on
+// one another, and a small one is all start-up: B = 2, T = 391, 4 heads of 64 x
+// 128 take 73 us as six launches and two sums, 48 us as two and one).
+struct TokenScan {
+    LinearScan p;
+    SegPlan plan;
+    float *slots;  // NULL: not cut
+};
+struct TokenScans {
+    TokenScan scan[3];
+    int count;
+};
+template <int K> constexpr int token_smem() { return kTile * (2 * K + kCtaRows); }  // floats
+
 template <typename T, int K>
-__global__ void __launch_bounds__(kScanThreads)
-    linear_token_kernel(const LinearScan p, SegPlan plan, const float *slots_in, float *slots_out,
-                        int *status) {
+__device__ __forceinline__ void token_scan(const LinearScan &p, const SegPlan &plan,
+                                           const float *slots_in, float *slots_out, float *sm,
+                                           int *status) {
     constexpr int C = K / 32;             // columns of a lane
     constexpr int QV = kTile * K / 8;     // 8-element pieces of a q or k tile
     constexpr int QN = (QV + kScanThreads - 1) / kScanThreads;
-    __shared__ __align__(16) float qs[kTile][K], ks[kTile][K], vs[kTile][kCtaRows];
+    float(*const qs)[K] = reinterpret_cast<float(*)[K]>(sm);
+    float(*const ks)[K] = qs + kTile;
+    float(*const vs)[kCtaRows] = reinterpret_cast<float(*)[kCtaRows]>(ks + kTile);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int blocks = p.V / kCtaRows;
     const int blk = blockIdx.x % blocks;
@@ -203,6 +220,20 @@ __global__ void __launch_bounds__(kScanThreads)
         for (int c = 0; c < C; ++c) end[(size_t)(row0 + r) * K + lane * C + c] = f * S[r][c];
 }
 
+// Scans 0 .. count - 1 in the y blocks; the last of three has its own width.
+template <typename T, int KA, int KB>
+__global__ void __launch_bounds__(kScanThreads)
+    linear_token_kernel(const __grid_constant__ TokenScans a, bool first_pass, int *status) {
+    constexpr int kFloats = token_smem<(KA > KB ? KA : KB)>();
+    __shared__ __align__(16) float sm[kFloats];
+    const TokenScan &s = a.scan[blockIdx.y];
+    if (first_pass && !s.slots) return;
+    const float *in = first_pass ? nullptr : s.slots;
+    float *out = first_pass ? s.slots : nullptr;
+    if (KA == KB || blockIdx.y < 2) token_scan<T, KA>(s.p, s.plan, in, out, sm, status);
+    else token_scan<T, KB>(s.p, s.plan, in, out, sm, status);
+}
+
 // Cuts as in linear_tc_plan, counted in token times: about six CTAs run on an
 // SM, one needs its segment's tokens and about 32 more to start and end, and a
 // first pass as long again.
@@ -227,27 +258,43 @@ SegPlan token_plan(int B, int T, int H, int V, bool packed) {
     return best;
 }
 
-template <typename T>
-cudaError_t launch_token(const LinearScan &p, float *slots, cudaStream_t st) {
+size_t token_slots(const LinearScan &p) {
     const SegPlan plan = token_plan(p.B, p.T, p.H, p.V, p.offsets != nullptr);
-    const bool cut = plan.items > p.B;
-    const long long grid = (long long)plan.items * p.H * (p.V / kCtaRows);
+    return plan.items > p.B ? (size_t)plan.items * p.H * p.V * p.K : 0;
+}
+
+template <typename T>
+cudaError_t launch_token(const LinearScan *p, int count, float *slots, cudaStream_t st) {
+    TokenScans a = {};
+    a.count = count;
+    long long grid = 0;
+    bool cut = false;
+    for (int i = 0; i < count; ++i) {
+        a.scan[i].p = p[i];
+        a.scan[i].plan = token_plan(p[i].B, p[i].T, p[i].H, p[i].V, p[i].offsets != nullptr);
+        const size_t n = token_slots(p[i]);
+        a.scan[i].slots = n ? slots : nullptr;
+        slots += n;
+        cut = cut || n;
+        const long long g = (long long)a.scan[i].plan.items * p[i].H * (p[i].V / kCtaRows);
+        grid = g > grid ? g : grid;
+    }
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     int *status = device_status_ptr();
-    auto run = [&](const float *in, float *out) {
-        switch (p.K) {
-            case 32: linear_token_kernel<T, 32><<<(unsigned)grid, kScanThreads, 0, st>>>(p, plan, in, out, status); break;
-            case 64: linear_token_kernel<T, 64><<<(unsigned)grid, kScanThreads, 0, st>>>(p, plan, in, out, status); break;
-            case 128: linear_token_kernel<T, 128><<<(unsigned)grid, kScanThreads, 0, st>>>(p, plan, in, out, status); break;
-            default: return cudaErrorInvalidValue;
-        }
+    const dim3 blocks((unsigned)grid, count);
+    auto run = [&](bool first) {
+        const int ka = p[0].K, kb = p[count - 1].K;
+        if (ka == 32) linear_token_kernel<T, 32, 32><<<blocks, kScanThreads, 0, st>>>(a, first, status);
+        else if (ka == 64) linear_token_kernel<T, 64, 64><<<blocks, kScanThreads, 0, st>>>(a, first, status);
+        else if (kb == 64) linear_token_kernel<T, 128, 64><<<blocks, kScanThreads, 0, st>>>(a, first, status);
+        else linear_token_kernel<T, 128, 128><<<blocks, kScanThreads, 0, st>>>(a, first, status);
         return cudaGetLastError();
     };
     if (cut) {
-        const cudaError_t e = run(nullptr, slots);
+        const cudaError_t e = run(true);
         if (e != cudaSuccess) return e;
     }
-    return run(cut ? slots : nullptr, nullptr);
+    return run(false);
 }
 
 // ------------------------------------------------------------------ step
@@ -336,16 +383,17 @@ cudaError_t launch_step(const void *q, const void *k, const void *v, const float
     }
 }
 
-// Sums over the heads of a group, in their order.
+// Sums over the heads of a group, in their order, of one tensor or two.
 template <typename T>
-__global__ void __launch_bounds__(256) group_sum_kernel(const float *x, T *y, long long pieces,
-                                                        int group, int D) {
+__global__ void __launch_bounds__(256) group_sum_kernel(const float *x0, const float *x1, T *y0,
+                                                        T *y1, long long pieces, int group, int D) {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= pieces) return;
     const int per = D / 8;
     const long long row = i / per;
-    const float *src = x + row * group * D + (i - row * per) * 8;
+    const float *src = (blockIdx.y ? x1 : x0) + row * group * D + (i - row * per) * 8;
     float s[8] = {};
+#pragma unroll 2
     for (int g = 0; g < group; ++g) {
         Vec8<float> v;
         v.load(src + (long long)g * D);
@@ -354,41 +402,42 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float *x, T *y, lo
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += u[e];
     }
-    Vec8<T>::store(y + i * 8, s);
+    Vec8<T>::store((blockIdx.y ? y1 : y0) + i * 8, s);
 }
 
 }  // namespace
 
 // bf16 runs on the tensor cores where a tile fills them
-static bool on_tensor_cores(int K, int V, gdn_dtype dt) {
+bool linear_on_tensor_cores(int K, int V, gdn_dtype dt) {
     return dt == GDN_BF16 && K >= 64 && V >= 64;
 }
 
 size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt) {
-    const SegPlan plan = on_tensor_cores(K, V, dt) ? linear_tc_plan(B, T, H, K, V, packed)
-                                                   : token_plan(B, T, H, V, packed);
+    const SegPlan plan = linear_on_tensor_cores(K, V, dt) ? linear_tc_plan(B, T, H, K, V, packed)
+                                                          : token_plan(B, T, H, V, packed);
     return plan.items > B ? (size_t)plan.items * H * V * K * sizeof(float) : 0;
 }
 
-cudaError_t launch_linear_scan(const LinearScan &a, gdn_dtype dt, void *workspace,
+cudaError_t launch_linear_scan(const LinearScan *a, int count, gdn_dtype dt, void *workspace,
                                cudaStream_t stream) {
     float *slots = static_cast<float *>(workspace);
-    if (on_tensor_cores(a.K, a.V, dt)) return launch_linear_tc(a, slots, stream);
-    return dt == GDN_BF16 ? launch_token<__nv_bfloat16>(a, slots, stream)
-                          : launch_token<float>(a, slots, stream);
+    if (linear_on_tensor_cores(a->K, a->V, dt)) return launch_linear_tc(*a, slots, stream);
+    return dt == GDN_BF16 ? launch_token<__nv_bfloat16>(a, count, slots, stream)
+                          : launch_token<float>(a, count, slots, stream);
 }
 
-cudaError_t launch_group_sum(const float *x, void *y, long long rows, int Hq, int group, int D,
-                             gdn_dtype dt, cudaStream_t stream) {
+cudaError_t launch_group_sum(const float *x0, const float *x1, void *y0, void *y1, long long rows,
+                             int Hq, int group, int D, gdn_dtype dt, cudaStream_t stream) {
     const long long pieces = rows * Hq * (D / 8), grid = (pieces + 255) / 256;
     if (grid == 0) return cudaSuccess;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const dim3 blocks((unsigned)grid, x1 ? 2 : 1);
     if (dt == GDN_BF16)
-        group_sum_kernel<<<(unsigned)grid, 256, 0, stream>>>(x, static_cast<__nv_bfloat16 *>(y),
-                                                             pieces, group, D);
+        group_sum_kernel<<<blocks, 256, 0, stream>>>(x0, x1, static_cast<__nv_bfloat16 *>(y0),
+                                                     static_cast<__nv_bfloat16 *>(y1), pieces, group, D);
     else
-        group_sum_kernel<<<(unsigned)grid, 256, 0, stream>>>(x, static_cast<float *>(y), pieces,
-                                                             group, D);
+        group_sum_kernel<<<blocks, 256, 0, stream>>>(x0, x1, static_cast<float *>(y0),
+                                                     static_cast<float *>(y1), pieces, group, D);
     return cudaGetLastError();
 }
 
