@@ -20,9 +20,11 @@
 // chunks would be cut, not rounded, at every product).
 //
 // One CTA runs one segment of one (sequence, head), 20 warps in groups of 4:
-//   0-7   rows (two warps share 32 of them): P, from Q K^T in TMEM, weighted,
-//         back to TMEM as bf16 (over the columns that it came from) for the
-//         product with V; then O from TMEM, scaled, to shared memory (in K's
+//   0-3   P: row t of Q K^T from TMEM, weighted, back to TMEM as bf16 (over the
+//         columns that it came from) for the product with V.  (Eight warps that
+//         shared P's columns and then O's: gradients of B = 8, T = 4096, H = 16,
+//         128 x 128 in 273 us instead of 269.)
+//   4-7   O: row t from TMEM, scaled, to shared memory (in K's
 //         place) and out by TMA (ragged chunks: plain stores)
 //   8-15  state: two groups of 128 threads; each chunk's V in two halves of
 //         tokens, transposed, weighted and split: two pieces to TMEM, the
@@ -35,7 +37,7 @@
 //   17    issues the MMAs; 19 sends O
 // Launched with 96 registers a thread (5 groups x 128 threads x 96 = 61440);
 // the groups then share the same 480 registers a lane of the five as
-// 2 x 96 + 2 x 128 + 32 (K = 64: 2 x 96 + 2 x 112 + 64), with which nothing
+// 2 x 96 + 2 x 128 + 32 (K = 64: 2 x 104 + 2 x 96 + 80), with which nothing
 // spills: with some 20 registers of the rows spilled a chunk took half as long
 // again.
 // TMEM (512 columns): Q K^T and P 128 | O 128 | D 128 | V pieces 64 + 64.
@@ -51,7 +53,7 @@ namespace {
 constexpr int kC = 128;             // tokens of a chunk
 constexpr int kStages = 2;
 constexpr int kWarps = 20;
-constexpr int kBarRows = 1, kBarS = 2, kBarPair = 3;  // named barriers (kBarPair + 0 .. 3)
+constexpr int kBarP = 1, kBarS = 2;  // named barriers
 constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColHi = 384, kColMid = 448;
 
 template <int K, int V>
@@ -294,19 +296,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 mbar_init(&bar.used[s], 1);
                 mbar_init(&bar.sent[s], 1);
             }
-            mbar_init(&bar.staged, 8);
+            mbar_init(&bar.staged, 4);
             mbar_init(&bar.qfull, 1);
             mbar_init(&bar.qs, 1);
             mbar_init(&bar.d0, 1);
             mbar_init(&bar.dfree, 8);
             mbar_init(&bar.scores, 1);
-            mbar_init(&bar.p, 8);
+            mbar_init(&bar.p, 4);
             mbar_init(&bar.vw[0], 8);
             mbar_init(&bar.vw[1], 8);
             mbar_init(&bar.d, 1);
             mbar_init(&bar.s, 8);
             mbar_init(&bar.o, 1);
-            mbar_init(&bar.ofree, 8);
+            mbar_init(&bar.ofree, 4);
             mbar_init(&bar.tail, 8);
             abort_flag = 0;
             fence_mbar_init();
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
     if (warp < 8) {
         // ---------------------------------------------------------------- rows
-        // (keeps the 96 registers of the launch)
+        if constexpr (K == 64) reg_inc<104>();
         if (help) {
 #pragma unroll 1
             for (int i = 0; i < nc && updates(i); ++i) {
@@ -419,12 +421,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 arrive_warp(&bar.vw[1]);
             }
         }
-        if (want_o) {
-            const int t = (warp & 3) * 32 + lane, part = warp >> 2;
+        const int t = (warp & 3) * 32 + lane;
+        if (want_o && warp < 4) {
             // the powers within a block of 32 columns; a row's factor of the block
             // takes the rest of the lag
-            if (part == 0 && t < 32) colfac[t] = p.write_scale * exp2f((float)(rev ? t : 31 - t) * lg);
-            named_sync(kBarRows, 256);
+            if (t < 32) colfac[t] = p.write_scale * exp2f((float)(rev ? t : 31 - t) * lg);
+            named_sync(kBarP, 128);
 #pragma unroll 1
             for (int i = 0; i < nc; ++i) {
                 const int n = chunk_n(i), lead = chunk_lead(i);
@@ -432,27 +434,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const float lrho = fmaxf((float)pt * lg, -64.f);
                 wait_warp(&bar.scores, i);
                 tc_fence_after();
-                // P: this warp takes two blocks of 32 columns of its 32 rows.
-                // Rolled: twenty warps in their roles, unrolled, missed the
-                // instruction cache at every chunk (a quarter of all stalls).
+                // In blocks of 32 columns.  Rolled: twenty warps in their roles,
+                // unrolled, missed the instruction cache at every chunk (a quarter
+                // of all stalls).
 #pragma unroll 1
-                for (int b = 2 * part; b < 2 * part + 2; ++b) {
+                for (int b = 0; b < 4; ++b) {
                     uint32_t w[16];
-                    const int q = warp & 3;
-                    const bool blank = rev ? b < q : b > q;
+                    const bool blank = rev ? b < warp : b > warp;
                     float x[32];
                     // one power for the row and block: within the diagonal block
                     // it reaches a^-31, so that where a < 1/4 its scores are
                     // weighted one by one instead
-                    const bool each = b == q && lg < -2.f;
+                    const bool each = b == warp && lg < -2.f;
                     const int far = rev ? 32 * b - t : t - 32 * b - 31;
                     if (!blank) {
                         if (each) weigh_each(tmem + quad + kColP + 32 * b, rev ? far : far + 31, rev, lg, lrho);
                         tmem_ld32(tmem + quad + kColP + 32 * b, x);
                         tmem_ld_wait();
                     }
-                    // blocks 2 and 3 of P go over the scores' block 1
-                    if (b == 1 || b == 2) named_sync(kBarPair + q, 64);
                     if (blank) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) w[e] = 0;
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                             mul2(x[4 * e + 2], x[4 * e + 3], rf, rf);
                         }
                         pack_row(x, w);
-                        if (b == q) {  // the columns at or before this row, in scan order
+                        if (b == warp) {  // the columns at or before this row, in scan order
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 // 16 bits of a pair for each of its columns that counts
@@ -483,27 +482,31 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_warp(&bar.p);
-
-                // O: half of this row's columns
-                const float rho = p.read_scale * exp2f(lrho);
+            }
+        } else if (want_o) {
+#pragma unroll 1
+            for (int i = 0; i < nc; ++i) {
+                const int n = chunk_n(i);
+                const int pt = (rev ? n - 1 - t : t) + chunk_lead(i);
+                const float rho = p.read_scale * ex2(fmaxf((float)pt * lg, -64.f));
                 const bool whole = n == kC && !p.o_float;
-                constexpr int kCols = V / 2;  // of a warp
-                uint8_t *const stage = o_place(i) + part * (kC * 2 * kCols);
+                constexpr int kCols = V / 2;  // of a tile on its way out
+                uint8_t *const stage = o_place(i);
                 if (!o_in_k && i > 0) wait_warp(&bar.sent[(i - 1) % kStages], (i - 1) / kStages);
                 wait_warp(&bar.o, i);
                 tc_fence_after();
 #pragma unroll 1
-                for (int b = 0; b < kCols / 32; ++b) {
+                for (int b = 0; b < V / 32; ++b) {
                     float x[32];
-                    tmem_ld32(tmem + quad + kColO + part * kCols + 32 * b, x);
+                    tmem_ld32(tmem + quad + kColO + 32 * b, x);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) mul2(x[2 * e], x[2 * e + 1], rho, rho);
                     if (whole) {
-                        store_row_out<kCols>(stage, t, b, x);
+                        store_row_out<kCols>(stage + 32 * b / kCols * (kC * 2 * kCols), t, b % (kCols / 32), x);
                     } else if (t < n && !dead) {
                         const size_t at = ((size_t)(it.first + f0 + chunk_at(i) + t) * p.H + h) * V +
-                                          part * kCols + 32 * b;
+                                          32 * b;
                         if (p.o_float) {
                             float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at);
 #pragma unroll
@@ -528,7 +531,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- state
-        reg_inc<K == 128 ? 128 : 112>();
+        if constexpr (K == 128) reg_inc<128>();
         constexpr int NS = K / 2;
         const int g = (warp - 8) >> 2;
         const int v = (warp & 3) * 32 + lane;
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 dst[e] = make_float4(f * S[4 * e], f * S[4 * e + 1], f * S[4 * e + 2], f * S[4 * e + 3]);
         }
     } else {
-        reg_dec<K == 128 ? 32 : 64>();
+        reg_dec<K == 128 ? 32 : 80>();
         // ---------------------------------------------------------------- loads
         auto token_at = [&](int i) { return (p.offsets ? it.base : 0) + f0 + chunk_at(i); };
         const int c3 = p.offsets ? 0 : it.seq;
