@@ -14,11 +14,11 @@
 //     dx   = r (h - c r^2 x (x . h))
 //
 // Bound by memory: x read once and y written once (backward: x and dy read,
-// dx written).  A row of D channels is held by D / 8 lanes, two pieces of 4
+// dx written).  A row of D channels is held by D / 16 lanes, two pieces of 8
 // channels each, chosen so that a lane holds both channels of its pairs: only
 // the sums over a row are exchanged by shuffles.  (With 8 consecutive channels a
 // lane the half layout took 8 more shuffles a row, and the angles' reads met 8 a
-// bank: 160 us where this takes 93 for B = 8, T = 4096, 16 + 16 heads of
+// bank: 160 us where this takes 90 for B = 8, T = 4096, 16 + 16 heads of
 // 128 channels in bf16.)  A thread has the loads of several rows in flight
 // before it works on the first.
 //
@@ -29,7 +29,7 @@
 // position in wrapping integers is that fraction to pos 2^-56 turns.  (In
 // float32 an angle of 1e6 has lost 4 of its digits; in float64, at the 2 lanes
 // a clock of an SM here, the products took a third of the pass.)
-#include "gdn_internal.cuh"
+#include "gdn_vec8.cuh"
 
 namespace gdn {
 namespace {
@@ -37,11 +37,11 @@ namespace {
 constexpr int kThreads = 256;
 
 // CTAs of an SM, and rows in flight of a thread.  For B = 8, T = 4096, 16 + 16
-// heads of 128 channels in bf16: forward, 4 rows, 3 CTAs 93 us, 4 CTAs 103, 5 118
-// (3 CTAs of 3 or 8 rows: 100); backward, 4 rows, 2 CTAs 170 us, 3 CTAs 179, 1
-// CTA 262 (2 rows, 3 CTAs: 178).
-constexpr int norm_ctas(bool back, bool wide) { return back || wide ? 2 : 3; }
-constexpr int norm_rows(bool wide) { return wide ? 2 : 4; }
+// heads of 128 channels in bf16: forward, 2 CTAs of 4 rows 90 us, 3 CTAs 98 (2
+// rows: 100), 4 CTAs of 2 rows 98; backward, 2 CTAs of 2 rows 157 us (3 rows: 166,
+// 4: 200, spilled), 3 CTAs 160 (1 row) and 227.
+constexpr int kNormCtas = 2;
+constexpr int norm_rows(bool back, bool wide) { return (back ? 2 : 4) / (wide ? 2 : 1); }
 
 // One of q and k: its rows are taken by CTAs of its own, so that nothing is
 // chosen row by row (issue slots are what runs short beside memory).
@@ -70,38 +70,6 @@ template <int LPR> __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// Four consecutive values of the run dtype.
-template <typename T> struct Vec4;
-template <> struct Vec4<__nv_bfloat16> {
-    uint2 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-        a = __ldcs(reinterpret_cast<const uint2 *>(p));
-    }
-    __device__ __forceinline__ void get(float *x) const {
-        x[0] = __uint_as_float(a.x << 16);
-        x[1] = __uint_as_float(a.x & 0xffff0000u);
-        x[2] = __uint_as_float(a.y << 16);
-        x[3] = __uint_as_float(a.y & 0xffff0000u);
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[0], x[1]), c = __floats2bfloat162_rn(x[2], x[3]);
-        __stcs(reinterpret_cast<uint2 *>(p), make_uint2(*reinterpret_cast<const uint32_t *>(&b),
-                                                        *reinterpret_cast<const uint32_t *>(&c)));
-    }
-};
-template <> struct Vec4<float> {
-    float4 a;
-    __device__ __forceinline__ void load(const float *p) {
-        a = __ldcs(reinterpret_cast<const float4 *>(p));
-    }
-    __device__ __forceinline__ void get(float *x) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float *x) {
-        __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
-    }
-};
-
 // Packed float32 operations: a *= f, b *= g, and a = a f + c, b = b g + d.
 __device__ __forceinline__ void mul2(float &a, float &b, float f, float g) {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
@@ -115,12 +83,15 @@ __device__ __forceinline__ void fma2(float &a, float &b, float f, float g, float
         : "+f"(a), "+f"(b)
         : "f"(f), "f"(g), "f"(c), "f"(d));
 }
+// The two pieces of a lane's channels.
+__device__ __forceinline__ float (&lower(float (&x)[16]))[8] { return reinterpret_cast<float(&)[8]>(x[0]); }
+__device__ __forceinline__ float (&upper(float (&x)[16]))[8] { return reinterpret_cast<float(&)[8]>(x[8]); }
 // sum of x_i y_i
-__device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) {
+__device__ __forceinline__ float dot16(const float (&x)[16], const float (&y)[16]) {
     float s0 = x[0], s1 = x[1];
     mul2(s0, s1, y[0], y[1]);
 #pragma unroll
-    for (int i = 2; i < 8; i += 2) {
+    for (int i = 2; i < 16; i += 2) {
         float a = x[i], b = x[i + 1];
         fma2(a, b, y[i], y[i + 1], s0, s1);
         s0 = a;
@@ -129,43 +100,48 @@ __device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) 
     return s0 + s1;
 }
 
-// First channels of lane c's two pieces: of a half layout's rotated lanes 4 c
-// and R/2 + 4 c, else 8 c and 8 c + 4.
+// First channels of lane c's two pieces: of a half layout's rotated lanes 8 c
+// and R/2 + 8 c, else 16 c and 16 c + 8.
 template <bool HALF> __device__ __forceinline__ int piece_a(int c, int R) {
-    return HALF && 8 * c < R ? 4 * c : 8 * c;
+    return HALF && 16 * c < R ? 8 * c : 16 * c;
 }
 template <bool HALF> __device__ __forceinline__ int piece_b(int c, int R) {
-    return HALF && 8 * c < R ? (R >> 1) + 4 * c : 8 * c + 4;
+    return HALF && 16 * c < R ? (R >> 1) + 8 * c : 16 * c + 8;
 }
 
-// The lane's pairs turned by frequencies 4 c .. 4 c + 3 of `cs` (a token's
-// angles: 4 cosines and 4 sines a lane); BACK: turned back.
+// The lane's pairs turned by frequencies 8 c .. 8 c + 7 of `cs` (a token's
+// angles: cosines, then sines; of each the lanes' first four side by side, then
+// their last four); BACK: turned back.
 template <bool HALF, bool BACK>
-__device__ __forceinline__ void rotate8(float (&x)[8], const float4 *cs, int R, int c) {
-    if (8 * c >= R) return;
-    const float4 u = cs[c], v = cs[(R >> 3) + c];
-    const float co[4] = {u.x, u.y, u.z, u.w};
-    float si[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (BACK) {
+__device__ __forceinline__ void rotate16(float (&x)[16], const float4 *cs, int R, int c) {
+    if (16 * c >= R) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) si[i] = -si[i];
-    }
-    if constexpr (HALF) {
+    for (int j = 0; j < 2; ++j) {
+        const float4 u = cs[j * (R >> 4) + c], v = cs[(R >> 3) + j * (R >> 4) + c];
+        const float co[4] = {u.x, u.y, u.z, u.w};
+        float si[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (BACK) {
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            float a0 = x[i], a1 = x[i + 1];
-            float t0 = -x[4 + i], t1 = -x[5 + i];
-            mul2(t0, t1, si[i], si[i + 1]);
-            fma2(x[i], x[i + 1], co[i], co[i + 1], t0, t1);
-            mul2(a0, a1, si[i], si[i + 1]);
-            fma2(x[4 + i], x[5 + i], co[i], co[i + 1], a0, a1);
+            for (int i = 0; i < 4; ++i) si[i] = -si[i];
         }
-    } else {
+        if constexpr (HALF) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = fmaf(a, co[i], -b * si[i]);
-            x[2 * i + 1] = fmaf(a, si[i], b * co[i]);
+            for (int i = 0; i < 4; i += 2) {
+                const int a = 4 * j + i, b = 8 + a;
+                float a0 = x[a], a1 = x[a + 1];
+                float t0 = -x[b], t1 = -x[b + 1];
+                mul2(t0, t1, si[i], si[i + 1]);
+                fma2(x[a], x[a + 1], co[i], co[i + 1], t0, t1);
+                mul2(a0, a1, si[i], si[i + 1]);
+                fma2(x[b], x[b + 1], co[i], co[i + 1], a0, a1);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[8 * j + 2 * i], b = x[8 * j + 2 * i + 1];
+                x[8 * j + 2 * i] = fmaf(a, co[i], -b * si[i]);
+                x[8 * j + 2 * i + 1] = fmaf(a, si[i], b * co[i]);
+            }
         }
     }
 }
@@ -188,19 +164,20 @@ __device__ __forceinline__ void fill_angles(float *cs, const unsigned long long 
         const unsigned long long x = (unsigned long long)p.pos[t0 + t] * turns[f];
         float s, c;
         sincospif((float)(int)(x >> 32) * 0x1p-31f, &s, &c);
-        cs[2 * t * half + f] = c;
-        cs[(2 * t + 1) * half + f] = s;
+        const int at = ((f >> 2) & 1) * (half >> 1) + (f >> 3) * 4 + (f & 3);
+        cs[2 * t * half + at] = c;
+        cs[(2 * t + 1) * half + at] = s;
     }
 }
 
 // A CTA takes tiles of some tokens with all heads of q or of k, a lane group of
-// D / 8 lanes U rows at a time.
+// D / 16 lanes U rows at a time.
 template <typename T, int D, bool HALF, bool BACK>
-__global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
+__global__ void __launch_bounds__(kThreads, kNormCtas)
     qk_norm_kernel(const QkNormArgs p, float c_norm) {
-    constexpr int LPR = D / 8;             // lanes of a row
+    constexpr int LPR = D / 16;            // lanes of a row
     constexpr int ROWS = kThreads / LPR;   // rows at a time
-    constexpr int U = norm_rows(sizeof(T) == 4);
+    constexpr int U = norm_rows(BACK, sizeof(T) == 4);
     extern __shared__ __align__(16) unsigned long long turns[];
     float *const cs2 = reinterpret_cast<float *>(turns + (p.R >> 1));  // two tiles
     const bool isk = (int)blockIdx.x >= p.first;
@@ -214,10 +191,10 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
     const int ab = pb - pa;
     const long long ld = sd.ld;
     const int ldy = heads * D;
-    float w[8], dw[8];
+    float w[16], dw[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[i] = sd.w ? sd.w[i < 4 ? pa + i : pb + i - 4] : 1.f;
+    for (int i = 0; i < 16; ++i) {
+        w[i] = sd.w ? sd.w[i < 8 ? pa + i : pb + i - 8] : 1.f;
         dw[i] = 0.f;
     }
     auto token_of = [&](int r) { return magic ? (int)__umulhi((unsigned)r, magic) : r; };
@@ -225,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
     __syncthreads();
     const long long tile0 = (long long)(isk ? blockIdx.x - p.first : blockIdx.x) * TT;
     const long long step = (long long)(isk ? gridDim.x - p.first : p.first) * TT;
-    Vec4<T> xa[U], xb[U], ga[BACK ? U : 1], gb[BACK ? U : 1];
+    Vec8<T> xa[U], xb[U], ga[BACK ? U : 1], gb[BACK ? U : 1];
     // row u of the batch from row r0 of the tile of tokens t0 ..
     auto fetch = [&](int u, long long t0, int r0) {
         const int r = r0 + u * ROWS + gi;
@@ -257,31 +234,31 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
                 const int r = r0 + u * ROWS + gi;
                 const bool live = r < rows;
                 const int t = live ? token_of(r) : 0;
-                float x[8] = {}, g[8] = {};
+                float x[16] = {}, g[16] = {};
                 if (live) {
-                    xa[u].get(x);
-                    xb[u].get(x + 4);
+                    xa[u].get(lower(x));
+                    xb[u].get(upper(x));
                     if constexpr (BACK) {
-                        ga[u].get(g);
-                        gb[u].get(g + 4);
+                        ga[u].get(lower(g));
+                        gb[u].get(upper(g));
                     }
                 }
                 // its place is free: the next batch's row, of the next tile at the end
                 fetch(u, more ? t0 : t0 + step, more ? r0 + U * ROWS : 0);
-                const float ss = row_sum<LPR>(dot8(x, x));
+                const float ss = row_sum<LPR>(dot16(x, x));
                 const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
                 const float4 *ct = reinterpret_cast<const float4 *>(cs + t * p.R);
                 if constexpr (!BACK) {
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         mul2(x[i], x[i + 1], rn, rn);
                         mul2(x[i], x[i + 1], w[i], w[i + 1]);
                     }
-                    rotate8<HALF, false>(x, ct, p.R, c);
+                    rotate16<HALF, false>(x, ct, p.R, c);
                 } else {
-                    rotate8<HALF, true>(g, ct, p.R, c);
+                    rotate16<HALF, true>(g, ct, p.R, c);
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         float d0 = x[i], d1 = x[i + 1];
                         mul2(d0, d1, rn, rn);
                         fma2(d0, d1, g[i], g[i + 1], dw[i], dw[i + 1]);
@@ -289,17 +266,17 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
                         dw[i + 1] = d1;
                         mul2(g[i], g[i + 1], w[i], w[i + 1]);
                     }
-                    const float f = -row_sum<LPR>(dot8(x, g)) * c_norm * rn * rn;
+                    const float f = -row_sum<LPR>(dot16(x, g)) * c_norm * rn * rn;
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         fma2(x[i], x[i + 1], f, f, g[i], g[i + 1]);
                         mul2(x[i], x[i + 1], rn, rn);
                     }
                 }
                 if (live) {
                     T *y = dst + (t0 * ldy + r * D);
-                    Vec4<T>::store(y, x);
-                    Vec4<T>::store(y + ab, x + 4);
+                    Vec8<T>::store(y, lower(x));
+                    Vec8<T>::store(y + ab, upper(x));
                 }
             }
         }
@@ -310,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, norm_ctas(BACK, sizeof(T) == 4))
         float *red = cs2;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) red[gi * D + (i < 4 ? pa + i : pb + i - 4)] = dw[i];
+        for (int i = 0; i < 16; ++i) red[gi * D + (i < 8 ? pa + i : pb + i - 8)] = dw[i];
         __syncthreads();
         for (int d = threadIdx.x; d < D; d += kThreads) {
             float s = 0.f;
@@ -347,7 +324,7 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float *partial, 
 int tile_tokens(int heads, int D) {
     // about 8 rows a lane group: the angles of a tile then cost one sincospi
     // or two a thread next to 8 rows of work (at most 2 x 16 KB of angles)
-    const int tokens = heads ? 8 * kThreads / (D / 8) / heads : 1, most = 4096 / D;
+    const int tokens = heads ? 8 * kThreads / (D / 16) / heads : 1, most = 4096 / D;
     return tokens < 1 ? 1 : (tokens > most ? most : tokens);
 }
 
@@ -355,10 +332,10 @@ int tile_tokens(int heads, int D) {
 struct NormGrid {
     int first, all;
 };
-NormGrid norm_grid(long long N, int Hq, int Hk, int D, int per_sm) {
+NormGrid norm_grid(long long N, int Hq, int Hk, int D) {
     const long long tq = Hq ? (N + tile_tokens(Hq, D) - 1) / tile_tokens(Hq, D) : 0;
     const long long tk = Hk ? (N + tile_tokens(Hk, D) - 1) / tile_tokens(Hk, D) : 0;
-    const long long most = (long long)per_sm * (sm_count() > 0 ? sm_count() : 152);
+    const long long most = (long long)kNormCtas * (sm_count() > 0 ? sm_count() : 152);
     if (tq + tk <= most) return {(int)tq, (int)(tq + tk)};
     long long q = (most * Hq + (Hq + Hk) / 2) / (Hq + Hk);
     q = Hq && q < 1 ? 1 : Hk && q > most - 1 ? most - 1 : q;
@@ -384,7 +361,7 @@ cudaError_t launch_any(const QkNormArgs &p, int D, float c, bool half, gdn_dtype
                        cudaStream_t st) {
     const int tokens = p.side[0].tokens > p.side[1].tokens ? p.side[0].tokens : p.side[1].tokens;
     size_t smem = (size_t)2 * tokens * p.R * sizeof(float);
-    if (BACK && smem < kThreads * 8 * sizeof(float)) smem = kThreads * 8 * sizeof(float);
+    if (BACK && smem < kThreads * 16 * sizeof(float)) smem = kThreads * 16 * sizeof(float);
     smem += (p.R / 2) * sizeof(unsigned long long);
     if (dt == GDN_BF16)
         return half ? launch_d<__nv_bfloat16, true, BACK>(p, D, c, grid, smem, st)
@@ -400,16 +377,15 @@ QkSide side(const void *x, const void *dy, const float *w, void *y, long long ld
 
 }  // namespace
 
-// (as many partial sums as the most CTAs that either type runs with)
 int qk_norm_backward_grid(long long N, int Hq, int Hk, int D) {
-    return norm_grid(N, Hq, Hk, D, norm_ctas(true, false)).all;
+    return norm_grid(N, Hq, Hk, D).all;
 }
 
 cudaError_t launch_qk_norm(const void *q, const void *k, const float *wq, const float *wk,
                            const long long *pos, const float *inv_freq, void *yq, void *yk,
                            long long N, int Hq, int Hk, int D, int R, long long ldq, long long ldk,
                            bool l2, bool half, float eps, gdn_dtype dt, cudaStream_t st) {
-    const NormGrid g = norm_grid(N, Hq, Hk, D, norm_ctas(false, dt != GDN_BF16));
+    const NormGrid g = norm_grid(N, Hq, Hk, D);
     const QkNormArgs p = {{side(q, nullptr, wq, yq, ldq, Hq, D), side(k, nullptr, wk, yk, ldk, Hk, D)},
                           g.first, pos, inv_freq, nullptr, N, R, eps};
     return launch_any<false>(p, D, l2 ? 1.f : 1.f / D, half, dt, g.all, st);
@@ -422,7 +398,7 @@ cudaError_t launch_qk_norm_backward(const void *q, const void *k, const float *w
                                     int R, long long ldq, long long ldk, bool l2, bool half,
                                     float eps, gdn_dtype dt, float *partial, cudaStream_t st) {
     const bool want = dwq || dwk;
-    const NormGrid g = norm_grid(N, Hq, Hk, D, norm_ctas(true, dt != GDN_BF16));
+    const NormGrid g = norm_grid(N, Hq, Hk, D);
     const QkNormArgs p = {{side(q, dyq, wq, dq, ldq, Hq, D), side(k, dyk, wk, dk, ldk, Hk, D)},
                           g.first, pos, inv_freq, want ? partial : nullptr, N, R, eps};
     const cudaError_t e = launch_any<true>(p, D, l2 ? 1.f : 1.f / D, half, dt, g.all, st);
