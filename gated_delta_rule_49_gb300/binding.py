@@ -628,16 +628,17 @@ def _token_stride(where, name, x, dtype, device):
     st = x.stride()
     if st[-1] != 1 or (st[-2] != D and heads > 1):
         _reject(where, f"{name}'s heads and channels are not dense (strides {st})")
-    step, span = 0, 1  # of the tokens seen so far, innermost first
+    step, span = None, 1  # of the tokens seen so far, innermost first
     for n, s in zip(reversed(x.shape[:-2]), reversed(st[:-2])):
         if n == 1:
             continue
-        if not step:
+        if step is None:
             step = s
-        elif s != step * span:
-            _reject(where, f"{name}'s tokens do not lie evenly (strides {st})")
+        # a step of 0 (a broadcast) or of less than a token has no memory of its own for each
+        if s != step * span or step < heads * D:
+            _reject(where, f"{name}'s tokens do not lie evenly, a whole token apart (strides {st})")
         span *= n
-    return step or heads * D
+    return heads * D if step is None else step
 
 
 def _dense(where, name, x, dtype, device, shape):
