@@ -523,9 +523,10 @@ GDN_API int gdn_qk_norm_rotate_backward(const void *q, const void *k, const floa
  *   S_T   [B, H, V, K] float32, or NULL; may be S0
  *   offsets  NULL, or [B + 1] int32 on the device: the B sequences lie packed
  *         in T tokens, sequence b in [offsets[b], offsets[b + 1]) (an empty one
- *         has S_T = S0).  Offsets that do not rise, or pass T, make that
- *         sequence empty and set GDN_ERR_DEVICE_BOUNDS; tokens of no sequence
- *         keep what o held.
+ *         has S_T = S0).  A sequence whose offsets fall, pass T, or start
+ *         before the end of an earlier one (of those that neither fall nor
+ *         pass T) is taken for empty, and GDN_ERR_DEVICE_BOUNDS is set; tokens
+ *         of no sequence keep what o held.
  *
  * (K, V) in (32, 32), (64, 64), (64, 128), (128, 128).  A value that is not
  * finite reaches the outputs of its own sequence only, where it gives infinities
