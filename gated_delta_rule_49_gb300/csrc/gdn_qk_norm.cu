@@ -246,7 +246,9 @@ __global__ void __launch_bounds__(kThreads, kNormCtas)
                 // its place is free: the next batch's row, of the next tile at the end
                 fetch(u, more ? t0 : t0 + step, more ? r0 + U * ROWS : 0);
                 const float ss = row_sum<LPR>(dot16(x, x));
-                const float rn = rsqrtf(fmaf(c_norm, ss, p.eps));
+                // a lane group without a row has no norm: with eps = 0 it would be infinite,
+                // and 0 times it would reach the weights' gradient
+                const float rn = !BACK || live ? rsqrtf(fmaf(c_norm, ss, p.eps)) : 0.f;
                 const float4 *ct = reinterpret_cast<const float4 *>(cs + t * p.R);
                 if constexpr (!BACK) {
 #pragma unroll
