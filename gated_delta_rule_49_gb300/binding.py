@@ -210,6 +210,45 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+# A call may be given another stream than torch's current one, where torch's
+# allocator takes memory that is let go of for free at once: scratch memory comes
+# from the other stream's pool, and new outputs, which belong to the caller's
+# stream, are kept until the other stream is done with them.
+
+def _other_stream(stream):
+    """The torch stream of `stream` where it is not the current one, else None."""
+    if stream is None:
+        return None
+    handle = _stream(stream)
+    if handle == _stream(None):
+        return None
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _scratch(need, device, stream):
+    """`need` bytes of device memory for a call on the stream; None for 0."""
+    if not need:
+        return None
+    import torch
+    other = _other_stream(stream)
+    if other is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(other):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _written_on(stream, *new):
+    """Keeps what a call on the stream writes to (tensors or None) until it is written."""
+    other = _other_stream(stream)
+    if other is not None:
+        for x in new:
+            if x is not None:
+                x.record_stream(other)
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.bfloat16:
@@ -314,9 +353,10 @@ def prefill_gated_chunked(q, k, v, alpha, beta=None, b=None, w=None, S0=None, ga
     ST = torch.empty((B, H, V, K), dtype=torch.float32, device=v.device) if want_state else None
     need = gdn_prefill_gated_chunked_workspace_size(B, T, H, K, V, GATES[gate], _dtype_code(v))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=v.device)
+        workspace = _scratch(max(need, 1), v.device, stream)
     gdn_prefill_gated_chunked(q, k, v, alpha, beta, b, w, S0, o, ST, B, T, H, K, V, GATES[gate],
                               _dtype_code(v), workspace, workspace.numel(), stream)
+    _written_on(stream, o, ST)
     return o, ST
 
 
@@ -340,6 +380,7 @@ def prefill_gated(q, k, v, alpha, beta=None, b=None, w=None, S0=None, gate="kda"
     ST = torch.empty((B, H, V, K), dtype=torch.float32, device=v.device) if want_state else None
     gdn_prefill_gated(q, k, v, alpha, beta, b, w, S0, o, ST, B, T, H, K, V, GATES[gate],
                       _dtype_code(v), stream)
+    _written_on(stream, o, ST)
     return o, ST
 
 
@@ -367,6 +408,7 @@ def state_truncate(S, r, want_sigma=False, max_sweeps=30, stream=None):
     sigma = (torch.empty(S.shape[:-2] + (min(V, K),), dtype=torch.float32, device=S.device)
              if want_sigma else None)
     gdn_state_truncate(S, BH, V, K, r, sigma, max_sweeps, stream)
+    _written_on(stream, sigma)
     return sigma
 
 
@@ -381,9 +423,10 @@ def prefill_truncated(q, k, v, alpha, beta, S0=None, seg_len=256, r=32, max_swee
     dt = _dtype_code(v)
     L = min(seg_len, T) if T > 0 else 0
     need = max([gdn_prefill_workspace_size(B, n, H, K, V, dt) for n in (L, T % seg_len) if n] + [0])
-    ws = torch.empty(need, dtype=torch.uint8, device=v.device) if need else None
+    ws = _scratch(need, v.device, stream)
     gdn_prefill_truncated(q, k, v, alpha, beta, S0, o, ST, B, T, H, K, V, dt, seg_len, r,
                           max_sweeps, ws, need, stream)
+    _written_on(stream, o, ST)
     return o, ST
 
 
@@ -411,8 +454,9 @@ def channel_gram(k, q, stream=None):
     B, T, H, K = k.shape
     G = torch.empty((H, K, K), dtype=torch.float32, device=k.device)
     need = gdn_channel_gram_workspace_size(B, T, H, K)
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=k.device)
+    ws = _scratch(max(need, 1), k.device, stream)
     gdn_channel_gram(k, q, B, T, H, K, _dtype_code(k), G, ws, need, stream)
+    _written_on(stream, G)
     return G
 
 
@@ -425,6 +469,7 @@ def drrqr_select(G, k, f=2.0, max_swaps=1000, stream=None):
     rho = torch.empty(H, dtype=torch.float32, device=G.device)
     sw = torch.empty(H, dtype=torch.int32, device=G.device)
     gdn_drrqr_select(G, H, n, k, f, max_swaps, idx, rho, sw, stream)
+    _written_on(stream, idx, rho, sw)
     return idx, rho, sw
 
 
@@ -466,9 +511,10 @@ def prefill_gathered(q_full, k_full, idx, v, alpha, beta, S0=None, want_o=True, 
     o = torch.empty((B, T, H, V), dtype=v.dtype, device=v.device) if want_o else None
     ST = torch.empty((B, H, V, K), dtype=torch.float32, device=v.device) if want_state else None
     need = gdn_prefill_gathered_workspace_size(B, T, H, K_in, K, V, dt)
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=v.device)
+    ws = _scratch(max(need, 1), v.device, stream)
     gdn_prefill_gathered(q_full, k_full, idx, K_in, v, alpha, beta, S0, o, ST, B, T, H, K, V, dt,
                          ws, need, stream)
+    _written_on(stream, o, ST)
     return o, ST
 
 
@@ -481,6 +527,7 @@ def gather_normalize(x, idx, stream=None):
     N = x.numel() // (H * K_in)
     y = torch.empty(x.shape[:-1] + (K_out,), dtype=x.dtype, device=x.device)
     gdn_gather_normalize(x, idx, y, N, H, K_in, K_out, _dtype_code(x), stream)
+    _written_on(stream, y)
     return y
 
 
@@ -580,8 +627,9 @@ def prefill(q, k, v, alpha, beta, S0=None, want_o=True, want_state=True, out_sta
     ws_bytes = gdn_prefill_workspace_size(B, T, H, K, V, dt)
     if two_pass:
         ws_bytes = max(ws_bytes, gdn_prefill_two_pass_workspace_size(B, T, H, K, V, dt))
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=k.device) if ws_bytes else None
+    ws = _scratch(ws_bytes, k.device, stream)
     gdn_prefill(q, k, v, alpha, beta, S0, o, ST, B, T, H, K, V, dt, ws, ws_bytes, stream)
+    _written_on(stream, o, None if ST is out_state else ST)
     return o, ST
 
 
@@ -591,9 +639,12 @@ def decode_step(q, k, v, alpha, beta, S, o=None, stream=None):
     import torch
     B, H, K = k.shape
     V = v.shape[-1]
+    given = o
     if o is None:
         o = torch.empty((B, H, V), dtype=k.dtype, device=k.device)
     gdn_decode_step(q, k, v, alpha, beta, S, o, B, H, K, V, _dtype_code(k), stream)
+    if given is None:
+        _written_on(stream, o)
     return o
 
 
@@ -607,6 +658,7 @@ def state_rank(S, max_iter=500, tol=1e-7, stream=None):
         BH *= d
     outs = [torch.empty(lead, dtype=torch.float32, device=S.device) for _ in range(3)]
     gdn_state_rank(S, BH, V, K, *outs, max_iter=max_iter, tol=tol, stream=stream)
+    _written_on(stream, *outs)
     return tuple(outs)
 
 
@@ -649,14 +701,11 @@ def _dense(where, name, x, dtype, device, shape):
                        f"device {device}; it is {x.dtype}, {tuple(x.shape)} on {x.device}")
 
 
-def _workspace(given, need, like):
+def _workspace(given, need, like, stream):
     """(workspace, its bytes): the one given, or a new one where one is needed."""
     if given is not None:
         return given, given.numel() * given.element_size()
-    if not need:
-        return None, 0
-    import torch
-    return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    return _scratch(need, like.device, stream), need
 
 
 def _qk_norm_args(where, q, k, pos, inv_freq, wq, wk, norm, pairing):
@@ -709,6 +758,8 @@ def qk_norm_rotate(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms", 
             _dense(where, "out[1]", yk, q.dtype, q.get_device(), k.shape)
     gdn_qk_norm_rotate(q, k, wq, wk, pos, inv_freq, yq, yk, N, Hq, Hk, D, R, ldq, ldk, nrm, pair,
                        eps, _dtype_code(q), stream)
+    if out is None:
+        _written_on(stream, yq, yk)
     return yq, yk
 
 
@@ -729,10 +780,11 @@ def qk_norm_rotate_backward(q, k, pos, inv_freq, dyq, dyk, wq=None, wk=None, nor
     need = 0
     if wq is not None or wk is not None:
         need = gdn_qk_norm_rotate_backward_workspace_size(N, Hq, Hk, D)
-    workspace, need = _workspace(workspace, need, q)
+    workspace, need = _workspace(workspace, need, q, stream)
     gdn_qk_norm_rotate_backward(q, k, wq, wk, pos, inv_freq, dyq, dyk, dq, dk, dwq, dwk, N, Hq, Hk,
                                 D, R, ldq, ldk, nrm, pair, eps, _dtype_code(q), workspace, need,
                                 stream)
+    _written_on(stream, dq, dk, dwq, dwk)
     return dq, dk, dwq, dwk
 
 
@@ -781,9 +833,10 @@ def linear_prefill(q, k, v, alpha, S0=None, scale=1.0, offsets=None, want_o=True
     if want_state and ST is None:
         ST = torch.empty(shape, dtype=torch.float32, device=v.device)
     workspace, need = _workspace(workspace, gdn_linear_prefill_workspace_size(
-        B, T, H, K, V, offsets is not None, dt), v)
+        B, T, H, K, V, offsets is not None, dt), v, stream)
     gdn_linear_prefill(q, k, v, alpha, S0, o, ST, offsets, B, T, Hq, H, K, V, ldq, ldk, ldv, scale,
                        dt, workspace, need, stream)
+    _written_on(stream, o, None if ST is out_state else ST)
     return o, ST
 
 
@@ -805,9 +858,10 @@ def linear_backward(q, k, v, alpha, do, S0=None, dS_T=None, scale=1.0, offsets=N
     if want_dS0 or (want_dS0 is None and S0 is not None):
         dS0 = torch.empty(shape, dtype=torch.float32, device=v.device)
     workspace, need = _workspace(workspace, gdn_linear_backward_workspace_size(
-        B, T, Hq, H, K, V, offsets is not None, dt), v)
+        B, T, Hq, H, K, V, offsets is not None, dt), v, stream)
     gdn_linear_backward(q, k, v, alpha, do, S0, dS_T, dq, dk, dv, dS0, offsets, B, T, Hq, H, K, V,
                         ldq, ldk, ldv, scale, dt, workspace, need, stream)
+    _written_on(stream, dq, dk, dv, dS0)
     return dq, dk, dv, dS0
 
 
@@ -824,6 +878,7 @@ def linear_decode_step(q, k, v, alpha, S, scale=1.0, S_out=None, o=None, stream=
     dt, dev, shape = v.dtype, v.get_device(), (B, H, V, K)
     if S_out is None:
         S_out = S
+    given = o
     if o is None:
         o = torch.empty_like(v)
     _dense(where, "q", q, dt, dev, qs)
@@ -835,4 +890,6 @@ def linear_decode_step(q, k, v, alpha, S, scale=1.0, S_out=None, o=None, stream=
     _dense(where, "S_out", S_out, torch.float32, dev, shape)
     gdn_linear_decode_step(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale, _dtype_code(v),
                            stream)
+    if given is None:
+        _written_on(stream, o)
     return o
