@@ -104,11 +104,11 @@ __device__ __forceinline__ void token_scan(const LinearScan &p, const SegPlan &p
                           : 0.f;
     if (slots_in) {
         if (p.S0) add_slot(it.slot0 + (p.reverse ? 0 : it.n - 1),
-                           exp2f((float)start_steps(it, plan.seg_len, p.reverse) * lg));
+                           decay_power(start_steps(it, plan.seg_len, p.reverse), lg));
 #pragma unroll 4
         for (int i = p.reverse ? it.j + 1 : 0; i < (p.reverse ? it.n : it.j); ++i)
             add_slot(it.slot0 + i,
-                     exp2f((float)tokens_between(i, it.j, it.len, plan.seg_len, p.reverse) * lg));
+                     decay_power(tokens_between(i, it.j, it.len, plan.seg_len, p.reverse), lg));
     }
     const T *qp = static_cast<const T *>(p.q) + (long long)hq * K;
     const T *kp = static_cast<const T *>(p.k) + (long long)hk * K;

@@ -34,7 +34,15 @@ struct SegPlan {
 
 // log2 of a decay; 0 becomes a number whose multiples exp2 takes to 0 while
 // 0 times it stays 0 (a^0 = 1).
-__device__ __forceinline__ float decay_log2(float a) { return fmaxf(log2f(a), -1e30f); }
+// A decay that is not a number stays one.
+__device__ __forceinline__ float decay_log2(float a) {
+    const float x = log2f(a);
+    return x < -1e30f ? -1e30f : x;
+}
+// a^n from its log2; a^0 = 1 whatever a is.
+__device__ __forceinline__ float decay_power(int n, float lg) {
+    return n == 0 ? 1.f : exp2f((float)n * lg);
+}
 
 // Tokens between the end of segment i and the start (in scan order) of
 // segment j of a sequence, i before j in scan order.

@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
             for (int e = 0; e < NS; ++e) S[e] = 0.f;
             if (p.S0) {
-                const float f = exp2f((float)start_steps(it, arg.plan.seg_len, rev) * lg);
+                const float f = decay_power(start_steps(it, arg.plan.seg_len, rev), lg);
                 if (arg.slots_in) {
                     const float4 *src = reinterpret_cast<const float4 *>(
                         arg.slots_in + (((size_t)(it.slot0 + (rev ? 0 : it.n - 1)) * p.H + h) * V + v) * K + k0);
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             if (arg.slots_in) {
                 for (int j = rev ? it.j + 1 : 0; j < (rev ? it.n : it.j); ++j) {
                     const int gap = tokens_between(j, it.j, it.len, arg.plan.seg_len, rev);
-                    const float f = exp2f((float)gap * lg);
+                    const float f = decay_power(gap, lg);
                     const float4 *src = reinterpret_cast<const float4 *>(
                         arg.slots_in + (((size_t)(it.slot0 + j) * p.H + h) * V + v) * K + k0);
 #pragma unroll
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 arrive_warp(&bar.vw[c]);
             }
             if (c == 0 && i > 0 && updates(i - 1)) {
-                const float ac = exp2f((float)(chunk_n(i - 1) + chunk_lead(i - 1) - 1) * lg);
+                const float ac = decay_power(chunk_n(i - 1) + chunk_lead(i - 1) - 1, lg);
                 wait_warp(&bar.d, i - 1);
                 tc_fence_after();
                 if (mine) {

@@ -1,5 +1,5 @@
 """Edges of linear attention on the GPU: bad offsets of batches that are cut into
-segments."""
+segments, decays that are not a number."""
 import pytest
 from test_gpu_linear import Problem, clean_status, torch  # noqa: F401
 
@@ -35,3 +35,43 @@ def test_bad_offsets_of_sequences_that_are_cut(torch, K, V, dtype):  # noqa: F81
     for i, start in ((1, p.S0), (5, p.dST)):
         for s in range(4):
             assert torch.equal(got[i][s], start[s] if s in (1, 2) else want[i][s])
+
+
+WIDTHS = [("bf16", 128, 128), ("bf16", 64, 64), ("bf16", 64, 128), ("bf16", 32, 32),
+          ("fp32", 64, 128)]
+
+
+@pytest.mark.parametrize("dtype,K,V", WIDTHS)
+@pytest.mark.parametrize("T", [5, 300, 3000])
+def test_a_decay_that_is_not_a_number(torch, K, V, dtype, T):  # noqa: F811
+    """Its head has no number left, the others keep their bits."""
+    from gated_delta_rule_49_gb300 import binding
+    for start in (True, False):
+        p = Problem(torch, 14, 1, T, 3, 3, K, V, dtype, start)
+        clean = binding.linear_prefill(p.q, p.k, p.v, p.a, p.S0) + binding.linear_backward(
+            p.q, p.k, p.v, p.a, p.do, p.S0, p.dST, want_dS0=True)
+        p.a[1] = float("nan")
+        got = binding.linear_prefill(p.q, p.k, p.v, p.a, p.S0) + binding.linear_backward(
+            p.q, p.k, p.v, p.a, p.do, p.S0, p.dST, want_dS0=True)
+        for i, (a, b) in enumerate(zip(clean, got)):
+            heads = 1 if i in (1, 5) else 2  # states, tokens
+            for h in (0, 2):
+                assert torch.equal(a.select(heads, h), b.select(heads, h))
+            bad = b.select(heads, 1)
+            # the last token's gradients of k and v come before any decay
+            assert (bad[:, :-1] if i in (3, 4) else bad).isnan().all(), i
+        x = [y[:, 0].contiguous() for y in (p.q, p.k, p.v)]
+        if start:
+            S = p.S0.clone()
+            o = binding.linear_decode_step(*x, p.a, S)
+            assert o[:, 1].isnan().all() and S[:, 1].isnan().all() and S[:, 0].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,K,V", WIDTHS)
+def test_empty_sequences_keep_their_states_at_any_decay(torch, K, V, dtype):  # noqa: F811
+    from gated_delta_rule_49_gb300 import binding
+    p = Problem(torch, 15, 0, 0, 2, 2, K, V, dtype, True, [3000, 0, 40])
+    p.a[0] = float("nan")
+    _, S = binding.linear_prefill(p.q, p.k, p.v, p.a, p.S0, offsets=p.offsets)
+    dS0 = binding.linear_backward(p.q, p.k, p.v, p.a, p.do, p.S0, p.dST, offsets=p.offsets)[3]
+    assert torch.equal(S[1], p.S0[1]) and torch.equal(dS0[1], p.dST[1])
