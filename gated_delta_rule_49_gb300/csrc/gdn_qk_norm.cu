@@ -146,12 +146,13 @@ __device__ __forceinline__ void rotate16(float (&x)[16], const float4 *cs, int R
     }
 }
 
-// The frequencies in turns, 2^64 a turn.
+// The frequencies in turns, 2^64 a turn; the lowest bit, else 0, says that one
+// is not finite.
 __device__ __forceinline__ void fill_turns(unsigned long long *turns, const QkNormArgs &p) {
     for (int f = threadIdx.x; f < (p.R >> 1); f += kThreads) {
         double x = (double)p.inv_freq[f] * 0.15915494309189533577;
-        x -= floor(x);  // [0, 1)
-        turns[f] = (unsigned long long)(x * 9223372036854775808.0) << 1;
+        x -= floor(x);  // [0, 1), or NaN
+        turns[f] = x == x ? (unsigned long long)(x * 9223372036854775808.0) << 1 : 1;
     }
 }
 
@@ -164,6 +165,7 @@ __device__ __forceinline__ void fill_angles(float *cs, const unsigned long long 
         const unsigned long long x = (unsigned long long)p.pos[t0 + t] * turns[f];
         float s, c;
         sincospif((float)(int)(x >> 32) * 0x1p-31f, &s, &c);
+        if (turns[f] & 1) s = c = __int_as_float(0x7fffffff);
         const int at = ((f >> 2) & 1) * (half >> 1) + (f >> 3) * 4 + (f & 3);
         cs[2 * t * half + at] = c;
         cs[(2 * t + 1) * half + at] = s;

@@ -1,4 +1,5 @@
-"""Edges of the norm with rotation on the GPU: no eps."""
+"""Edges of the norm with rotation on the GPU: no eps, frequencies that are not
+finite."""
 import linear_ref as ref
 import numpy as np
 import pytest
@@ -43,3 +44,22 @@ def test_gradients_without_eps(torch, N, H, D, norm, dtype):  # noqa: F811
         mag = (turned * np.abs(x) * r).reshape(-1, D).sum(0)
         off = np.abs(dw.double().cpu().numpy() - wantw)
         assert (off <= (f32 + 2.0 ** -24 * N * h) * 3 * mag).all()
+
+
+@pytest.mark.parametrize("pairing", ["half", "adjacent"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_frequencies_that_are_not_finite(torch, bad, pairing):  # noqa: F811
+    """Their pair is not a number, at every position (0 too); the other channels keep their bits."""
+    from gated_delta_rule_49_gb300 import binding
+    x = torch.randn(9, 3, 64, device="cuda")
+    pos = torch.arange(9, device="cuda")
+    f = torch.from_numpy(frequencies(32)).cuda()
+    g = f.clone()
+    g[5] = bad
+    pair = [5, 21] if pairing == "half" else [10, 11]
+    rest = [i for i in range(64) if i not in pair]
+    want, _ = binding.qk_norm_rotate(x, None, pos, f, pairing=pairing)
+    y, _ = binding.qk_norm_rotate(x, None, pos, g, pairing=pairing)
+    assert y[..., pair].isnan().all() and torch.equal(y[..., rest], want[..., rest])
+    dx = binding.qk_norm_rotate_backward(x, None, pos, g, x, None, pairing=pairing)[0]
+    assert dx.isnan().all()  # through the norm
