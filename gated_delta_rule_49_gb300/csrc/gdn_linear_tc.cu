@@ -227,9 +227,14 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t *b, uint32_t parity) {
     return ok != 0;
 }
 
+// acc stays 0 while the pairs of bf16 values that it meets are finite.
+__device__ __forceinline__ void note_not_finite(uint32_t &acc, uint32_t pair) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(pair), "r"(0u));
+}
+
 struct LinBars {
     uint64_t kfull[kStages], vfull[kStages], used[kStages], sent[kStages], staged, qfull, qs, d0, dfree;
-    uint64_t vw[2], scores, p, d, s, o, ofree, tail;
+    uint64_t vw[2], scores, p, d, s, o, ofree, tail, out;
 };
 
 struct LinTcArgs {
@@ -239,6 +244,83 @@ struct LinTcArgs {
     float *slots_out;
     int *status;
 };
+
+// P V meets the values of V with the zeros of P's other triangle too, so that
+// one that is not finite reaches the outputs of its channel from its chunk's
+// first token on.  A warp forms those before it again, token by token from the
+// segment's start (the rest are right, or not finite).  Such a value stays in
+// the state, so that a segment's end tells whether there is one and nothing is
+// looked at before (marks in the chunks' loop cost 2 to 9 % of the time).
+template <int K, int V>
+__device__ __forceinline__ void outputs_before_bad_value(const LinTcArgs &arg, const LinearItem &it, int h,
+                                                      int f0, int tokens, int ch) {
+    constexpr int C = K / 32;  // columns of a lane
+    const LinearScan &p = arg.a;
+    const int lane = threadIdx.x & 31;
+    const bool rev = p.reverse, first = rev ? it.j == it.n - 1 : it.j == 0;
+    const long long t0 = it.first + f0;
+    const __nv_bfloat16 *const v = static_cast<const __nv_bfloat16 *>(p.v) + h / (p.H / p.Hv) * V + ch;
+    auto token = [&](int y) { return t0 + (rev ? tokens - 1 - y : y); };
+    int bad = -1;  // scan position of the first that is not finite
+#pragma unroll 1
+    for (int y0 = 0; y0 < tokens && bad < 0; y0 += 32) {
+        const int y = y0 + lane;
+        const float x = y < tokens ? __bfloat162float(v[token(y) * p.ldv]) : 0.f;
+        const unsigned who = __ballot_sync(0xffffffffu, !(fabsf(x) < INFINITY));
+        if (who) bad = y0 + __ffs(who) - 1;
+    }
+    if (bad < 0) return;
+    // scan position of its chunk's first token
+    const int at = (rev ? tokens - 1 - bad : bad) / kC * kC;
+    const int from = rev ? tokens - min(tokens, at + kC) : at;
+    const float a = p.alpha[h], lg = decay_log2(a);
+    float S[C];
+    auto add_row = [&](size_t row, float f) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) S[c] = fmaf(f, arg.slots_in[(row * V + ch) * K + lane * C + c], S[c]);
+    };
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        S[c] = p.S0 && !arg.slots_in ? given_start(p.S0, p.s0_transposed, (size_t)it.seq * p.H + h, V, K,
+                                                   ch, lane * C + c)
+                                     : 0.f;
+    if (arg.slots_in) {
+        if (p.S0)
+            add_row((size_t)(it.slot0 + (rev ? 0 : it.n - 1)) * p.H + h,
+                    decay_power(start_steps(it, arg.plan.seg_len, rev), lg));
+        for (int j = rev ? it.j + 1 : 0; j < (rev ? it.n : it.j); ++j)
+            add_row((size_t)(it.slot0 + j) * p.H + h,
+                    decay_power(tokens_between(j, it.j, it.len, arg.plan.seg_len, rev), lg));
+    }
+    const __nv_bfloat16 *const k =
+        static_cast<const __nv_bfloat16 *>(p.k) + h / (p.H / p.Hk) * K + lane * C;
+    const __nv_bfloat16 *const q =
+        static_cast<const __nv_bfloat16 *>(p.q) + h / (p.H / p.Hq) * K + lane * C;
+    auto take = [&](int y) {
+        const long long t = token(y);
+        const float w = p.write_scale * __bfloat162float(v[t * p.ldv]);
+        const float d = rev && first && y == 0 ? 1.f : a;
+#pragma unroll
+        for (int c = 0; c < C; ++c) S[c] = fmaf(w, __bfloat162float(k[t * p.ldk + c]), d * S[c]);
+    };
+#pragma unroll 4
+    for (int y = 0; y < from; ++y) take(y);
+#pragma unroll 1
+    for (int y = from; y < bad; ++y) {
+        take(y);
+        const long long t = token(y);
+        float o = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) o = fmaf(S[c], __bfloat162float(q[t * p.ldq + c]), o);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
+        if (lane == 0) {
+            const size_t e = ((size_t)t * p.H + h) * V + ch;
+            if (p.o_float) static_cast<float *>(p.o)[e] = p.read_scale * o;
+            else static_cast<__nv_bfloat16 *>(p.o)[e] = __float2bfloat16_rn(p.read_scale * o);
+        }
+    }
+}
 
 template <int K, int V>
 __global__ void __launch_bounds__(kWarps * 32, 1)
@@ -310,6 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             mbar_init(&bar.o, 1);
             mbar_init(&bar.ofree, 4);
             mbar_init(&bar.tail, 8);
+            mbar_init(&bar.out, 1);
             abort_flag = 0;
             fence_mbar_init();
         }
@@ -658,6 +741,37 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 if (want_o && i < nc) store_state();
             }
         }
+        if (want_o && nc > 0 && g == 0 && (warp & 3) * 32 < V) {
+            float z = 0.f;
+#pragma unroll
+            for (int e = 0; e < NS; ++e) z = fmaf(S[e], 0.f, z);
+            unsigned channels = __ballot_sync(0xffffffffu, z != 0.f);
+            if (!end) {  // the last chunk has not been taken up
+                const uint8_t *const vt = smem + L::VV + ((nc - 1) % kStages) * L::VSLOT +
+                                          ((warp & 3) >> 1) * (kC * 128);
+                uint32_t acc = 0;
+#pragma unroll 1
+                for (uint32_t tok = lane; tok < kC; tok += 32)
+#pragma unroll
+                    for (uint32_t x = 0; x < 4; ++x) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(
+                            vt + swz128(tok, 4 * (warp & 1) + x));
+                        note_not_finite(acc, y.x);
+                        note_not_finite(acc, y.y);
+                        note_not_finite(acc, y.z);
+                        note_not_finite(acc, y.w);
+                    }
+                if (__any_sync(0xffffffffu, acc != 0)) channels = ~0u;
+            }
+            if (channels) {
+                wait_warp(&bar.out, 0);  // all outputs are in memory
+                if (!__any_sync(0xffffffffu, dead))
+                    for (; channels; channels &= channels - 1)
+                        outputs_before_bad_value<K, V>(arg, it, h, f0, tokens,
+                                                       (warp & 3) * 32 + __ffs(channels) - 1);
+            }
+        }
+        if (want_o) named_sync(kBarS, 256);  // the end states may take the start states' place
         if (end && mine && !dead) {
             // the state that a reversed scan returns has decayed once more
             const float f = !slot && rev && it.len > 0 ? exp2f(lg) : 1.f;
@@ -747,6 +861,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 mbar_arrive(&bar.sent[i % kStages]);
             }
             bulk_wait_all();
+            mbar_arrive(&bar.out);
         }
         // ---------------------------------------------------------------- MMAs
         if (warp == 17 && elect_one()) {

@@ -529,9 +529,8 @@ GDN_API int gdn_qk_norm_rotate_backward(const void *q, const void *k, const floa
  *         of no sequence keep what o held.
  *
  * (K, V) in (32, 32), (64, 64), (64, 128), (128, 128).  A value that is not
- * finite reaches the outputs of its own sequence only, where it gives infinities
- * or NaN; it may reach tokens up to 127 before it, which are computed in one
- * block with it.
+ * finite reaches what the recurrence carries it to and nothing else, and gives
+ * infinities or NaN there.
  * workspace: gdn_linear_prefill_workspace_size bytes (0 where the sequences
  * alone fill the device), 256-byte aligned.
  */
