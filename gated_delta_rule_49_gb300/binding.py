@@ -242,6 +242,8 @@ def _scratch(need, device, stream):
 
 def _written_on(stream, *new):
     """Keeps what a call on the stream writes to (tensors or None) until it is written."""
+    if stream is None:
+        return
     other = _other_stream(stream)
     if other is not None:
         for x in new:
@@ -701,9 +703,26 @@ def _dense(where, name, x, dtype, device, shape):
                        f"device {device}; it is {x.dtype}, {tuple(x.shape)} on {x.device}")
 
 
-def _workspace(given, need, like, stream):
+_current_device = None
+
+
+def _on_this_gpu(where, device):
+    """The operands' device (a number; the last check of a call) is the GPU it runs on."""
+    if device < 0:
+        _reject(where, "its tensors are on the CPU, not on a GPU")
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if device != _current_device():
+        _reject(where, f"its tensors are on GPU {device}, not on the current one")
+
+
+def _workspace(where, given, need, like, stream):
     """(workspace, its bytes): the one given, or a new one where one is needed."""
     if given is not None:
+        if given.get_device() != like.get_device() or not given.is_contiguous():
+            _reject(where, f"workspace must be contiguous on device {like.device}")
         return given, given.numel() * given.element_size()
     return _scratch(need, like.device, stream), need
 
@@ -756,6 +775,7 @@ def qk_norm_rotate(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms", 
         _dense(where, "out[0]", yq, q.dtype, q.get_device(), q.shape)
         if k is not None:
             _dense(where, "out[1]", yk, q.dtype, q.get_device(), k.shape)
+    _on_this_gpu(where, q.get_device())
     gdn_qk_norm_rotate(q, k, wq, wk, pos, inv_freq, yq, yk, N, Hq, Hk, D, R, ldq, ldk, nrm, pair,
                        eps, _dtype_code(q), stream)
     if out is None:
@@ -773,6 +793,7 @@ def qk_norm_rotate_backward(q, k, pos, inv_freq, dyq, dyk, wq=None, wk=None, nor
     _dense(where, "dyq", dyq, q.dtype, q.get_device(), q.shape)
     if k is not None:
         _dense(where, "dyk", dyk, q.dtype, q.get_device(), k.shape)
+    _on_this_gpu(where, q.get_device())
     dq = _new(q)
     dk = None if k is None else _new(k)
     dwq = None if wq is None else _new(wq)
@@ -780,7 +801,7 @@ def qk_norm_rotate_backward(q, k, pos, inv_freq, dyq, dyk, wq=None, wk=None, nor
     need = 0
     if wq is not None or wk is not None:
         need = gdn_qk_norm_rotate_backward_workspace_size(N, Hq, Hk, D)
-    workspace, need = _workspace(workspace, need, q, stream)
+    workspace, need = _workspace(where, workspace, need, q, stream)
     gdn_qk_norm_rotate_backward(q, k, wq, wk, pos, inv_freq, dyq, dyk, dq, dk, dwq, dwk, N, Hq, Hk,
                                 D, R, ldq, ldk, nrm, pair, eps, _dtype_code(q), workspace, need,
                                 stream)
@@ -827,12 +848,13 @@ def linear_prefill(q, k, v, alpha, S0=None, scale=1.0, offsets=None, want_o=True
     dev, shape = v.get_device(), (B, H, V, K)
     _dense(where, "S0", S0, torch.float32, dev, shape)
     _dense(where, "out_state", out_state, torch.float32, dev, shape)
+    _on_this_gpu(where, dev)
     dt = _dtype_code(v)
     o = _new(v) if want_o else None
     ST = out_state
     if want_state and ST is None:
         ST = torch.empty(shape, dtype=torch.float32, device=v.device)
-    workspace, need = _workspace(workspace, gdn_linear_prefill_workspace_size(
+    workspace, need = _workspace(where, workspace, gdn_linear_prefill_workspace_size(
         B, T, H, K, V, offsets is not None, dt), v, stream)
     gdn_linear_prefill(q, k, v, alpha, S0, o, ST, offsets, B, T, Hq, H, K, V, ldq, ldk, ldv, scale,
                        dt, workspace, need, stream)
@@ -852,12 +874,13 @@ def linear_backward(q, k, v, alpha, do, S0=None, dS_T=None, scale=1.0, offsets=N
     _dense(where, "S0", S0, torch.float32, dev, shape)
     _dense(where, "dS_T", dS_T, torch.float32, dev, shape)
     _dense(where, "do", do, v.dtype, dev, v.shape)
+    _on_this_gpu(where, dev)
     dt = _dtype_code(v)
     dq, dk, dv = _new(q), _new(k), _new(v)
     dS0 = None
     if want_dS0 or (want_dS0 is None and S0 is not None):
         dS0 = torch.empty(shape, dtype=torch.float32, device=v.device)
-    workspace, need = _workspace(workspace, gdn_linear_backward_workspace_size(
+    workspace, need = _workspace(where, workspace, gdn_linear_backward_workspace_size(
         B, T, Hq, H, K, V, offsets is not None, dt), v, stream)
     gdn_linear_backward(q, k, v, alpha, do, S0, dS_T, dq, dk, dv, dS0, offsets, B, T, Hq, H, K, V,
                         ldq, ldk, ldv, scale, dt, workspace, need, stream)
@@ -888,6 +911,7 @@ def linear_decode_step(q, k, v, alpha, S, scale=1.0, S_out=None, o=None, stream=
     _dense(where, "alpha", alpha, torch.float32, dev, (H,))
     _dense(where, "S", S, torch.float32, dev, shape)
     _dense(where, "S_out", S_out, torch.float32, dev, shape)
+    _on_this_gpu(where, dev)
     gdn_linear_decode_step(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale, _dtype_code(v),
                            stream)
     if given is None:

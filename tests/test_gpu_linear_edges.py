@@ -1,5 +1,5 @@
 """Edges of linear attention on the GPU: bad offsets of batches that are cut into
-segments, decays that are not a number."""
+segments, decays that are not a number, workspaces of the caller."""
 import pytest
 from test_gpu_linear import Problem, clean_status, torch  # noqa: F401
 
@@ -75,3 +75,31 @@ def test_empty_sequences_keep_their_states_at_any_decay(torch, K, V, dtype):  # 
     _, S = binding.linear_prefill(p.q, p.k, p.v, p.a, p.S0, offsets=p.offsets)
     dS0 = binding.linear_backward(p.q, p.k, p.v, p.a, p.do, p.S0, p.dST, offsets=p.offsets)[3]
     assert torch.equal(S[1], p.S0[1]) and torch.equal(dS0[1], p.dST[1])
+
+
+def test_workspaces_of_the_caller(torch):  # noqa: F811
+    """One of its own gives the same bits; one on the CPU, in pieces or too small is refused."""
+    from gated_delta_rule_49_gb300 import binding
+    p = Problem(torch, 16, 1, 3000, 1, 2, 64, 64, "bf16")
+    f, pos = torch.ones(32, device="cuda"), torch.zeros(1, 3000, dtype=torch.int64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    calls = (
+        (lambda ws: binding.linear_prefill(p.q, p.k, p.v, p.a, p.S0, workspace=ws),
+         binding.gdn_linear_prefill_workspace_size(1, 3000, 2, 64, 64, False, binding.GDN_BF16)),
+        (lambda ws: binding.linear_backward(p.q, p.k, p.v, p.a, p.do, workspace=ws)[:3],
+         binding.gdn_linear_backward_workspace_size(1, 3000, 1, 2, 64, 64, False, binding.GDN_BF16)),
+        (lambda ws: binding.qk_norm_rotate_backward(p.q, p.k, pos, f, p.q, p.k, w, w, workspace=ws),
+         binding.gdn_qk_norm_rotate_backward_workspace_size(3000, 1, 1, 64)))
+    for call, need in calls:
+        assert need > 0
+        want = call(None)
+        got = call(torch.empty(need, dtype=torch.uint8, device="cuda"))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for bad, status in ((torch.empty(need, dtype=torch.uint8), binding.GDN_ERR_INVALID_ARG),
+                            (torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2],
+                             binding.GDN_ERR_INVALID_ARG),
+                            (torch.empty(need - 4, dtype=torch.uint8, device="cuda"),
+                             binding.GDN_ERR_WORKSPACE)):
+            with pytest.raises(binding.GDNError) as e:
+                call(bad)
+            assert e.value.status == status

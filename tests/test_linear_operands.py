@@ -67,3 +67,17 @@ def test_strides_of_what_has_memory():
     assert stride(wide[:0, :, :3]) == 3 * 64
     assert stride(wide[:, :, 2:3]) == 6 * 64
     assert stride(wide[1, 2, 1:4]) == 3 * 64  # no leading dimension
+
+
+def test_host_tensors_are_refused():
+    """All on the CPU, so that they agree with one another: host pointers must not reach a kernel."""
+    q, v, S = torch.zeros(2, 5, 4, 64), torch.zeros(2, 5, 4, 128), torch.zeros(2, 4, 128, 64)
+    alpha, pos, f = torch.ones(4), torch.zeros(2, 5, dtype=torch.int64), torch.ones(32)
+    refused("on the CPU", binding.linear_prefill, q, q, v, alpha, S0=S)
+    refused("on the CPU", binding.linear_prefill, q[0], q[0], v[0], alpha,
+            offsets=torch.tensor([0, 5], dtype=torch.int32))
+    refused("on the CPU", binding.linear_backward, q, q, v, alpha, v)
+    refused("on the CPU", binding.linear_decode_step, q[:, 0].contiguous(), q[:, 0].contiguous(),
+            v[:, 0].contiguous(), alpha, S)
+    refused("on the CPU", binding.qk_norm_rotate, q, q, pos, f)
+    refused("on the CPU", binding.qk_norm_rotate_backward, q, q, pos, f, q, q)
