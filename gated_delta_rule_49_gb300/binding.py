@@ -185,7 +185,7 @@ def status_string(status: int) -> str:
 
 
 def _ptr(x):
-    if x is None or type(x) is int:
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 

@@ -81,3 +81,14 @@ def test_host_tensors_are_refused():
             v[:, 0].contiguous(), alpha, S)
     refused("on the CPU", binding.qk_norm_rotate, q, q, pos, f)
     refused("on the CPU", binding.qk_norm_rotate_backward, q, q, pos, f, q, q)
+
+
+def test_addresses_of_any_whole_number_type():
+    """A raw address may come as a subclass of int (an enum's, a wrapper's own)."""
+    class Address(int):
+        pass
+
+    assert binding._ptr(Address(0x10000)) == 0x10000
+    assert binding._ptr(0x10000) == 0x10000 and binding._ptr(None) is None
+    x = torch.zeros(4)
+    assert binding._ptr(x) == x.data_ptr()
