@@ -607,9 +607,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     __syncwarp();
                 }
                 tc_fence_before();
-                arrive_warp(&bar.ofree);
                 fence_proxy_async_smem();
+                // first: O's columns free, another warp may come to stage the next chunk
                 arrive_warp(&bar.staged);
+                arrive_warp(&bar.ofree);
             }
         }
     } else if (warp < 16) {
