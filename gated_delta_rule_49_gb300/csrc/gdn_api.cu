@@ -606,7 +606,7 @@ namespace {
 size_t linear_backward_slots(int B, int T, int H, int K, int V, bool packed, gdn_dtype dtype) {
     const size_t dv = gdn::linear_scan_workspace(B, T, H, K, V, packed, dtype);
     const size_t dqk = gdn::linear_scan_workspace(B, T, H, V, K, packed, dtype);
-    const size_t n = !gdn::linear_on_tensor_cores(K, V, dtype) ? 2 * dqk + dv : dqk > dv ? dqk : dv;
+    const size_t n = !gdn::linear_on_tensor_cores(T, K, V, dtype) ? 2 * dqk + dv : dqk > dv ? dqk : dv;
     return (n + 255) & ~size_t(255);
 }
 // One head's part of a gradient that a group of heads shares, in float32 (bytes).
@@ -620,7 +620,7 @@ size_t gdn_linear_backward_workspace_size(int B, int T, int Hq, int H, int K, in
     if (B <= 0 || T <= 0 || H <= 0 || Hq <= 0 || !linear_kv(K, V)) return 0;
     const size_t n = linear_backward_slots(B, T, H, K, V, packed != 0, dtype);
     if (Hq == H) return n;
-    return n + (gdn::linear_on_tensor_cores(K, V, dtype) ? 1 : 2) * linear_part(B, T, H, K, packed != 0);
+    return n + (gdn::linear_on_tensor_cores(T, K, V, dtype) ? 1 : 2) * linear_part(B, T, H, K, packed != 0);
 }
 
 int gdn_linear_backward(const void *q, const void *k, const void *v, const float *alpha,
@@ -645,7 +645,7 @@ int gdn_linear_backward(const void *q, const void *k, const void *v, const float
     const long long tokens = offsets ? T : (long long)B * T;
     char *const parts = static_cast<char *>(workspace) +
                         linear_backward_slots(B, T, H, K, V, offsets != nullptr, dtype);
-    const bool together = !gdn::linear_on_tensor_cores(K, V, dtype);
+    const bool together = !gdn::linear_on_tensor_cores(T, K, V, dtype);
     const int group = H / Hq;
     float *const part_q = reinterpret_cast<float *>(parts);
     float *const part_k = together ? reinterpret_cast<float *>(

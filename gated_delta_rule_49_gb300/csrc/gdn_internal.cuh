@@ -196,7 +196,7 @@ struct LinearScan {
     bool exact;  // the state to float32 accuracy (else to that of bf16 operands)
 };
 // Whether a scan runs on the tensor cores; bytes of workspace of one scan.
-bool linear_on_tensor_cores(int K, int V, gdn_dtype dt);
+bool linear_on_tensor_cores(int T, int K, int V, gdn_dtype dt);
 size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt);
 // One scan, or on the CUDA cores up to three independent ones (the first two of
 // one width K), each with its own workspace one after another.

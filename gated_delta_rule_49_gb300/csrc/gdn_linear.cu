@@ -407,13 +407,21 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float *x0, const f
 
 }  // namespace
 
-// bf16 runs on the tensor cores where a tile fills them
-bool linear_on_tensor_cores(int K, int V, gdn_dtype dt) {
-    return dt == GDN_BF16 && K >= 64 && V >= 64;
+// bf16 runs on the tensor cores where a tile fills them and there are more than
+// eight tokens (in all, where packed).  The outputs of one or two tokens may be
+// what is left of terms that cancel (one token's dq is one number for each head,
+// summed over the heads that share it, times k): rounded scores then showed as
+// up to a third of the result, where the token kernel is off by float32 steps.
+// It is also the faster one there (16 heads, 128 x 128, device, prompt / gradients:
+// 1 token 5 / 6 us against 21 / 37 on the tensor cores; 64 sequences of 8 tokens
+// 65 / 248 against 152 / 261; of 16 tokens 91 / 322 against 153 / 265).
+constexpr int kFewTokens = 8;
+bool linear_on_tensor_cores(int T, int K, int V, gdn_dtype dt) {
+    return dt == GDN_BF16 && K >= 64 && V >= 64 && T > kFewTokens;
 }
 
 size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn_dtype dt) {
-    const SegPlan plan = linear_on_tensor_cores(K, V, dt) ? linear_tc_plan(B, T, H, K, V, packed)
+    const SegPlan plan = linear_on_tensor_cores(T, K, V, dt) ? linear_tc_plan(B, T, H, K, V, packed)
                                                           : token_plan(B, T, H, V, packed);
     return plan.items > B ? (size_t)plan.items * H * V * K * sizeof(float) : 0;
 }
@@ -421,7 +429,7 @@ size_t linear_scan_workspace(int B, int T, int H, int K, int V, bool packed, gdn
 cudaError_t launch_linear_scan(const LinearScan *a, int count, gdn_dtype dt, void *workspace,
                                cudaStream_t stream) {
     float *slots = static_cast<float *>(workspace);
-    if (linear_on_tensor_cores(a->K, a->V, dt)) return launch_linear_tc(*a, slots, stream);
+    if (linear_on_tensor_cores(a->T, a->K, a->V, dt)) return launch_linear_tc(*a, slots, stream);
     return dt == GDN_BF16 ? launch_token<__nv_bfloat16>(a, count, slots, stream)
                           : launch_token<float>(a, count, slots, stream);
 }

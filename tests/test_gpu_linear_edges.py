@@ -1,5 +1,7 @@
 """Edges of linear attention on the GPU: bad offsets of batches that are cut into
-segments, decays that are not a number, workspaces of the caller."""
+segments, decays that are not a number, workspaces of the caller, sums of few terms."""
+import linear_ref as ref
+import numpy as np
 import pytest
 from test_gpu_linear import Problem, clean_status, torch  # noqa: F401
 
@@ -103,3 +105,29 @@ def test_workspaces_of_the_caller(torch):  # noqa: F811
             with pytest.raises(binding.GDNError) as e:
                 call(bad)
             assert e.value.status == status
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("T", [1, 2, 8])
+def test_few_tokens_whose_terms_cancel(torch, T, K, V):  # noqa: F811
+    """bf16 outputs of a few tokens: half a step of the output's type, and float32 steps of the
+    terms' magnitudes (no rounding of an operand), whatever is left of the terms."""
+    from gated_delta_rule_49_gb300 import binding
+
+    def held(got, want, mag, width):
+        got = got.double().cpu().numpy()
+        bound = ref.U["bf16"] * np.abs(want) + ref.steps("fp32", T, width) * mag * 1.01
+        assert (np.abs(got - want) <= bound + 1e-30).all()
+
+    for seed in range(20):
+        for packed in (False, True):
+            p = Problem(torch, seed, 1, T, 1, 4, K, V, "bf16", seed % 2 == 0, [T] if packed else None)
+            o, S = binding.linear_prefill(p.q, p.k, p.v, p.a, p.S0, scale=0.5, offsets=p.offsets)
+            (o64, S64), (om, Sm) = p.forward(0.5)
+            held(o, o64, om, K)
+            assert (np.abs(S.double().cpu().numpy() - S64) <= ref.state_steps("fp32", T) * Sm).all()
+            got = binding.linear_backward(p.q, p.k, p.v, p.a, p.do, p.S0, p.dST, scale=0.5,
+                                          offsets=p.offsets)
+            want, mag = p.backward(0.5)
+            for i in range(3):
+                held(got[i], want[i], mag[i], K + V + 4)
