@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 arrive_warp(&bar.vw[c]);
             }
             if (c == 0 && i > 0 && updates(i - 1)) {
-                const float ac = decay_power(chunk_n(i - 1) + chunk_lead(i - 1) - 1, lg);
+                const float ac = exp2f((float)(chunk_n(i - 1) + chunk_lead(i - 1) - 1) * lg);
                 wait_warp(&bar.d, i - 1);
                 tc_fence_after();
                 if (mine) {
