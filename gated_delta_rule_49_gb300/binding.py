@@ -841,7 +841,8 @@ def linear_prefill(q, k, v, alpha, S0=None, scale=1.0, offsets=None, want_o=True
     o_t = scale S_t q_t (gdn_linear_prefill): q, k [B, T, Hq, K], v [B, T, H, V] (bf16 or fp32;
     H a multiple of Hq; slices of one projection will do), alpha [H] fp32, S0 [B, H, V, K] fp32 or
     None.  With offsets [B + 1] int32 the sequences lie packed: q, k [tokens, Hq, K],
-    v [tokens, H, V].  Returns (o, S_T); out_state may be S0."""
+    v [tokens, H, V]; outputs of tokens of no sequence are not written.  Returns (o, S_T);
+    out_state may be S0."""
     import torch
     where = "linear_prefill"
     B, T, Hq, H, K, V, ldq, ldk, ldv = _linear_args(where, q, k, v, alpha, offsets)
@@ -866,7 +867,7 @@ def linear_backward(q, k, v, alpha, do, S0=None, dS_T=None, scale=1.0, offsets=N
                     want_dS0=None, workspace=None, stream=None):
     """Gradients of linear_prefill from its inputs, do (dense, as v) and dS_T (fp32 or None).
     Returns (dq, dk, dv, dS0); dS0 is formed if S0 is given or want_dS0 is true, else None.
-    alpha is a constant and has none."""
+    alpha is a constant and has none.  Gradients of tokens of no sequence are not written."""
     import torch
     where = "linear_backward"
     B, T, Hq, H, K, V, ldq, ldk, ldv = _linear_args(where, q, k, v, alpha, offsets)

@@ -42,7 +42,7 @@ template <> struct Cols<4> {
 //
 // Up to three scans run in one launch (a backward pass: they do not depend on
 // one another, and a small one is all start-up: B = 2, T = 391, 4 heads of 64 x
-// 128 take 73 us as six launches and two sums, 48 us as two and one).
+// 128 take 73 us as six launches and two sums, 49 us as two and one).
 struct TokenScan {
     LinearScan p;
     SegPlan plan;

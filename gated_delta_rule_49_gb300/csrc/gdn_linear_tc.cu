@@ -23,7 +23,7 @@
 //   0-3   P: row t of Q K^T from TMEM, weighted, back to TMEM as bf16 (over the
 //         columns that it came from) for the product with V.  (Eight warps that
 //         shared P's columns and then O's: gradients of B = 8, T = 4096, H = 16,
-//         128 x 128 in 273 us instead of 269.)
+//         128 x 128 took 4 us more than the 273 of now.)
 //   4-7   O: row t from TMEM, scaled, to shared memory (in K's
 //         place) and out by TMA (ragged chunks: plain stores)
 //   8-15  state: two groups of 128 threads; each chunk's V in two halves of
@@ -1010,7 +1010,7 @@ cudaError_t launch_kv(const LinearScan &a, float *slots, cudaStream_t st) {
 // The cost of a cut is counted in chunk times: a CTA (one an SM) takes its
 // segment's chunks and about four more to start and end; a first pass over all
 // but the last segments takes 0.6 of that, and its launch three.  (B = 1,
-// T = 65536, H = 16, 128 x 128: 4 segments a sequence 616 us, 9 371 us.)  Packed
+// T = 65536, H = 16, 128 x 128: 4 segments a sequence 622 us, 9 322 us.)  Packed
 // sequences' lengths are not known here: the longest is taken for four times the
 // mean, and the work for evenly spread.
 SegPlan linear_tc_plan(int B, int T, int H, int K, int V, bool packed) {
