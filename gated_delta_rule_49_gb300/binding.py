@@ -42,6 +42,11 @@ GDN_PAIR_HALF = 0
 GDN_PAIR_ADJACENT = 1
 PAIRINGS = {"half": GDN_PAIR_HALF, "adjacent": GDN_PAIR_ADJACENT}
 
+GDN_SCAN_DECAY = 0
+GDN_SCAN_SIGMOID = 1
+SCANS = {"decay": GDN_SCAN_DECAY, "sigmoid": GDN_SCAN_SIGMOID}
+GDN_SCAN_BLOCK = 64  # tokens between the states that a scan keeps
+
 EXPORTS = (
     "gdn_prefill",
     "gdn_prefill_workspace_size",
@@ -77,6 +82,14 @@ EXPORTS = (
     "gdn_linear_backward",
     "gdn_linear_backward_workspace_size",
     "gdn_linear_decode_step",
+    "gdn_scan_prefill",
+    "gdn_scan_prefill_workspace_size",
+    "gdn_scan_backward",
+    "gdn_scan_backward_workspace_size",
+    "gdn_scan_decode_step",
+    "gdn_layer_norm",
+    "gdn_layer_norm_backward",
+    "gdn_layer_norm_backward_workspace_size",
 )
 
 _lock = threading.Lock()
@@ -173,6 +186,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gdn_linear_backward_workspace_size.restype = sz
         lib.gdn_linear_decode_step.argtypes = [vp] * 7 + [i] * 5 + [f, i, vp]
         lib.gdn_linear_decode_step.restype = i
+        lib.gdn_scan_prefill.argtypes = [vp] * 7 + [i] * 3 + [ll] * 2 + [i, i, vp, sz, vp]
+        lib.gdn_scan_prefill.restype = i
+        lib.gdn_scan_prefill_workspace_size.argtypes = [i] * 4
+        lib.gdn_scan_prefill_workspace_size.restype = sz
+        lib.gdn_scan_backward.argtypes = [vp] * 10 + [i] * 3 + [ll] * 2 + [i, i, vp, sz, vp]
+        lib.gdn_scan_backward.restype = i
+        lib.gdn_scan_backward_workspace_size.argtypes = [i] * 5
+        lib.gdn_scan_backward_workspace_size.restype = sz
+        lib.gdn_scan_decode_step.argtypes = [vp] * 5 + [i] * 2 + [ll] * 2 + [i, i, vp]
+        lib.gdn_scan_decode_step.restype = i
+        lib.gdn_layer_norm.argtypes = [vp] * 7 + [ll, i, ll, ll, f, i, vp]
+        lib.gdn_layer_norm.restype = i
+        lib.gdn_layer_norm_backward.argtypes = [vp] * 8 + [ll, i, ll, i, vp, sz, vp]
+        lib.gdn_layer_norm_backward.restype = i
+        lib.gdn_layer_norm_backward_workspace_size.argtypes = [ll, i]
+        lib.gdn_layer_norm_backward_workspace_size.restype = sz
         _lib = lib
         return lib
 
@@ -592,6 +621,59 @@ def gdn_linear_decode_step(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale, d
     return _check(st, "gdn_linear_decode_step")
 
 
+def gdn_scan_prefill(x, gate, h0, h, h_T, states, offsets, B, T, D, x_stride, gate_stride, kind,
+                     dtype, workspace=None, workspace_bytes=0, stream=None) -> int:
+    st = load().gdn_scan_prefill(_ptr(x), _ptr(gate), _ptr(h0), _ptr(h), _ptr(h_T), _ptr(states),
+                                 _ptr(offsets), B, T, D, x_stride, gate_stride, kind, dtype,
+                                 _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "gdn_scan_prefill")
+
+
+def gdn_scan_prefill_workspace_size(B, T, D, packed) -> int:
+    return int(load().gdn_scan_prefill_workspace_size(B, T, D, int(packed)))
+
+
+def gdn_scan_backward(x, gate, dh, h0, dh_T, states, dx, dgate, dh0, offsets, B, T, D, x_stride,
+                      gate_stride, kind, dtype, workspace=None, workspace_bytes=0,
+                      stream=None) -> int:
+    st = load().gdn_scan_backward(_ptr(x), _ptr(gate), _ptr(dh), _ptr(h0), _ptr(dh_T),
+                                  _ptr(states), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(offsets), B,
+                                  T, D, x_stride, gate_stride, kind, dtype, _ptr(workspace),
+                                  workspace_bytes, _stream(stream))
+    return _check(st, "gdn_scan_backward")
+
+
+def gdn_scan_backward_workspace_size(B, T, D, packed, kept) -> int:
+    return int(load().gdn_scan_backward_workspace_size(B, T, D, int(packed), int(kept)))
+
+
+def gdn_scan_decode_step(x, gate, h, h_out, y, B, D, x_stride, gate_stride, kind, dtype,
+                         stream=None) -> int:
+    st = load().gdn_scan_decode_step(_ptr(x), _ptr(gate), _ptr(h), _ptr(h_out), _ptr(y), B, D,
+                                     x_stride, gate_stride, kind, dtype, _stream(stream))
+    return _check(st, "gdn_scan_decode_step")
+
+
+def gdn_layer_norm(x, residual, w, b, y, s, stats, N, D, x_stride, residual_stride, eps, dtype,
+                   stream=None) -> int:
+    st = load().gdn_layer_norm(_ptr(x), _ptr(residual), _ptr(w), _ptr(b), _ptr(y), _ptr(s),
+                               _ptr(stats), N, D, x_stride, residual_stride, eps, dtype,
+                               _stream(stream))
+    return _check(st, "gdn_layer_norm")
+
+
+def gdn_layer_norm_backward(s, dy, stats, w, ds, dx, dw, db, N, D, s_stride, dtype, workspace=None,
+                            workspace_bytes=0, stream=None) -> int:
+    st = load().gdn_layer_norm_backward(_ptr(s), _ptr(dy), _ptr(stats), _ptr(w), _ptr(ds),
+                                        _ptr(dx), _ptr(dw), _ptr(db), N, D, s_stride, dtype,
+                                        _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "gdn_layer_norm_backward")
+
+
+def gdn_layer_norm_backward_workspace_size(N, D) -> int:
+    return int(load().gdn_layer_norm_backward_workspace_size(N, D))
+
+
 def gdn_get_last_device_status(stream=None) -> int:
     return int(load().gdn_get_last_device_status(_stream(stream)))
 
@@ -918,3 +1000,191 @@ def linear_decode_step(q, k, v, alpha, S, scale=1.0, S_out=None, o=None, stream=
     if given is None:
         _written_on(stream, o)
     return o
+
+
+def _row_stride(where, name, x, dtype, device):
+    """Elements between consecutive rows of x [..., D]: a row is dense, and the leading dimensions
+    step evenly, as in a part of a wider projection."""
+    if x.is_contiguous() and x.dtype is dtype and x.get_device() == device:
+        return x.shape[-1]
+    return _token_stride(where, name, x.unsqueeze(-2), dtype, device)
+
+
+def _scan_args(where, x, gate, kind, offsets):
+    """B, T, D and the token strides of x and gate, [B, T, D] or with offsets [tokens, D]."""
+    import torch
+    if kind not in SCANS:
+        _reject(where, f"kind {kind!r}")
+    xs = x.shape
+    if len(xs) != (3 if offsets is None else 2) or gate.shape != xs:
+        _reject(where, f"x {tuple(xs)}, gate {tuple(gate.shape)}"
+                       + ("" if offsets is None else " with offsets"))
+    dev = x.get_device()
+    if offsets is None:
+        B, T, D = xs
+    else:
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            _reject(where, "offsets must be [sequences + 1]")
+        B, (T, D) = offsets.shape[0] - 1, xs
+        _dense(where, "offsets", offsets, torch.int32, dev, (B + 1,))
+    ldx = _row_stride(where, "x", x, x.dtype, dev)
+    ldg = _row_stride(where, "gate", gate, torch.float32 if kind == "decay" else x.dtype, dev)
+    return B, T, D, ldx, ldg
+
+
+def _states_shape(B, T, D, packed):
+    blocks = -(-T // GDN_SCAN_BLOCK)
+    return (blocks, D) if packed else (B, blocks, D)
+
+
+def scan_prefill(x, gate, h0=None, kind="sigmoid", offsets=None, want_h=True, want_state=True,
+                 out_state=None, keep_states=False, workspace=None, stream=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + b_t x_t, channel by channel
+    (gdn_scan_prefill): x, gate [B, T, D] (slices of one projection will do); kind "sigmoid":
+    a = sigmoid(gate), b = 1 - a, gate of x's type (bf16 or fp32); "decay": a = gate, fp32, b = 1.
+    h0 [B, D] fp32 or None.  With offsets [B + 1] int32 the sequences lie packed: x, gate
+    [tokens, D]; outputs of tokens of no sequence are not written.  Returns (h, h_T, states): h as
+    x, h_T [B, D] fp32 (out_state may be h0), and with keep_states what scan_backward starts from
+    (the state before every 64th token, fp32), else None."""
+    import torch
+    where = "scan_prefill"
+    B, T, D, ldx, ldg = _scan_args(where, x, gate, kind, offsets)
+    dev = x.get_device()
+    _dense(where, "h0", h0, torch.float32, dev, (B, D))
+    _dense(where, "out_state", out_state, torch.float32, dev, (B, D))
+    _on_this_gpu(where, dev)
+    packed = offsets is not None
+    h = _new(x) if want_h else None
+    h_T = out_state
+    if want_state and h_T is None:
+        h_T = torch.empty((B, D), dtype=torch.float32, device=x.device)
+    states = None
+    if keep_states:
+        states = torch.empty(_states_shape(B, T, D, packed), dtype=torch.float32, device=x.device)
+    need = gdn_scan_prefill_workspace_size(B, T, D, packed) if packed else 0
+    workspace, need = _workspace(where, workspace, need, x, stream)
+    gdn_scan_prefill(x, gate, h0, h, h_T, states, offsets, B, T, D, ldx, ldg, SCANS[kind],
+                     _dtype_code(x), workspace, need, stream)
+    _written_on(stream, h, None if h_T is out_state else h_T, states)
+    return h, h_T, states
+
+
+def scan_backward(x, gate, dh, h0=None, dh_T=None, states=None, kind="sigmoid", offsets=None,
+                  want_dh0=None, workspace=None, stream=None):
+    """Gradients of scan_prefill from its inputs, dh (dense, as x) and dh_T [B, D] (fp32 or None).
+    states: as the forward pass kept them for the same inputs, or None (formed again).  Returns
+    (dx, dgate, dh0), dgate as gate; dh0 is formed if h0 is given or want_dh0 is true, else None.
+    Gradients of tokens of no sequence are not written."""
+    import torch
+    where = "scan_backward"
+    B, T, D, ldx, ldg = _scan_args(where, x, gate, kind, offsets)
+    dev, packed = x.get_device(), offsets is not None
+    _dense(where, "h0", h0, torch.float32, dev, (B, D))
+    _dense(where, "dh_T", dh_T, torch.float32, dev, (B, D))
+    _dense(where, "dh", dh, x.dtype, dev, x.shape)
+    _dense(where, "states", states, torch.float32, dev, _states_shape(B, T, D, packed))
+    _on_this_gpu(where, dev)
+    dx, dgate, dh0 = _new(x), _new(gate), None
+    if want_dh0 or (want_dh0 is None and h0 is not None):
+        dh0 = torch.empty((B, D), dtype=torch.float32, device=x.device)
+    need = 0
+    if packed or states is None:
+        need = gdn_scan_backward_workspace_size(B, T, D, packed, states is not None)
+    workspace, need = _workspace(where, workspace, need, x, stream)
+    gdn_scan_backward(x, gate, dh, h0, dh_T, states, dx, dgate, dh0, offsets, B, T, D, ldx, ldg,
+                      SCANS[kind], _dtype_code(x), workspace, need, stream)
+    _written_on(stream, dx, dgate, dh0)
+    return dx, dgate, dh0
+
+
+def scan_decode_step(x, gate, h, kind="sigmoid", h_out=None, y=None, stream=None):
+    """One token of scan_prefill: x, gate [B, D] (slices of one projection will do); h [B, D] fp32,
+    updated in place unless h_out is given.  Returns y [B, D], the new state rounded to x's type."""
+    import torch
+    where = "scan_decode_step"
+    if kind not in SCANS or x.dim() != 2 or gate.shape != x.shape:
+        _reject(where, f"kind {kind!r}, x {tuple(x.shape)}, gate {tuple(gate.shape)}")
+    B, D = x.shape
+    dev = x.get_device()
+    if h_out is None:
+        h_out = h
+    ldx = _row_stride(where, "x", x, x.dtype, dev)
+    ldg = _row_stride(where, "gate", gate, torch.float32 if kind == "decay" else x.dtype, dev)
+    _dense(where, "h", h, torch.float32, dev, x.shape)
+    _dense(where, "h_out", h_out, torch.float32, dev, x.shape)
+    _dense(where, "y", y, x.dtype, dev, x.shape)
+    _on_this_gpu(where, dev)
+    given = y
+    if y is None:
+        y = _new(x)
+    gdn_scan_decode_step(x, gate, h, h_out, y, B, D, ldx, ldg, SCANS[kind], _dtype_code(x), stream)
+    if given is None:
+        _written_on(stream, y)
+    return y
+
+
+def layer_norm(x, w=None, b=None, residual=None, eps=1e-5, want_stats=False, out=None,
+               stream=None):
+    """y = (s - mean) / sqrt(var + eps) * w + b over the channels of s = x [..., D], or of
+    s = x + residual rounded to x's type (gdn_layer_norm); w, b [D] fp32 or None.  x and residual
+    may be slices of a projection.  Returns (y, s, stats): s None without a residual, stats
+    [..., 2] fp32 (what layer_norm_backward needs) or None.  out: (y, s) to write to, dense; they
+    may hold dense x and residual themselves."""
+    import torch
+    where = "layer_norm"
+    dev, D, lead = x.get_device(), x.shape[-1], x.shape[:-1]
+    ldx = _row_stride(where, "x", x, x.dtype, dev)
+    ldr = 0
+    if residual is not None:
+        if residual.shape != x.shape:
+            _reject(where, f"x {tuple(x.shape)}, residual {tuple(residual.shape)}")
+        ldr = _row_stride(where, "residual", residual, x.dtype, dev)
+    _dense(where, "w", w, torch.float32, dev, (D,))
+    _dense(where, "b", b, torch.float32, dev, (D,))
+    if out is not None:
+        y, s = out
+        if y is None or (s is None) != (residual is None):
+            _reject(where, "out must be (y, s), with s None where there is no residual")
+        _dense(where, "out[0]", y, x.dtype, dev, x.shape)
+        _dense(where, "out[1]", s, x.dtype, dev, x.shape)
+    _on_this_gpu(where, dev)
+    if out is None:
+        y = _new(x)
+        s = None if residual is None else _new(x)
+    stats = None
+    if want_stats:
+        stats = torch.empty(lead + (2,), dtype=torch.float32, device=x.device)
+    gdn_layer_norm(x, residual, w, b, y, s, stats, lead.numel(), D, ldx, ldr, eps, _dtype_code(x),
+                   stream)
+    if out is None:
+        _written_on(stream, y, s, stats)
+    else:
+        _written_on(stream, stats)
+    return y, s, stats
+
+
+def layer_norm_backward(s, dy, stats, w=None, ds=None, want_db=False, workspace=None, stream=None):
+    """Gradients of layer_norm from s (x where there was no residual), dy (dense), its stats and
+    ds, the gradient that reaches s past the norm (dense, or None).  Returns (dx, dw, db): dx is
+    the gradient of x and of the residual; dw None unless w is given, db None unless wanted."""
+    import torch
+    where = "layer_norm_backward"
+    dev, D, lead = s.get_device(), s.shape[-1], s.shape[:-1]
+    lds = _row_stride(where, "s", s, s.dtype, dev)
+    _dense(where, "dy", dy, s.dtype, dev, s.shape)
+    _dense(where, "ds", ds, s.dtype, dev, s.shape)
+    _dense(where, "stats", stats, torch.float32, dev, lead + (2,))
+    _dense(where, "w", w, torch.float32, dev, (D,))
+    _on_this_gpu(where, dev)
+    N = lead.numel()
+    dx = _new(s)
+    dw = None if w is None else _new(w)
+    db = torch.empty(D, dtype=torch.float32, device=s.device) if want_db else None
+    need = 0
+    if w is not None or want_db:
+        need = gdn_layer_norm_backward_workspace_size(N, D)
+    workspace, need = _workspace(where, workspace, need, s, stream)
+    gdn_layer_norm_backward(s, dy, stats, w, ds, dx, dw, db, N, D, lds, _dtype_code(s), workspace,
+                            need, stream)
+    _written_on(stream, dx, dw, db)
+    return dx, dw, db

@@ -131,6 +131,37 @@ int check_linear(int B, int T, int Hq, int H, int K, int V, long long q_stride, 
     return GDN_OK;
 }
 
+// The checks that the recurrence's calls share.
+int check_scan(const void *x, const void *gate, int B, int T, int D, bool packed,
+               long long x_stride, long long gate_stride, int kind, int dtype) {
+    if (B < 0 || T < 0 || D < 0) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
+    if (kind != GDN_SCAN_DECAY && kind != GDN_SCAN_SIGMOID) return GDN_ERR_INVALID_ARG;
+    if (D % 8) return GDN_ERR_UNSUPPORTED;
+    const int unit = dtype == GDN_BF16 ? 8 : 4;  // elements of 16 bytes
+    const int gate_unit = kind == GDN_SCAN_DECAY ? 4 : unit;
+    // the strides' bound is a tensor map's
+    if (x_stride < D || gate_stride < D || x_stride % unit || gate_stride % gate_unit ||
+        x_stride > (1LL << 36) || gate_stride > (1LL << 36))
+        return GDN_ERR_INVALID_ARG;
+    const long long most = (1LL << 31) - 1024;  // tokens are 32-bit coordinates of a tile
+    if ((packed ? T : (long long)B * T) > most || (long long)B * D > (1LL << 36))
+        return GDN_ERR_INVALID_ARG;
+    return aligned16(x) && aligned16(gate) ? GDN_OK : GDN_ERR_ALIGNMENT;
+}
+
+// Bytes of the states before every 64th token, rounded up.
+size_t scan_states_bytes(int B, int T, int D, bool packed) {
+    const size_t rows = (size_t)(packed ? 1 : B) * ((T + gdn::kScanBlock - 1) / gdn::kScanBlock);
+    return (rows * D * sizeof(float) + 255) & ~size_t(255);
+}
+
+int check_layer_norm(long long N, int D, int dtype) {
+    if (N < 0 || N > (1LL << 40) || D < 0) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
+    return D % 8 || D > 16384 ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -723,6 +754,140 @@ int gdn_linear_decode_step(const void *q, const void *k, const void *v, const fl
         if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
     return from_cuda(gdn::launch_linear_decode(q, k, v, alpha, S, S_out, o, B, Hq, H, K, V, scale,
                                                dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_scan_prefill_workspace_size(int B, int T, int D, int packed) {
+    if (B <= 0 || T <= 0 || D <= 0 || !packed) return 0;
+    return gdn::scan_map_bytes(T);
+}
+
+int gdn_scan_prefill(const void *x, const void *gate, const float *h0, void *h, float *h_T,
+                     float *states, const int *offsets, int B, int T, int D, long long x_stride,
+                     long long gate_stride, gdn_scan_kind kind, gdn_dtype dtype, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    const bool packed = offsets != nullptr;
+    const int e = check_scan(x, gate, B, T, D, packed, x_stride, gate_stride, kind, dtype);
+    if (e != GDN_OK) return e;
+    const void *ptrs[] = {h0, h, h_T, states, offsets, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    if (B == 0 || D == 0) return GDN_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return empty_prefill(h0, h_T, B, 1, D, 1, st);
+    if (!x || !gate || (!h && !h_T && !states) || h == x || h == gate) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn_scan_prefill_workspace_size(B, T, D, packed);
+    if (workspace_bytes < need || (need && !workspace)) return GDN_ERR_WORKSPACE;
+    gdn::ScanArgs a = {};
+    a.x = x; a.gate = gate; a.h0 = h0; a.h = h; a.h_T = h_T; a.states = states;
+    a.offsets = offsets; a.B = B; a.T = T; a.D = D; a.ldx = x_stride; a.ldg = gate_stride;
+    a.sigmoid = kind == GDN_SCAN_SIGMOID;
+    return from_cuda(gdn::launch_scan(a, dtype, workspace, st));
+}
+
+size_t gdn_scan_backward_workspace_size(int B, int T, int D, int packed, int kept) {
+    if (B <= 0 || T <= 0 || D <= 0) return 0;
+    return (packed ? gdn::scan_map_bytes(T) : 0) +
+           (kept ? 0 : scan_states_bytes(B, T, D, packed != 0));
+}
+
+int gdn_scan_backward(const void *x, const void *gate, const void *dh, const float *h0,
+                      const float *dh_T, const float *states, void *dx, void *dgate, float *dh0,
+                      const int *offsets, int B, int T, int D, long long x_stride,
+                      long long gate_stride, gdn_scan_kind kind, gdn_dtype dtype, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    const bool packed = offsets != nullptr;
+    const int e = check_scan(x, gate, B, T, D, packed, x_stride, gate_stride, kind, dtype);
+    if (e != GDN_OK) return e;
+    const void *ptrs[] = {dh, h0, dh_T, states, dx, dgate, dh0, offsets, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    if (B == 0 || D == 0) return GDN_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return empty_prefill(dh_T, dh0, B, 1, D, 1, st);
+    if (!x || !gate || !dh || !dx || !dgate) return GDN_ERR_INVALID_ARG;
+    // every tile's inputs are read while the outputs of others are written
+    const void *ins[] = {x, gate, dh};
+    for (const void *p : ins)
+        if (p == dx || p == dgate) return GDN_ERR_INVALID_ARG;
+    if (dx == dgate) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn_scan_backward_workspace_size(B, T, D, packed, states != nullptr);
+    if (workspace_bytes < need || (need && !workspace)) return GDN_ERR_WORKSPACE;
+    gdn::ScanArgs a = {};
+    a.x = x; a.gate = gate; a.dh = dh; a.h0 = h0; a.dh_T = dh_T; a.states = const_cast<float *>(states);
+    a.dx = dx; a.dgate = dgate; a.dh0 = dh0;
+    a.offsets = offsets; a.B = B; a.T = T; a.D = D; a.ldx = x_stride; a.ldg = gate_stride;
+    a.sigmoid = kind == GDN_SCAN_SIGMOID;
+    return from_cuda(gdn::launch_scan_backward(a, dtype, workspace, st));
+}
+
+int gdn_scan_decode_step(const void *x, const void *gate, const float *h, float *h_out, void *y,
+                         int B, int D, long long x_stride, long long gate_stride,
+                         gdn_scan_kind kind, gdn_dtype dtype, void *stream) {
+    const int e = check_scan(x, gate, B, 1, D, false, x_stride, gate_stride, kind, dtype);
+    if (e != GDN_OK) return e;
+    if (!aligned16(h) || !aligned16(h_out) || !aligned16(y)) return GDN_ERR_ALIGNMENT;
+    if (B == 0 || D == 0) return GDN_OK;
+    if (!x || !gate || !h || !h_out || (y && (y == h || y == h_out))) return GDN_ERR_INVALID_ARG;
+    return from_cuda(gdn::launch_scan_step(x, gate, h, h_out, y, B, D, x_stride, gate_stride,
+                                           kind == GDN_SCAN_SIGMOID, dtype,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_layer_norm(const void *x, const void *residual, const float *w, const float *b, void *y,
+                   void *s, float *stats, long long N, int D, long long x_stride,
+                   long long residual_stride, float eps, gdn_dtype dtype, void *stream) {
+    const int e = check_layer_norm(N, D, dtype);
+    if (e != GDN_OK) return e;
+    if (!(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    const int unit = dtype == GDN_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (x_stride < D || x_stride % unit ||
+        (residual && (residual_stride < D || residual_stride % unit)))
+        return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {x, residual, w, b, y, s, stats};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    if (N == 0 || D == 0) return GDN_OK;
+    if (!x || !y || (s && !residual) || s == y) return GDN_ERR_INVALID_ARG;
+    // in place only where the rows lie as the outputs do
+    if (((y == x || s == x) && x_stride != D) ||
+        (residual && (y == residual || s == residual) && residual_stride != D))
+        return GDN_ERR_INVALID_ARG;
+    return from_cuda(gdn::launch_layer_norm(x, residual, w, b, y, s, stats, N, D, x_stride,
+                                            residual_stride, eps, dtype,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_layer_norm_backward_workspace_size(long long N, int D) {
+    if (N <= 0 || D <= 0 || D > 16384) return 0;
+    return (size_t)gdn::layer_norm_parts(N, D) * 2 * D * sizeof(float);
+}
+
+int gdn_layer_norm_backward(const void *s, const void *dy, const float *stats, const float *w,
+                            const void *ds, void *dx, float *dw, float *db, long long N, int D,
+                            long long s_stride, gdn_dtype dtype, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    const int e = check_layer_norm(N, D, dtype);
+    if (e != GDN_OK) return e;
+    if (s_stride < D || s_stride % (dtype == GDN_BF16 ? 8 : 4)) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {s, dy, stats, w, ds, dx, dw, db, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
+    if (D == 0) return GDN_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N == 0) {  // sums over nothing
+        cudaError_t c = cudaSuccess;
+        if (dw) c = cudaMemsetAsync(dw, 0, sizeof(float) * D, st);
+        if (db && c == cudaSuccess) c = cudaMemsetAsync(db, 0, sizeof(float) * D, st);
+        return from_cuda(c);
+    }
+    if (!s || !dy || !stats || !dx || (dw && dw == db)) return GDN_ERR_INVALID_ARG;
+    // in place only where the rows lie as the output's do
+    if (dx == s && s_stride != D) return GDN_ERR_INVALID_ARG;
+    if ((dw || db) &&
+        (!workspace || workspace_bytes < gdn_layer_norm_backward_workspace_size(N, D)))
+        return GDN_ERR_WORKSPACE;
+    return from_cuda(gdn::launch_layer_norm_backward(s, dy, stats, w, ds, dx, dw, db, N, D, s_stride,
+                                                     dtype, static_cast<float *>(workspace), st));
 }
 
 int gdn_get_last_device_status(void *stream) {

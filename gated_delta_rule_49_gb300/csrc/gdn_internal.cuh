@@ -210,6 +210,43 @@ cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, co
                                  const float *S, float *S_out, void *o, int B, int Hq, int H,
                                  int K, int V, float scale, gdn_dtype dt, cudaStream_t stream);
 
+// The gated linear recurrence over channels: tokens between the kept states,
+// the call's arguments, and its launches.
+constexpr int kScanBlock = 64;
+struct ScanArgs {
+    const void *x, *gate, *dh;  // [tokens, D], token strides ldx, ldg, D
+    const float *h0;            // [B, D] or NULL
+    const float *dh_T;          // backward: [B, D] or NULL
+    float *states;              // [B, ceil(T / 64), D] (packed: [ceil(T / 64), D]) or NULL
+    void *h;                    // forward: [tokens, D] or NULL
+    float *h_T;                 // forward: [B, D] or NULL
+    void *dx, *dgate;           // backward: [tokens, D]
+    float *dh0;                 // backward: [B, D] or NULL
+    const int *offsets;         // [B + 1] or NULL: B x T tokens
+    int B, T, D;
+    long long ldx, ldg;
+    bool sigmoid;
+};
+// Bytes of the table of packed tokens' sequences, at the workspace's start.
+size_t scan_map_bytes(int T);
+cudaError_t launch_scan(const ScanArgs &a, gdn_dtype dt, void *workspace, cudaStream_t stream);
+cudaError_t launch_scan_backward(const ScanArgs &a, gdn_dtype dt, void *workspace,
+                                 cudaStream_t stream);
+cudaError_t launch_scan_step(const void *x, const void *gate, const float *h, float *h_out, void *y,
+                             int B, int D, long long ldx, long long ldg, bool sigmoid, gdn_dtype dt,
+                             cudaStream_t stream);
+
+// Layer norm of rows, and its gradients; the weights' need layer_norm_parts rows
+// of 2 D floats.
+int layer_norm_parts(long long N, int D);
+cudaError_t launch_layer_norm(const void *x, const void *res, const float *w, const float *b,
+                              void *y, void *s, float *stats, long long N, int D, long long ldx,
+                              long long ldr, float eps, gdn_dtype dt, cudaStream_t stream);
+cudaError_t launch_layer_norm_backward(const void *s, const void *dy, const float *stats,
+                                       const float *w, const void *ds, void *dx, float *dw,
+                                       float *db, long long N, int D, long long lds, gdn_dtype dt,
+                                       float *parts, cudaStream_t stream);
+
 // Programmatic dependent launch: a kernel launched this way may be scheduled
 // while the previous kernel on the stream finishes; it must execute
 // pdl_wait() before its first global-memory access (which then sees all of

@@ -588,6 +588,117 @@ GDN_API int gdn_linear_decode_step(const void *q, const void *k, const void *v,
                                    gdn_dtype dtype, void *stream);
 
 /*
+ * gdn_scan_prefill -- the gated linear recurrence, one number of state a
+ * channel, over the tokens of B sequences:
+ *
+ *     h_t = a_t h_{t-1} + b_t x_t
+ *     GDN_SCAN_DECAY    a_t = gate_t (float32, in [0, 1]; not checked), b_t = 1
+ *     GDN_SCAN_SIGMOID  a_t = 1 / (1 + exp(-gate_t)) (dtype), b_t = 1 - a_t
+ *
+ *   x     [B, T, D] (dtype), gate [B, T, D] (float32 or dtype, as above);
+ *         consecutive tokens lie x_stride / gate_stride elements apart (at least
+ *         D, a multiple of 16 bytes), so that they may be parts of one projection
+ *   h0    [B, D] float32, or NULL = zero
+ *   h     [B, T, D] (dtype), dense, or NULL; not x or gate
+ *   h_T   [B, D] float32, or NULL; may be h0
+ *   states  NULL, or [B, ceil(T / 64), D] float32: the state before every 64th
+ *         token, which gdn_scan_backward starts from
+ *   offsets  NULL, or [B + 1] int32 on the device: the B sequences lie packed
+ *         in T tokens as for gdn_linear_prefill (bad offsets as there); states is
+ *         then [ceil(T / 64), D], of the T tokens (a row whose token starts a
+ *         sequence or belongs to none is undefined), and tokens of no sequence
+ *         keep what h held.
+ *
+ * D a multiple of 8 (else GDN_ERR_UNSUPPORTED); at most 2^31 - 1024 tokens in
+ * all.  Everything is float32 from the load to the one rounding of h.  A value
+ * that is not finite reaches what the recurrence carries it to and nothing else.
+ * workspace: gdn_scan_prefill_workspace_size bytes (0 unless packed).
+ */
+typedef enum { GDN_SCAN_DECAY = 0, GDN_SCAN_SIGMOID = 1 } gdn_scan_kind;
+GDN_API size_t gdn_scan_prefill_workspace_size(int B, int T, int D, int packed);
+GDN_API int gdn_scan_prefill(const void *x, const void *gate, const float *h0, void *h, float *h_T,
+                             float *states, const int *offsets, int B, int T, int D,
+                             long long x_stride, long long gate_stride, gdn_scan_kind kind,
+                             gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * gdn_scan_backward -- gradients of gdn_scan_prefill from its inputs, dh
+ * [B, T, D] (dtype, dense) and dh_T [B, D] float32 (NULL = zero):
+ *
+ *     G_t = dh_t + a_{t+1} G_{t+1}   (the last token's takes dh_T up),   dx_t = b_t G_t,
+ *     dgate_t = G_t h_{t-1}                      (GDN_SCAN_DECAY, float32)
+ *     dgate_t = G_t (h_{t-1} - x_t) a_t b_t      (GDN_SCAN_SIGMOID, dtype)
+ *     dh0 = a_1 G_1
+ *
+ * dx, dgate [B, T, D] dense; dh0 [B, D] float32, or NULL; may be dh_T.  Tokens
+ * of no sequence keep what dx and dgate held.
+ * states: as gdn_scan_prefill wrote them for the same inputs, or NULL: they are
+ * then formed by a pass over x and gate of the call's own.
+ * workspace: gdn_scan_backward_workspace_size bytes (kept: states are given; 0
+ * for dense sequences with states).
+ */
+GDN_API size_t gdn_scan_backward_workspace_size(int B, int T, int D, int packed, int kept);
+GDN_API int gdn_scan_backward(const void *x, const void *gate, const void *dh, const float *h0,
+                              const float *dh_T, const float *states, void *dx, void *dgate,
+                              float *dh0, const int *offsets, int B, int T, int D,
+                              long long x_stride, long long gate_stride, gdn_scan_kind kind,
+                              gdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * gdn_scan_decode_step -- one token of gdn_scan_prefill: x, gate [B, D] (rows
+ * x_stride / gate_stride elements apart); reads h [B, D] float32 and writes
+ * h_out, which may be h, and y [B, D] (dtype, dense), the rounded state, or NULL.
+ */
+GDN_API int gdn_scan_decode_step(const void *x, const void *gate, const float *h, float *h_out,
+                                 void *y, int B, int D, long long x_stride, long long gate_stride,
+                                 gdn_scan_kind kind, gdn_dtype dtype, void *stream);
+
+/*
+ * gdn_layer_norm -- the norm of N rows over their D channels, with the sum that
+ * runs past a layer:
+ *
+ *     s = x, or x + residual rounded to dtype
+ *     m = sum_i s_i / D,   r = (sum_i (s_i - m)^2 / D + eps)^(-1/2)
+ *     y = (s - m) r .* w + b
+ *
+ *   x, residual [N, D] (dtype), rows x_stride / residual_stride elements apart
+ *          (>= D, a multiple of 16 bytes); residual may be NULL
+ *   w, b   [D] float32, or NULL for ones / zeros
+ *   y      [N, D] (dtype), dense; may be x or residual where those are dense
+ *   s      [N, D] (dtype), dense, or NULL; needs residual; may be x or residual
+ *          where those are dense, not y
+ *   stats  [N, 2] float32: m and r of each row, for gdn_layer_norm_backward; or
+ *          NULL
+ *
+ * D a multiple of 8 up to 16384 (else GDN_ERR_UNSUPPORTED).  Everything is
+ * float32 from the load to the rounding of s and y.
+ */
+GDN_API int gdn_layer_norm(const void *x, const void *residual, const float *w, const float *b,
+                           void *y, void *s, float *stats, long long N, int D, long long x_stride,
+                           long long residual_stride, float eps, gdn_dtype dtype, void *stream);
+
+/*
+ * gdn_layer_norm_backward -- gradients of gdn_layer_norm from s (x where there
+ * was no residual; rows s_stride elements apart), dy [N, D], the forward pass's
+ * stats and ds [N, D] (dtype, dense, or NULL = zero), the gradient that reaches s
+ * past the norm.  With n = (s - m) r and g = w .* dy:
+ *
+ *     dx = r (g - sum g / D - n (sum g n) / D) + ds     (of x and of the residual)
+ *     dw = sum over rows of dy .* n,   db = sum over rows of dy
+ *
+ * dx [N, D] (dtype, dense; may be dy or ds); dw, db [D] float32, each may be
+ * NULL.  Where one is wanted: workspace of gdn_layer_norm_backward_workspace_size
+ * bytes.  The rows are summed in a fixed order: equal inputs give equal bits.
+ */
+GDN_API size_t gdn_layer_norm_backward_workspace_size(long long N, int D);
+GDN_API int gdn_layer_norm_backward(const void *s, const void *dy, const float *stats,
+                                    const float *w, const void *ds, void *dx, float *dw, float *db,
+                                    long long N, int D, long long s_stride, gdn_dtype dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * gdn_get_last_device_status -- synchronise `stream`, then read and clear the
  * current device's status word.  Returns GDN_OK, GDN_ERR_TIMEOUT,
  * GDN_ERR_DEVICE_BOUNDS, GDN_WARN_NOT_CONVERGED, GDN_WARN_RANK_DEFICIENT or
