@@ -7,18 +7,57 @@
 //
 //     G_t = dh_t + a_{t+1} G_{t+1},  dx = b G,  da = G (h_{t-1} - [sigmoid] x),
 //     dg = da a b,  dh0 = a_1 G_1
+//
+// Bound by memory: 6 bytes a value forward (sigmoid, bf16), 10 backward.  What a
+// piece of tokens does to the state is h -> P h + H, and pieces compose: a CTA
+// owns 64 channels of a stream of tokens and takes tiles of 8 R of them, each of
+// its 8 warps a run of R consecutive tokens, a lane two channels.  A warp finds
+// P and H of its run, the runs' are joined through shared memory, and a second
+// walk over the values, still in registers, gives the outputs: the inputs are
+// read once.  Gradients go the other way with the same P: what leaves a run
+// towards earlier tokens is u -> P u + V; the states h_{t-1} that they need start
+// from those that the forward pass kept every 64 tokens, a tile of the gradients.
+//
+// Few streams of few channels: a cluster of 2 to 8 CTAs takes consecutive tiles
+// of one stream, and every CTA sends its tile's P and H to the others' shared
+// memory, so that a long sequence is still read once.
+//
+// A stream is one sequence, or several: packed ones (a table gives each token's
+// sequence) or dense ones of at most a tile.  There a run knows which of its tokens
+// start or end a sequence or belong to none; a start takes h0 in the place of the
+// state that arrives, by selection, never by a factor of 0 (a NaN would pass).
+#include <cudaTypedefs.h>
+
+#include "gdn_sm100.cuh"
 #include "gdn_vec8.cuh"
-#include "gdn_linear_item.cuh"
 
 namespace gdn {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 namespace {
 
+using namespace sm100;
+
+constexpr int kChannels = 64;  // of a CTA
+constexpr int kWarps = 8;      // runs of a tile
+constexpr int kScanThreads = kWarps * 32;
+constexpr int kMaxCluster = 8;
+constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
+
 // a and b of a gate.  b = 1 - a is formed without the difference: a near 1
-// would leave nothing of it.
-template <bool SIG> __device__ __forceinline__ void gate_ab(float g, float &a, float &b) {
+// would leave nothing of it.  bf16 runs take the fast exp and quotient (a few
+// float32 steps; exp(|g|) is held at 2^125 so that b stays a number).
+template <typename T, bool SIG> __device__ __forceinline__ void gate_ab(float g, float &a, float &b) {
     if constexpr (!SIG) {
         a = g;
         b = 1.f;
+    } else if constexpr (sizeof(T) == 2) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+        asm("min.NaN.f32 %0, %0, %1;" : "+f"(e) : "f"(0x1p125f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
+        b = e * a;
     } else {
         const float e = expf(-fabsf(g)), r = 1.f / (1.f + e), s = e * r;
         a = g < 0.f ? s : r;
@@ -29,68 +68,623 @@ template <bool SIG> __device__ __forceinline__ void gate_ab(float g, float &a, f
 template <typename T, bool SIG> struct GateType { using type = T; };
 template <typename T> struct GateType<T, false> { using type = float; };
 
-// One thread a sequence and channel.
-template <typename T, bool SIG>
-__global__ void scan_kernel(const ScanArgs p, int *status) {
-    using G = typename GateType<T, SIG>::type;
-    const int seq = blockIdx.x, c = blockIdx.y * blockDim.x + threadIdx.x;
-    const LinearItem it = linear_item(p.offsets, p.B, p.T, p.T, seq, blockIdx.y == 0 ? status : nullptr);
-    if (c >= p.D || it.seq < 0) return;
-    const long long at = (long long)seq * p.D + c;
-    float h = p.h0 ? p.h0[at] : 0.f;
-    const int blocks = (p.T + kScanBlock - 1) / kScanBlock;
-    for (int i = 0; i < it.len; ++i) {
-        const int t = it.base + i;  // packed: of all tokens
-        const long long tok = it.first + i;
-        if (p.states && t % kScanBlock == 0)
-            p.states[((p.offsets ? 0 : (long long)seq * blocks) + t / kScanBlock) * p.D + c] = h;
-        float a, b;
-        gate_ab<SIG>(to_f32(static_cast<const G *>(p.gate)[tok * p.ldg + c]), a, b);
-        h = fmaf(a, h, b * to_f32(static_cast<const T *>(p.x)[tok * p.ldx + c]));
-        if (p.h) static_cast<T *>(p.h)[tok * p.D + c] = from_f32<T>(h);
-    }
-    if (p.h_T) p.h_T[at] = h;
+// A lane's two channels.
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void store2(float *p, float x, float y) {
+    *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+}
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
 }
 
-template <typename T, bool SIG>
-__global__ void scan_backward_kernel(const ScanArgs p, int *status) {
+// Tokens of a warp's run and tiles in flight, by the bytes of a token's channel.
+// (Registers hold two or three float32 a token and channel.)
+template <typename T, bool SIG, bool BACK> struct Shape {
     using G = typename GateType<T, SIG>::type;
-    const int seq = blockIdx.x, c = blockIdx.y * blockDim.x + threadIdx.x;
-    const LinearItem it = linear_item(p.offsets, p.B, p.T, p.T, seq, blockIdx.y == 0 ? status : nullptr);
-    if (c >= p.D || it.seq < 0) return;
-    const long long at = (long long)seq * p.D + c;
-    float u = p.dh_T ? p.dh_T[at] : 0.f;
-    const int blocks = (p.T + kScanBlock - 1) / kScanBlock;
-    const int t0 = it.base, t1 = it.base + it.len;
-    const long long shift = it.first - it.base;
-    float past[kScanBlock];
-    for (int blk = (t1 - 1) / kScanBlock; it.len && blk >= t0 / kScanBlock; --blk) {
-        const int lo = max(t0, blk * kScanBlock), hi = min(t1, (blk + 1) * kScanBlock);
-        float h = lo == t0 ? (p.h0 ? p.h0[at] : 0.f)
-                           : p.states[((p.offsets ? 0 : (long long)seq * blocks) + blk) * p.D + c];
-        for (int t = lo; t < hi; ++t) {
-            const long long tok = shift + t;
-            float a, b;
-            gate_ab<SIG>(to_f32(static_cast<const G *>(p.gate)[tok * p.ldg + c]), a, b);
-            past[t - lo] = h;
-            h = fmaf(a, h, b * to_f32(static_cast<const T *>(p.x)[tok * p.ldx + c]));
-        }
-        for (int t = hi - 1; t >= lo; --t) {
-            const long long tok = shift + t;
-            float a, b;
-            gate_ab<SIG>(to_f32(static_cast<const G *>(p.gate)[tok * p.ldg + c]), a, b);
-            const float x = to_f32(static_cast<const T *>(p.x)[tok * p.ldx + c]);
-            const float g = to_f32(static_cast<const T *>(p.dh)[tok * p.D + c]) + u;
-            static_cast<T *>(p.dx)[tok * p.D + c] = from_f32<T>(b * g);
-            const float da = SIG ? g * (past[t - lo] - x) * a * b : g * past[t - lo];
-            static_cast<G *>(p.dgate)[tok * p.D + c] = from_f32<G>(da);
-            u = a * g;
-        }
-    }
-    if (p.dh0) p.dh0[at] = u;
+    static constexpr int kRun = !BACK && sizeof(T) + sizeof(G) == 4 ? 16 : 8;
+    static constexpr int kTokens = kRun * kWarps;  // of a tile
+    static constexpr int kXBytes = kTokens * kChannels * (int)sizeof(T);
+    static constexpr int kGBytes = kTokens * kChannels * (int)sizeof(G);
+    static constexpr int kStage = kXBytes * (BACK ? 2 : 1) + kGBytes;
+    static constexpr int kStages = 98304 / kStage < 3 ? 3 : 98304 / kStage;
+};
+
+struct ScanRun {
+    const float *h0, *dh_T;
+    float *states;
+    void *h, *dx, *dgate;
+    float *h_T, *dh0;
+    const int *map;    // packed: the sequence of each token, or -1
+    int D, groups, cluster;
+    int total;         // tokens
+    int stream;        // tokens of a stream
+    int step;          // tokens of a tile that are its own
+    int rows;          // tokens of a box
+    int T, blocks;     // dense sequences: tokens, and kept states
+    int *status;
+};
+
+struct Totals {        // of a tile, sent through a cluster
+    float4 ph[2][kMaxCluster][32];
+    int reset[2][kMaxCluster];
+};
+struct ScanShared {
+    float4 run[2][kWarps][32];  // P, H of a lane's channels (backward: P and V)
+    float2 hrun[2][kWarps][32]; // backward: H
+    int reset[2][kWarps];       // bit 0: a start among the run's tokens, bit 1: an end
+    Totals totals;
+    uint64_t full[8], sent[2];
+    int abort;
+};
+
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, uint64_t *bar, int c,
+                                         int t) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t peer(const void *p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void send4(uint32_t dst, uint32_t bar, float4 v) {
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+        "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void send1(uint32_t dst, uint32_t bar, int v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(dst),
+                 "r"(v), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
-// One token: a thread takes eight channels, all of its loads before any arithmetic.
+// A wait with a limit; the first that runs out ends all others of the CTA.
+template <bool CLUSTER>
+__device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, ScanShared &sh, int *status) {
+    auto ready = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (ready()) return;
+    const long long t0 = clock64();
+    volatile int *const abort = &sh.abort;
+    while (!ready()) {
+        if (*abort) return;
+        if (clock64() - t0 > kWaitLimit) {
+            *abort = 1;
+            if (status) atomicOr(status, kStatusTimeout);
+            return;
+        }
+    }
+}
+
+// The joins of pieces, on two channels: what the state becomes over one.
+__device__ __forceinline__ void over(float2 &c, const float4 &ph, bool reset) {
+    c.x = reset ? ph.z : fmaf(ph.x, c.x, ph.z);
+    c.y = reset ? ph.w : fmaf(ph.y, c.y, ph.w);
+}
+
+// Which of a run's tokens are in a sequence, start one, end one; lane l holds
+// the sequence of token l - 1 of the run.
+struct RunMask {
+    unsigned act, start, end;
+    int seq;
+};
+template <bool MASKED, int R>
+__device__ __forceinline__ RunMask run_mask(const ScanRun &p, int base, int len, int tile0, int r0) {
+    // tile0: the tile's first token in the stream, r0: the run's in the tile
+    RunMask m;
+    constexpr unsigned all = (1u << R) - 1u;
+    if constexpr (!MASKED) {
+        const int n = min(max(len - (tile0 + r0), 0), R);
+        m.act = n >= R ? all : (1u << n) - 1u;
+        m.start = m.end = 0;
+        m.seq = 0;
+    } else {
+        const int lane = threadIdx.x & 31;
+        const int k = r0 + lane - 1, t = tile0 + k;
+        int s = -1;
+        // a neighbour of another tile counts only where the table is absolute
+        if (lane < R + 2 && t >= 0 && t < len) {
+            if (p.map) s = p.map[t];
+            else if (k >= 0 && k < p.step) s = (base + t) / p.T;
+        }
+        const int before = __shfl_up_sync(0xffffffffu, s, 1), after = __shfl_down_sync(0xffffffffu, s, 1);
+        const bool mine = s >= 0 && lane >= 1 && lane <= R;
+        m.act = (__ballot_sync(0xffffffffu, mine) >> 1) & all;
+        m.start = (__ballot_sync(0xffffffffu, mine && s != before) >> 1) & all;
+        m.end = (__ballot_sync(0xffffffffu, mine && s != after) >> 1) & all;
+        m.seq = s;
+    }
+    return m;
+}
+__device__ __forceinline__ int run_seq(const RunMask &m, int i) {
+    return __shfl_sync(0xffffffffu, m.seq, i + 1);
+}
+
+// A tile's totals to every CTA of the cluster (by one warp), and the pieces of the
+// CTAs before this one (rank) applied to c; returns what all of them make of it.
+// `before` gets the state that this CTA's tile starts from.
+__device__ __forceinline__ void send_totals(ScanShared &sh, int buf, int rank, int cluster,
+                                            const float4 &ph, int reset) {
+    const int lane = threadIdx.x & 31;
+    for (int r = 0; r < cluster; ++r) {
+        const uint32_t bar = peer(&sh.sent[buf], r);
+        send4(peer(&sh.totals.ph[buf][rank][lane], r), bar, ph);
+        if (lane == 0) send1(peer(&sh.totals.reset[buf][rank], r), bar, reset);
+    }
+}
+__device__ __forceinline__ void expect_totals(ScanShared &sh, int buf, int cluster) {
+    mbar_arrive_expect_tx(&sh.sent[buf], cluster * (32 * sizeof(float4) + sizeof(int)));
+}
+
+// ------------------------------------------------------------------ forward
+
+template <typename T, bool SIG, bool MASKED, bool CLUSTER>
+__global__ void __launch_bounds__(kScanThreads, 2)
+    scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
+                const ScanRun p) {
+    using S = Shape<T, SIG, false>;
+    using G = typename S::G;
+    constexpr int R = S::kRun, ST = S::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ ScanShared sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cluster = CLUSTER ? p.cluster : 1;
+    const int rank = CLUSTER ? (int)(blockIdx.x % cluster) : 0;
+    const int item = CLUSTER ? (int)(blockIdx.x / cluster) : (int)blockIdx.x;
+    const int stream = item / p.groups, group = item - stream * p.groups;
+    const int base = stream * p.stream, len = min(p.stream, p.total - base);
+    const int tiles = (len + p.step - 1) / p.step, slabs = (tiles + cluster - 1) / cluster;
+    const int c0 = group * kChannels, c = c0 + 2 * lane;
+    const bool live = c < p.D;
+    const uint32_t bytes = p.rows * kChannels * (sizeof(T) + sizeof(G));
+    auto fetch = [&](int n) {  // by one thread
+        const int j = n * cluster + rank, s = n % ST;
+        if (j >= tiles) return;
+        mbar_arrive_expect_tx(&sh.full[s], bytes);
+        load_box(smem + s * S::kStage, &mx, &sh.full[s], c0, base + j * p.step);
+        load_box(smem + s * S::kStage + S::kXBytes, &mg, &sh.full[s], c0, base + j * p.step);
+    };
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        for (int s = 0; s < ST; ++s) mbar_init(&sh.full[s], 1);
+        mbar_init(&sh.sent[0], 1);
+        mbar_init(&sh.sent[1], 1);
+        fence_mbar_init();
+        for (int n = 0; n < ST; ++n) fetch(n);
+    }
+    float2 carry = make_float2(0.f, 0.f);
+    if (!MASKED && p.h0 && live) carry = load2(p.h0 + (long long)stream * p.D + c);
+    if constexpr (CLUSTER) cluster_sync();
+    else __syncthreads();
+    T *const out = static_cast<T *>(p.h);
+    for (int n = 0; n < slabs; ++n) {
+        const int j = n * cluster + rank, buf = n & 1, s = n % ST;
+        const int tile0 = j * p.step, t0 = tile0 + warp * R;
+        const RunMask m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
+        if (CLUSTER && threadIdx.x == 0) expect_totals(sh, buf, cluster);
+        const T *const xs = reinterpret_cast<const T *>(smem + s * S::kStage) + warp * R * kChannels + 2 * lane;
+        const G *const gs = reinterpret_cast<const G *>(smem + s * S::kStage + S::kXBytes) +
+                            warp * R * kChannels + 2 * lane;
+        if (j < tiles) wait_full<false>(&sh.full[s], (n / ST) & 1, sh, p.status);
+        float2 a[R], u[R], P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
+        constexpr unsigned all = (1u << R) - 1u;
+        const bool plain = m.act == all && (!MASKED || m.start == 0);
+        if (plain) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
+                float b0, b1;
+                gate_ab<T, SIG>(g.x, a[i].x, b0);
+                gate_ab<T, SIG>(g.y, a[i].y, b1);
+                u[i] = make_float2(b0 * x.x, b1 * x.y);
+                P.x *= a[i].x;
+                P.y *= a[i].y;
+                H.x = fmaf(a[i].x, H.x, u[i].x);
+                H.y = fmaf(a[i].y, H.y, u[i].y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {  // the starts' states, all loads in flight
+                u[i] = make_float2(0.f, 0.f);
+                if (MASKED && (m.start >> i & 1)) {
+                    const long long at = (long long)run_seq(m, i) * p.D + c;
+                    if (p.h0 && live) u[i] = load2(p.h0 + at);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool in = m.act >> i & 1, start = MASKED && (m.start >> i & 1);
+                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
+                float2 b;
+                gate_ab<T, SIG>(g.x, a[i].x, b.x);
+                gate_ab<T, SIG>(g.y, a[i].y, b.y);
+                b = make_float2(b.x * x.x, b.y * x.y);
+                if (start) {
+                    b.x = fmaf(a[i].x, u[i].x, b.x);
+                    b.y = fmaf(a[i].y, u[i].y, b.y);
+                }
+                u[i] = in ? b : make_float2(0.f, 0.f);
+                if (!in) a[i] = make_float2(1.f, 1.f);
+                P.x *= a[i].x;
+                P.y *= a[i].y;
+                H.x = start ? u[i].x : fmaf(a[i].x, H.x, u[i].x);
+                H.y = start ? u[i].y : fmaf(a[i].y, H.y, u[i].y);
+            }
+        }
+        sh.run[buf][warp][lane] = make_float4(P.x, P.y, H.x, H.y);
+        if (MASKED && lane == 0) sh.reset[buf][warp] = m.start != 0;
+        __syncthreads();
+        // the stage is in registers
+        if (threadIdx.x == 0 && !sh.abort) fetch(n + ST);
+        float2 h = carry;
+        if constexpr (CLUSTER) {
+            if (warp == 0) {
+                float4 t = sh.run[buf][0][lane];
+                int reset = MASKED ? sh.reset[buf][0] : 0;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 ph = sh.run[buf][w][lane];
+                    const int r = MASKED ? sh.reset[buf][w] : 0;
+                    float2 z = make_float2(t.z, t.w);
+                    over(z, ph, r);
+                    t = make_float4(t.x * ph.x, t.y * ph.y, z.x, z.y);
+                    reset |= r;
+                }
+                send_totals(sh, buf, rank, cluster, t, reset);
+            }
+            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, sh, p.status);
+            for (int r = 0; r < cluster; ++r) {
+                if (r == rank) h = carry;
+                over(carry, sh.totals.ph[buf][r][lane], MASKED && sh.totals.reset[buf][r]);
+            }
+            for (int w = 0; w < warp; ++w) over(h, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
+        } else {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) h = carry;
+                over(carry, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
+            }
+        }
+        // the state before every 64th token (short dense sequences: at their starts)
+        const bool mapped = !MASKED || p.map;
+        if (p.states && mapped && t0 % kScanBlock == 0 && t0 < len && live)
+            store2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + t0 / kScanBlock) * p.D + c, h.x, h.y);
+        T *o = out + ((long long)(base + t0) * p.D + c);
+        if (plain && (!MASKED || m.end == 0)) {
+            if (out && live) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    h.x = fmaf(a[i].x, h.x, u[i].x);
+                    h.y = fmaf(a[i].y, h.y, u[i].y);
+                    store2(o + (long long)i * p.D, h.x, h.y);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool in = m.act >> i & 1, start = MASKED && (m.start >> i & 1);
+                h.x = start ? u[i].x : fmaf(a[i].x, h.x, u[i].x);
+                h.y = start ? u[i].y : fmaf(a[i].y, h.y, u[i].y);
+                if (out && live && in) store2(o + (long long)i * p.D, h.x, h.y);
+                if (MASKED && !p.map && p.states && start) {
+                    const long long at = (long long)run_seq(m, i) * p.D + c;
+                    const float2 z = p.h0 && live ? load2(p.h0 + at) : make_float2(0.f, 0.f);
+                    if (live) store2(p.states + at, z.x, z.y);
+                }
+                if (MASKED && p.h_T && (m.end >> i & 1)) {
+                    const long long at = (long long)run_seq(m, i) * p.D + c;
+                    if (live) store2(p.h_T + at, h.x, h.y);
+                }
+            }
+        }
+    }
+    if (!MASKED && p.h_T && rank == 0 && warp == 0 && live)
+        store2(p.h_T + (long long)stream * p.D + c, carry.x, carry.y);
+    // copies in flight land, and no CTA sends to one that has ended
+    if (sh.abort && threadIdx.x == 0)
+        for (int s = 0; s < ST; ++s) {
+            mbar_wait(&sh.full[s], 0, kWaitLimit / 16);
+            mbar_wait(&sh.full[s], 1, kWaitLimit / 16);
+        }
+    if constexpr (CLUSTER) cluster_sync();
+}
+
+// ------------------------------------------------------------------ backward
+
+// Tiles last to first: rank 0 of a cluster has the latest.
+template <typename T, bool SIG, bool MASKED, bool CLUSTER>
+__global__ void __launch_bounds__(kScanThreads, 2)
+    scan_backward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
+                         const __grid_constant__ CUtensorMap md, const ScanRun p) {
+    using S = Shape<T, SIG, true>;
+    using G = typename S::G;
+    constexpr int R = S::kRun, ST = S::kStages;
+    static_assert(S::kTokens == kScanBlock, "a tile starts from a kept state");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ ScanShared sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cluster = CLUSTER ? p.cluster : 1;
+    const int rank = CLUSTER ? (int)(blockIdx.x % cluster) : 0;
+    const int item = CLUSTER ? (int)(blockIdx.x / cluster) : (int)blockIdx.x;
+    const int stream = item / p.groups, group = item - stream * p.groups;
+    const int base = stream * p.stream, len = min(p.stream, p.total - base);
+    const int tiles = (len + p.step - 1) / p.step, slabs = (tiles + cluster - 1) / cluster;
+    const int c0 = group * kChannels, c = c0 + 2 * lane;
+    const bool live = c < p.D;
+    const uint32_t bytes = p.rows * kChannels * (2 * sizeof(T) + sizeof(G));
+    auto fetch = [&](int n) {  // by one thread
+        const int j = tiles - 1 - (n * cluster + rank), s = n % ST;
+        if (j < 0) return;
+        uint8_t *const at = smem + s * S::kStage;
+        mbar_arrive_expect_tx(&sh.full[s], bytes);
+        load_box(at, &mx, &sh.full[s], c0, base + j * p.step);
+        load_box(at + S::kXBytes, &mg, &sh.full[s], c0, base + j * p.step);
+        load_box(at + S::kXBytes + S::kGBytes, &md, &sh.full[s], c0, base + j * p.step);
+    };
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        for (int s = 0; s < ST; ++s) mbar_init(&sh.full[s], 1);
+        mbar_init(&sh.sent[0], 1);
+        mbar_init(&sh.sent[1], 1);
+        fence_mbar_init();
+        for (int n = 0; n < ST; ++n) fetch(n);
+    }
+    float2 carry = make_float2(0.f, 0.f);  // a G of the token after
+    if (!MASKED && p.dh_T && live) carry = load2(p.dh_T + (long long)stream * p.D + c);
+    if constexpr (CLUSTER) cluster_sync();
+    else __syncthreads();
+    for (int n = 0; n < slabs; ++n) {
+        const int j = tiles - 1 - (n * cluster + rank), buf = n & 1, s = n % ST;
+        const int tile0 = j * p.step, t0 = tile0 + warp * R;
+        RunMask m = {0, 0, 0, -1};
+        float2 h = make_float2(0.f, 0.f);
+        if (j >= 0) {
+            m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
+            if ((!MASKED || p.map) && live)
+                h = load2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + j) * p.D + c);
+        }
+        if (CLUSTER && threadIdx.x == 0) expect_totals(sh, buf, cluster);
+        const uint8_t *const stage = smem + s * S::kStage;
+        const int at0 = warp * R * kChannels + 2 * lane;
+        const T *const xs = reinterpret_cast<const T *>(stage) + at0;
+        const G *const gs = reinterpret_cast<const G *>(stage + S::kXBytes) + at0;
+        const T *const ds = reinterpret_cast<const T *>(stage + S::kXBytes + S::kGBytes) + at0;
+        if (j >= 0) wait_full<false>(&sh.full[s], (n / ST) & 1, sh, p.status);
+        float2 a[R], b[R];
+        float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f), V = make_float2(0.f, 0.f);
+        constexpr unsigned all = (1u << R) - 1u;
+        const bool plain = m.act == all && (!MASKED || (m.start | m.end) == 0);
+        // h0 of a start, dh_T of an end
+        auto start_state = [&](int i) {
+            const long long at = (long long)run_seq(m, i) * p.D + c;
+            return p.h0 && live ? load2(p.h0 + at) : make_float2(0.f, 0.f);
+        };
+        auto end_grad = [&](int i) {
+            const long long at = (long long)run_seq(m, i) * p.D + c;
+            return p.dh_T && live ? load2(p.dh_T + at) : make_float2(0.f, 0.f);
+        };
+        if (plain) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
+                gate_ab<T, SIG>(g.x, a[i].x, b[i].x);
+                gate_ab<T, SIG>(g.y, a[i].y, b[i].y);
+                P.x *= a[i].x;
+                P.y *= a[i].y;
+                H.x = fmaf(a[i].x, H.x, b[i].x * x.x);
+                H.y = fmaf(a[i].y, H.y, b[i].y * x.y);
+            }
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                const float2 d = load2(ds + i * kChannels);
+                V.x = a[i].x * (d.x + V.x);
+                V.y = a[i].y * (d.y + V.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool in = m.act >> i & 1;
+                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
+                gate_ab<T, SIG>(g.x, a[i].x, b[i].x);
+                gate_ab<T, SIG>(g.y, a[i].y, b[i].y);
+                if (!in) a[i] = make_float2(1.f, 1.f);
+                if (MASKED && (m.start >> i & 1)) H = start_state(i);
+                P.x *= a[i].x;
+                P.y *= a[i].y;
+                H.x = fmaf(a[i].x, H.x, in ? b[i].x * x.x : 0.f);
+                H.y = fmaf(a[i].y, H.y, in ? b[i].y * x.y : 0.f);
+            }
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                const bool in = m.act >> i & 1;
+                float2 d = load2(ds + i * kChannels);
+                if (!in) d = make_float2(0.f, 0.f);
+                if (MASKED && (m.end >> i & 1)) V = end_grad(i);
+                V.x = a[i].x * (d.x + V.x);
+                V.y = a[i].y * (d.y + V.y);
+            }
+        }
+        sh.run[buf][warp][lane] = make_float4(P.x, P.y, V.x, V.y);
+        sh.hrun[buf][warp][lane] = H;
+        if (MASKED && lane == 0) sh.reset[buf][warp] = (m.start != 0) | (m.end != 0) << 1;
+        __syncthreads();
+        // every warp is through with the tile before
+        if (threadIdx.x == 0 && n > 0 && !sh.abort) fetch(n - 1 + ST);
+        for (int w = 0; w < warp; ++w) {
+            const float4 ph = sh.run[buf][w][lane];
+            const float2 z = sh.hrun[buf][w][lane];
+            over(h, make_float4(ph.x, ph.y, z.x, z.y), MASKED && (sh.reset[buf][w] & 1));
+        }
+        float2 u = carry;
+        if constexpr (CLUSTER) {
+            if (warp == 0) {
+                float4 t = sh.run[buf][kWarps - 1][lane];
+                int reset = MASKED ? sh.reset[buf][kWarps - 1] >> 1 : 0;
+#pragma unroll
+                for (int w = kWarps - 2; w >= 0; --w) {
+                    const float4 ph = sh.run[buf][w][lane];
+                    const int r = MASKED ? sh.reset[buf][w] >> 1 : 0;
+                    float2 z = make_float2(t.z, t.w);
+                    over(z, ph, r);
+                    t = make_float4(t.x * ph.x, t.y * ph.y, z.x, z.y);
+                    reset |= r;
+                }
+                send_totals(sh, buf, rank, cluster, t, reset);
+            }
+            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, sh, p.status);
+            for (int r = 0; r < cluster; ++r) {
+                if (r == rank) u = carry;
+                over(carry, sh.totals.ph[buf][r][lane], MASKED && sh.totals.reset[buf][r]);
+            }
+            for (int w = kWarps - 1; w > warp; --w)
+                over(u, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
+        } else {
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w) {
+                if (w == warp) u = carry;
+                over(carry, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
+            }
+        }
+        if (m.act) {
+            T *const dx = static_cast<T *>(p.dx) + ((long long)(base + t0) * p.D + c);
+            G *const dg = static_cast<G *>(p.dgate) + ((long long)(base + t0) * p.D + c);
+            float2 past[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float2 x = load2(xs + i * kChannels);
+                const bool in = plain || (m.act >> i & 1);
+                if (MASKED && !plain && (m.start >> i & 1)) h = start_state(i);
+                past[i] = h;
+                h.x = fmaf(a[i].x, h.x, in ? b[i].x * x.x : 0.f);
+                h.y = fmaf(a[i].y, h.y, in ? b[i].y * x.y : 0.f);
+            }
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                const bool in = plain || (m.act >> i & 1);
+                const float2 x = load2(xs + i * kChannels);
+                float2 d = load2(ds + i * kChannels);
+                if (!in) d = make_float2(0.f, 0.f);
+                if (MASKED && !plain && (m.end >> i & 1)) u = end_grad(i);
+                const float2 g = make_float2(d.x + u.x, d.y + u.y);
+                if (in && live) {
+                    store2(dx + (long long)i * p.D, b[i].x * g.x, b[i].y * g.y);
+                    if constexpr (SIG)
+                        store2(dg + (long long)i * p.D, g.x * (past[i].x - x.x) * (a[i].x * b[i].x),
+                               g.y * (past[i].y - x.y) * (a[i].y * b[i].y));
+                    else
+                        store2(dg + (long long)i * p.D, g.x * past[i].x, g.y * past[i].y);
+                }
+                u = make_float2(a[i].x * g.x, a[i].y * g.y);
+                if (MASKED && !plain && p.dh0 && (m.start >> i & 1)) {
+                    const long long at = (long long)run_seq(m, i) * p.D + c;
+                    if (live) store2(p.dh0 + at, u.x, u.y);
+                }
+            }
+        }
+    }
+    if (!MASKED && p.dh0 && rank == 0 && warp == 0 && live)
+        store2(p.dh0 + (long long)stream * p.D + c, carry.x, carry.y);
+    if (sh.abort && threadIdx.x == 0)
+        for (int s = 0; s < ST; ++s) {
+            mbar_wait(&sh.full[s], 0, kWaitLimit / 16);
+            mbar_wait(&sh.full[s], 1, kWaitLimit / 16);
+        }
+    if constexpr (CLUSTER) cluster_sync();
+}
+
+// ------------------------------------------------------------------ packed tokens
+
+// The sequence of each token, or -1, 1024 tokens a CTA; and the end states of
+// sequences without tokens (end = start or 0), shared out among the CTAs.  A
+// sequence whose offsets fall, pass T or start before the end of an earlier one
+// (of those that neither fall nor pass T) has none and sets the bounds bit.
+constexpr int kMapThreads = 1024;
+__global__ void __launch_bounds__(kMapThreads)
+    scan_map_kernel(const int *offsets, int B, int T, int *map, const float *start, float *end, int D,
+                    int *status) {
+    __shared__ int mark[kMapThreads], far[32], empty[kMapThreads], empties;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long w0 = (long long)blockIdx.x * kMapThreads;
+    mark[tid] = -1;
+    int upto = 0;  // the furthest end so far
+    for (int s0 = 0; s0 < B; s0 += kMapThreads) {
+        const int s = s0 + tid;
+        int a = 0, b = 0;
+        bool good = false;
+        if (s < B) {
+            a = offsets[s];
+            b = offsets[s + 1];
+            good = a >= 0 && b >= a && b <= T;
+        }
+        int most = good ? b : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, most, off);
+            if (lane >= off) most = max(most, y);
+        }
+        if (lane == 31) far[warp] = most;
+        if (tid == 0) empties = 0;
+        __syncthreads();
+        int before = upto;  // the furthest end before this sequence
+        for (int w = 0; w < warp; ++w) before = max(before, far[w]);
+        const int prev = __shfl_up_sync(0xffffffffu, most, 1);
+        if (lane) before = max(before, prev);
+        for (int w = 0; w < 32; ++w) upto = max(upto, far[w]);
+        if (s < B) {
+            good = good && a >= before;
+            if (!good && blockIdx.x == 0 && status) atomicOr(status, kStatusBounds);
+            if (good && b > a) {
+                if (b > w0 && a < w0 + kMapThreads) mark[a > w0 ? a - w0 : 0] = s;
+            } else if (end && s % gridDim.x == blockIdx.x) {
+                empty[atomicAdd(&empties, 1)] = s;
+            }
+        }
+        __syncthreads();
+        for (int i = 0; i < empties; ++i) {
+            const long long at = (long long)empty[i] * D;
+            for (int c = tid; c < D; c += kMapThreads) end[at + c] = start ? start[at + c] : 0.f;
+        }
+        __syncthreads();
+    }
+    __syncthreads();
+    // the last sequence that starts at or before each token
+    int q = mark[tid];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, q, off);
+        if (lane >= off) q = max(q, y);
+    }
+    if (lane == 31) far[warp] = q;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) q = max(q, far[w]);
+    const long long t = w0 + tid;
+    if (t < T) map[t] = q >= 0 && t < offsets[q + 1] ? q : -1;
+}
+
+// ------------------------------------------------------------------ one token
+
+// A thread takes eight channels, all of its loads before any arithmetic.
 constexpr int kStepThreads = 128;
 template <typename T, bool SIG>
 __global__ void __launch_bounds__(kStepThreads)
@@ -118,87 +712,201 @@ __global__ void __launch_bounds__(kStepThreads)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         float a, b;
-        gate_ab<SIG>(gs[e], a, b);
+        gate_ab<T, SIG>(gs[e], a, b);
         s[e] = fmaf(a, s[e], b * xs[e]);
     }
     Vec8<float>::store(h_out + i * 8, s);
     if (y) Vec8<T>::store(y + i * 8, s);
 }
 
-template <typename F> cudaError_t by_type(gdn_dtype dt, bool sigmoid, F &&f) {
-    if (dt == GDN_BF16) {
-        if (sigmoid) f.template operator()<__nv_bfloat16, true>();
-        else f.template operator()<__nv_bfloat16, false>();
+// ------------------------------------------------------------------ host
+
+// [tokens, D] with the token stride ld, in boxes of 64 channels x rows tokens.
+template <typename E> bool box_map(CUtensorMap *m, const void *p, long long tokens, int D, long long ld, int rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)tokens};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * sizeof(E)};
+    cuuint32_t box[2] = {kChannels, (cuuint32_t)rows}, es[2] = {1, 1};
+    return enc(m, sizeof(E) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+               const_cast<void *>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How the tokens lie in streams, tiles and clusters.
+struct ScanPlan {
+    bool masked;
+    int streams, cluster;
+    ScanRun run;
+};
+ScanPlan scan_plan(const ScanArgs &a, int tile, const int *map) {
+    ScanPlan s = {};
+    ScanRun &r = s.run;
+    const int nsm = sm_count() > 0 ? sm_count() : 152;
+    r.h0 = a.h0; r.dh_T = a.dh_T; r.states = a.states; r.h = a.h; r.h_T = a.h_T;
+    r.dx = a.dx; r.dgate = a.dgate; r.dh0 = a.dh0;
+    r.map = map;
+    r.D = a.D;
+    r.groups = (a.D + kChannels - 1) / kChannels;
+    r.T = a.T;
+    r.blocks = (a.T + kScanBlock - 1) / kScanBlock;
+    r.total = a.offsets ? a.T : a.B * a.T;
+    r.status = device_status_ptr();
+    r.step = tile;
+    if (a.offsets) {
+        s.masked = true;
+        s.streams = 1;
+        r.stream = a.T;
+    } else if (a.T <= kScanBlock && a.B > 1) {
+        // whole sequences in a tile, and tiles of as many streams as the SMs take at once
+        s.masked = true;
+        const int per = tile / a.T, tiles = (a.B + per - 1) / per;
+        r.step = per * a.T;
+        long long streams = (2LL * nsm + r.groups - 1) / r.groups;
+        if (streams > tiles) streams = tiles;
+        const int each = (int)((tiles + streams - 1) / streams);
+        s.streams = (tiles + each - 1) / each;
+        r.stream = each * r.step;
     } else {
-        if (sigmoid) f.template operator()<float, true>();
-        else f.template operator()<float, false>();
+        s.streams = a.B;
+        r.stream = a.T;
     }
+    r.rows = r.step < r.stream ? r.step : r.stream;
+    const int tiles = (r.stream + r.step - 1) / r.step;
+    s.cluster = 1;
+    while (s.cluster < kMaxCluster && 2 * s.cluster <= tiles &&
+           4LL * r.groups * s.streams * s.cluster < 3LL * nsm)
+        s.cluster *= 2;
+    r.cluster = s.cluster;
+    return s;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_clustered(K kern, uintptr_t (&set)[64], const ScanPlan &s, size_t smem,
+                             cudaStream_t st, const A &...args) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (set[dev] != context_key()) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        set[dev] = context_key();
+    }
+    const long long grid = (long long)s.run.groups * s.streams * s.cluster;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = s.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename T, bool SIG, bool MASKED, bool CLUSTER>
+cudaError_t forward(const ScanArgs &a, const ScanPlan &s, cudaStream_t st) {
+    using S = Shape<T, SIG, false>;
+    static uintptr_t set[64] = {};
+    CUtensorMap mx, mg;
+    if (!box_map<T>(&mx, a.x, s.run.total, a.D, a.ldx, s.run.rows) ||
+        !box_map<typename S::G>(&mg, a.gate, s.run.total, a.D, a.ldg, s.run.rows))
+        return cudaErrorInvalidValue;
+    return launch_clustered(scan_kernel<T, SIG, MASKED, CLUSTER>, set, s, S::kStages * S::kStage, st, mx,
+                            mg, s.run);
+}
+template <typename T, bool SIG, bool MASKED, bool CLUSTER>
+cudaError_t backward(const ScanArgs &a, const ScanPlan &s, cudaStream_t st) {
+    using S = Shape<T, SIG, true>;
+    static uintptr_t set[64] = {};
+    CUtensorMap mx, mg, md;
+    if (!box_map<T>(&mx, a.x, s.run.total, a.D, a.ldx, s.run.rows) ||
+        !box_map<typename S::G>(&mg, a.gate, s.run.total, a.D, a.ldg, s.run.rows) ||
+        !box_map<T>(&md, a.dh, s.run.total, a.D, a.D, s.run.rows))
+        return cudaErrorInvalidValue;
+    return launch_clustered(scan_backward_kernel<T, SIG, MASKED, CLUSTER>, set, s, S::kStages * S::kStage,
+                            st, mx, mg, md, s.run);
+}
+
+template <typename T, bool SIG, bool BACK>
+cudaError_t launch_any(const ScanArgs &a, const int *map, cudaStream_t st) {
+    const ScanPlan s = scan_plan(a, Shape<T, SIG, BACK>::kTokens, map);
+    const bool cl = s.cluster > 1;
+    if constexpr (BACK)
+        return s.masked ? (cl ? backward<T, SIG, true, true>(a, s, st) : backward<T, SIG, true, false>(a, s, st))
+                        : (cl ? backward<T, SIG, false, true>(a, s, st) : backward<T, SIG, false, false>(a, s, st));
+    else
+        return s.masked ? (cl ? forward<T, SIG, true, true>(a, s, st) : forward<T, SIG, true, false>(a, s, st))
+                        : (cl ? forward<T, SIG, false, true>(a, s, st) : forward<T, SIG, false, false>(a, s, st));
+}
+template <bool BACK> cudaError_t launch_type(const ScanArgs &a, gdn_dtype dt, const int *map, cudaStream_t st) {
+    if (dt == GDN_BF16)
+        return a.sigmoid ? launch_any<__nv_bfloat16, true, BACK>(a, map, st)
+                         : launch_any<__nv_bfloat16, false, BACK>(a, map, st);
+    return a.sigmoid ? launch_any<float, true, BACK>(a, map, st) : launch_any<float, false, BACK>(a, map, st);
+}
+
+// The table of packed tokens, and what sequences without tokens end with.
+cudaError_t launch_map(const ScanArgs &a, int *map, const float *start, float *end, cudaStream_t st) {
+    scan_map_kernel<<<(unsigned)((a.T + (long long)kMapThreads - 1) / kMapThreads), kMapThreads, 0, st>>>(
+        a.offsets, a.B, a.T, map, start, end, a.D, device_status_ptr());
     return cudaGetLastError();
+}
+
+template <typename T, bool SIG>
+cudaError_t step(const void *x, const void *gate, const float *h, float *h_out, void *y, int B, int D,
+                 long long ldx, long long ldg, cudaStream_t st) {
+    using G = typename GateType<T, SIG>::type;
+    const long long pieces = (long long)B * (D / 8), grid = (pieces + kStepThreads - 1) / kStepThreads;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(scan_step_kernel<T, SIG>, (unsigned)grid, kStepThreads, 0, st,
+                      static_cast<const T *>(x), static_cast<const G *>(gate), h, h_out,
+                      static_cast<T *>(y), pieces, D / 8, ldx, ldg);
 }
 
 }  // namespace
 
 size_t scan_map_bytes(int T) { return ((size_t)T * sizeof(int) + 255) & ~size_t(255); }
 
-namespace {
-struct Forward {
-    const ScanArgs &a;
-    cudaStream_t st;
-    template <typename T, bool SIG> void operator()() {
-        scan_kernel<T, SIG><<<dim3(a.B, (a.D + 63) / 64), 64, 0, st>>>(a, device_status_ptr());
-    }
-};
-struct Backward {
-    const ScanArgs &a;
-    cudaStream_t st;
-    template <typename T, bool SIG> void operator()() {
-        scan_backward_kernel<T, SIG><<<dim3(a.B, (a.D + 63) / 64), 64, 0, st>>>(a, device_status_ptr());
-    }
-};
-struct Step {
-    const void *x, *gate;
-    const float *h;
-    float *h_out;
-    void *y;
-    int B, D;
-    long long ldx, ldg;
-    cudaStream_t st;
-    cudaError_t e = cudaSuccess;
-    template <typename T, bool SIG> void operator()() {
-        const long long pieces = (long long)B * (D / 8);
-        const long long grid = (pieces + kStepThreads - 1) / kStepThreads;
-        using G = typename GateType<T, SIG>::type;
-        e = grid > 0x7fffffffLL ? cudaErrorInvalidConfiguration
-                                : launch_pdl(scan_step_kernel<T, SIG>, (unsigned)grid, kStepThreads, 0,
-                                             st, static_cast<const T *>(x), static_cast<const G *>(gate),
-                                             h, h_out, static_cast<T *>(y), pieces, D / 8, ldx, ldg);
-    }
-};
-}  // namespace
-
 cudaError_t launch_scan(const ScanArgs &a, gdn_dtype dt, void *workspace, cudaStream_t st) {
-    (void)workspace;
-    return by_type(dt, a.sigmoid, Forward{a, st});
-}
-
-cudaError_t launch_scan_backward(const ScanArgs &a, gdn_dtype dt, void *workspace,
-                                 cudaStream_t st) {
-    ScanArgs b = a;
-    if (!b.states) {
-        b.states = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                             (a.offsets ? scan_map_bytes(a.T) : 0));
-        const cudaError_t e = by_type(dt, b.sigmoid, Forward{b, st});
+    int *const map = a.offsets ? static_cast<int *>(workspace) : nullptr;
+    if (map) {
+        const cudaError_t e = launch_map(a, map, a.h0, a.h_T, st);
         if (e != cudaSuccess) return e;
     }
-    return by_type(dt, b.sigmoid, Backward{b, st});
+    return launch_type<false>(a, dt, map, st);
+}
+
+cudaError_t launch_scan_backward(const ScanArgs &a, gdn_dtype dt, void *workspace, cudaStream_t st) {
+    int *const map = a.offsets ? static_cast<int *>(workspace) : nullptr;
+    if (map) {
+        const cudaError_t e = launch_map(a, map, a.dh_T, a.dh0, st);
+        if (e != cudaSuccess) return e;
+    }
+    ScanArgs b = a;
+    if (!b.states) {  // a forward pass that only keeps them
+        ScanArgs f = a;
+        f.states = b.states = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                                        (map ? scan_map_bytes(a.T) : 0));
+        const cudaError_t e = launch_type<false>(f, dt, map, st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_type<true>(b, dt, map, st);
 }
 
 cudaError_t launch_scan_step(const void *x, const void *gate, const float *h, float *h_out, void *y,
                              int B, int D, long long ldx, long long ldg, bool sigmoid, gdn_dtype dt,
                              cudaStream_t st) {
-    Step f{x, gate, h, h_out, y, B, D, ldx, ldg, st};
-    const cudaError_t e = by_type(dt, sigmoid, f);
-    return f.e != cudaSuccess ? f.e : e;
+    if (dt == GDN_BF16)
+        return sigmoid ? step<__nv_bfloat16, true>(x, gate, h, h_out, y, B, D, ldx, ldg, st)
+                       : step<__nv_bfloat16, false>(x, gate, h, h_out, y, B, D, ldx, ldg, st);
+    return sigmoid ? step<float, true>(x, gate, h, h_out, y, B, D, ldx, ldg, st)
+                   : step<float, false>(x, gate, h, h_out, y, B, D, ldx, ldg, st);
 }
 
 }  // namespace gdn
