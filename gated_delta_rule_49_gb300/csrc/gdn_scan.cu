@@ -43,6 +43,7 @@ constexpr int kChannels = 64;  // of a CTA
 constexpr int kWarps = 8;      // runs of a tile
 constexpr int kScanThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
+constexpr int kStageBytes = 90112;  // of tiles in flight
 constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
 
 // a and b of a gate.  b = 1 - a is formed without the difference: a near 1
@@ -68,17 +69,82 @@ template <typename T, bool SIG> __device__ __forceinline__ void gate_ab(float g,
 template <typename T, bool SIG> struct GateType { using type = T; };
 template <typename T> struct GateType<T, false> { using type = float; };
 
-// A lane's two channels.
-__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+// A lane's two channels, in the registers that packed float32 operations take.
+struct Pair {
+    unsigned long long v;
+};
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
 }
-__device__ __forceinline__ void store2(float *p, float x, float y) {
-    *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+__device__ __forceinline__ Pair both(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 split(Pair a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
 }
-__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Pair either(bool first, Pair a, Pair b) { return {first ? a.v : b.v}; }
+
+__device__ __forceinline__ Pair load2(const float *p) {
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    return pair(x.x, x.y);
+}
+__device__ __forceinline__ Pair unpack(uint32_t w) {
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ Pair load2(const __nv_bfloat16 *p) {
+    return unpack(*reinterpret_cast<const uint32_t *>(p));
+}
+__device__ __forceinline__ void store2(float *p, Pair x) { *reinterpret_cast<float2 *>(p) = split(x); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, Pair x) {
+    const float2 f = split(x);
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(f.x, f.y);
+}
+
+// a and b of a lane's gates in shared memory (without a sigmoid b is not used).
+// bf16 gates are held at -87: exp(87) stays a number and so does b.
+template <typename T, bool SIG>
+__device__ __forceinline__ void gates2(const typename GateType<T, SIG>::type *p, Pair &a, Pair &b) {
+    if constexpr (!SIG) {
+        a = load2(p);
+        b = a;
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xc2aec2aeu));
+        const float2 g = split(mul2(unpack(w), both(-1.4426950408889634f)));
+        float2 e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(g.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(g.y));
+        const Pair ep = pair(e.x, e.y);
+        const float2 d = split(add2(ep, both(1.f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+        a = pair(r.x, r.y);
+        b = mul2(ep, a);
+    } else {
+        const float2 g = *reinterpret_cast<const float2 *>(p);
+        float2 x, y;
+        gate_ab<T, SIG>(g.x, x.x, y.x);
+        gate_ab<T, SIG>(g.y, x.y, y.y);
+        a = pair(x.x, x.y);
+        b = pair(y.x, y.y);
+    }
 }
 
 // Tokens of a warp's run and tiles in flight, by the bytes of a token's channel.
@@ -90,7 +156,8 @@ template <typename T, bool SIG, bool BACK> struct Shape {
     static constexpr int kXBytes = kTokens * kChannels * (int)sizeof(T);
     static constexpr int kGBytes = kTokens * kChannels * (int)sizeof(G);
     static constexpr int kStage = kXBytes * (BACK ? 2 : 1) + kGBytes;
-    static constexpr int kStages = 98304 / kStage < 3 ? 3 : 98304 / kStage;
+    // two CTAs an SM; three tiles of one where two of them do not fit twice
+    static constexpr int kStages = kStageBytes / kStage < 2 ? 3 : kStageBytes / kStage;
 };
 
 struct ScanRun {
@@ -108,15 +175,18 @@ struct ScanRun {
     int *status;
 };
 
+struct Piece {         // what a run or a tile does to a lane's channels: c -> p c + h
+    Pair p, h;
+};
 struct Totals {        // of a tile, sent through a cluster
-    float4 ph[2][kMaxCluster][32];
+    Piece piece[2][kMaxCluster][32];
     int reset[2][kMaxCluster];
 };
-struct ScanShared {
-    float4 run[2][kWarps][32];  // P, H of a lane's channels (backward: P and V)
-    float2 hrun[2][kWarps][32]; // backward: H
-    int reset[2][kWarps];       // bit 0: a start among the run's tokens, bit 1: an end
-    Totals totals;
+template <bool BACK, bool CLUSTER> struct ScanShared {
+    Piece run[2][kWarps][32];
+    Pair state[BACK ? 2 : 1][BACK ? kWarps : 1][32];  // backward: the forward pass's h
+    int reset[2][kWarps];  // bit 0: a start among the run's tokens, bit 1: an end
+    Totals totals[CLUSTER ? 1 : 0];
     uint64_t full[8], sent[2];
     int abort;
 };
@@ -134,10 +204,10 @@ __device__ __forceinline__ uint32_t peer(const void *p, int rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void send4(uint32_t dst, uint32_t bar, float4 v) {
+__device__ __forceinline__ void send4(uint32_t dst, uint32_t bar, const Piece &v) {
     asm volatile(
-        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
-        "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(dst),
+        "l"(v.p.v), "l"(v.h.v), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void send1(uint32_t dst, uint32_t bar, int v) {
@@ -162,25 +232,29 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
 
 // A wait with a limit; the first that runs out ends all others of the CTA.
 template <bool CLUSTER>
-__device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, ScanShared &sh, int *status) {
+__device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, int *abort, int *status) {
     auto ready = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
     if (ready()) return;
     const long long t0 = clock64();
-    volatile int *const abort = &sh.abort;
+    volatile int *const flag = abort;
     while (!ready()) {
-        if (*abort) return;
+        if (*flag) return;
         if (clock64() - t0 > kWaitLimit) {
-            *abort = 1;
+            *flag = 1;
             if (status) atomicOr(status, kStatusTimeout);
             return;
         }
     }
 }
 
-// The joins of pieces, on two channels: what the state becomes over one.
-__device__ __forceinline__ void over(float2 &c, const float4 &ph, bool reset) {
-    c.x = reset ? ph.z : fmaf(ph.x, c.x, ph.z);
-    c.y = reset ? ph.w : fmaf(ph.y, c.y, ph.w);
+// The state after a piece.
+__device__ __forceinline__ void over(Pair &c, const Piece &k, bool reset) {
+    c = either(reset, k.h, fma2(k.p, c, k.h));
+}
+// Two pieces as one.
+__device__ __forceinline__ void join(Piece &t, const Piece &k, bool reset) {
+    over(t.h, k, reset);
+    t.p = mul2(t.p, k.p);
 }
 
 // Which of a run's tokens are in a sequence, start one, end one; lane l holds
@@ -221,20 +295,18 @@ __device__ __forceinline__ int run_seq(const RunMask &m, int i) {
     return __shfl_sync(0xffffffffu, m.seq, i + 1);
 }
 
-// A tile's totals to every CTA of the cluster (by one warp), and the pieces of the
-// CTAs before this one (rank) applied to c; returns what all of them make of it.
-// `before` gets the state that this CTA's tile starts from.
-__device__ __forceinline__ void send_totals(ScanShared &sh, int buf, int rank, int cluster,
-                                            const float4 &ph, int reset) {
+// A tile's totals to every CTA of the cluster, by one warp.
+__device__ __forceinline__ void send_totals(Totals &to, uint64_t *sent, int buf, int rank, int cluster,
+                                            const Piece &t, int reset) {
     const int lane = threadIdx.x & 31;
     for (int r = 0; r < cluster; ++r) {
-        const uint32_t bar = peer(&sh.sent[buf], r);
-        send4(peer(&sh.totals.ph[buf][rank][lane], r), bar, ph);
-        if (lane == 0) send1(peer(&sh.totals.reset[buf][rank], r), bar, reset);
+        const uint32_t bar = peer(&sent[buf], r);
+        send4(peer(&to.piece[buf][rank][lane], r), bar, t);
+        if (lane == 0) send1(peer(&to.reset[buf][rank], r), bar, reset);
     }
 }
-__device__ __forceinline__ void expect_totals(ScanShared &sh, int buf, int cluster) {
-    mbar_arrive_expect_tx(&sh.sent[buf], cluster * (32 * sizeof(float4) + sizeof(int)));
+__device__ __forceinline__ void expect_totals(uint64_t *sent, int buf, int cluster) {
+    mbar_arrive_expect_tx(&sent[buf], cluster * (32 * sizeof(Piece) + sizeof(int)));
 }
 
 // ------------------------------------------------------------------ forward
@@ -247,7 +319,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     using G = typename S::G;
     constexpr int R = S::kRun, ST = S::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ ScanShared sh;
+    __shared__ ScanShared<false, CLUSTER> sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cluster = CLUSTER ? p.cluster : 1;
     const int rank = CLUSTER ? (int)(blockIdx.x % cluster) : 0;
@@ -273,7 +345,8 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         fence_mbar_init();
         for (int n = 0; n < ST; ++n) fetch(n);
     }
-    float2 carry = make_float2(0.f, 0.f);
+    const Pair zero = both(0.f), one = both(1.f);
+    Pair carry = zero;
     if (!MASKED && p.h0 && live) carry = load2(p.h0 + (long long)stream * p.D + c);
     if constexpr (CLUSTER) cluster_sync();
     else __syncthreads();
@@ -282,31 +355,29 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         const int j = n * cluster + rank, buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
         const RunMask m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
-        if (CLUSTER && threadIdx.x == 0) expect_totals(sh, buf, cluster);
+        if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
         const T *const xs = reinterpret_cast<const T *>(smem + s * S::kStage) + warp * R * kChannels + 2 * lane;
         const G *const gs = reinterpret_cast<const G *>(smem + s * S::kStage + S::kXBytes) +
                             warp * R * kChannels + 2 * lane;
-        if (j < tiles) wait_full<false>(&sh.full[s], (n / ST) & 1, sh, p.status);
-        float2 a[R], u[R], P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
+        if (j < tiles) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p.status);
+        Pair a[R], u[R];
+        Piece k = {one, zero};
         constexpr unsigned all = (1u << R) - 1u;
         const bool plain = m.act == all && (!MASKED || m.start == 0);
         if (plain) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
-                float b0, b1;
-                gate_ab<T, SIG>(g.x, a[i].x, b0);
-                gate_ab<T, SIG>(g.y, a[i].y, b1);
-                u[i] = make_float2(b0 * x.x, b1 * x.y);
-                P.x *= a[i].x;
-                P.y *= a[i].y;
-                H.x = fmaf(a[i].x, H.x, u[i].x);
-                H.y = fmaf(a[i].y, H.y, u[i].y);
+                Pair b;
+                gates2<T, SIG>(gs + i * kChannels, a[i], b);
+                u[i] = load2(xs + i * kChannels);
+                if constexpr (SIG) u[i] = mul2(b, u[i]);
+                k.p = mul2(k.p, a[i]);
+                k.h = fma2(a[i], k.h, u[i]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) {  // the starts' states, all loads in flight
-                u[i] = make_float2(0.f, 0.f);
+                u[i] = zero;
                 if (MASKED && (m.start >> i & 1)) {
                     const long long at = (long long)run_seq(m, i) * p.D + c;
                     if (p.h0 && live) u[i] = load2(p.h0 + at);
@@ -315,92 +386,80 @@ __global__ void __launch_bounds__(kScanThreads, 2)
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const bool in = m.act >> i & 1, start = MASKED && (m.start >> i & 1);
-                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
-                float2 b;
-                gate_ab<T, SIG>(g.x, a[i].x, b.x);
-                gate_ab<T, SIG>(g.y, a[i].y, b.y);
-                b = make_float2(b.x * x.x, b.y * x.y);
-                if (start) {
-                    b.x = fmaf(a[i].x, u[i].x, b.x);
-                    b.y = fmaf(a[i].y, u[i].y, b.y);
-                }
-                u[i] = in ? b : make_float2(0.f, 0.f);
-                if (!in) a[i] = make_float2(1.f, 1.f);
-                P.x *= a[i].x;
-                P.y *= a[i].y;
-                H.x = start ? u[i].x : fmaf(a[i].x, H.x, u[i].x);
-                H.y = start ? u[i].y : fmaf(a[i].y, H.y, u[i].y);
+                Pair b, x = load2(xs + i * kChannels);
+                gates2<T, SIG>(gs + i * kChannels, a[i], b);
+                if constexpr (SIG) x = mul2(b, x);
+                if (start) x = fma2(a[i], u[i], x);
+                u[i] = either(in, x, zero);
+                a[i] = either(in, a[i], one);
+                k.p = mul2(k.p, a[i]);
+                k.h = either(start, u[i], fma2(a[i], k.h, u[i]));
             }
         }
-        sh.run[buf][warp][lane] = make_float4(P.x, P.y, H.x, H.y);
+        sh.run[buf][warp][lane] = k;
         if (MASKED && lane == 0) sh.reset[buf][warp] = m.start != 0;
         __syncthreads();
         // the stage is in registers
         if (threadIdx.x == 0 && !sh.abort) fetch(n + ST);
-        float2 h = carry;
+        Pair h = carry;
         if constexpr (CLUSTER) {
+            Totals &to = sh.totals[0];
             if (warp == 0) {
-                float4 t = sh.run[buf][0][lane];
+                Piece t = sh.run[buf][0][lane];
                 int reset = MASKED ? sh.reset[buf][0] : 0;
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) {
-                    const float4 ph = sh.run[buf][w][lane];
                     const int r = MASKED ? sh.reset[buf][w] : 0;
-                    float2 z = make_float2(t.z, t.w);
-                    over(z, ph, r);
-                    t = make_float4(t.x * ph.x, t.y * ph.y, z.x, z.y);
+                    join(t, sh.run[buf][w][lane], r);
                     reset |= r;
                 }
-                send_totals(sh, buf, rank, cluster, t, reset);
+                send_totals(to, sh.sent, buf, rank, cluster, t, reset);
             }
-            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, sh, p.status);
+            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
             for (int r = 0; r < cluster; ++r) {
                 if (r == rank) h = carry;
-                over(carry, sh.totals.ph[buf][r][lane], MASKED && sh.totals.reset[buf][r]);
+                over(carry, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
             }
             for (int w = 0; w < warp; ++w) over(h, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
         } else {
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) h = carry;
+                h = either(w == warp, carry, h);
                 over(carry, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
             }
         }
         // the state before every 64th token (short dense sequences: at their starts)
         const bool mapped = !MASKED || p.map;
         if (p.states && mapped && t0 % kScanBlock == 0 && t0 < len && live)
-            store2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + t0 / kScanBlock) * p.D + c, h.x, h.y);
+            store2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + t0 / kScanBlock) * p.D + c, h);
         T *o = out + ((long long)(base + t0) * p.D + c);
         if (plain && (!MASKED || m.end == 0)) {
             if (out && live) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    h.x = fmaf(a[i].x, h.x, u[i].x);
-                    h.y = fmaf(a[i].y, h.y, u[i].y);
-                    store2(o + (long long)i * p.D, h.x, h.y);
+                    h = fma2(a[i], h, u[i]);
+                    store2(o + (long long)i * p.D, h);
                 }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const bool in = m.act >> i & 1, start = MASKED && (m.start >> i & 1);
-                h.x = start ? u[i].x : fmaf(a[i].x, h.x, u[i].x);
-                h.y = start ? u[i].y : fmaf(a[i].y, h.y, u[i].y);
-                if (out && live && in) store2(o + (long long)i * p.D, h.x, h.y);
+                h = either(start, u[i], fma2(a[i], h, u[i]));
+                if (out && live && in) store2(o + (long long)i * p.D, h);
                 if (MASKED && !p.map && p.states && start) {
                     const long long at = (long long)run_seq(m, i) * p.D + c;
-                    const float2 z = p.h0 && live ? load2(p.h0 + at) : make_float2(0.f, 0.f);
-                    if (live) store2(p.states + at, z.x, z.y);
+                    if (live) store2(p.states + at, p.h0 ? load2(p.h0 + at) : zero);
                 }
                 if (MASKED && p.h_T && (m.end >> i & 1)) {
                     const long long at = (long long)run_seq(m, i) * p.D + c;
-                    if (live) store2(p.h_T + at, h.x, h.y);
+                    if (live) store2(p.h_T + at, h);
                 }
             }
         }
     }
     if (!MASKED && p.h_T && rank == 0 && warp == 0 && live)
-        store2(p.h_T + (long long)stream * p.D + c, carry.x, carry.y);
+        store2(p.h_T + (long long)stream * p.D + c, carry);
     // copies in flight land, and no CTA sends to one that has ended
     if (sh.abort && threadIdx.x == 0)
         for (int s = 0; s < ST; ++s) {
@@ -422,7 +481,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     constexpr int R = S::kRun, ST = S::kStages;
     static_assert(S::kTokens == kScanBlock, "a tile starts from a kept state");
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ ScanShared sh;
+    __shared__ ScanShared<true, CLUSTER> sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cluster = CLUSTER ? p.cluster : 1;
     const int rank = CLUSTER ? (int)(blockIdx.x % cluster) : 0;
@@ -450,7 +509,8 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         fence_mbar_init();
         for (int n = 0; n < ST; ++n) fetch(n);
     }
-    float2 carry = make_float2(0.f, 0.f);  // a G of the token after
+    const Pair zero = both(0.f), one = both(1.f), minus = both(-1.f);
+    Pair carry = zero;  // a G of the token after
     if (!MASKED && p.dh_T && live) carry = load2(p.dh_T + (long long)stream * p.D + c);
     if constexpr (CLUSTER) cluster_sync();
     else __syncthreads();
@@ -458,153 +518,151 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         const int j = tiles - 1 - (n * cluster + rank), buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
         RunMask m = {0, 0, 0, -1};
-        float2 h = make_float2(0.f, 0.f);
+        Pair h = zero;
         if (j >= 0) {
             m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
             if ((!MASKED || p.map) && live)
                 h = load2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + j) * p.D + c);
         }
-        if (CLUSTER && threadIdx.x == 0) expect_totals(sh, buf, cluster);
+        if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
         const uint8_t *const stage = smem + s * S::kStage;
         const int at0 = warp * R * kChannels + 2 * lane;
         const T *const xs = reinterpret_cast<const T *>(stage) + at0;
         const G *const gs = reinterpret_cast<const G *>(stage + S::kXBytes) + at0;
         const T *const ds = reinterpret_cast<const T *>(stage + S::kXBytes + S::kGBytes) + at0;
-        if (j >= 0) wait_full<false>(&sh.full[s], (n / ST) & 1, sh, p.status);
-        float2 a[R], b[R];
-        float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f), V = make_float2(0.f, 0.f);
+        if (j >= 0) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p.status);
+        Pair a[R] = {}, b[R] = {};
+        Pair H = zero;
+        Piece k = {one, zero};
         constexpr unsigned all = (1u << R) - 1u;
         const bool plain = m.act == all && (!MASKED || (m.start | m.end) == 0);
         // h0 of a start, dh_T of an end
         auto start_state = [&](int i) {
             const long long at = (long long)run_seq(m, i) * p.D + c;
-            return p.h0 && live ? load2(p.h0 + at) : make_float2(0.f, 0.f);
+            return p.h0 && live ? load2(p.h0 + at) : zero;
         };
         auto end_grad = [&](int i) {
             const long long at = (long long)run_seq(m, i) * p.D + c;
-            return p.dh_T && live ? load2(p.dh_T + at) : make_float2(0.f, 0.f);
+            return p.dh_T && live ? load2(p.dh_T + at) : zero;
+        };
+        // one token on: the state, and its input
+        auto forth = [&](int i, Pair z, bool in) {
+            Pair x = load2(xs + i * kChannels);
+            if constexpr (SIG) x = mul2(b[i], x);
+            return fma2(a[i], z, either(in, x, zero));
         };
         if (plain) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
-                gate_ab<T, SIG>(g.x, a[i].x, b[i].x);
-                gate_ab<T, SIG>(g.y, a[i].y, b[i].y);
-                P.x *= a[i].x;
-                P.y *= a[i].y;
-                H.x = fmaf(a[i].x, H.x, b[i].x * x.x);
-                H.y = fmaf(a[i].y, H.y, b[i].y * x.y);
+                gates2<T, SIG>(gs + i * kChannels, a[i], b[i]);
+                k.p = mul2(k.p, a[i]);
+                H = forth(i, H, true);
             }
 #pragma unroll
-            for (int i = R - 1; i >= 0; --i) {
-                const float2 d = load2(ds + i * kChannels);
-                V.x = a[i].x * (d.x + V.x);
-                V.y = a[i].y * (d.y + V.y);
-            }
+            for (int i = R - 1; i >= 0; --i) k.h = mul2(a[i], add2(load2(ds + i * kChannels), k.h));
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const bool in = m.act >> i & 1;
-                const float2 x = load2(xs + i * kChannels), g = load2(gs + i * kChannels);
-                gate_ab<T, SIG>(g.x, a[i].x, b[i].x);
-                gate_ab<T, SIG>(g.y, a[i].y, b[i].y);
-                if (!in) a[i] = make_float2(1.f, 1.f);
+                gates2<T, SIG>(gs + i * kChannels, a[i], b[i]);
+                a[i] = either(in, a[i], one);
                 if (MASKED && (m.start >> i & 1)) H = start_state(i);
-                P.x *= a[i].x;
-                P.y *= a[i].y;
-                H.x = fmaf(a[i].x, H.x, in ? b[i].x * x.x : 0.f);
-                H.y = fmaf(a[i].y, H.y, in ? b[i].y * x.y : 0.f);
+                k.p = mul2(k.p, a[i]);
+                H = forth(i, H, in);
             }
 #pragma unroll
             for (int i = R - 1; i >= 0; --i) {
                 const bool in = m.act >> i & 1;
-                float2 d = load2(ds + i * kChannels);
-                if (!in) d = make_float2(0.f, 0.f);
-                if (MASKED && (m.end >> i & 1)) V = end_grad(i);
-                V.x = a[i].x * (d.x + V.x);
-                V.y = a[i].y * (d.y + V.y);
+                if (MASKED && (m.end >> i & 1)) k.h = end_grad(i);
+                k.h = mul2(a[i], add2(either(in, load2(ds + i * kChannels), zero), k.h));
             }
         }
-        sh.run[buf][warp][lane] = make_float4(P.x, P.y, V.x, V.y);
-        sh.hrun[buf][warp][lane] = H;
+        sh.run[buf][warp][lane] = k;
+        sh.state[buf][warp][lane] = H;
         if (MASKED && lane == 0) sh.reset[buf][warp] = (m.start != 0) | (m.end != 0) << 1;
         __syncthreads();
         // every warp is through with the tile before
         if (threadIdx.x == 0 && n > 0 && !sh.abort) fetch(n - 1 + ST);
-        for (int w = 0; w < warp; ++w) {
-            const float4 ph = sh.run[buf][w][lane];
-            const float2 z = sh.hrun[buf][w][lane];
-            over(h, make_float4(ph.x, ph.y, z.x, z.y), MASKED && (sh.reset[buf][w] & 1));
-        }
-        float2 u = carry;
+        for (int w = 0; w < warp; ++w)
+            over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, MASKED && (sh.reset[buf][w] & 1));
+        Pair u = carry;
         if constexpr (CLUSTER) {
+            Totals &to = sh.totals[0];
             if (warp == 0) {
-                float4 t = sh.run[buf][kWarps - 1][lane];
+                Piece t = sh.run[buf][kWarps - 1][lane];
                 int reset = MASKED ? sh.reset[buf][kWarps - 1] >> 1 : 0;
 #pragma unroll
                 for (int w = kWarps - 2; w >= 0; --w) {
-                    const float4 ph = sh.run[buf][w][lane];
                     const int r = MASKED ? sh.reset[buf][w] >> 1 : 0;
-                    float2 z = make_float2(t.z, t.w);
-                    over(z, ph, r);
-                    t = make_float4(t.x * ph.x, t.y * ph.y, z.x, z.y);
+                    join(t, sh.run[buf][w][lane], r);
                     reset |= r;
                 }
-                send_totals(sh, buf, rank, cluster, t, reset);
+                send_totals(to, sh.sent, buf, rank, cluster, t, reset);
             }
-            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, sh, p.status);
+            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
             for (int r = 0; r < cluster; ++r) {
                 if (r == rank) u = carry;
-                over(carry, sh.totals.ph[buf][r][lane], MASKED && sh.totals.reset[buf][r]);
+                over(carry, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
             }
             for (int w = kWarps - 1; w > warp; --w)
                 over(u, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
         } else {
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
-                if (w == warp) u = carry;
+                u = either(w == warp, carry, u);
                 over(carry, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
             }
         }
         if (m.act) {
             T *const dx = static_cast<T *>(p.dx) + ((long long)(base + t0) * p.D + c);
             G *const dg = static_cast<G *>(p.dgate) + ((long long)(base + t0) * p.D + c);
-            float2 past[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const float2 x = load2(xs + i * kChannels);
-                const bool in = plain || (m.act >> i & 1);
-                if (MASKED && !plain && (m.start >> i & 1)) h = start_state(i);
-                past[i] = h;
-                h.x = fmaf(a[i].x, h.x, in ? b[i].x * x.x : 0.f);
-                h.y = fmaf(a[i].y, h.y, in ? b[i].y * x.y : 0.f);
-            }
-#pragma unroll
-            for (int i = R - 1; i >= 0; --i) {
-                const bool in = plain || (m.act >> i & 1);
-                const float2 x = load2(xs + i * kChannels);
-                float2 d = load2(ds + i * kChannels);
-                if (!in) d = make_float2(0.f, 0.f);
-                if (MASKED && !plain && (m.end >> i & 1)) u = end_grad(i);
-                const float2 g = make_float2(d.x + u.x, d.y + u.y);
-                if (in && live) {
-                    store2(dx + (long long)i * p.D, b[i].x * g.x, b[i].y * g.y);
-                    if constexpr (SIG)
-                        store2(dg + (long long)i * p.D, g.x * (past[i].x - x.x) * (a[i].x * b[i].x),
-                               g.y * (past[i].y - x.y) * (a[i].y * b[i].y));
-                    else
-                        store2(dg + (long long)i * p.D, g.x * past[i].x, g.y * past[i].y);
+            Pair past[R] = {};
+            // the gradients of token i, whose state's comes as u
+            auto token = [&](int i, Pair d, bool out) {
+                const Pair g = add2(d, u);
+                if (out) {
+                    if constexpr (SIG) {
+                        const Pair x = load2(xs + i * kChannels);
+                        store2(dx + (long long)i * p.D, mul2(b[i], g));
+                        store2(dg + (long long)i * p.D,
+                               mul2(mul2(g, fma2(x, minus, past[i])), mul2(a[i], b[i])));
+                    } else {
+                        store2(dx + (long long)i * p.D, g);
+                        store2(dg + (long long)i * p.D, mul2(g, past[i]));
+                    }
                 }
-                u = make_float2(a[i].x * g.x, a[i].y * g.y);
-                if (MASKED && !plain && p.dh0 && (m.start >> i & 1)) {
-                    const long long at = (long long)run_seq(m, i) * p.D + c;
-                    if (live) store2(p.dh0 + at, u.x, u.y);
+                u = mul2(a[i], g);
+            };
+            if (plain) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    past[i] = h;
+                    h = forth(i, h, true);
+                }
+#pragma unroll
+                for (int i = R - 1; i >= 0; --i) token(i, load2(ds + i * kChannels), live);
+            } else {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    if (MASKED && (m.start >> i & 1)) h = start_state(i);
+                    past[i] = h;
+                    h = forth(i, h, m.act >> i & 1);
+                }
+#pragma unroll
+                for (int i = R - 1; i >= 0; --i) {
+                    const bool in = m.act >> i & 1;
+                    if (MASKED && (m.end >> i & 1)) u = end_grad(i);
+                    token(i, either(in, load2(ds + i * kChannels), zero), in && live);
+                    if (MASKED && p.dh0 && (m.start >> i & 1)) {
+                        const long long at = (long long)run_seq(m, i) * p.D + c;
+                        if (live) store2(p.dh0 + at, u);
+                    }
                 }
             }
         }
     }
     if (!MASKED && p.dh0 && rank == 0 && warp == 0 && live)
-        store2(p.dh0 + (long long)stream * p.D + c, carry.x, carry.y);
+        store2(p.dh0 + (long long)stream * p.D + c, carry);
     if (sh.abort && threadIdx.x == 0)
         for (int s = 0; s < ST; ++s) {
             mbar_wait(&sh.full[s], 0, kWaitLimit / 16);
