@@ -43,7 +43,6 @@ constexpr int kChannels = 64;  // of a CTA
 constexpr int kWarps = 8;      // runs of a tile
 constexpr int kScanThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
-constexpr int kStageBytes = 90112;  // of tiles in flight
 constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
 
 // a and b of a gate.  b = 1 - a is formed without the difference: a near 1
@@ -151,13 +150,12 @@ __device__ __forceinline__ void gates2(const typename GateType<T, SIG>::type *p,
 // (Registers hold two or three float32 a token and channel.)
 template <typename T, bool SIG, bool BACK> struct Shape {
     using G = typename GateType<T, SIG>::type;
-    static constexpr int kRun = !BACK && sizeof(T) + sizeof(G) == 4 ? 16 : 8;
+    static constexpr int kRun = !BACK && sizeof(T) == 2 ? 16 : 8;
     static constexpr int kTokens = kRun * kWarps;  // of a tile
     static constexpr int kXBytes = kTokens * kChannels * (int)sizeof(T);
     static constexpr int kGBytes = kTokens * kChannels * (int)sizeof(G);
     static constexpr int kStage = kXBytes * (BACK ? 2 : 1) + kGBytes;
-    // two CTAs an SM; three tiles of one where two of them do not fit twice
-    static constexpr int kStages = kStageBytes / kStage < 2 ? 3 : kStageBytes / kStage;
+    static constexpr int kStages = BACK ? 3 : 2;
 };
 
 struct ScanRun {
@@ -514,16 +512,19 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     if (!MASKED && p.dh_T && live) carry = load2(p.dh_T + (long long)stream * p.D + c);
     if constexpr (CLUSTER) cluster_sync();
     else __syncthreads();
+    // the state that the forward pass kept before a tile
+    auto kept = [&](int j) {
+        if ((MASKED && !p.map) || j < 0 || !live) return zero;
+        return load2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + j) * p.D + c);
+    };
+    Pair next = kept(tiles - 1 - rank);
     for (int n = 0; n < slabs; ++n) {
         const int j = tiles - 1 - (n * cluster + rank), buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
         RunMask m = {0, 0, 0, -1};
-        Pair h = zero;
-        if (j >= 0) {
-            m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
-            if ((!MASKED || p.map) && live)
-                h = load2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + j) * p.D + c);
-        }
+        if (j >= 0) m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
+        Pair h = next;
+        next = kept(j - cluster);
         if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
         const uint8_t *const stage = smem + s * S::kStage;
         const int at0 = warp * R * kChannels + 2 * lane;
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         const G *const gs = reinterpret_cast<const G *>(stage + S::kXBytes) + at0;
         const T *const ds = reinterpret_cast<const T *>(stage + S::kXBytes + S::kGBytes) + at0;
         if (j >= 0) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p.status);
-        Pair a[R] = {}, b[R] = {};
+        Pair a[R] = {}, b[R] = {}, u[R] = {};  // u = b x
         Pair H = zero;
         Piece k = {one, zero};
         constexpr unsigned all = (1u << R) - 1u;
@@ -545,36 +546,35 @@ __global__ void __launch_bounds__(kScanThreads, 2)
             const long long at = (long long)run_seq(m, i) * p.D + c;
             return p.dh_T && live ? load2(p.dh_T + at) : zero;
         };
-        // one token on: the state, and its input
-        auto forth = [&](int i, Pair z, bool in) {
-            Pair x = load2(xs + i * kChannels);
-            if constexpr (SIG) x = mul2(b[i], x);
-            return fma2(a[i], z, either(in, x, zero));
-        };
         if (plain) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 gates2<T, SIG>(gs + i * kChannels, a[i], b[i]);
+                u[i] = load2(xs + i * kChannels);
+                if constexpr (SIG) u[i] = mul2(b[i], u[i]);
                 k.p = mul2(k.p, a[i]);
-                H = forth(i, H, true);
+                H = fma2(a[i], H, u[i]);
             }
 #pragma unroll
-            for (int i = R - 1; i >= 0; --i) k.h = mul2(a[i], add2(load2(ds + i * kChannels), k.h));
+            for (int i = R - 1; i >= 0; --i) k.h = fma2(a[i], k.h, mul2(a[i], load2(ds + i * kChannels)));
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const bool in = m.act >> i & 1;
                 gates2<T, SIG>(gs + i * kChannels, a[i], b[i]);
                 a[i] = either(in, a[i], one);
+                u[i] = load2(xs + i * kChannels);
+                if constexpr (SIG) u[i] = mul2(b[i], u[i]);
+                u[i] = either(in, u[i], zero);
                 if (MASKED && (m.start >> i & 1)) H = start_state(i);
                 k.p = mul2(k.p, a[i]);
-                H = forth(i, H, in);
+                H = fma2(a[i], H, u[i]);
             }
 #pragma unroll
             for (int i = R - 1; i >= 0; --i) {
                 const bool in = m.act >> i & 1;
                 if (MASKED && (m.end >> i & 1)) k.h = end_grad(i);
-                k.h = mul2(a[i], add2(either(in, load2(ds + i * kChannels), zero), k.h));
+                k.h = fma2(a[i], k.h, mul2(a[i], either(in, load2(ds + i * kChannels), zero)));
             }
         }
         sh.run[buf][warp][lane] = k;
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         if (threadIdx.x == 0 && n > 0 && !sh.abort) fetch(n - 1 + ST);
         for (int w = 0; w < warp; ++w)
             over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, MASKED && (sh.reset[buf][w] & 1));
-        Pair u = carry;
+        Pair v = carry;  // a G of the run's next token
         if constexpr (CLUSTER) {
             Totals &to = sh.totals[0];
             if (warp == 0) {
@@ -601,15 +601,15 @@ __global__ void __launch_bounds__(kScanThreads, 2)
             }
             wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
             for (int r = 0; r < cluster; ++r) {
-                if (r == rank) u = carry;
+                if (r == rank) v = carry;
                 over(carry, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
             }
             for (int w = kWarps - 1; w > warp; --w)
-                over(u, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
+                over(v, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
         } else {
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
-                u = either(w == warp, carry, u);
+                v = either(w == warp, carry, v);
                 over(carry, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
             }
         }
@@ -617,27 +617,24 @@ __global__ void __launch_bounds__(kScanThreads, 2)
             T *const dx = static_cast<T *>(p.dx) + ((long long)(base + t0) * p.D + c);
             G *const dg = static_cast<G *>(p.dgate) + ((long long)(base + t0) * p.D + c);
             Pair past[R] = {};
-            // the gradients of token i, whose state's comes as u
+            // the gradients of token i: v becomes a G, dgate = a G (b h_{t-1} - b x)
             auto token = [&](int i, Pair d, bool out) {
-                const Pair g = add2(d, u);
-                if (out) {
-                    if constexpr (SIG) {
-                        const Pair x = load2(xs + i * kChannels);
-                        store2(dx + (long long)i * p.D, mul2(b[i], g));
-                        store2(dg + (long long)i * p.D,
-                               mul2(mul2(g, fma2(x, minus, past[i])), mul2(a[i], b[i])));
-                    } else {
-                        store2(dx + (long long)i * p.D, g);
-                        store2(dg + (long long)i * p.D, mul2(g, past[i]));
-                    }
+                const Pair g = add2(d, v);
+                v = mul2(a[i], g);
+                if (!out) return;
+                if constexpr (SIG) {
+                    store2(dx + (long long)i * p.D, mul2(b[i], g));
+                    store2(dg + (long long)i * p.D, mul2(v, fma2(u[i], minus, mul2(b[i], past[i]))));
+                } else {
+                    store2(dx + (long long)i * p.D, g);
+                    store2(dg + (long long)i * p.D, mul2(g, past[i]));
                 }
-                u = mul2(a[i], g);
             };
             if (plain) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     past[i] = h;
-                    h = forth(i, h, true);
+                    h = fma2(a[i], h, u[i]);
                 }
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) token(i, load2(ds + i * kChannels), live);
@@ -646,16 +643,16 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 for (int i = 0; i < R; ++i) {
                     if (MASKED && (m.start >> i & 1)) h = start_state(i);
                     past[i] = h;
-                    h = forth(i, h, m.act >> i & 1);
+                    h = fma2(a[i], h, u[i]);
                 }
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
                     const bool in = m.act >> i & 1;
-                    if (MASKED && (m.end >> i & 1)) u = end_grad(i);
+                    if (MASKED && (m.end >> i & 1)) v = end_grad(i);
                     token(i, either(in, load2(ds + i * kChannels), zero), in && live);
                     if (MASKED && p.dh0 && (m.start >> i & 1)) {
                         const long long at = (long long)run_seq(m, i) * p.D + c;
-                        if (live) store2(p.dh0 + at, u);
+                        if (live) store2(p.dh0 + at, v);
                     }
                 }
             }
