@@ -261,31 +261,34 @@ struct RunMask {
     unsigned act, start, end;
     int seq;
 };
+// The sequence of this lane's token, ahead of the tile that needs it.  tile0: the
+// tile's first token in the stream, r0: the run's in the tile.
 template <bool MASKED, int R>
-__device__ __forceinline__ RunMask run_mask(const ScanRun &p, int base, int len, int tile0, int r0) {
-    // tile0: the tile's first token in the stream, r0: the run's in the tile
+__device__ __forceinline__ int run_entry(const ScanRun &p, int base, int len, int tile0, int r0) {
+    if constexpr (!MASKED) return 0;
+    const int lane = threadIdx.x & 31;
+    const int k = r0 + lane - 1, t = tile0 + k;
+    if (lane >= R + 2 || t < 0 || t >= len) return -1;
+    if (p.map) return p.map[t];
+    // whole sequences in a tile: a neighbour is one of the tile's own tokens
+    return k >= 0 && k < p.step ? (base + t) / p.T : -1;
+}
+template <bool MASKED, int R>
+__device__ __forceinline__ RunMask run_mask(int seq, int len, int t0) {
     RunMask m;
     constexpr unsigned all = (1u << R) - 1u;
+    m.seq = seq;
     if constexpr (!MASKED) {
-        const int n = min(max(len - (tile0 + r0), 0), R);
+        const int n = min(max(len - t0, 0), R);
         m.act = n >= R ? all : (1u << n) - 1u;
         m.start = m.end = 0;
-        m.seq = 0;
     } else {
         const int lane = threadIdx.x & 31;
-        const int k = r0 + lane - 1, t = tile0 + k;
-        int s = -1;
-        // a neighbour of another tile counts only where the table is absolute
-        if (lane < R + 2 && t >= 0 && t < len) {
-            if (p.map) s = p.map[t];
-            else if (k >= 0 && k < p.step) s = (base + t) / p.T;
-        }
-        const int before = __shfl_up_sync(0xffffffffu, s, 1), after = __shfl_down_sync(0xffffffffu, s, 1);
-        const bool mine = s >= 0 && lane >= 1 && lane <= R;
+        const int before = __shfl_up_sync(0xffffffffu, seq, 1), after = __shfl_down_sync(0xffffffffu, seq, 1);
+        const bool mine = seq >= 0 && lane >= 1 && lane <= R;
         m.act = (__ballot_sync(0xffffffffu, mine) >> 1) & all;
-        m.start = (__ballot_sync(0xffffffffu, mine && s != before) >> 1) & all;
-        m.end = (__ballot_sync(0xffffffffu, mine && s != after) >> 1) & all;
-        m.seq = s;
+        m.start = (__ballot_sync(0xffffffffu, mine && seq != before) >> 1) & all;
+        m.end = (__ballot_sync(0xffffffffu, mine && seq != after) >> 1) & all;
     }
     return m;
 }
@@ -349,19 +352,32 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     if constexpr (CLUSTER) cluster_sync();
     else __syncthreads();
     T *const out = static_cast<T *>(p.h);
+    if constexpr (MASKED) pdl_wait();  // for the table
+    int entry = run_entry<MASKED, R>(p, base, len, rank * p.step, warp * R);
     for (int n = 0; n < slabs; ++n) {
         const int j = n * cluster + rank, buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
-        const RunMask m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
+        const RunMask m = run_mask<MASKED, R>(entry, len, t0);
+        entry = run_entry<MASKED, R>(p, base, len, tile0 + cluster * p.step, warp * R);
         if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
         const T *const xs = reinterpret_cast<const T *>(smem + s * S::kStage) + warp * R * kChannels + 2 * lane;
         const G *const gs = reinterpret_cast<const G *>(smem + s * S::kStage + S::kXBytes) +
                             warp * R * kChannels + 2 * lane;
-        if (j < tiles) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p.status);
         Pair a[R], u[R];
         Piece k = {one, zero};
         constexpr unsigned all = (1u << R) - 1u;
         const bool plain = m.act == all && (!MASKED || m.start == 0);
+        if (MASKED && !plain) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {  // the starts' states, all loads in flight
+                u[i] = zero;
+                if (m.start >> i & 1) {
+                    const long long at = (long long)run_seq(m, i) * p.D + c;
+                    if (p.h0 && live) u[i] = load2(p.h0 + at);
+                }
+            }
+        }
+        if (j < tiles) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p.status);
         if (plain) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -373,14 +389,6 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 k.h = fma2(a[i], k.h, u[i]);
             }
         } else {
-#pragma unroll
-            for (int i = 0; i < R; ++i) {  // the starts' states, all loads in flight
-                u[i] = zero;
-                if (MASKED && (m.start >> i & 1)) {
-                    const long long at = (long long)run_seq(m, i) * p.D + c;
-                    if (p.h0 && live) u[i] = load2(p.h0 + at);
-                }
-            }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const bool in = m.act >> i & 1, start = MASKED && (m.start >> i & 1);
@@ -517,12 +525,15 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         if ((MASKED && !p.map) || j < 0 || !live) return zero;
         return load2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + j) * p.D + c);
     };
+    if constexpr (MASKED) pdl_wait();  // for the table
     Pair next = kept(tiles - 1 - rank);
+    int entry = run_entry<MASKED, R>(p, base, len, (tiles - 1 - rank) * p.step, warp * R);
     for (int n = 0; n < slabs; ++n) {
         const int j = tiles - 1 - (n * cluster + rank), buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
         RunMask m = {0, 0, 0, -1};
-        if (j >= 0) m = run_mask<MASKED, R>(p, base, len, tile0, warp * R);
+        if (j >= 0) m = run_mask<MASKED, R>(entry, len, t0);
+        entry = run_entry<MASKED, R>(p, base, len, tile0 - cluster * p.step, warp * R);
         Pair h = next;
         next = kept(j - cluster);
         if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
@@ -681,6 +692,7 @@ __global__ void __launch_bounds__(kMapThreads)
     __shared__ int mark[kMapThreads], far[32], empty[kMapThreads], empties;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long w0 = (long long)blockIdx.x * kMapThreads;
+    pdl_trigger();  // the scan waits for this kernel's end before it reads the table
     mark[tid] = -1;
     int upto = 0;  // the furthest end so far
     for (int s0 = 0; s0 < B; s0 += kMapThreads) {
@@ -831,7 +843,7 @@ ScanPlan scan_plan(const ScanArgs &a, int tile, const int *map) {
     const int tiles = (r.stream + r.step - 1) / r.step;
     s.cluster = 1;
     while (s.cluster < kMaxCluster && 2 * s.cluster <= tiles &&
-           4LL * r.groups * s.streams * s.cluster < 3LL * nsm)
+           2LL * r.groups * s.streams * s.cluster < 3LL * nsm)
         s.cluster *= 2;
     r.cluster = s.cluster;
     return s;
@@ -839,7 +851,7 @@ ScanPlan scan_plan(const ScanArgs &a, int tile, const int *map) {
 
 template <typename K, typename... A>
 cudaError_t launch_clustered(K kern, uintptr_t (&set)[64], const ScanPlan &s, size_t smem,
-                             cudaStream_t st, const A &...args) {
+                             bool after_map, cudaStream_t st, const A &...args) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (set[dev] != context_key()) {
@@ -855,28 +867,35 @@ cudaError_t launch_clustered(K kern, uintptr_t (&set)[64], const ScanPlan &s, si
     cfg.blockDim = dim3(kScanThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = s.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = s.cluster > 1 ? 1 : 0;
+    if (s.cluster > 1) {
+        cudaLaunchAttribute &x = attr[cfg.numAttrs++];
+        x.id = cudaLaunchAttributeClusterDimension;
+        x.val.clusterDim.x = s.cluster;
+        x.val.clusterDim.y = x.val.clusterDim.z = 1;
+    }
+    if (after_map) {  // its first loads do not wait for the table
+        cudaLaunchAttribute &x = attr[cfg.numAttrs++];
+        x.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        x.val.programmaticStreamSerializationAllowed = 1;
+    }
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <typename T, bool SIG, bool MASKED, bool CLUSTER>
-cudaError_t forward(const ScanArgs &a, const ScanPlan &s, cudaStream_t st) {
+cudaError_t forward(const ScanArgs &a, const ScanPlan &s, bool after_map, cudaStream_t st) {
     using S = Shape<T, SIG, false>;
     static uintptr_t set[64] = {};
     CUtensorMap mx, mg;
     if (!box_map<T>(&mx, a.x, s.run.total, a.D, a.ldx, s.run.rows) ||
         !box_map<typename S::G>(&mg, a.gate, s.run.total, a.D, a.ldg, s.run.rows))
         return cudaErrorInvalidValue;
-    return launch_clustered(scan_kernel<T, SIG, MASKED, CLUSTER>, set, s, S::kStages * S::kStage, st, mx,
-                            mg, s.run);
+    return launch_clustered(scan_kernel<T, SIG, MASKED, CLUSTER>, set, s, S::kStages * S::kStage, after_map,
+                            st, mx, mg, s.run);
 }
 template <typename T, bool SIG, bool MASKED, bool CLUSTER>
-cudaError_t backward(const ScanArgs &a, const ScanPlan &s, cudaStream_t st) {
+cudaError_t backward(const ScanArgs &a, const ScanPlan &s, bool after_map, cudaStream_t st) {
     using S = Shape<T, SIG, true>;
     static uintptr_t set[64] = {};
     CUtensorMap mx, mg, md;
@@ -885,25 +904,31 @@ cudaError_t backward(const ScanArgs &a, const ScanPlan &s, cudaStream_t st) {
         !box_map<T>(&md, a.dh, s.run.total, a.D, a.D, s.run.rows))
         return cudaErrorInvalidValue;
     return launch_clustered(scan_backward_kernel<T, SIG, MASKED, CLUSTER>, set, s, S::kStages * S::kStage,
-                            st, mx, mg, md, s.run);
+                            after_map, st, mx, mg, md, s.run);
 }
 
-template <typename T, bool SIG, bool BACK>
-cudaError_t launch_any(const ScanArgs &a, const int *map, cudaStream_t st) {
-    const ScanPlan s = scan_plan(a, Shape<T, SIG, BACK>::kTokens, map);
-    const bool cl = s.cluster > 1;
-    if constexpr (BACK)
-        return s.masked ? (cl ? backward<T, SIG, true, true>(a, s, st) : backward<T, SIG, true, false>(a, s, st))
-                        : (cl ? backward<T, SIG, false, true>(a, s, st) : backward<T, SIG, false, false>(a, s, st));
-    else
-        return s.masked ? (cl ? forward<T, SIG, true, true>(a, s, st) : forward<T, SIG, true, false>(a, s, st))
-                        : (cl ? forward<T, SIG, false, true>(a, s, st) : forward<T, SIG, false, false>(a, s, st));
+template <typename T, bool SIG, bool BACK, bool MASKED, bool CLUSTER>
+cudaError_t launch_one(const ScanArgs &a, const ScanPlan &s, bool after_map, cudaStream_t st) {
+    if constexpr (BACK) return backward<T, SIG, MASKED, CLUSTER>(a, s, after_map, st);
+    else return forward<T, SIG, MASKED, CLUSTER>(a, s, after_map, st);
 }
-template <bool BACK> cudaError_t launch_type(const ScanArgs &a, gdn_dtype dt, const int *map, cudaStream_t st) {
+template <typename T, bool SIG, bool BACK>
+cudaError_t launch_any(const ScanArgs &a, const int *map, bool after_map, cudaStream_t st) {
+    const ScanPlan s = scan_plan(a, Shape<T, SIG, BACK>::kTokens, map);
+    if (s.masked)
+        return s.cluster > 1 ? launch_one<T, SIG, BACK, true, true>(a, s, after_map, st)
+                             : launch_one<T, SIG, BACK, true, false>(a, s, after_map, st);
+    return s.cluster > 1 ? launch_one<T, SIG, BACK, false, true>(a, s, after_map, st)
+                         : launch_one<T, SIG, BACK, false, false>(a, s, after_map, st);
+}
+// after_map: the launch comes directly after the table's.
+template <bool BACK>
+cudaError_t launch_type(const ScanArgs &a, gdn_dtype dt, const int *map, bool after_map, cudaStream_t st) {
     if (dt == GDN_BF16)
-        return a.sigmoid ? launch_any<__nv_bfloat16, true, BACK>(a, map, st)
-                         : launch_any<__nv_bfloat16, false, BACK>(a, map, st);
-    return a.sigmoid ? launch_any<float, true, BACK>(a, map, st) : launch_any<float, false, BACK>(a, map, st);
+        return a.sigmoid ? launch_any<__nv_bfloat16, true, BACK>(a, map, after_map, st)
+                         : launch_any<__nv_bfloat16, false, BACK>(a, map, after_map, st);
+    return a.sigmoid ? launch_any<float, true, BACK>(a, map, after_map, st)
+                     : launch_any<float, false, BACK>(a, map, after_map, st);
 }
 
 // The table of packed tokens, and what sequences without tokens end with.
@@ -934,7 +959,7 @@ cudaError_t launch_scan(const ScanArgs &a, gdn_dtype dt, void *workspace, cudaSt
         const cudaError_t e = launch_map(a, map, a.h0, a.h_T, st);
         if (e != cudaSuccess) return e;
     }
-    return launch_type<false>(a, dt, map, st);
+    return launch_type<false>(a, dt, map, map != nullptr, st);
 }
 
 cudaError_t launch_scan_backward(const ScanArgs &a, gdn_dtype dt, void *workspace, cudaStream_t st) {
@@ -948,10 +973,10 @@ cudaError_t launch_scan_backward(const ScanArgs &a, gdn_dtype dt, void *workspac
         ScanArgs f = a;
         f.states = b.states = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                                         (map ? scan_map_bytes(a.T) : 0));
-        const cudaError_t e = launch_type<false>(f, dt, map, st);
+        const cudaError_t e = launch_type<false>(f, dt, map, map != nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    return launch_type<true>(b, dt, map, st);
+    return launch_type<true>(b, dt, map, map && a.states, st);
 }
 
 cudaError_t launch_scan_step(const void *x, const void *gate, const float *h, float *h_out, void *y,
