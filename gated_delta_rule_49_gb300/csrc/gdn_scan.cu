@@ -255,6 +255,22 @@ __device__ __forceinline__ void join(Piece &t, const Piece &k, bool reset) {
     t.p = mul2(t.p, k.p);
 }
 
+// f with the warp's number as a constant: the walks over the other runs' pieces
+// are straight lines then (as loops they were a third of the gradients' instructions).
+template <int N> struct Number { static constexpr int value = N; };
+template <typename F> __device__ __forceinline__ void as_constant(int warp, F &&f) {
+    switch (warp) {
+        case 0: f(Number<0>()); break;
+        case 1: f(Number<1>()); break;
+        case 2: f(Number<2>()); break;
+        case 3: f(Number<3>()); break;
+        case 4: f(Number<4>()); break;
+        case 5: f(Number<5>()); break;
+        case 6: f(Number<6>()); break;
+        default: f(Number<7>()); break;
+    }
+}
+
 // Which of a run's tokens are in a sequence, start one, end one; lane l holds
 // the sequence of token l - 1 of the run.
 struct RunMask {
@@ -426,14 +442,17 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 if (r == rank) h = carry;
                 over(carry, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
             }
-            for (int w = 0; w < warp; ++w) over(h, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
-        } else {
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                h = either(w == warp, carry, h);
-                over(carry, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
-            }
         }
+        as_constant(warp, [&](auto number) {
+            constexpr int W = decltype(number)::value;
+#pragma unroll
+            for (int w = 0; w < W; ++w) over(h, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
+            if constexpr (!CLUSTER) {
+                carry = h;
+#pragma unroll
+                for (int w = W; w < kWarps; ++w) over(carry, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
+            }
+        });
         // the state before every 64th token (short dense sequences: at their starts)
         const bool mapped = !MASKED || p.map;
         if (p.states && mapped && t0 % kScanBlock == 0 && t0 < len && live)
@@ -594,8 +613,6 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         __syncthreads();
         // every warp is through with the tile before
         if (threadIdx.x == 0 && n > 0 && !sh.abort) fetch(n - 1 + ST);
-        for (int w = 0; w < warp; ++w)
-            over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, MASKED && (sh.reset[buf][w] & 1));
         Pair v = carry;  // a G of the run's next token
         if constexpr (CLUSTER) {
             Totals &to = sh.totals[0];
@@ -615,15 +632,22 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 if (r == rank) v = carry;
                 over(carry, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
             }
-            for (int w = kWarps - 1; w > warp; --w)
-                over(v, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
-        } else {
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                v = either(w == warp, carry, v);
-                over(carry, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
-            }
         }
+        as_constant(warp, [&](auto number) {
+            constexpr int W = decltype(number)::value;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, MASKED && (sh.reset[buf][w] & 1));
+#pragma unroll
+            for (int w = kWarps - 1; w > W; --w)
+                over(v, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
+            if constexpr (!CLUSTER) {
+                carry = v;
+#pragma unroll
+                for (int w = W; w >= 0; --w)
+                    over(carry, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
+            }
+        });
         if (m.act) {
             T *const dx = static_cast<T *>(p.dx) + ((long long)(base + t0) * p.D + c);
             G *const dg = static_cast<G *>(p.dgate) + ((long long)(base + t0) * p.D + c);
