@@ -5,48 +5,50 @@
 //     dx = r (g - mean g - n mean(g n)) + ds,  dw = sum dy .* n,  db = sum dy
 //
 // Bound by memory: every input read once, every output written once (8 bytes a
-// value with the sum, 4 without; gradients 8 or 6, in bf16).  A row is held by a
-// group of threads, each with 8 (up to 32) of its channels, so that a thread's
-// channels are the same in every row: w, b and the sums for dw and db stay in its
-// registers.  The deviation is taken from the mean, not from the squares' sum: a
-// row about a large mean keeps it.  A group works on U rows at once: their loads
-// are in flight together, the next rows' go out as soon as these are summed, and
-// one exchange between the group's warps serves all U.
-#include "gdn_vec8.cuh"
+// value with the sum, 4 without; gradients 8 or 6, in bf16).  A team (a warp, or
+// the threads of one wide row) has a ring of blocks of rows in shared memory, which
+// one thread keeps full by bulk copies: what is in flight does not depend on
+// registers.  (Rows fetched ahead into registers spilled: 124 us for 32768 rows of
+// 2048 bf16 channels with the sum.)  The deviation is taken from the mean, not from
+// the squares' sum: a row about a large mean keeps it.
+#include "gdn_pair.cuh"
+#include "gdn_sm100.cuh"
 
 namespace gdn {
 namespace {
 
-// Threads of a row, pieces of 8 channels of a thread.  Up to 2048 channels a piece
-// is all: a group is the next power of two of pieces, and as many groups as fill
-// 256 threads are a CTA.
-template <int TPR_, int VPT_> struct RowShape {
-    static constexpr int TPR = TPR_, VPT = VPT_;
-    static constexpr int kThreads = TPR < 256 ? 256 : TPR;
-    static constexpr int kGroups = kThreads / TPR;
-};
-// Rows at once, by what a row takes of a thread's registers.
-template <typename T, int VPT> constexpr int rows_at_once(bool back) {
-    const int u = (back ? 2 : 4) / (VPT * (int)sizeof(T) / 2);
-    return u < 1 ? 1 : u;
-}
-// CTAs of 256 threads an SM.
-constexpr int kNormCtas = 2;
-constexpr int resident(int threads) { return kNormCtas * 256 / threads < 1 ? 1 : kNormCtas * 256 / threads; }
-// Whether the next rows' loads go out before these are done: their registers.
-template <typename T, int VPT> constexpr bool fetch_ahead(bool back) {
-    return VPT * (int)sizeof(T) <= (back ? 4 : 8);
-}
-// Gradients of more than 8192 channels: the sums for dw and db in shared memory.
-template <int VPT> constexpr bool sums_shared() { return VPT > 2; }
+constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
 
-// Sums of U values over a group of TPR threads, the same in all of them and in a
-// fixed order.  Groups of several warps meet at a barrier of their own; the two
+// Threads of a row and pieces of 8 channels of a thread.  A team is a warp, of one
+// row or several, or the threads of a row.
+template <int TPR_, int VPT_> struct RowShape {
+    enum {
+        TPR = TPR_,
+        VPT = VPT_,
+        kTeam = TPR < 32 ? 32 : TPR,
+        kAbreast = kTeam / TPR,  // rows side by side in a team
+        // Outputs: one CTA an SM, of up to 20 warps, fewer where the rows are few (24
+        // warps spilled; two CTAs of 8 would each hold the weights).  Gradients: 16
+        // warps an SM.
+        kTeams = kTeam < 640 ? 640 / kTeam : 1,
+        kThreads = kTeams * kTeam,
+        kBackThreads = kTeam < 256 ? 256 : kTeam,
+        kBackTeams = kBackThreads / kTeam,
+        kBackCtas = 512 / kBackThreads
+    };
+};
+// Rows of a thread at once: their chains of sums overlap, and one meeting of a
+// team's warps serves them all.
+constexpr int rows_at_once(int vpt, bool back) { return back ? (vpt == 1 ? 2 : 1) : (vpt < 4 ? 4 / vpt : 1); }
+constexpr int kMaxSlots = 4;  // blocks of a team in shared memory
+
+// Sums of U values over the threads of a row, the same in all of them and in a
+// fixed order.  Rows of several warps meet at a barrier of their team's; the two
 // buffers of `red` take turns.
-template <int TPR, int U> struct GroupSum {
+template <int TPR, int U> struct RowSum {
     static constexpr int kWarps = TPR / 32;
-    float (*red)[kWarps > 0 ? kWarps : 1][U];  // [2][warps][U], the group's
-    int group, turn;
+    float (*red)[kWarps > 0 ? kWarps : 1][U];  // [2][warps][U], the team's
+    int team, turn;
     __device__ __forceinline__ void operator()(float (&x)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -59,7 +61,7 @@ template <int TPR, int U> struct GroupSum {
 #pragma unroll
                 for (int u = 0; u < U; ++u) red[turn][warp][u] = x[u];
             }
-            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+            sm100::named_sync(team + 1, TPR);
 #pragma unroll
             for (int u = 0; u < U; ++u) x[u] = red[turn][0][u];
 #pragma unroll
@@ -81,290 +83,428 @@ struct NormArgs {
     int D;
     long long ldx, ldr;
     float eps;
+    int rows, slots;      // of a block; blocks of a team
+    int *status;
 };
 
-template <typename T, int VPT>
-__device__ __forceinline__ void load_columns(float (&v)[VPT][8], const float *p, float other, int first,
-                                             int step, int D) {
+// A team's ring: block i of the team's is in slot i % slots, its tensors one after
+// another, the rows dense.
+template <typename T, int TENSORS> struct Ring {
+    uint8_t *base;
+    uint64_t *full;
+    const T *src[TENSORS];
+    long long ld[TENSORS];
+    int bytes;  // of a slot's tensor
+    // by one thread
+    __device__ __forceinline__ void fetch(const NormArgs &p, int slot, long long row0) const {
+        if (row0 >= p.N) return;
+        const int n = (int)min((long long)p.rows, p.N - row0), row = p.D * (int)sizeof(T);
+        uint8_t *const at = base + slot * TENSORS * bytes;
+        sm100::mbar_arrive_expect_tx(&full[slot], TENSORS * n * row);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int c = first + k * step;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] = other;
-        if (p && c < D) {
-            Vec8<float> q;
-            q.load_cached(p + c);
-            q.get(v[k]);
+        for (int t = 0; t < TENSORS; ++t) {
+            const T *const from = src[t] + row0 * ld[t];
+            if (ld[t] == p.D) {
+                sm100::bulk_load(at + t * bytes, from, n * row, &full[slot]);
+            } else {
+                for (int i = 0; i < n; ++i)
+                    sm100::bulk_load(at + t * bytes + i * row, from + i * ld[t], row, &full[slot]);
+            }
         }
     }
-}
-// Eight values rounded to the type, as held by Vec8.
-__device__ __forceinline__ void round8(Vec8<float> &v, const float (&x)[8]) {
-    v.a = make_float4(x[0], x[1], x[2], x[3]);
-    v.b = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void round8(Vec8<__nv_bfloat16> &v, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    __device__ __forceinline__ const T *row(const NormArgs &p, int slot, int tensor, int i) const {
+        return reinterpret_cast<const T *>(base + (slot * TENSORS + tensor) * bytes) + (long long)i * p.D;
     }
-    v.a = make_uint4(w[0], w[1], w[2], w[3]);
+};
+// A wait with a limit; the first that runs out ends all others of the CTA.
+__device__ __forceinline__ void wait_block(uint64_t *bar, uint32_t parity, int *abort, int *status) {
+    volatile int *const flag = abort;
+    if (sm100::mbar_wait_or_abort(bar, parity, kWaitLimit, flag) || *flag) return;
+    *flag = 1;
+    if (status) atomicOr(status, kStatusTimeout);
 }
-__device__ __forceinline__ void put8(__nv_bfloat16 *p, const Vec8<__nv_bfloat16> &v) {
-    *reinterpret_cast<uint4 *>(p) = v.a;
+// Copies in flight land before the CTA ends (where nothing went wrong none are).
+__device__ __forceinline__ void drain(uint64_t *full, int slots) {
+    for (int i = 0; i < slots; ++i) {
+        sm100::mbar_wait(&full[i], 0, kWaitLimit / 16);
+        sm100::mbar_wait(&full[i], 1, kWaitLimit / 16);
+    }
 }
-__device__ __forceinline__ void put8(float *p, const Vec8<float> &v) {
-    reinterpret_cast<float4 *>(p)[0] = v.a;
-    reinterpret_cast<float4 *>(p)[1] = v.b;
+// From here on the values are unpacked again: kept as floats from one phase to the
+// next, they took twice the registers and spilled.
+__device__ __forceinline__ void repack(Vec8<float> &) {}
+__device__ __forceinline__ void repack(Vec8<__nv_bfloat16> &v) {
+    asm volatile("" : "+r"(v.a.x), "+r"(v.a.y), "+r"(v.a.z), "+r"(v.a.w));
+}
+
+// A thread's channels of a weight: eight from `p` (or `other` where there is none).
+__device__ __forceinline__ void column(Pair (&v)[4], const float *p, float other, int c, int D) {
+    if (p && c < D) {
+        Vec8<float> q;
+        q.load_cached(p + c);
+        get4(q, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = both(other);
+    }
+}
+// Where w and b of a piece come from: a thread's registers, where it has one piece;
+// shared memory, staged once by the CTA, up to 2048 channels; else the L1 cache.
+enum { kRegisters, kStaged, kCached };
+template <typename S> constexpr int weights_in(bool back) {
+    return S::VPT == 1 || (back && S::VPT == 2) ? kRegisters
+           : !back && S::TPR * S::VPT * 8 <= 2048 ? kStaged : kCached;
+}
+// Staged: the lower and the upper four channels of every piece apart, so that
+// neighbouring lanes read neighbouring 16 bytes.
+template <int PIECES>
+__device__ __forceinline__ void stage_column(float4 *dst, const float *p, float other, int D) {
+    for (int i = threadIdx.x; i < PIECES; i += blockDim.x) {
+        float4 lo = make_float4(other, other, other, other), hi = lo;
+        if (p && 8 * i < D) {
+            lo = reinterpret_cast<const float4 *>(p)[2 * i];
+            hi = reinterpret_cast<const float4 *>(p)[2 * i + 1];
+        }
+        dst[i] = lo;
+        dst[PIECES + i] = hi;
+    }
+}
+template <int PIECES> __device__ __forceinline__ void staged(Pair (&v)[4], const float4 *src, int i) {
+    const float4 lo = src[i], hi = src[PIECES + i];
+    v[0] = pair(lo.x, lo.y);
+    v[1] = pair(lo.z, lo.w);
+    v[2] = pair(hi.x, hi.y);
+    v[3] = pair(hi.z, hi.w);
+}
+__device__ __forceinline__ float sum2(Pair x) {
+    const float2 f = split(x);
+    return f.x + f.y;
 }
 
 template <typename T, typename S, bool RES>
-__global__ void __launch_bounds__(S::kThreads, resident(S::kThreads))
+__global__ void __launch_bounds__(S::kThreads, 1)
     layer_norm_kernel(const NormArgs p) {
-    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T, VPT>(false);
-    constexpr bool kHold = VPT <= 2;  // w and b in registers
-    __shared__ float red[S::kGroups][2][TPR >= 32 ? TPR / 32 : 1][U];
-    const int group = threadIdx.x / TPR, l = threadIdx.x % TPR, c0 = l * 8;
-    GroupSum<TPR, U> sum = {red[group], group, 0};
-    const float inv = 1.f / p.D;
-    float w[kHold ? VPT : 1][8], b[kHold ? VPT : 1][8];
-    if constexpr (kHold) {
-        load_columns<T, VPT>(w, p.w, 1.f, c0, TPR * 8, p.D);
-        load_columns<T, VPT>(b, p.b, 0.f, c0, TPR * 8, p.D);
+    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once(VPT, false);
+    constexpr int TENSORS = RES ? 2 : 1, BATCH = U * S::kAbreast;
+    constexpr int kWeights = weights_in<S>(false), PIECES = TPR * VPT;
+    __shared__ float4 weights[kWeights == kStaged ? 4 * PIECES : 1];
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[S::kTeams][2][TPR >= 32 ? TPR / 32 : 1][U];
+    __shared__ uint64_t full[S::kTeams][kMaxSlots];
+    __shared__ int abort;
+    const int team = threadIdx.x / S::kTeam, lead = threadIdx.x % S::kTeam == 0;
+    const int l = threadIdx.x % TPR, c0 = l * 8, abreast = threadIdx.x % S::kTeam / TPR;
+    Ring<T, TENSORS> ring;
+    ring.bytes = p.rows * p.D * (int)sizeof(T);
+    ring.base = smem + (size_t)team * p.slots * TENSORS * ring.bytes;
+    ring.full = full[team];
+    ring.src[0] = static_cast<const T *>(p.x);
+    ring.ld[0] = p.ldx;
+    if constexpr (RES) {
+        ring.src[1] = static_cast<const T *>(p.res);
+        ring.ld[1] = p.ldr;
     }
-    const T *const x = static_cast<const T *>(p.x), *const res = static_cast<const T *>(p.res);
+    const int teams = blockDim.x / S::kTeam;
+    const long long first = ((long long)blockIdx.x * teams + team) * p.rows;
+    const long long step = (long long)gridDim.x * teams * p.rows;
+    if (threadIdx.x == 0) abort = 0;
+    if (lead) {
+        for (int i = 0; i < p.slots; ++i) sm100::mbar_init(&full[team][i], 1);
+        sm100::fence_mbar_init();
+        for (int i = 0; i < p.slots; ++i) ring.fetch(p, i, first + i * step);
+    }
+    RowSum<TPR, U> sum = {red[team], team, 0};
+    const float inv = 1.f / p.D;
+    Pair w[4], b[4];
+    if constexpr (kWeights == kRegisters) {
+        column(w, p.w, 1.f, c0, p.D);
+        column(b, p.b, 0.f, c0, p.D);
+    } else if constexpr (kWeights == kStaged) {
+        stage_column<PIECES>(weights, p.w, 1.f, p.D);
+        stage_column<PIECES>(weights + 2 * PIECES, p.b, 0.f, p.D);
+    }
     T *const y = static_cast<T *>(p.y), *const sums = static_cast<T *>(p.s);
-    Vec8<T> rx[U][VPT], rr[RES ? U : 1][VPT];
-    auto fetch = [&](long long row0) {
+    __syncthreads();
+    int slot = 0;
+    uint32_t parity = 0;
+    for (long long block = first; block < p.N; block += step) {
+        const int n = (int)min((long long)p.rows, p.N - block);
+        wait_block(&full[team][slot], parity, &abort, p.status);
+        for (int i0 = 0; i0 < n; i0 += BATCH) {
+            Vec8<T> sv[U][VPT];
+            float m[U], q[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * S::kAbreast + abreast;
+                Pair t = both(0.f);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = c0 + k * TPR * 8;
-                if (row0 + u < p.N && c < p.D) {
-                    rx[u][k].load(x + ((row0 + u) * p.ldx + c));
-                    if constexpr (RES) rr[u][k].load(res + ((row0 + u) * p.ldr + c));
-                }
-            }
-    };
-    const long long first = ((long long)blockIdx.x * S::kGroups + group) * U;
-    const long long step = (long long)gridDim.x * S::kGroups * U;
-    // groups of a warp or less go round together: their shuffles name all lanes
-    const long long end = TPR < 32 ? p.N + (long long)(group % (32 / (TPR < 32 ? TPR : 32))) * U : p.N;
-    constexpr bool kAhead = fetch_ahead<T, VPT>(false);
-    if constexpr (kAhead) fetch(first);
-    for (long long row0 = first; row0 < end; row0 += step) {
-        if constexpr (!kAhead) fetch(row0);
-        Vec8<T> sv[U][VPT];
-        float m[U], q[U];
+                for (int k = 0; k < VPT; ++k) {
+                    const int c = c0 + k * TPR * 8;
+                    sv[u][k] = {};
+                    if (i < n && c < p.D) {
+                        from_shared(sv[u][k], ring.row(p, slot, 0, i) + c);
+                        Pair f[4];
+                        get4(sv[u][k], f);
+                        if constexpr (RES) {
+                            Vec8<T> rv;
+                            Pair r[4];
+                            from_shared(rv, ring.row(p, slot, 1, i) + c);
+                            get4(rv, r);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            m[u] = 0.f;
+                            for (int e = 0; e < 4; ++e) f[e] = add2(f[e], r[e]);
+                            set4(sv[u][k], f);
+                            get4(sv[u][k], f);
+                        }
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float f[8] = {};
-                if (row0 + u < p.N && c0 + k * TPR * 8 < p.D) {
-                    rx[u][k].get(f);
-                    if constexpr (RES) {
-                        float r[8];
-                        rr[u][k].get(r);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] += r[e];
+                        for (int e = 0; e < 4; ++e) t = add2(t, f[e]);
                     }
                 }
-                round8(sv[u][k], f);
-                if constexpr (RES) sv[u][k].get(f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m[u] += f[e];
+                m[u] = sum2(t);
             }
-        }
-        if constexpr (kAhead) fetch(row0 + step);
-        sum(m);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            m[u] *= inv;
-            q[u] = 0.f;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                if (c0 + k * TPR * 8 >= p.D) continue;
-                float f[8];
-                sv[u][k].get(f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) q[u] = fmaf(f[e] - m[u], f[e] - m[u], q[u]);
+            sum(m);
+            if (i0 + BATCH >= n) {  // the block is in registers
+                if constexpr (TPR <= 32) __syncwarp();
+                if (lead && !abort) ring.fetch(p, slot, block + p.slots * step);
             }
-        }
-        sum(q);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long row = row0 + u;
-            if (row >= p.N) continue;
-            const float r = rsqrtf(fmaf(q[u], inv, p.eps));
-            if (p.stats && l == 0) *reinterpret_cast<float2 *>(p.stats + 2 * row) = make_float2(m[u], r);
+            for (int u = 0; u < U; ++u) {
+                m[u] *= inv;
+                const Pair minus = both(-m[u]);
+                Pair t = both(0.f);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = c0 + k * TPR * 8;
-                if (c >= p.D) continue;
-                if (RES && sums) put8(sums + (row * p.D + c), sv[u][k]);
-                float f[8], wk[1][8], bk[1][8];
-                if constexpr (!kHold) {
-                    load_columns<T, 1>(wk, p.w, 1.f, c, 0, p.D);
-                    load_columns<T, 1>(bk, p.b, 0.f, c, 0, p.D);
+                for (int k = 0; k < VPT; ++k) {
+                    if (c0 + k * TPR * 8 < p.D) {
+                        Pair f[4];
+                        repack(sv[u][k]);
+                        get4(sv[u][k], f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f[e] = add2(f[e], minus);
+                            t = fma2(f[e], f[e], t);
+                        }
+                    }
                 }
-                sv[u][k].get(f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[e] = fmaf((f[e] - m[u]) * r, kHold ? w[kHold ? k : 0][e] : wk[0][e],
-                                kHold ? b[kHold ? k : 0][e] : bk[0][e]);
-                Vec8<T>::store(y + (row * p.D + c), f);
+                q[u] = sum2(t);
             }
+            sum(q);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * S::kAbreast + abreast;
+                if (i >= n) continue;
+                const long long row = block + i;
+                const float r = rsqrtf(fmaf(q[u], inv, p.eps));
+                if (p.stats && l == 0) *reinterpret_cast<float2 *>(p.stats + 2 * row) = make_float2(m[u], r);
+                const Pair minus = both(-m[u]), scale = both(r);
+                T *const yr = y + (row * p.D + c0), *const sr = sums + (row * p.D + c0);
+#pragma unroll
+                for (int k = 0; k < VPT; ++k) {
+                    if (c0 + k * TPR * 8 < p.D) {
+                        if (RES && sums) put8(sr + k * TPR * 8, sv[u][k]);
+                        if constexpr (kWeights == kStaged) {
+                            staged<PIECES>(w, weights, k * TPR + l);
+                            staged<PIECES>(b, weights + 2 * PIECES, k * TPR + l);
+                        } else if constexpr (kWeights == kCached) {
+                            column(w, p.w, 1.f, c0 + k * TPR * 8, p.D);
+                            column(b, p.b, 0.f, c0 + k * TPR * 8, p.D);
+                        }
+                        Pair f[4];
+                        repack(sv[u][k]);
+                        get4(sv[u][k], f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            f[e] = fma2(mul2(add2(f[e], minus), scale), w[e], b[e]);
+                        Vec8<T> out;
+                        set4(out, f);
+                        put8(yr + k * TPR * 8, out);
+                    }
+                }
+            }
+        }
+        if (++slot == p.slots) {
+            slot = 0;
+            parity ^= 1;
         }
     }
+    if (lead && abort) drain(full[team], p.slots);
 }
 
-// A group's rows leave their sums for dw and db in its registers; the CTA's
-// groups add theirs up in shared memory, in their order, and the CTA writes one
-// row of `parts`.
+// A thread's rows leave their sums for dw and db in its registers; the CTA's row
+// groups add theirs up in shared memory, in their order, and the CTA writes one row
+// of `parts`.
 template <typename T, typename S, bool PAST>
-__global__ void __launch_bounds__(S::kThreads, resident(S::kThreads))
+__global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
     layer_norm_backward_kernel(const NormArgs p) {
-    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T, VPT>(true);
-    constexpr bool kHold = VPT <= 2;
-    __shared__ float red[S::kGroups][2][TPR >= 32 ? TPR / 32 : 1][2 * U];
-    extern __shared__ float acc[];  // [groups - 1][2][8][TPR], or [VPT][2][8][TPR]
-    const int group = threadIdx.x / TPR, l = threadIdx.x % TPR, c0 = l * 8;
-    GroupSum<TPR, 2 * U> sum = {red[group], group, 0};
+    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once(VPT, true);
+    constexpr int TENSORS = PAST ? 3 : 2, BATCH = U * S::kAbreast;
+    constexpr bool kHold = weights_in<S>(true) == kRegisters;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[S::kBackTeams][2][TPR >= 32 ? TPR / 32 : 1][2 * U];
+    __shared__ uint64_t full[S::kBackTeams][kMaxSlots];
+    __shared__ int abort;
+    const int team = threadIdx.x / S::kTeam, lead = threadIdx.x % S::kTeam == 0;
+    const int l = threadIdx.x % TPR, c0 = l * 8, abreast = threadIdx.x % S::kTeam / TPR;
+    Ring<T, TENSORS> ring;
+    ring.bytes = p.rows * p.D * (int)sizeof(T);
+    ring.base = smem + (size_t)team * p.slots * TENSORS * ring.bytes;
+    ring.full = full[team];
+    ring.src[0] = static_cast<const T *>(p.x);
+    ring.src[1] = static_cast<const T *>(p.dy);
+    ring.ld[0] = p.ldx;
+    ring.ld[1] = p.D;
+    if constexpr (PAST) {
+        ring.src[2] = static_cast<const T *>(p.res);
+        ring.ld[2] = p.D;
+    }
+    const long long first = ((long long)blockIdx.x * S::kBackTeams + team) * p.rows;
+    const long long step = (long long)gridDim.x * S::kBackTeams * p.rows;
+    if (threadIdx.x == 0) abort = 0;
+    if (lead) {
+        for (int i = 0; i < p.slots; ++i) sm100::mbar_init(&full[team][i], 1);
+        sm100::fence_mbar_init();
+        for (int i = 0; i < p.slots; ++i) ring.fetch(p, i, first + i * step);
+    }
+    RowSum<TPR, 2 * U> sum = {red[team], team, 0};
     const float inv = 1.f / p.D;
-    constexpr bool kShared = sums_shared<VPT>();
-    float w[kHold ? VPT : 1][8], dw[VPT][8] = {}, db[VPT][8] = {};
-    if constexpr (kShared)  // a thread's own channels: no other meets them
-        for (int k = 0; k < VPT; ++k)
-            for (int e = 0; e < 8; ++e) acc[(k * 16 + e) * TPR + l] = acc[(k * 16 + 8 + e) * TPR + l] = 0.f;
-    if constexpr (kHold) load_columns<T, VPT>(w, p.w, 1.f, c0, TPR * 8, p.D);
-    const T *const s = static_cast<const T *>(p.x), *const dy = static_cast<const T *>(p.dy);
-    const T *const ds = static_cast<const T *>(p.res);
+    Pair w[kHold ? VPT : 1][4], dw[VPT][4], db[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        if constexpr (kHold) column(w[k], p.w, 1.f, c0 + k * TPR * 8, p.D);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dw[k][e] = db[k][e] = both(0.f);
+    }
     T *const dx = static_cast<T *>(p.y);
-    Vec8<T> rs[U][VPT], rd[U][VPT], rp[PAST ? U : 1][VPT];
     float2 st[U];
-    auto fetch = [&](long long row0) {
+    auto statistics = [&](long long block, int i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long row = row0 + u;
-            if (row >= p.N) continue;
-            st[u] = *reinterpret_cast<const float2 *>(p.stats + 2 * row);
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = c0 + k * TPR * 8;
-                if (c >= p.D) continue;
-                rs[u][k].load(s + (row * p.ldx + c));
-                rd[u][k].load(dy + (row * p.D + c));
-                if constexpr (PAST) rp[u][k].load(ds + (row * p.D + c));
-            }
+            const int i = i0 + u * S::kAbreast + abreast;
+            st[u] = make_float2(0.f, 0.f);
+            if (i < p.rows && block + i < p.N) st[u] = *reinterpret_cast<const float2 *>(p.stats + 2 * (block + i));
         }
     };
-    const long long first = ((long long)blockIdx.x * S::kGroups + group) * U;
-    const long long step = (long long)gridDim.x * S::kGroups * U;
-    const long long end = TPR < 32 ? p.N + (long long)(group % (32 / (TPR < 32 ? TPR : 32))) * U : p.N;
-    constexpr bool kAhead = fetch_ahead<T, VPT>(true);
-    if constexpr (kAhead) fetch(first);
-    for (long long row0 = first; row0 < end; row0 += step) {
-        if constexpr (!kAhead) fetch(row0);
-        Vec8<T> ns[U][VPT], nd[U][VPT], np[PAST ? U : 1][VPT];
-        float2 nst[U];
-        float t[2 * U];
+    statistics(first, 0);
+    __syncthreads();
+    int slot = 0;
+    uint32_t parity = 0;
+    for (long long block = first; block < p.N; block += step) {
+        const int n = (int)min((long long)p.rows, p.N - block);
+        wait_block(&full[team][slot], parity, &abort, p.status);
+        for (int i0 = 0; i0 < n; i0 += BATCH) {
+            float2 now[U];
+            float t[2 * U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            nst[u] = st[u];
-            t[2 * u] = t[2 * u + 1] = 0.f;
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * S::kAbreast + abreast;
+                now[u] = st[u];
+                const Pair minus = both(-now[u].x), scale = both(now[u].y);
+                Pair t0 = both(0.f), t1 = t0;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = c0 + k * TPR * 8;
-                if (row0 + u >= p.N || c >= p.D) continue;
-                ns[u][k] = rs[u][k];
-                nd[u][k] = rd[u][k];
-                if constexpr (PAST) np[u][k] = rp[u][k];
-                float wk[1][8], f[8], d[8];
-                if constexpr (!kHold) load_columns<T, 1>(wk, p.w, 1.f, c, 0, p.D);
-                ns[u][k].get(f);
-                nd[u][k].get(d);
+                for (int k = 0; k < VPT; ++k) {
+                    const int c = c0 + k * TPR * 8;
+                    if (i < n && c < p.D) {
+                        Vec8<T> sv, dv;
+                        Pair f[4], d[4];
+                        if constexpr (!kHold) column(w[0], p.w, 1.f, c, p.D);
+                        from_shared(sv, ring.row(p, slot, 0, i) + c);
+                        from_shared(dv, ring.row(p, slot, 1, i) + c);
+                        get4(sv, f);
+                        get4(dv, d);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = (f[e] - nst[u].x) * nst[u].y;
-                    if constexpr (kShared) {
-                        float *const at = acc + (k * 16 + e) * TPR + l;
-                        at[0] = fmaf(d[e], n, at[0]);
-                        at[8 * TPR] += d[e];
-                    } else {
-                        dw[k][e] = fmaf(d[e], n, dw[k][e]);
-                        db[k][e] += d[e];
+                        for (int e = 0; e < 4; ++e) {
+                            const Pair z = mul2(add2(f[e], minus), scale);
+                            const Pair g = mul2(d[e], w[kHold ? k : 0][e]);
+                            dw[k][e] = fma2(d[e], z, dw[k][e]);
+                            db[k][e] = add2(db[k][e], d[e]);
+                            t0 = add2(t0, g);
+                            t1 = fma2(g, z, t1);
+                        }
                     }
-                    const float g = d[e] * (kHold ? w[kHold ? k : 0][e] : wk[0][e]);
-                    t[2 * u] += g;
-                    t[2 * u + 1] = fmaf(g, n, t[2 * u + 1]);
+                }
+                t[2 * u] = sum2(t0);
+                t[2 * u + 1] = sum2(t1);
+            }
+            if (i0 + BATCH < n) statistics(block, i0 + BATCH);
+            else statistics(block + step, 0);
+            sum(t);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * S::kAbreast + abreast;
+                if (i >= n) continue;
+                const Pair minus = both(-now[u].x), scale = both(now[u].y);
+                const Pair mg = both(-t[2 * u] * inv), mgn = both(-t[2 * u + 1] * inv);
+                T *const xr = dx + ((block + i) * p.D + c0);
+#pragma unroll
+                for (int k = 0; k < VPT; ++k) {
+                    const int c = c0 + k * TPR * 8;
+                    if (c < p.D) {
+                        Vec8<T> sv, dv;
+                        Pair f[4], d[4], past[4];
+                        if constexpr (!kHold) column(w[0], p.w, 1.f, c, p.D);
+                        from_shared(sv, ring.row(p, slot, 0, i) + c);
+                        from_shared(dv, ring.row(p, slot, 1, i) + c);
+                        get4(sv, f);
+                        get4(dv, d);
+                        if constexpr (PAST) {
+                            from_shared(sv, ring.row(p, slot, 2, i) + c);
+                            get4(sv, past);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const Pair z = mul2(add2(f[e], minus), scale);
+                            const Pair v = fma2(z, mgn, fma2(d[e], w[kHold ? k : 0][e], mg));
+                            if constexpr (PAST) f[e] = fma2(v, scale, past[e]);
+                            else f[e] = mul2(v, scale);
+                        }
+                        set4(sv, f);
+                        put8(xr + k * TPR * 8, sv);
+                    }
                 }
             }
         }
-        if constexpr (kAhead) fetch(row0 + step);
-        sum(t);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long row = row0 + u;
-            if (row >= p.N) continue;
-            const float mg = t[2 * u] * inv, mgn = t[2 * u + 1] * inv;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = c0 + k * TPR * 8;
-                if (c >= p.D) continue;
-                float wk[1][8], f[8], d[8], z[8] = {};
-                if constexpr (!kHold) load_columns<T, 1>(wk, p.w, 1.f, c, 0, p.D);
-                ns[u][k].get(f);
-                nd[u][k].get(d);
-                if constexpr (PAST) np[u][k].get(z);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = (f[e] - nst[u].x) * nst[u].y;
-                    const float g = fmaf(d[e], kHold ? w[kHold ? k : 0][e] : wk[0][e], -mg);
-                    const float v = fmaf(-n, mgn, g);
-                    f[e] = PAST ? fmaf(v, nst[u].y, z[e]) : v * nst[u].y;
-                }
-                Vec8<T>::store(dx + (row * p.D + c), f);
-            }
+        // the team is through with the block
+        if constexpr (TPR <= 32) __syncwarp();
+        else sm100::named_sync(team + 1, TPR);
+        if (lead && !abort) ring.fetch(p, slot, block + p.slots * step);
+        if (++slot == p.slots) {
+            slot = 0;
+            parity ^= 1;
         }
     }
+    if (lead && abort) drain(full[team], p.slots);
     if (!p.parts) return;
-    constexpr int W = TPR * 8;  // channels of a group's first pieces
-    if constexpr (S::kGroups > 1) {
+    constexpr int kRowGroups = S::kBackThreads / TPR, W = TPR * 8;  // W: channels of a group's first pieces
+    float *const acc = reinterpret_cast<float *>(smem);  // [groups - 1][2][8][TPR]
+    const int group = threadIdx.x / TPR;
+    if constexpr (kRowGroups > 1) {
         static_assert(VPT == 1, "several groups have one piece a thread");
         __syncthreads();
         if (group > 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc[((group - 1) * 2) * W + e * TPR + l] = dw[0][e];
-                acc[((group - 1) * 2 + 1) * W + e * TPR + l] = db[0][e];
+            for (int e = 0; e < 4; ++e) {
+                store2(acc + ((group - 1) * 2) * W + (e * TPR + l) * 2, dw[0][e]);
+                store2(acc + ((group - 1) * 2 + 1) * W + (e * TPR + l) * 2, db[0][e]);
             }
         }
         __syncthreads();
         if (group > 0) return;
-        for (int q = 1; q < S::kGroups; ++q)
+        for (int q = 1; q < kRowGroups; ++q)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dw[0][e] += acc[((q - 1) * 2) * W + e * TPR + l];
-                db[0][e] += acc[((q - 1) * 2 + 1) * W + e * TPR + l];
+            for (int e = 0; e < 4; ++e) {
+                dw[0][e] = add2(dw[0][e], load2(acc + ((q - 1) * 2) * W + (e * TPR + l) * 2));
+                db[0][e] = add2(db[0][e], load2(acc + ((q - 1) * 2 + 1) * W + (e * TPR + l) * 2));
             }
     }
     float *const out = p.parts + (long long)blockIdx.x * 2 * p.D;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = c0 + k * TPR * 8;
-        if (c >= p.D) continue;
-        if constexpr (kShared)
-            for (int e = 0; e < 8; ++e) {
-                dw[k][e] = acc[(k * 16 + e) * TPR + l];
-                db[k][e] = acc[(k * 16 + 8 + e) * TPR + l];
-            }
-        Vec8<float>::store(out + c, dw[k]);
-        Vec8<float>::store(out + p.D + c, db[k]);
+        if (c < p.D) {
+            Vec8<float> v;
+            set4(v, dw[k]);
+            put8(out + c, v);
+            set4(v, db[k]);
+            put8(out + p.D + c, v);
+        }
     }
 }
 
@@ -391,16 +531,54 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// CTAs: no more than fit at once, nor than there are rows.
-template <typename T, typename S> int norm_grid(long long N, bool back) {
-    const long long rows = (long long)S::kGroups * rows_at_once<T, S::VPT>(back);
-    const long long need = (N + rows - 1) / rows;
-    const long long most = (long long)resident(S::kThreads) * (sm_count() > 0 ? sm_count() : 152);
-    return (int)(need < most ? need : most);
+// Rows of a block, blocks of a team, CTAs, their threads and shared memory.  A
+// team's block takes about 4 KB a warp and tensor; the rings of an SM's CTAs share
+// its memory.
+constexpr int kShared = 216 * 1024;  // of an SM
+struct NormPlan {
+    int rows, slots, grid, threads;
+    size_t smem, most;  // of this call, and of any width of the shape
+};
+template <typename T, typename S> NormPlan norm_plan(long long N, int D, int tensors, bool back) {
+    NormPlan r;
+    const int nsm = sm_count() > 0 ? sm_count() : 152, ctas = back ? S::kBackCtas : 1;
+    const int row = D * (int)sizeof(T), batch = rows_at_once(S::VPT, back) * S::kAbreast;
+    r.rows = 4096 * (S::kTeam / 32) / row / batch * batch;
+    if (r.rows < batch) r.rows = batch;
+    int teams = back ? S::kBackTeams : S::kTeams;
+    const long long blocks = (N + r.rows - 1) / r.rows;
+    if (!back && blocks < (long long)teams * nsm) teams = (int)((blocks + nsm - 1) / nsm);
+    r.threads = teams * S::kTeam;
+    const int fixed = !back && weights_in<S>(back) == kStaged ? 64 * S::TPR * S::VPT : 0;
+    const int room = (kShared / ctas - fixed) / (teams * tensors * r.rows * row);
+    r.slots = room < 1 ? 1 : room > kMaxSlots ? kMaxSlots : room;
+    r.smem = (size_t)r.slots * teams * tensors * r.rows * row;
+    // the sums of the row groups but one, at the end
+    const size_t sums = back ? (size_t)(S::kBackThreads / S::TPR - 1) * 16 * S::TPR * sizeof(float) : 0;
+    if (r.smem < sums) r.smem = sums;
+    r.most = kShared / ctas - fixed;
+    const long long need = (blocks + teams - 1) / teams, most = (long long)ctas * nsm;
+    r.grid = (int)(need < most ? need : most);
+    return r;
 }
 
-// f for the shape of D channels.
-template <typename F> auto by_width(int D, F &&f) {
+// f for the shape of D channels.  Outputs: a warp or less a row up to 2048 bf16
+// channels, no barrier; gradients: one piece a thread as far as it goes, for the
+// sums in registers.
+template <typename T, typename F> auto by_width(int D, F &&f) {
+    const int pieces = D / 8;
+    constexpr int V = 16 / (int)sizeof(T), W = 32 * 8 / V;  // pieces of a thread, threads of 256 pieces
+    if (pieces <= 8) return f(RowShape<8, 1>());
+    if (pieces <= 16) return f(RowShape<16, 1>());
+    if (pieces <= 32) return f(RowShape<32, 1>());
+    if (pieces <= 64) return f(RowShape<32, 2>());
+    if (pieces <= 128) return f(RowShape<32, 4>());
+    if (pieces <= 256) return f(RowShape<W, V>());
+    if (pieces <= 512) return f(RowShape<2 * W, V>());
+    if (pieces <= 1024) return f(RowShape<4 * W, V>());
+    return f(RowShape<8 * W, V>());
+}
+template <typename F> auto by_width_backward(int D, F &&f) {
     const int pieces = D / 8;
     if (pieces <= 8) return f(RowShape<8, 1>());
     if (pieces <= 16) return f(RowShape<16, 1>());
@@ -413,43 +591,42 @@ template <typename F> auto by_width(int D, F &&f) {
     return f(RowShape<512, 4>());
 }
 
+template <typename K>
+cudaError_t launch(K kern, uintptr_t (&set)[64], NormArgs p, const NormPlan &plan, cudaStream_t st) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (set[dev] != context_key()) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.most);
+        if (e != cudaSuccess) return e;
+        set[dev] = context_key();
+    }
+    p.rows = plan.rows;
+    p.slots = plan.slots;
+    p.status = device_status_ptr();
+    kern<<<plan.grid, plan.threads, plan.smem, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T> cudaError_t forward(const NormArgs &p, cudaStream_t st) {
-    return by_width(p.D, [&](auto shape) {
+    return by_width<T>(p.D, [&](auto shape) {
         using S = decltype(shape);
-        const int grid = norm_grid<T, S>(p.N, false);
-        if (p.res) layer_norm_kernel<T, S, true><<<grid, S::kThreads, 0, st>>>(p);
-        else layer_norm_kernel<T, S, false><<<grid, S::kThreads, 0, st>>>(p);
-        return cudaGetLastError();
+        static uintptr_t set[2][64] = {};
+        const NormPlan plan = norm_plan<T, S>(p.N, p.D, p.res ? 2 : 1, false);
+        return p.res ? launch(layer_norm_kernel<T, S, true>, set[1], p, plan, st)
+                     : launch(layer_norm_kernel<T, S, false>, set[0], p, plan, st);
     });
 }
 
-// More shared memory than a launch may have without asking; once a context.
-template <typename K> cudaError_t allow_smem(K kern, uintptr_t (&set)[64], size_t bytes) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (set[dev] == context_key()) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) set[dev] = context_key();
-    return e;
-}
-
 template <typename T> cudaError_t backward(const NormArgs &p, float *dw, float *db, cudaStream_t st) {
-    return by_width(p.D, [&](auto shape) {
+    return by_width_backward(p.D, [&](auto shape) {
         using S = decltype(shape);
-        const int grid = norm_grid<T, S>(p.N, true);
-        constexpr int kept = sums_shared<S::VPT>() ? S::VPT : S::kGroups - 1;
-        constexpr size_t smem = (size_t)kept * 16 * S::TPR * sizeof(float);
-        if constexpr (smem > 48 * 1024) {
-            static uintptr_t set[2][64] = {};
-            const cudaError_t e = p.res ? allow_smem(layer_norm_backward_kernel<T, S, true>, set[1], smem)
-                                        : allow_smem(layer_norm_backward_kernel<T, S, false>, set[0], smem);
-            if (e != cudaSuccess) return e;
-        }
-        if (p.res) layer_norm_backward_kernel<T, S, true><<<grid, S::kThreads, smem, st>>>(p);
-        else layer_norm_backward_kernel<T, S, false><<<grid, S::kThreads, smem, st>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        static uintptr_t set[2][64] = {};
+        const NormPlan plan = norm_plan<T, S>(p.N, p.D, p.res ? 3 : 2, true);
+        const cudaError_t e =
+            p.res ? launch(layer_norm_backward_kernel<T, S, true>, set[1], p, plan, st)
+                  : launch(layer_norm_backward_kernel<T, S, false>, set[0], p, plan, st);
         if (e != cudaSuccess || !p.parts) return e;
-        layer_norm_sum_kernel<<<(2 * p.D + 31) / 32, 1024, 0, st>>>(p.parts, grid, p.D, dw, db);
+        layer_norm_sum_kernel<<<(2 * p.D + 31) / 32, 1024, 0, st>>>(p.parts, plan.grid, p.D, dw, db);
         return cudaGetLastError();
     });
 }
@@ -457,11 +634,17 @@ template <typename T> cudaError_t backward(const NormArgs &p, float *dw, float *
 }  // namespace
 
 int layer_norm_parts(long long N, int D) {
-    // the larger of the two types' grids
-    return by_width(D, [&](auto shape) {
+    // the larger of the types' and the forms' grids
+    return by_width_backward(D, [&](auto shape) {
         using S = decltype(shape);
-        const int a = norm_grid<__nv_bfloat16, S>(N, true), b = norm_grid<float, S>(N, true);
-        return a > b ? a : b;
+        int most = 0;
+        for (int tensors = 2; tensors <= 3; ++tensors) {
+            const int a = norm_plan<__nv_bfloat16, S>(N, D, tensors, true).grid;
+            const int b = norm_plan<float, S>(N, D, tensors, true).grid;
+            most = most > a ? most : a;
+            most = most > b ? most : b;
+        }
+        return most;
     });
 }
 

@@ -28,8 +28,8 @@
 // state that arrives, by selection, never by a factor of 0 (a NaN would pass).
 #include <cudaTypedefs.h>
 
+#include "gdn_pair.cuh"
 #include "gdn_sm100.cuh"
-#include "gdn_vec8.cuh"
 
 namespace gdn {
 
@@ -67,54 +67,6 @@ template <typename T, bool SIG> __device__ __forceinline__ void gate_ab(float g,
 
 template <typename T, bool SIG> struct GateType { using type = T; };
 template <typename T> struct GateType<T, false> { using type = float; };
-
-// A lane's two channels, in the registers that packed float32 operations take.
-struct Pair {
-    unsigned long long v;
-};
-__device__ __forceinline__ Pair pair(float x, float y) {
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ Pair both(float x) { return pair(x, x); }
-__device__ __forceinline__ float2 split(Pair a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-    Pair r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ Pair either(bool first, Pair a, Pair b) { return {first ? a.v : b.v}; }
-
-__device__ __forceinline__ Pair load2(const float *p) {
-    const float2 x = *reinterpret_cast<const float2 *>(p);
-    return pair(x.x, x.y);
-}
-__device__ __forceinline__ Pair unpack(uint32_t w) {
-    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ Pair load2(const __nv_bfloat16 *p) {
-    return unpack(*reinterpret_cast<const uint32_t *>(p));
-}
-__device__ __forceinline__ void store2(float *p, Pair x) { *reinterpret_cast<float2 *>(p) = split(x); }
-__device__ __forceinline__ void store2(__nv_bfloat16 *p, Pair x) {
-    const float2 f = split(x);
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(f.x, f.y);
-}
 
 // a and b of a lane's gates in shared memory (without a sigmoid b is not used).
 // bf16 gates are held at -87: exp(87) stays a number and so does b.
