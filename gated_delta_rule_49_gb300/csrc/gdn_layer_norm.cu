@@ -149,11 +149,11 @@ __device__ __forceinline__ void column(Pair (&v)[4], const float *p, float other
     }
 }
 // Where w and b of a piece come from: a thread's registers, where it has one piece;
-// shared memory, staged once by the CTA, up to 2048 channels; else the L1 cache.
+// shared memory, staged once by the CTA, up to 8192 channels; else the L1 cache.
 enum { kRegisters, kStaged, kCached };
 template <typename S> constexpr int weights_in(bool back) {
     return S::VPT == 1 || (back && S::VPT == 2) ? kRegisters
-           : !back && S::TPR * S::VPT * 8 <= 2048 ? kStaged : kCached;
+           : !back && S::TPR * S::VPT * 8 <= 8192 ? kStaged : kCached;
 }
 // Staged: the lower and the upper four channels of every piece apart, so that
 // neighbouring lanes read neighbouring 16 bytes.
@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once(VPT, false);
     constexpr int TENSORS = RES ? 2 : 1, BATCH = U * S::kAbreast;
     constexpr int kWeights = weights_in<S>(false), PIECES = TPR * VPT;
-    __shared__ float4 weights[kWeights == kStaged ? 4 * PIECES : 1];
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[S::kTeams][2][TPR >= 32 ? TPR / 32 : 1][U];
     __shared__ uint64_t full[S::kTeams][kMaxSlots];
@@ -196,7 +195,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     const int l = threadIdx.x % TPR, c0 = l * 8, abreast = threadIdx.x % S::kTeam / TPR;
     Ring<T, TENSORS> ring;
     ring.bytes = p.rows * p.D * (int)sizeof(T);
-    ring.base = smem + (size_t)team * p.slots * TENSORS * ring.bytes;
+    float4 *const weights = reinterpret_cast<float4 *>(smem);
+    ring.base = smem + (kWeights == kStaged ? 64 * PIECES : 0) + (size_t)team * p.slots * TENSORS * ring.bytes;
     ring.full = full[team];
     ring.src[0] = static_cast<const T *>(p.x);
     ring.ld[0] = p.ldx;
@@ -426,6 +426,11 @@ __global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
             if (i0 + BATCH < n) statistics(block, i0 + BATCH);
             else statistics(block + step, 0);
             sum(t);
+            if (i0 == 0) {  // the team has met: all of it is through with the block before
+                if constexpr (TPR <= 32) __syncwarp();
+                if (lead && block != first && p.slots > 1 && !abort)
+                    ring.fetch(p, slot ? slot - 1 : p.slots - 1, block + (p.slots - 1) * step);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = i0 + u * S::kAbreast + abreast;
@@ -461,16 +466,18 @@ __global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
                 }
             }
         }
-        // the team is through with the block
-        if constexpr (TPR <= 32) __syncwarp();
-        else sm100::named_sync(team + 1, TPR);
-        if (lead && !abort) ring.fetch(p, slot, block + p.slots * step);
+        if (p.slots == 1) {
+            if constexpr (TPR <= 32) __syncwarp();
+            else sm100::named_sync(team + 1, TPR);
+            if (lead && !abort) ring.fetch(p, 0, block + step);
+        }
         if (++slot == p.slots) {
             slot = 0;
             parity ^= 1;
         }
     }
     if (lead && abort) drain(full[team], p.slots);
+    pdl_trigger();
     if (!p.parts) return;
     constexpr int kRowGroups = S::kBackThreads / TPR, W = TPR * 8;  // W: channels of a group's first pieces
     float *const acc = reinterpret_cast<float *>(smem);  // [groups - 1][2][8][TPR]
@@ -515,6 +522,7 @@ __global__ void __launch_bounds__(1024)
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
+    pdl_wait();  // launched beside the rows' kernel
     float s = 0.f;
     if (col < 2 * D) {
 #pragma unroll 8
@@ -532,8 +540,8 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Rows of a block, blocks of a team, CTAs, their threads and shared memory.  A
-// team's block takes about 4 KB a warp and tensor; the rings of an SM's CTAs share
-// its memory.
+// team's block takes about 4 KB a warp and tensor (gradients: 1 KB, so that several
+// fit); the rings of an SM's CTAs share its memory.
 constexpr int kShared = 216 * 1024;  // of an SM
 struct NormPlan {
     int rows, slots, grid, threads;
@@ -543,20 +551,21 @@ template <typename T, typename S> NormPlan norm_plan(long long N, int D, int ten
     NormPlan r;
     const int nsm = sm_count() > 0 ? sm_count() : 152, ctas = back ? S::kBackCtas : 1;
     const int row = D * (int)sizeof(T), batch = rows_at_once(S::VPT, back) * S::kAbreast;
-    r.rows = 4096 * (S::kTeam / 32) / row / batch * batch;
+    r.rows = (back ? 1024 : 4096) * (S::kTeam / 32) / row / batch * batch;
     if (r.rows < batch) r.rows = batch;
+    const int fixed = !back && weights_in<S>(back) == kStaged ? 64 * S::TPR * S::VPT : 0;
+    const int block = tensors * r.rows * row, room = kShared / ctas - fixed;
     int teams = back ? S::kBackTeams : S::kTeams;
+    if (teams > room / block) teams = room / block;
     const long long blocks = (N + r.rows - 1) / r.rows;
     if (!back && blocks < (long long)teams * nsm) teams = (int)((blocks + nsm - 1) / nsm);
     r.threads = teams * S::kTeam;
-    const int fixed = !back && weights_in<S>(back) == kStaged ? 64 * S::TPR * S::VPT : 0;
-    const int room = (kShared / ctas - fixed) / (teams * tensors * r.rows * row);
-    r.slots = room < 1 ? 1 : room > kMaxSlots ? kMaxSlots : room;
-    r.smem = (size_t)r.slots * teams * tensors * r.rows * row;
+    r.slots = room / (teams * block) > kMaxSlots ? kMaxSlots : room / (teams * block);
+    r.smem = fixed + (size_t)r.slots * teams * block;
     // the sums of the row groups but one, at the end
     const size_t sums = back ? (size_t)(S::kBackThreads / S::TPR - 1) * 16 * S::TPR * sizeof(float) : 0;
     if (r.smem < sums) r.smem = sums;
-    r.most = kShared / ctas - fixed;
+    r.most = kShared / ctas;
     const long long need = (blocks + teams - 1) / teams, most = (long long)ctas * nsm;
     r.grid = (int)(need < most ? need : most);
     return r;
@@ -626,8 +635,8 @@ template <typename T> cudaError_t backward(const NormArgs &p, float *dw, float *
             p.res ? launch(layer_norm_backward_kernel<T, S, true>, set[1], p, plan, st)
                   : launch(layer_norm_backward_kernel<T, S, false>, set[0], p, plan, st);
         if (e != cudaSuccess || !p.parts) return e;
-        layer_norm_sum_kernel<<<(2 * p.D + 31) / 32, 1024, 0, st>>>(p.parts, plan.grid, p.D, dw, db);
-        return cudaGetLastError();
+        return launch_pdl(layer_norm_sum_kernel, (2 * p.D + 31) / 32, 1024, 0, st,
+                          static_cast<const float *>(p.parts), plan.grid, p.D, dw, db);
     });
 }
 
