@@ -29,7 +29,7 @@ template <int TPR_, int VPT_> struct RowShape {
         kAbreast = kTeam / TPR,  // rows side by side in a team
         // Outputs: one CTA an SM, of up to 20 warps, fewer where the rows are few (24
         // warps spilled; two CTAs of 8 would each hold the weights).  Gradients: 16
-        // warps an SM.
+        // warps an SM (24 spilled: 94 -> 116 us for 512 channels).
         kTeams = kTeam < 640 ? 640 / kTeam : 1,
         kThreads = kTeams * kTeam,
         kBackThreads = kTeam < 256 ? 256 : kTeam,
@@ -39,7 +39,9 @@ template <int TPR_, int VPT_> struct RowShape {
 };
 // Rows of a thread at once: their chains of sums overlap, and one meeting of a
 // team's warps serves them all.
-constexpr int rows_at_once(int vpt, bool back) { return back ? (vpt == 1 ? 2 : 1) : (vpt < 4 ? 4 / vpt : 1); }
+template <typename T> constexpr int rows_at_once(int tpr, int vpt, bool back) {
+    return !back ? (vpt < 4 ? 4 / vpt : 1) : vpt > 1 ? 1 : tpr > 32 && sizeof(T) == 2 ? 4 : 2;
+}
 constexpr int kMaxSlots = 4;  // blocks of a team in shared memory
 
 // Sums of U values over the threads of a row, the same in all of them and in a
@@ -47,28 +49,71 @@ constexpr int kMaxSlots = 4;  // blocks of a team in shared memory
 // buffers of `red` take turns.
 template <int TPR, int U> struct RowSum {
     static constexpr int kWarps = TPR / 32;
-    float (*red)[kWarps > 0 ? kWarps : 1][U];  // [2][warps][U], the team's
+    float (*red)[(kWarps > 0 ? kWarps : 1) * U];  // [2][warps x U], the team's
     int team, turn;
+    // Half of the values for the lanes with the bit `off`, half for those without:
+    // each lane adds what its partner has of its half.
+    template <int N>
+    static __device__ __forceinline__ void share(float (&x)[N], int off) {
+        const bool high = threadIdx.x & off;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float mine = high ? x[i + N / 2] : x[i], its = high ? x[i] : x[i + N / 2];
+            x[i] = mine + __shfl_xor_sync(0xffffffffu, its, off);
+        }
+    }
+    // The sum of value lane / (32 / U) over a warp (of four values in 6 exchanges, one
+    // by one 20).
+    static __device__ __forceinline__ float shared_out(const float (&x)[U]) {
+        static_assert(U == 1 || U == 2 || U == 4 || U == 8, "a power of two of values");
+        float y[8] = {};
+#pragma unroll
+        for (int u = 0; u < U; ++u) y[u] = x[u];
+        int off = 16;
+        if constexpr (U == 8) {
+            share<8>(y, off);
+            off >>= 1;
+        }
+        if constexpr (U >= 4) {
+            share<4>(reinterpret_cast<float (&)[4]>(y), off);
+            off >>= 1;
+        }
+        if constexpr (U >= 2) {
+            share<2>(reinterpret_cast<float (&)[2]>(y), off);
+            off >>= 1;
+        }
+        float r = y[0];
+#pragma unroll
+        for (int o = 16 / U; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        return r;
+    }
     __device__ __forceinline__ void operator()(float (&x)[U]) {
+        if constexpr (TPR < 32) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int off = (TPR < 32 ? TPR : 32) / 2; off > 0; off >>= 1)
-                x[u] += __shfl_xor_sync(0xffffffffu, x[u], off);
-        if constexpr (TPR > 32) {
-            const int warp = (threadIdx.x % TPR) >> 5;
-            if ((threadIdx.x & 31) == 0) {
+                for (int off = TPR / 2; off > 0; off >>= 1) x[u] += __shfl_xor_sync(0xffffffffu, x[u], off);
+        } else {
+            const float r = shared_out(x);
+            const int lane = threadIdx.x & 31;
+            if constexpr (TPR == 32) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) red[turn][warp][u] = x[u];
+                for (int u = 0; u < U; ++u) x[u] = __shfl_sync(0xffffffffu, r, u * (32 / U));
+            } else {
+                const int warp = (threadIdx.x % TPR) >> 5;
+                if (lane % (32 / U) == 0) red[turn][warp * U + lane / (32 / U)] = r;
+                sm100::named_sync(team + 1, TPR);
+                // lanes add the warps' sums of value lane % U, and hand them round
+                constexpr int ALL = kWarps * U;
+                float z = red[turn][lane % ALL];
+#pragma unroll
+                for (int i = 32; i < ALL; i += 32) z += red[turn][i + lane];
+#pragma unroll
+                for (int o = U; o < (ALL < 32 ? ALL : 32); o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+#pragma unroll
+                for (int u = 0; u < U; ++u) x[u] = __shfl_sync(0xffffffffu, z, u);
+                turn ^= 1;
             }
-            sm100::named_sync(team + 1, TPR);
-#pragma unroll
-            for (int u = 0; u < U; ++u) x[u] = red[turn][0][u];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w)
-#pragma unroll
-                for (int u = 0; u < U; ++u) x[u] += red[turn][w][u];
-            turn ^= 1;
         }
     }
 };
@@ -184,11 +229,11 @@ __device__ __forceinline__ float sum2(Pair x) {
 template <typename T, typename S, bool RES>
 __global__ void __launch_bounds__(S::kThreads, 1)
     layer_norm_kernel(const NormArgs p) {
-    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once(VPT, false);
+    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T>(TPR, VPT, false);
     constexpr int TENSORS = RES ? 2 : 1, BATCH = U * S::kAbreast;
     constexpr int kWeights = weights_in<S>(false), PIECES = TPR * VPT;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float red[S::kTeams][2][TPR >= 32 ? TPR / 32 : 1][U];
+    __shared__ __align__(16) float red[S::kTeams][2][(TPR >= 32 ? TPR / 32 : 1) * U];
     __shared__ uint64_t full[S::kTeams][kMaxSlots];
     __shared__ int abort;
     const int team = threadIdx.x / S::kTeam, lead = threadIdx.x % S::kTeam == 0;
@@ -334,11 +379,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 template <typename T, typename S, bool PAST>
 __global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
     layer_norm_backward_kernel(const NormArgs p) {
-    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once(VPT, true);
+    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T>(TPR, VPT, true);
     constexpr int TENSORS = PAST ? 3 : 2, BATCH = U * S::kAbreast;
     constexpr bool kHold = weights_in<S>(true) == kRegisters;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float red[S::kBackTeams][2][TPR >= 32 ? TPR / 32 : 1][2 * U];
+    __shared__ __align__(16) float red[S::kBackTeams][2][(TPR >= 32 ? TPR / 32 : 1) * 2 * U];
     __shared__ uint64_t full[S::kBackTeams][kMaxSlots];
     __shared__ int abort;
     const int team = threadIdx.x / S::kTeam, lead = threadIdx.x % S::kTeam == 0;
@@ -540,8 +585,8 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Rows of a block, blocks of a team, CTAs, their threads and shared memory.  A
-// team's block takes about 4 KB a warp and tensor (gradients: 1 KB, so that several
-// fit); the rings of an SM's CTAs share its memory.
+// team's block takes about 4 KB a warp and tensor (gradients of wide rows: 1 KB, so
+// that several fit); the rings of an SM's CTAs share its memory.
 constexpr int kShared = 216 * 1024;  // of an SM
 struct NormPlan {
     int rows, slots, grid, threads;
@@ -550,8 +595,8 @@ struct NormPlan {
 template <typename T, typename S> NormPlan norm_plan(long long N, int D, int tensors, bool back) {
     NormPlan r;
     const int nsm = sm_count() > 0 ? sm_count() : 152, ctas = back ? S::kBackCtas : 1;
-    const int row = D * (int)sizeof(T), batch = rows_at_once(S::VPT, back) * S::kAbreast;
-    r.rows = (back ? 1024 : 4096) * (S::kTeam / 32) / row / batch * batch;
+    const int row = D * (int)sizeof(T), batch = rows_at_once<T>(S::TPR, S::VPT, back) * S::kAbreast;
+    r.rows = (back && S::TPR > 32 ? 1024 : 4096) * (S::kTeam / 32) / row / batch * batch;
     if (r.rows < batch) r.rows = batch;
     const int fixed = !back && weights_in<S>(back) == kStaged ? 64 * S::TPR * S::VPT : 0;
     const int block = tensors * r.rows * row, room = kShared / ctas - fixed;
