@@ -264,18 +264,33 @@ __device__ __forceinline__ int run_seq(const RunMask &m, int i) {
     return __shfl_sync(0xffffffffu, m.seq, i + 1);
 }
 
-// A tile's totals to every CTA of the cluster, by one warp.
+// A tile's totals to the CTAs of the cluster: every warp has them and sends them to
+// one.
 __device__ __forceinline__ void send_totals(Totals &to, uint64_t *sent, int buf, int rank, int cluster,
                                             const Piece &t, int reset) {
-    const int lane = threadIdx.x & 31;
-    for (int r = 0; r < cluster; ++r) {
-        const uint32_t bar = peer(&sent[buf], r);
-        send4(peer(&to.piece[buf][rank][lane], r), bar, t);
-        if (lane == 0) send1(peer(&to.reset[buf][rank], r), bar, reset);
-    }
+    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+    if (r >= cluster) return;
+    const uint32_t bar = peer(&sent[buf], r);
+    send4(peer(&to.piece[buf][rank][lane], r), bar, t);
+    if (lane == 0) send1(peer(&to.reset[buf][rank], r), bar, reset);
 }
 __device__ __forceinline__ void expect_totals(uint64_t *sent, int buf, int cluster) {
     mbar_arrive_expect_tx(&sent[buf], cluster * (32 * sizeof(Piece) + sizeof(int)));
+}
+// The tiles' totals applied to c, this CTA's state of the stream before them: c
+// becomes what it is after them; returns what it is before this CTA's tile.
+template <bool MASKED>
+__device__ __forceinline__ Pair apply_totals(const Totals &to, int buf, int rank, int cluster, Pair &c) {
+    const int lane = threadIdx.x & 31;
+    Pair mine = c;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+        if (r < cluster) {
+            mine = either(r == rank, c, mine);
+            over(c, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
+        }
+    }
+    return mine;
 }
 
 // ------------------------------------------------------------------ forward
@@ -376,35 +391,40 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         // the stage is in registers
         if (threadIdx.x == 0 && !sh.abort) fetch(n + ST);
         Pair h = carry;
+        auto reset = [&](int w) { return MASKED ? sh.reset[buf][w] : 0; };
         if constexpr (CLUSTER) {
-            Totals &to = sh.totals[0];
-            if (warp == 0) {
-                Piece t = sh.run[buf][0][lane];
-                int reset = MASKED ? sh.reset[buf][0] : 0;
+            Piece before = {one, zero}, t;
+            int cut = 0, all_cut;
+            as_constant(warp, [&](auto number) {
+                constexpr int W = decltype(number)::value;
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) {
-                    const int r = MASKED ? sh.reset[buf][w] : 0;
-                    join(t, sh.run[buf][w][lane], r);
-                    reset |= r;
+                for (int w = 0; w < W; ++w) {
+                    join(before, sh.run[buf][w][lane], reset(w));
+                    cut |= reset(w);
                 }
-                send_totals(to, sh.sent, buf, rank, cluster, t, reset);
-            }
-            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
-            for (int r = 0; r < cluster; ++r) {
-                if (r == rank) h = carry;
-                over(carry, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
-            }
-        }
-        as_constant(warp, [&](auto number) {
-            constexpr int W = decltype(number)::value;
+                t = before;
+                all_cut = cut;
 #pragma unroll
-            for (int w = 0; w < W; ++w) over(h, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
-            if constexpr (!CLUSTER) {
+                for (int w = W; w < kWarps; ++w) {
+                    join(t, sh.run[buf][w][lane], reset(w));
+                    all_cut |= reset(w);
+                }
+            });
+            Totals &to = sh.totals[0];
+            send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
+            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
+            h = apply_totals<MASKED>(to, buf, rank, cluster, carry);
+            over(h, before, cut);
+        } else {
+            as_constant(warp, [&](auto number) {
+                constexpr int W = decltype(number)::value;
+#pragma unroll
+                for (int w = 0; w < W; ++w) over(h, sh.run[buf][w][lane], reset(w));
                 carry = h;
 #pragma unroll
-                for (int w = W; w < kWarps; ++w) over(carry, sh.run[buf][w][lane], MASKED && sh.reset[buf][w]);
-            }
-        });
+                for (int w = W; w < kWarps; ++w) over(carry, sh.run[buf][w][lane], reset(w));
+            });
+        }
         // the state before every 64th token (short dense sequences: at their starts)
         const bool mapped = !MASKED || p.map;
         if (p.states && mapped && t0 % kScanBlock == 0 && t0 < len && live)
@@ -566,40 +586,46 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         // every warp is through with the tile before
         if (threadIdx.x == 0 && n > 0 && !sh.abort) fetch(n - 1 + ST);
         Pair v = carry;  // a G of the run's next token
+        auto reset = [&](int w, int bit) { return MASKED ? sh.reset[buf][w] & bit : 0; };
         if constexpr (CLUSTER) {
-            Totals &to = sh.totals[0];
-            if (warp == 0) {
-                Piece t = sh.run[buf][kWarps - 1][lane];
-                int reset = MASKED ? sh.reset[buf][kWarps - 1] >> 1 : 0;
+            Piece after = {one, zero}, t;
+            int cut = 0, all_cut;
+            as_constant(warp, [&](auto number) {
+                constexpr int W = decltype(number)::value;
 #pragma unroll
-                for (int w = kWarps - 2; w >= 0; --w) {
-                    const int r = MASKED ? sh.reset[buf][w] >> 1 : 0;
-                    join(t, sh.run[buf][w][lane], r);
-                    reset |= r;
+                for (int w = kWarps - 1; w > W; --w) {
+                    join(after, sh.run[buf][w][lane], reset(w, 2));
+                    cut |= reset(w, 2);
                 }
-                send_totals(to, sh.sent, buf, rank, cluster, t, reset);
-            }
+                t = after;
+                all_cut = cut;
+#pragma unroll
+                for (int w = W; w >= 0; --w) {
+                    join(t, sh.run[buf][w][lane], reset(w, 2));
+                    all_cut |= reset(w, 2);
+                }
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, reset(w, 1));
+            });
+            Totals &to = sh.totals[0];
+            send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
             wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
-            for (int r = 0; r < cluster; ++r) {
-                if (r == rank) v = carry;
-                over(carry, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
-            }
-        }
-        as_constant(warp, [&](auto number) {
-            constexpr int W = decltype(number)::value;
+            v = apply_totals<MASKED>(to, buf, rank, cluster, carry);
+            over(v, after, cut);
+        } else {
+            as_constant(warp, [&](auto number) {
+                constexpr int W = decltype(number)::value;
 #pragma unroll
-            for (int w = 0; w < W; ++w)
-                over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, MASKED && (sh.reset[buf][w] & 1));
+                for (int w = 0; w < W; ++w)
+                    over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, reset(w, 1));
 #pragma unroll
-            for (int w = kWarps - 1; w > W; --w)
-                over(v, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
-            if constexpr (!CLUSTER) {
+                for (int w = kWarps - 1; w > W; --w) over(v, sh.run[buf][w][lane], reset(w, 2));
                 carry = v;
 #pragma unroll
-                for (int w = W; w >= 0; --w)
-                    over(carry, sh.run[buf][w][lane], MASKED && (sh.reset[buf][w] & 2));
-            }
-        });
+                for (int w = W; w >= 0; --w) over(carry, sh.run[buf][w][lane], reset(w, 2));
+            });
+        }
         if (m.act) {
             T *const dx = static_cast<T *>(p.dx) + ((long long)(base + t0) * p.D + c);
             G *const dg = static_cast<G *>(p.dgate) + ((long long)(base + t0) * p.D + c);
