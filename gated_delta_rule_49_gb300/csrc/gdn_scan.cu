@@ -42,7 +42,6 @@ using namespace sm100;
 constexpr int kChannels = 64;  // of a CTA
 constexpr int kWarps = 8;      // runs of a tile
 constexpr int kScanThreads = kWarps * 32;
-constexpr int kMaxCluster = 8;
 constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
 
 // a and b of a gate.  b = 1 - a is formed without the difference: a near 1
@@ -107,7 +106,10 @@ template <typename T, bool SIG, bool BACK> struct Shape {
     static constexpr int kXBytes = kTokens * kChannels * (int)sizeof(T);
     static constexpr int kGBytes = kTokens * kChannels * (int)sizeof(G);
     static constexpr int kStage = kXBytes * (BACK ? 2 : 1) + kGBytes;
-    static constexpr int kStages = BACK ? 3 : 2;
+    // two CTAs an SM: a third tile of 48 KB would leave one (float32 gradients 143 -> 115 us)
+    static constexpr int kStages = BACK && kStage <= 32768 ? 3 : 2;
+    // most CTAs of a cluster: the totals of more would leave one CTA an SM
+    static constexpr int kCluster = BACK && kStages * kStage > 81920 ? 4 : 8;
 };
 
 struct ScanRun {
@@ -128,15 +130,15 @@ struct ScanRun {
 struct Piece {         // what a run or a tile does to a lane's channels: c -> p c + h
     Pair p, h;
 };
-struct Totals {        // of a tile, sent through a cluster
-    Piece piece[2][kMaxCluster][32];
-    int reset[2][kMaxCluster];
+template <int N> struct Totals {  // of a tile, sent through a cluster
+    Piece piece[2][N][32];
+    int reset[2][N];
 };
-template <bool BACK, bool CLUSTER> struct ScanShared {
+template <typename S, bool BACK, bool CLUSTER> struct ScanShared {
     Piece run[2][kWarps][32];
     Pair state[BACK ? 2 : 1][BACK ? kWarps : 1][32];  // backward: the forward pass's h
     int reset[2][kWarps];  // bit 0: a start among the run's tokens, bit 1: an end
-    Totals totals[CLUSTER ? 1 : 0];
+    Totals<S::kCluster> totals[CLUSTER ? 1 : 0];
     uint64_t full[8], sent[2];
     int abort;
 };
@@ -266,7 +268,8 @@ __device__ __forceinline__ int run_seq(const RunMask &m, int i) {
 
 // A tile's totals to the CTAs of the cluster: every warp has them and sends them to
 // one.
-__device__ __forceinline__ void send_totals(Totals &to, uint64_t *sent, int buf, int rank, int cluster,
+template <int N>
+__device__ __forceinline__ void send_totals(Totals<N> &to, uint64_t *sent, int buf, int rank, int cluster,
                                             const Piece &t, int reset) {
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
     if (r >= cluster) return;
@@ -279,12 +282,12 @@ __device__ __forceinline__ void expect_totals(uint64_t *sent, int buf, int clust
 }
 // The tiles' totals applied to c, this CTA's state of the stream before them: c
 // becomes what it is after them; returns what it is before this CTA's tile.
-template <bool MASKED>
-__device__ __forceinline__ Pair apply_totals(const Totals &to, int buf, int rank, int cluster, Pair &c) {
+template <bool MASKED, int N>
+__device__ __forceinline__ Pair apply_totals(const Totals<N> &to, int buf, int rank, int cluster, Pair &c) {
     const int lane = threadIdx.x & 31;
     Pair mine = c;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
+    for (int r = 0; r < N; ++r) {
         if (r < cluster) {
             mine = either(r == rank, c, mine);
             over(c, to.piece[buf][r][lane], MASKED && to.reset[buf][r]);
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     using G = typename S::G;
     constexpr int R = S::kRun, ST = S::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ ScanShared<false, CLUSTER> sh;
+    __shared__ ScanShared<S, false, CLUSTER> sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cluster = CLUSTER ? p.cluster : 1;
     const int rank = CLUSTER ? (int)(blockIdx.x % cluster) : 0;
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                     all_cut |= reset(w);
                 }
             });
-            Totals &to = sh.totals[0];
+            auto &to = sh.totals[0];
             send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
             wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
             h = apply_totals<MASKED>(to, buf, rank, cluster, carry);
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     constexpr int R = S::kRun, ST = S::kStages;
     static_assert(S::kTokens == kScanBlock, "a tile starts from a kept state");
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ ScanShared<true, CLUSTER> sh;
+    __shared__ ScanShared<S, true, CLUSTER> sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cluster = CLUSTER ? p.cluster : 1;
     const int rank = CLUSTER ? (int)(blockIdx.x % cluster) : 0;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 for (int w = 0; w < W; ++w)
                     over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, reset(w, 1));
             });
-            Totals &to = sh.totals[0];
+            auto &to = sh.totals[0];
             send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
             wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
             v = apply_totals<MASKED>(to, buf, rank, cluster, carry);
@@ -809,7 +812,7 @@ struct ScanPlan {
     int streams, cluster;
     ScanRun run;
 };
-ScanPlan scan_plan(const ScanArgs &a, int tile, const int *map) {
+ScanPlan scan_plan(const ScanArgs &a, int tile, int most, const int *map) {
     ScanPlan s = {};
     ScanRun &r = s.run;
     const int nsm = sm_count() > 0 ? sm_count() : 152;
@@ -844,7 +847,7 @@ ScanPlan scan_plan(const ScanArgs &a, int tile, const int *map) {
     r.rows = r.step < r.stream ? r.step : r.stream;
     const int tiles = (r.stream + r.step - 1) / r.step;
     s.cluster = 1;
-    while (s.cluster < kMaxCluster && 2 * s.cluster <= tiles &&
+    while (s.cluster < most && 2 * s.cluster <= tiles &&
            2LL * r.groups * s.streams * s.cluster < 3LL * nsm)
         s.cluster *= 2;
     r.cluster = s.cluster;
@@ -916,7 +919,7 @@ cudaError_t launch_one(const ScanArgs &a, const ScanPlan &s, bool after_map, cud
 }
 template <typename T, bool SIG, bool BACK>
 cudaError_t launch_any(const ScanArgs &a, const int *map, bool after_map, cudaStream_t st) {
-    const ScanPlan s = scan_plan(a, Shape<T, SIG, BACK>::kTokens, map);
+    const ScanPlan s = scan_plan(a, Shape<T, SIG, BACK>::kTokens, Shape<T, SIG, BACK>::kCluster, map);
     if (s.masked)
         return s.cluster > 1 ? launch_one<T, SIG, BACK, true, true>(a, s, after_map, st)
                              : launch_one<T, SIG, BACK, true, false>(a, s, after_map, st);
