@@ -809,7 +809,7 @@ int gdn_scan_backward(const void *x, const void *gate, const void *dh, const flo
     const void *ins[] = {x, gate, dh};
     for (const void *p : ins)
         if (p == dx || p == dgate) return GDN_ERR_INVALID_ARG;
-    if (dx == dgate) return GDN_ERR_INVALID_ARG;
+    if (dx == dgate || (dh0 && dh0 == dh_T)) return GDN_ERR_INVALID_ARG;
     const size_t need = gdn_scan_backward_workspace_size(B, T, D, packed, states != nullptr);
     if (workspace_bytes < need || (need && !workspace)) return GDN_ERR_WORKSPACE;
     gdn::ScanArgs a = {};

@@ -42,9 +42,10 @@ __device__ __forceinline__ Pair unpack(uint32_t w) {
     return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// (As one register pair: put together from two, a load ahead of its use was waited
+// for where it stood.)
 __device__ __forceinline__ Pair load2(const float *p) {
-    const float2 x = *reinterpret_cast<const float2 *>(p);
-    return pair(x.x, x.y);
+    return {*reinterpret_cast<const unsigned long long *>(p)};
 }
 __device__ __forceinline__ void store2(float *p, Pair x) { *reinterpret_cast<float2 *>(p) = split(x); }
 __device__ __forceinline__ Pair load2(const __nv_bfloat16 *p) {

@@ -360,6 +360,8 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 if (m.start >> i & 1) {
                     const long long at = (long long)run_seq(m, i) * p.D + c;
                     if (p.h0 && live) u[i] = load2(p.h0 + at);
+                    // kept states of short dense sequences: their starts
+                    if (!p.map && p.states && live) store2(p.states + at, u[i]);
                 }
             }
         }
@@ -428,7 +430,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 for (int w = W; w < kWarps; ++w) over(carry, sh.run[buf][w][lane], reset(w));
             });
         }
-        // the state before every 64th token (short dense sequences: at their starts)
+        // the state before every 64th token
         const bool mapped = !MASKED || p.map;
         if (p.states && mapped && t0 % kScanBlock == 0 && t0 < len && live)
             store2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + t0 / kScanBlock) * p.D + c, h);
@@ -447,10 +449,6 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 const bool in = m.act >> i & 1, start = MASKED && (m.start >> i & 1);
                 h = either(start, u[i], fma2(a[i], h, u[i]));
                 if (out && live && in) store2(o + (long long)i * p.D, h);
-                if (MASKED && !p.map && p.states && start) {
-                    const long long at = (long long)run_seq(m, i) * p.D + c;
-                    if (live) store2(p.states + at, p.h0 ? load2(p.h0 + at) : zero);
-                }
                 if (MASKED && p.h_T && (m.end >> i & 1)) {
                     const long long at = (long long)run_seq(m, i) * p.D + c;
                     if (live) store2(p.h_T + at, h);
@@ -514,11 +512,12 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     if (!MASKED && p.dh_T && live) carry = load2(p.dh_T + (long long)stream * p.D + c);
     if constexpr (CLUSTER) cluster_sync();
     else __syncthreads();
-    // the state that the forward pass kept before a tile
-    auto kept = [&](int j) {
-        if ((MASKED && !p.map) || j < 0 || !live) return zero;
-        return load2(p.states + ((MASKED ? 0 : (long long)stream * p.blocks) + j) * p.D + c);
-    };
+    // The state that the forward pass kept before a tile.  Always a load, and what it
+    // gives taken as it is (where there is no tile, no such channel or a start it goes
+    // nowhere): a choice would wait for the load where it stands, a tile ahead of its
+    // use (8 x 4096 tokens: 136 us for 110).
+    const float *const kept0 = p.states + (MASKED ? 0 : (long long)stream * p.blocks) * p.D + (live ? c : 0);
+    auto kept = [&](int j) { return load2(kept0 + (long long)max(j, 0) * p.D); };
     if constexpr (MASKED) pdl_wait();  // for the table
     Pair next = kept(tiles - 1 - rank);
     int entry = run_entry<MASKED, R>(p, base, len, (tiles - 1 - rank) * p.step, warp * R);

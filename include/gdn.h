@@ -631,8 +631,8 @@ GDN_API int gdn_scan_prefill(const void *x, const void *gate, const float *h0, v
  *     dgate_t = G_t (h_{t-1} - x_t) a_t b_t      (GDN_SCAN_SIGMOID, dtype)
  *     dh0 = a_1 G_1
  *
- * dx, dgate [B, T, D] dense; dh0 [B, D] float32, or NULL; may be dh_T.  Tokens
- * of no sequence keep what dx and dgate held.
+ * dx, dgate [B, T, D] dense; dh0 [B, D] float32, or NULL; none of them one of
+ * the inputs.  Tokens of no sequence keep what dx and dgate held.
  * states: as gdn_scan_prefill wrote them for the same inputs, or NULL: they are
  * then formed by a pass over x and gate of the call's own.
  * workspace: gdn_scan_backward_workspace_size bytes (kept: states are given; 0

@@ -237,21 +237,13 @@ def test_in_place_and_carried(torch):
     """End states over start states, and a sequence in two calls."""
     from gated_delta_rule_49_gb300 import binding
     g = torch.Generator(device="cuda").manual_seed(2)
-    for B, T, D in ((2, 40, 64), (1, 3000, 64), (2, 700, 72)):
-        x, gate, dh = (torch.randn(B, T, D, generator=g, device="cuda") for _ in range(3))
-        h0, dhT = torch.randn(2, B, D, generator=g, device="cuda")
-        h, hT, _ = binding.scan_prefill(x, gate, h0)
+    for B, T, D in ((2, 40, 64), (300, 40, 64), (1, 3000, 64), (2, 700, 72)):
+        x, gate = (torch.randn(B, T, D, generator=g, device="cuda") for _ in range(2))
+        h0 = torch.randn(B, D, generator=g, device="cuda")
+        h, hT, kept = binding.scan_prefill(x, gate, h0, keep_states=True)
         state = h0.clone()
-        assert binding.scan_prefill(x, gate, state, out_state=state)[0].equal(h)
-        assert state.equal(hT)
-        dx, dg, dh0 = binding.scan_backward(x, gate, dh, h0, dhT)
-        grad = dhT.clone()
-        ws = torch.empty(binding.gdn_scan_backward_workspace_size(B, T, D, False, False),
-                         dtype=torch.uint8, device="cuda")
-        dx2, dg2 = torch.empty_like(dx), torch.empty_like(dg)
-        binding.gdn_scan_backward(x, gate, dh, h0, grad, None, dx2, dg2, grad, None, B, T, D, D, D,
-                                  binding.GDN_SCAN_SIGMOID, binding.GDN_FP32, ws, ws.numel())
-        assert dx2.equal(dx) and dg2.equal(dg) and grad.equal(dh0)
+        over = binding.scan_prefill(x, gate, state, out_state=state, keep_states=True)
+        assert over[0].equal(h) and over[2].equal(kept) and state.equal(hT)
         cut = T // 3
         first = binding.scan_prefill(x[:, :cut].contiguous(), gate[:, :cut].contiguous(), h0)
         last = binding.scan_prefill(x[:, cut:].contiguous(), gate[:, cut:].contiguous(), first[1])

@@ -60,7 +60,7 @@ def test_prefill_refusals(lib):
 def test_backward_refusals(lib):
     for kw, want in ((dict(T=-1), INV), (dict(dh=None), INV), (dict(dx=None), INV),
                      (dict(dgate=None), INV), (dict(dx=F), INV), (dict(dgate=F), INV),
-                     (dict(dgate=F + 4096), INV), (dict(dh=F + 2), ALI), (dict(dhT=F + 4), ALI),
+                     (dict(dgate=F + 4096), INV), (dict(dhT=F, dh0=F), INV), (dict(dh=F + 2), ALI), (dict(dhT=F + 4), ALI),
                      (dict(dh0=F + 4), ALI), (dict(states=F + 4), ALI), (dict(states=None), WS),
                      (dict(states=None, ws=F, wsb=16), WS), (dict(off=F), WS)):
         assert backward(lib, **kw) == want, kw
