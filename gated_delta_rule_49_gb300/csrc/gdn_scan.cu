@@ -45,53 +45,52 @@ constexpr int kScanThreads = kWarps * 32;
 constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
 
 // a and b of a gate.  b = 1 - a is formed without the difference: a near 1
-// would leave nothing of it.  bf16 runs take the fast exp and quotient (a few
-// float32 steps; exp(|g|) is held at 2^125 so that b stays a number).
-template <typename T, bool SIG> __device__ __forceinline__ void gate_ab(float g, float &a, float &b) {
+// would leave nothing of it.
+template <bool SIG> __device__ __forceinline__ void gate_ab(float g, float &a, float &b) {
     if constexpr (!SIG) {
         a = g;
         b = 1.f;
-    } else if constexpr (sizeof(T) == 2) {
-        float e;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-        asm("min.NaN.f32 %0, %0, %1;" : "+f"(e) : "f"(0x1p125f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
-        b = e * a;
     } else {
         const float e = expf(-fabsf(g)), r = 1.f / (1.f + e), s = e * r;
         a = g < 0.f ? s : r;
         b = g < 0.f ? r : s;
     }
 }
+// The same of two bf16 gates, by the fast exp and quotient; they are held at -87:
+// exp(87) stays a number and so does b.
+__device__ __forceinline__ void gate_ab2(uint32_t w, Pair &a, Pair &b) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xc2aec2aeu));
+    const float2 g = split(mul2(unpack(w), both(-1.4426950408889634f)));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(g.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(g.y));
+    const Pair ep = pair(e.x, e.y), minus_d = fma2(ep, both(-1.f), both(-1.f));
+    const float2 d = split(minus_d);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-d.y));
+    // one step of Newton's: products of thousands of a's gather a quotient's bias (1e-6
+    // of an end state for 1e-7)
+    const Pair q = pair(r.x, r.y);
+    a = fma2(fma2(minus_d, q, both(1.f)), q, q);
+    b = mul2(ep, a);
+}
 
 template <typename T, bool SIG> struct GateType { using type = T; };
 template <typename T> struct GateType<T, false> { using type = float; };
 
 // a and b of a lane's gates in shared memory (without a sigmoid b is not used).
-// bf16 gates are held at -87: exp(87) stays a number and so does b.
 template <typename T, bool SIG>
 __device__ __forceinline__ void gates2(const typename GateType<T, SIG>::type *p, Pair &a, Pair &b) {
     if constexpr (!SIG) {
         a = load2(p);
         b = a;
     } else if constexpr (sizeof(T) == 2) {
-        uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xc2aec2aeu));
-        const float2 g = split(mul2(unpack(w), both(-1.4426950408889634f)));
-        float2 e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(g.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(g.y));
-        const Pair ep = pair(e.x, e.y);
-        const float2 d = split(add2(ep, both(1.f)));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-        a = pair(r.x, r.y);
-        b = mul2(ep, a);
+        gate_ab2(*reinterpret_cast<const uint32_t *>(p), a, b);
     } else {
         const float2 g = *reinterpret_cast<const float2 *>(p);
         float2 x, y;
-        gate_ab<T, SIG>(g.x, x.x, y.x);
-        gate_ab<T, SIG>(g.y, x.y, y.y);
+        gate_ab<SIG>(g.x, x.x, y.x);
+        gate_ab<SIG>(g.y, x.y, y.y);
         a = pair(x.x, x.y);
         b = pair(y.x, y.y);
     }
@@ -770,24 +769,40 @@ __global__ void __launch_bounds__(kStepThreads)
     const int c = (int)(i - row * per) * 8;
     Vec8<T> xv;
     Vec8<G> gv;
-    float xs[8], gs[8], s[8];
+    Pair xs[4], s[4], a[4], b[4];
     xv.load(x + row * ldx + c);
     gv.load(gate + row * ldg + c);
-    const float4 lo = *reinterpret_cast<const float4 *>(h + i * 8);
-    const float4 hi = *reinterpret_cast<const float4 *>(h + i * 8 + 4);
-    pdl_trigger();
-    s[0] = lo.x; s[1] = lo.y; s[2] = lo.z; s[3] = lo.w;
-    s[4] = hi.x; s[5] = hi.y; s[6] = hi.z; s[7] = hi.w;
-    xv.get(xs);
-    gv.get(gs);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float a, b;
-        gate_ab<T, SIG>(gs[e], a, b);
-        s[e] = fmaf(a, s[e], b * xs[e]);
+    for (int e = 0; e < 4; ++e) s[e] = load2(h + i * 8 + 2 * e);
+    pdl_trigger();
+    get4(xv, xs);
+    if constexpr (SIG && sizeof(T) == 2) {
+        gate_ab2(gv.a.x, a[0], b[0]);
+        gate_ab2(gv.a.y, a[1], b[1]);
+        gate_ab2(gv.a.z, a[2], b[2]);
+        gate_ab2(gv.a.w, a[3], b[3]);
+    } else {
+        get4(gv, a);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 g = split(a[e]);
+            float2 u, v;
+            gate_ab<SIG>(g.x, u.x, v.x);
+            gate_ab<SIG>(g.y, u.y, v.y);
+            a[e] = pair(u.x, u.y);
+            b[e] = pair(v.x, v.y);
+        }
     }
-    Vec8<float>::store(h_out + i * 8, s);
-    if (y) Vec8<T>::store(y + i * 8, s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = fma2(a[e], s[e], SIG ? mul2(b[e], xs[e]) : xs[e]);
+    Vec8<float> hv;
+    set4(hv, s);
+    put8(h_out + i * 8, hv);
+    if (y) {
+        Vec8<T> yv;
+        set4(yv, s);
+        put8(y + i * 8, yv);
+    }
 }
 
 // ------------------------------------------------------------------ host

@@ -172,3 +172,40 @@ def test_more_sequences_than_a_grid_row(torch):  # noqa: F811
             for p, q in ((h[one], w[0]), (hT[one], w[1]), (dx[one], v[0]), (dg[one], v[1]),
                          (dh0[one], v[2])):
                 assert (p - q).abs().max() < 2e-4
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "decay"])
+@pytest.mark.parametrize("T", [500, 3000])
+def test_states_as_exact_as_float32(torch, T, kind):  # noqa: F811
+    """End states and start gradients of bf16 runs are float32 results: off by at most twice what the
+    recurrence token by token in float32 is, of the norm (a bias of the gates, small beside bf16,
+    grows with every token)."""
+    from gated_delta_rule_49_gb300 import binding
+    rng = np.random.default_rng(T)
+    B, D = 2, 512
+    x, dh = (torch.from_numpy(rng.standard_normal((B, T, D)).astype(np.float32)).cuda().bfloat16()
+             for _ in range(2))
+    g = rng.standard_normal((B, T, D)) + np.linspace(0, 7.5, D)
+    if kind == "decay":
+        gate = torch.from_numpy((1 / (1 + np.exp(-g))).astype(np.float32)).cuda()
+    else:
+        gate = torch.from_numpy(g.astype(np.float32)).cuda().bfloat16()
+    h0, dhT = (torch.from_numpy(rng.standard_normal((B, D)).astype(np.float32)).cuda() for _ in range(2))
+    hT = binding.scan_prefill(x, gate, h0, kind)[1]
+    dh0 = binding.scan_backward(x, gate, dh, h0, dhT, kind=kind)[2]
+
+    def ends(t):
+        """In type t, from the same inputs."""
+        gn, xn, dn = (number(z).astype(t) for z in (gate, x, dh))
+        a = gn if kind == "decay" else 1 / (1 + np.exp(-gn))
+        b = t(1) if kind == "decay" else 1 / (1 + np.exp(gn))
+        s, u, bx = number(h0).astype(t), number(dhT).astype(t), b * xn
+        for i in range(T):
+            s = a[:, i] * s + bx[:, i]
+        for i in reversed(range(T)):
+            u = a[:, i] * (dn[:, i] + u)
+        return s, u
+
+    for got, f32, f64 in zip((hT, dh0), ends(np.float32), ends(np.float64)):
+        off, may = np.linalg.norm(number(got) - f64), np.linalg.norm(f32 - f64)
+        assert off <= 2 * may, (off / np.linalg.norm(f64), may / np.linalg.norm(f64))
