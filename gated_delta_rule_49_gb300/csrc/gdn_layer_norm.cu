@@ -129,6 +129,7 @@ struct NormArgs {
     long long ldx, ldr;
     float eps;
     int rows, slots;      // of a block; blocks of a team
+    bool more;            // outputs: more chunks than SMs
     int *status;
 };
 
@@ -175,6 +176,64 @@ __device__ __forceinline__ void drain(uint64_t *full, int slots) {
         sm100::mbar_wait(&full[i], 1, kWaitLimit / 16);
     }
 }
+// Outputs: the chunks of a CTA, one block a team each.  The grid has as many CTAs as
+// there are chunks; one that runs takes over others that have not started, so that
+// an SM with more of the memory's bandwidth gets more of them (dealt out evenly, the
+// last SM ended 13 % after the mean).  A team draws its blocks one by one; who draws
+// a chunk's first asks for the next chunk.
+constexpr int kAsked = 4;  // chunks asked for and not yet handed out
+struct Chunks {
+    alignas(16) unsigned long long answer[kAsked][2];
+    uint64_t ready[kAsked];
+    int taken[kAsked];  // how often the answer has been read
+    int drawn;          // blocks drawn from the chunk that the CTA started with on
+};
+// One thread; chunk k >= 1.
+__device__ __forceinline__ void ask(Chunks &q, int k, int teams, int *abort, int *status) {
+    const int e = (k - 1) % kAsked, before = (k - 1) / kAsked * teams;
+    volatile int *const taken = &q.taken[e], *const flag = abort;
+    const long long t0 = clock64();
+    while (*taken != before) {  // the entry's last answer has been read by all
+        if (*flag) return;
+        if (clock64() - t0 > kWaitLimit) {
+            *flag = 1;
+            if (status) atomicOr(status, kStatusTimeout);
+            return;
+        }
+    }
+    sm100::fence_proxy_async_smem();
+    sm100::mbar_arrive_expect_tx(&q.ready[e], 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            sm100::smem_u32(q.answer[e])),
+        "r"(sm100::smem_u32(&q.ready[e]))
+        : "memory");
+}
+// A team's next block, or -1 (by one thread of the team, which draws no more then: all
+// teams have read the last answer before the CTA ends).
+__device__ __forceinline__ long long draw(Chunks &q, int teams, bool more, int *abort, int *status) {
+    const int n = atomicAdd(&q.drawn, 1), k = n / teams;
+    if (!more) return -1;
+    const int e = (k - 1) % kAsked;
+    wait_block(&q.ready[e], ((k - 1) / kAsked) & 1, abort, status);
+    if (*static_cast<volatile int *>(abort)) return -1;
+    uint32_t ok, chunk;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b64 lo, hi;\n\t"
+        "ld.shared.v2.b64 {lo, hi}, [%2];\n\tmov.b128 r, {lo, hi};\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(ok), "=r"(chunk)
+        : "r"(sm100::smem_u32(q.answer[e]))
+        : "memory");
+    __threadfence_block();
+    atomicAdd(&q.taken[e], 1);
+    if (!ok) return -1;
+    if (n % teams == 0) ask(q, k + 1, teams, abort, status);
+    return (long long)chunk * teams + n % teams;
+}
+
 // From here on the values are unpacked again: kept as floats from one phase to the
 // next, they took twice the registers and spilled.
 __device__ __forceinline__ void repack(Vec8<float> &) {}
@@ -234,15 +293,17 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     constexpr int kWeights = weights_in<S>(false), PIECES = TPR * VPT;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[S::kTeams][2][(TPR >= 32 ? TPR / 32 : 1) * U];
-    __shared__ uint64_t full[S::kTeams][kMaxSlots];
+    __shared__ uint64_t full[S::kTeams];
+    __shared__ long long row_of[S::kTeams];
+    __shared__ Chunks chunks;
     __shared__ int abort;
     const int team = threadIdx.x / S::kTeam, lead = threadIdx.x % S::kTeam == 0;
     const int l = threadIdx.x % TPR, c0 = l * 8, abreast = threadIdx.x % S::kTeam / TPR;
     Ring<T, TENSORS> ring;
     ring.bytes = p.rows * p.D * (int)sizeof(T);
     float4 *const weights = reinterpret_cast<float4 *>(smem);
-    ring.base = smem + (kWeights == kStaged ? 64 * PIECES : 0) + (size_t)team * p.slots * TENSORS * ring.bytes;
-    ring.full = full[team];
+    ring.base = smem + (kWeights == kStaged ? 64 * PIECES : 0) + (size_t)team * TENSORS * ring.bytes;
+    ring.full = &full[team];
     ring.src[0] = static_cast<const T *>(p.x);
     ring.ld[0] = p.ldx;
     if constexpr (RES) {
@@ -250,13 +311,27 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         ring.ld[1] = p.ldr;
     }
     const int teams = blockDim.x / S::kTeam;
-    const long long first = ((long long)blockIdx.x * teams + team) * p.rows;
-    const long long step = (long long)gridDim.x * teams * p.rows;
-    if (threadIdx.x == 0) abort = 0;
+    // The team's next block: its rows on the way, or word that it has none (of the last
+    // chunk) or that there is none.
+    constexpr long long kEnd = -1, kEmpty = -2;
+    auto fetch = [&](long long block) {
+        const long long row0 = block < 0 ? kEnd : block * p.rows >= p.N ? kEmpty : block * p.rows;
+        row_of[team] = row0;
+        if (row0 < 0) sm100::mbar_arrive(&full[team]);
+        else ring.fetch(p, 0, row0);
+    };
+    if (threadIdx.x == 0) {
+        abort = 0;
+        chunks.drawn = teams;
+        for (int e = 0; e < kAsked; ++e) {
+            chunks.taken[e] = 0;
+            sm100::mbar_init(&chunks.ready[e], 1);
+        }
+    }
     if (lead) {
-        for (int i = 0; i < p.slots; ++i) sm100::mbar_init(&full[team][i], 1);
+        sm100::mbar_init(&full[team], 1);
         sm100::fence_mbar_init();
-        for (int i = 0; i < p.slots; ++i) ring.fetch(p, i, first + i * step);
+        fetch((long long)blockIdx.x * teams + team);
     }
     RowSum<TPR, U> sum = {red[team], team, 0};
     const float inv = 1.f / p.D;
@@ -270,11 +345,23 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
     T *const y = static_cast<T *>(p.y), *const sums = static_cast<T *>(p.s);
     __syncthreads();
-    int slot = 0;
-    uint32_t parity = 0;
-    for (long long block = first; block < p.N; block += step) {
+    constexpr int slot = 0;
+    bool begin = p.more;
+    for (uint32_t parity = 0;; parity ^= 1) {
+        wait_block(&full[team], parity, &abort, p.status);
+        const long long block = row_of[team];
+        if (block == kEnd || *static_cast<volatile int *>(&abort)) break;
+        // (the first block of the first team has rows; the CTAs of the first round have
+        // started by the time that these are here)
+        if (threadIdx.x == 0 && begin) ask(chunks, 1, teams, &abort, p.status);
+        begin = false;
+        if (block == kEmpty) {
+            if constexpr (TPR <= 32) __syncwarp();
+            else sm100::named_sync(team + 1, TPR);
+            if (lead) fetch(draw(chunks, teams, p.more, &abort, p.status));
+            continue;
+        }
         const int n = (int)min((long long)p.rows, p.N - block);
-        wait_block(&full[team][slot], parity, &abort, p.status);
         for (int i0 = 0; i0 < n; i0 += BATCH) {
             Vec8<T> sv[U][VPT];
             float m[U], q[U];
@@ -309,7 +396,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             sum(m);
             if (i0 + BATCH >= n) {  // the block is in registers
                 if constexpr (TPR <= 32) __syncwarp();
-                if (lead && !abort) ring.fetch(p, slot, block + p.slots * step);
+                if (lead) fetch(draw(chunks, teams, p.more, &abort, p.status));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -365,12 +452,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                 }
             }
         }
-        if (++slot == p.slots) {
-            slot = 0;
-            parity ^= 1;
-        }
     }
-    if (lead && abort) drain(full[team], p.slots);
+    if (lead && abort) drain(&full[team], 1);
+    if (threadIdx.x == 0 && abort) drain(chunks.ready, kAsked);
 }
 
 // A thread's rows leave their sums for dw and db in its registers; the CTA's row
@@ -590,6 +674,7 @@ __global__ void __launch_bounds__(1024)
 constexpr int kShared = 216 * 1024;  // of an SM
 struct NormPlan {
     int rows, slots, grid, threads;
+    bool more;
     size_t smem, most;  // of this call, and of any width of the shape
 };
 template <typename T, typename S> NormPlan norm_plan(long long N, int D, int tensors, bool back) {
@@ -605,14 +690,16 @@ template <typename T, typename S> NormPlan norm_plan(long long N, int D, int ten
     const long long blocks = (N + r.rows - 1) / r.rows;
     if (!back && blocks < (long long)teams * nsm) teams = (int)((blocks + nsm - 1) / nsm);
     r.threads = teams * S::kTeam;
-    r.slots = room / (teams * block) > kMaxSlots ? kMaxSlots : room / (teams * block);
+    const int most_slots = back ? kMaxSlots : 1;
+    r.slots = room / (teams * block) > most_slots ? most_slots : room / (teams * block);
     r.smem = fixed + (size_t)r.slots * teams * block;
     // the sums of the row groups but one, at the end
     const size_t sums = back ? (size_t)(S::kBackThreads / S::TPR - 1) * 16 * S::TPR * sizeof(float) : 0;
     if (r.smem < sums) r.smem = sums;
     r.most = kShared / ctas;
-    const long long need = (blocks + teams - 1) / teams, most = (long long)ctas * nsm;
+    const long long need = (blocks + teams - 1) / teams, most = back ? (long long)ctas * nsm : 0x7fffffff;
     r.grid = (int)(need < most ? need : most);
+    r.more = need > nsm;
     return r;
 }
 
@@ -656,6 +743,7 @@ cudaError_t launch(K kern, uintptr_t (&set)[64], NormArgs p, const NormPlan &pla
     }
     p.rows = plan.rows;
     p.slots = plan.slots;
+    p.more = plan.more;
     p.status = device_status_ptr();
     kern<<<plan.grid, plan.threads, plan.smem, st>>>(p);
     return cudaGetLastError();
