@@ -181,6 +181,7 @@ __device__ __forceinline__ void drain(uint64_t *full, int slots) {
 // an SM with more of the memory's bandwidth gets more of them (dealt out evenly, the
 // last SM ended 13 % after the mean).  A team draws its blocks one by one; who draws
 // a chunk's first asks for the next chunk.
+constexpr int kOutSlots = 2;
 constexpr int kAsked = 4;  // chunks asked for and not yet handed out
 struct Chunks {
     alignas(16) unsigned long long answer[kAsked][2];
@@ -293,8 +294,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     constexpr int kWeights = weights_in<S>(false), PIECES = TPR * VPT;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[S::kTeams][2][(TPR >= 32 ? TPR / 32 : 1) * U];
-    __shared__ uint64_t full[S::kTeams];
-    __shared__ long long row_of[S::kTeams];
+    __shared__ uint64_t full[S::kTeams][kOutSlots];
+    __shared__ long long row_of[S::kTeams][kOutSlots];
     __shared__ Chunks chunks;
     __shared__ int abort;
     const int team = threadIdx.x / S::kTeam, lead = threadIdx.x % S::kTeam == 0;
@@ -302,8 +303,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     Ring<T, TENSORS> ring;
     ring.bytes = p.rows * p.D * (int)sizeof(T);
     float4 *const weights = reinterpret_cast<float4 *>(smem);
-    ring.base = smem + (kWeights == kStaged ? 64 * PIECES : 0) + (size_t)team * TENSORS * ring.bytes;
-    ring.full = &full[team];
+    ring.base = smem + (kWeights == kStaged ? 64 * PIECES : 0) + (size_t)team * p.slots * TENSORS * ring.bytes;
+    ring.full = full[team];
     ring.src[0] = static_cast<const T *>(p.x);
     ring.ld[0] = p.ldx;
     if constexpr (RES) {
@@ -314,12 +315,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     // The team's next block: its rows on the way, or word that it has none (of the last
     // chunk) or that there is none.
     constexpr long long kEnd = -1, kEmpty = -2;
-    auto fetch = [&](long long block) {
+    bool ended = false;
+    auto fetch = [&](int slot, long long block) {
         const long long row0 = block < 0 ? kEnd : block * p.rows >= p.N ? kEmpty : block * p.rows;
-        row_of[team] = row0;
-        if (row0 < 0) sm100::mbar_arrive(&full[team]);
-        else ring.fetch(p, 0, row0);
+        row_of[team][slot] = row0;
+        ended = block < 0;
+        if (row0 < 0) sm100::mbar_arrive(&full[team][slot]);
+        else ring.fetch(p, slot, row0);
     };
+    auto next = [&](int slot) { fetch(slot, ended ? -1 : draw(chunks, teams, p.more, &abort, p.status)); };
     if (threadIdx.x == 0) {
         abort = 0;
         chunks.drawn = teams;
@@ -329,9 +333,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
     }
     if (lead) {
-        sm100::mbar_init(&full[team], 1);
+        for (int i = 0; i < p.slots; ++i) sm100::mbar_init(&full[team][i], 1);
         sm100::fence_mbar_init();
-        fetch((long long)blockIdx.x * teams + team);
+        fetch(0, (long long)blockIdx.x * teams + team);
     }
     RowSum<TPR, U> sum = {red[team], team, 0};
     const float inv = 1.f / p.D;
@@ -345,20 +349,28 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
     T *const y = static_cast<T *>(p.y), *const sums = static_cast<T *>(p.s);
     __syncthreads();
-    constexpr int slot = 0;
-    bool begin = p.more;
-    for (uint32_t parity = 0;; parity ^= 1) {
-        wait_block(&full[team], parity, &abort, p.status);
-        const long long block = row_of[team];
+    int slot = 0;
+    uint32_t parity = 0;
+    for (bool begin = true;; begin = false) {
+        wait_block(&full[team][slot], parity, &abort, p.status);
+        const long long block = row_of[team][slot];
         if (block == kEnd || *static_cast<volatile int *>(&abort)) break;
-        // (the first block of the first team has rows; the CTAs of the first round have
-        // started by the time that these are here)
-        if (threadIdx.x == 0 && begin) ask(chunks, 1, teams, &abort, p.status);
-        begin = false;
+        if (begin) {
+            // (the first block of the first team has rows; the CTAs of the first round have
+            // started by the time that these are here)
+            if (threadIdx.x == 0 && p.more) ask(chunks, 1, teams, &abort, p.status);
+            if (lead)
+                for (int i = 1; i < p.slots; ++i) next(i);
+        }
+        const int at = slot;
+        if (++slot == p.slots) {
+            slot = 0;
+            parity ^= 1;
+        }
         if (block == kEmpty) {
             if constexpr (TPR <= 32) __syncwarp();
             else sm100::named_sync(team + 1, TPR);
-            if (lead) fetch(draw(chunks, teams, p.more, &abort, p.status));
+            if (lead) next(at);
             continue;
         }
         const int n = (int)min((long long)p.rows, p.N - block);
@@ -374,13 +386,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                     const int c = c0 + k * TPR * 8;
                     sv[u][k] = {};
                     if (i < n && c < p.D) {
-                        from_shared(sv[u][k], ring.row(p, slot, 0, i) + c);
+                        from_shared(sv[u][k], ring.row(p, at, 0, i) + c);
                         Pair f[4];
                         get4(sv[u][k], f);
                         if constexpr (RES) {
                             Vec8<T> rv;
                             Pair r[4];
-                            from_shared(rv, ring.row(p, slot, 1, i) + c);
+                            from_shared(rv, ring.row(p, at, 1, i) + c);
                             get4(rv, r);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) f[e] = add2(f[e], r[e]);
@@ -396,7 +408,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             sum(m);
             if (i0 + BATCH >= n) {  // the block is in registers
                 if constexpr (TPR <= 32) __syncwarp();
-                if (lead) fetch(draw(chunks, teams, p.more, &abort, p.status));
+                if (lead) next(at);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             }
         }
     }
-    if (lead && abort) drain(&full[team], 1);
+    if (lead && abort) drain(full[team], p.slots);
     if (threadIdx.x == 0 && abort) drain(chunks.ready, kAsked);
 }
 
@@ -690,7 +702,7 @@ template <typename T, typename S> NormPlan norm_plan(long long N, int D, int ten
     const long long blocks = (N + r.rows - 1) / r.rows;
     if (!back && blocks < (long long)teams * nsm) teams = (int)((blocks + nsm - 1) / nsm);
     r.threads = teams * S::kTeam;
-    const int most_slots = back ? kMaxSlots : 1;
+    const int most_slots = back ? kMaxSlots : kOutSlots;
     r.slots = room / (teams * block) > most_slots ? most_slots : room / (teams * block);
     r.smem = fixed + (size_t)r.slots * teams * block;
     // the sums of the row groups but one, at the end
