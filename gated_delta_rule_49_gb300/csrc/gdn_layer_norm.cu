@@ -129,7 +129,7 @@ struct NormArgs {
     long long ldx, ldr;
     float eps;
     int rows, slots;      // of a block; blocks of a team
-    bool more;            // outputs: more chunks than SMs
+    bool more;            // outputs: CTAs take over others
     int *status;
 };
 
@@ -176,11 +176,13 @@ __device__ __forceinline__ void drain(uint64_t *full, int slots) {
         sm100::mbar_wait(&full[i], 1, kWaitLimit / 16);
     }
 }
-// Outputs: the chunks of a CTA, one block a team each.  The grid has as many CTAs as
-// there are chunks; one that runs takes over others that have not started, so that
-// an SM with more of the memory's bandwidth gets more of them (dealt out evenly, the
-// last SM ended 13 % after the mean).  A team draws its blocks one by one; who draws
-// a chunk's first asks for the next chunk.
+// Outputs: the chunks of a CTA, one block a team each, which the teams draw one by one.
+// With the sum to form the grid has as many CTAs as there are chunks; one that runs
+// takes over others that have not started, so that an SM with more of the memory's
+// bandwidth gets more of them: dealt out evenly the last SM ended 13 % after the mean
+// (32768 rows of 2048 bf16 channels 92 us, taken over 85).  Without the sum half as much
+// moves, and the questions cost what they bring (512 channels: dealt out 46 us, taken
+// over 48; 2048: 47 and 46).  Who draws a chunk's first block asks for the next chunk.
 constexpr int kOutSlots = 2;
 constexpr int kAsked = 4;  // chunks asked for and not yet handed out
 struct Chunks {
@@ -210,11 +212,12 @@ __device__ __forceinline__ void ask(Chunks &q, int k, int teams, int *abort, int
         "r"(sm100::smem_u32(&q.ready[e]))
         : "memory");
 }
-// A team's next block, or -1 (by one thread of the team, which draws no more then: all
-// teams have read the last answer before the CTA ends).
+// A team's next block, or one past the rows where there is none (by one thread of the
+// team, which draws no more then: all teams have read the last answer before the CTA
+// ends).  Without taking over, a CTA's chunks lie a grid apart.
 __device__ __forceinline__ long long draw(Chunks &q, int teams, bool more, int *abort, int *status) {
     const int n = atomicAdd(&q.drawn, 1), k = n / teams;
-    if (!more) return -1;
+    if (!more) return ((long long)k * gridDim.x + blockIdx.x) * teams + n % teams;
     const int e = (k - 1) % kAsked;
     wait_block(&q.ready[e], ((k - 1) / kAsked) & 1, abort, status);
     if (*static_cast<volatile int *>(abort)) return -1;
@@ -231,6 +234,7 @@ __device__ __forceinline__ long long draw(Chunks &q, int teams, bool more, int *
     __threadfence_block();
     atomicAdd(&q.taken[e], 1);
     if (!ok) return -1;
+    // (after an answer that there is none no other may be asked for)
     if (n % teams == 0) ask(q, k + 1, teams, abort, status);
     return (long long)chunk * teams + n % teams;
 }
@@ -317,9 +321,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     constexpr long long kEnd = -1, kEmpty = -2;
     bool ended = false;
     auto fetch = [&](int slot, long long block) {
-        const long long row0 = block < 0 ? kEnd : block * p.rows >= p.N ? kEmpty : block * p.rows;
+        const long long row0 = block < 0 ? kEnd : block * p.rows < p.N ? block * p.rows : p.more ? kEmpty : kEnd;
         row_of[team][slot] = row0;
-        ended = block < 0;
+        ended = row0 == kEnd;
         if (row0 < 0) sm100::mbar_arrive(&full[team][slot]);
         else ring.fetch(p, slot, row0);
     };
@@ -709,9 +713,10 @@ template <typename T, typename S> NormPlan norm_plan(long long N, int D, int ten
     const size_t sums = back ? (size_t)(S::kBackThreads / S::TPR - 1) * 16 * S::TPR * sizeof(float) : 0;
     if (r.smem < sums) r.smem = sums;
     r.most = kShared / ctas;
-    const long long need = (blocks + teams - 1) / teams, most = back ? (long long)ctas * nsm : 0x7fffffff;
-    r.grid = (int)(need < most ? need : most);
-    r.more = need > nsm;
+    const long long need = (blocks + teams - 1) / teams, most = (long long)ctas * nsm;
+    r.more = !back && tensors == 2 && need > most && need <= 0x7fffffff;
+    const long long grid = r.more || need < most ? need : most;
+    r.grid = (int)grid;
     return r;
 }
 
