@@ -8,19 +8,22 @@
 //     G_t = dh_t + a_{t+1} G_{t+1},  dx = b G,  da = G (h_{t-1} - [sigmoid] x),
 //     dg = da a b,  dh0 = a_1 G_1
 //
-// Bound by memory: 6 bytes a value forward (sigmoid, bf16), 10 backward.  What a
-// piece of tokens does to the state is h -> P h + H, and pieces compose: a CTA
-// owns 64 channels of a stream of tokens and takes tiles of 8 R of them, each of
-// its 8 warps a run of R consecutive tokens, a lane two channels.  A warp finds
-// P and H of its run, the runs' are joined through shared memory, and a second
-// walk over the values, still in registers, gives the outputs: the inputs are
-// read once.  Gradients go the other way with the same P: what leaves a run
+// Bound by memory: 6 bytes a value forward (sigmoid, bf16), 10 backward (8 sequences
+// of 4096 tokens and 2048 channels: 63 us, 94 % of the copy bandwidth, and 114 us,
+// 87 %).  What a piece of tokens does to the state is h -> P h + H, and pieces
+// compose: a CTA owns 64 channels of a stream of tokens and takes tiles of 8 R of
+// them, each of its 8 warps a run of R consecutive tokens, a lane two channels.  A
+// warp finds P and H of its run, the runs' are joined through shared memory, and a
+// second walk over the values, still in registers, gives the outputs: the inputs
+// are read once.  Gradients go the other way with the same P: what leaves a run
 // towards earlier tokens is u -> P u + V; the states h_{t-1} that they need start
 // from those that the forward pass kept every 64 tokens, a tile of the gradients.
 //
 // Few streams of few channels: a cluster of 2 to 8 CTAs takes consecutive tiles
 // of one stream, and every CTA sends its tile's P and H to the others' shared
-// memory, so that a long sequence is still read once.
+// memory, so that a long sequence is still read once (65536 tokens 160 us, 99 %).
+// With fewer than 1.5 CTAs an SM a cluster is doubled (clusters of 4 and one CTA an SM:
+// 176 us).
 //
 // A stream is one sequence, or several: packed ones (a table gives each token's
 // sequence) or dense ones of at most a tile.  There a run knows which of its tokens
