@@ -145,7 +145,7 @@ int check_scan(const void *x, const void *gate, int B, int T, int D, bool packed
         x_stride > (1LL << 36) || gate_stride > (1LL << 36))
         return GDN_ERR_INVALID_ARG;
     const long long most = (1LL << 31) - 1024;  // tokens are 32-bit coordinates of a tile
-    if ((packed ? T : (long long)B * T) > most || (long long)B * D > (1LL << 36))
+    if ((packed ? T : (long long)B * T) > most || B > most || (long long)B * D > (1LL << 36))
         return GDN_ERR_INVALID_ARG;
     return aligned16(x) && aligned16(gate) ? GDN_OK : GDN_ERR_ALIGNMENT;
 }
@@ -775,6 +775,9 @@ int gdn_scan_prefill(const void *x, const void *gate, const float *h0, void *h, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) return empty_prefill(h0, h_T, B, 1, D, 1, st);
     if (!x || !gate || (!h && !h_T && !states) || h == x || h == gate) return GDN_ERR_INVALID_ARG;
+    // h0 is read while h and states are written; h_T may take its place
+    if ((h && (h == h0 || h == h_T)) || (states && (states == h0 || states == h_T || states == h)))
+        return GDN_ERR_INVALID_ARG;
     const size_t need = gdn_scan_prefill_workspace_size(B, T, D, packed);
     if (workspace_bytes < need || (need && !workspace)) return GDN_ERR_WORKSPACE;
     gdn::ScanArgs a = {};
@@ -809,7 +812,7 @@ int gdn_scan_backward(const void *x, const void *gate, const void *dh, const flo
     const void *ins[] = {x, gate, dh};
     for (const void *p : ins)
         if (p == dx || p == dgate) return GDN_ERR_INVALID_ARG;
-    if (dx == dgate || (dh0 && dh0 == dh_T)) return GDN_ERR_INVALID_ARG;
+    if (dx == dgate || (dh0 && (dh0 == dh_T || dh0 == h0))) return GDN_ERR_INVALID_ARG;
     const size_t need = gdn_scan_backward_workspace_size(B, T, D, packed, states != nullptr);
     if (workspace_bytes < need || (need && !workspace)) return GDN_ERR_WORKSPACE;
     gdn::ScanArgs a = {};
@@ -828,6 +831,10 @@ int gdn_scan_decode_step(const void *x, const void *gate, const float *h, float 
     if (!aligned16(h) || !aligned16(h_out) || !aligned16(y)) return GDN_ERR_ALIGNMENT;
     if (B == 0 || D == 0) return GDN_OK;
     if (!x || !gate || !h || !h_out || (y && (y == h || y == h_out))) return GDN_ERR_INVALID_ARG;
+    // x and gate have rows and types of their own
+    const void *ins[] = {x, gate};
+    for (const void *p : ins)
+        if (p == y || p == h_out) return GDN_ERR_INVALID_ARG;
     return from_cuda(gdn::launch_scan_step(x, gate, h, h_out, y, B, D, x_stride, gate_stride,
                                            kind == GDN_SCAN_SIGMOID, dtype,
                                            static_cast<cudaStream_t>(stream)));

@@ -599,10 +599,10 @@ GDN_API int gdn_linear_decode_step(const void *q, const void *k, const void *v,
  *         consecutive tokens lie x_stride / gate_stride elements apart (at least
  *         D, a multiple of 16 bytes), so that they may be parts of one projection
  *   h0    [B, D] float32, or NULL = zero
- *   h     [B, T, D] (dtype), dense, or NULL; not x or gate
+ *   h     [B, T, D] (dtype), dense, or NULL; no other tensor of the call
  *   h_T   [B, D] float32, or NULL; may be h0
  *   states  NULL, or [B, ceil(T / 64), D] float32: the state before every 64th
- *         token, which gdn_scan_backward starts from
+ *         token, which gdn_scan_backward starts from; no other tensor of the call
  *   offsets  NULL, or [B + 1] int32 on the device: the B sequences lie packed
  *         in T tokens as for gdn_linear_prefill (bad offsets as there); states is
  *         then [ceil(T / 64), D], of the T tokens (a row whose token starts a
@@ -610,8 +610,9 @@ GDN_API int gdn_linear_decode_step(const void *q, const void *k, const void *v,
  *         keep what h held.
  *
  * D a multiple of 8 (else GDN_ERR_UNSUPPORTED); at most 2^31 - 1024 tokens in
- * all.  Everything is float32 from the load to the one rounding of h.  A value
- * that is not finite reaches what the recurrence carries it to and nothing else.
+ * all, and as many sequences.  Everything is float32 from the load to the one
+ * rounding of h.  A value that is not finite reaches what the recurrence carries
+ * it to and nothing else.
  * workspace: gdn_scan_prefill_workspace_size bytes (0 unless packed).
  */
 typedef enum { GDN_SCAN_DECAY = 0, GDN_SCAN_SIGMOID = 1 } gdn_scan_kind;
@@ -649,7 +650,8 @@ GDN_API int gdn_scan_backward(const void *x, const void *gate, const void *dh, c
 /*
  * gdn_scan_decode_step -- one token of gdn_scan_prefill: x, gate [B, D] (rows
  * x_stride / gate_stride elements apart); reads h [B, D] float32 and writes
- * h_out, which may be h, and y [B, D] (dtype, dense), the rounded state, or NULL.
+ * h_out, which may be h, and y [B, D] (dtype, dense), the rounded state, or NULL;
+ * neither of them is x or gate.
  */
 GDN_API int gdn_scan_decode_step(const void *x, const void *gate, const float *h, float *h_out,
                                  void *y, int B, int D, long long x_stride, long long gate_stride,

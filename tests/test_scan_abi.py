@@ -30,7 +30,7 @@ def backward(lib, **kw):
 
 
 def step(lib, **kw):
-    a = dict(x=F, gate=F, h=F, h_out=F, y=F + 4096, B=2, D=64, ldx=64, ldg=128, kind=1, dt=0)
+    a = dict(x=F + 64, gate=F + 128, h=F, h_out=F, y=F + 4096, B=2, D=64, ldx=64, ldg=128, kind=1, dt=0)
     a.update(kw)
     return lib.gdn_scan_decode_step(*a.values(), None)
 
@@ -53,7 +53,10 @@ def test_prefill_refusals(lib):
                      (dict(B=1 << 20, T=1 << 12), INV), (dict(T=(1 << 31) - 1, B=1), INV),
                      (dict(h=F + 8), ALI), (dict(h0=F + 4), ALI), (dict(hT=F + 8), ALI),
                      (dict(states=F + 4), ALI), (dict(off=F + 4), ALI), (dict(off=F), WS),
-                     (dict(off=F, ws=F, wsb=16), WS), (dict(off=F, ws=F + 8, wsb=4096), ALI)):
+                     (dict(off=F, ws=F, wsb=16), WS), (dict(off=F, ws=F + 8, wsb=4096), ALI),
+                     (dict(h0=F + 4096), INV), (dict(hT=F + 4096), INV), (dict(states=F), INV),
+                     (dict(h0=F + 64, states=F + 64), INV), (dict(states=F + 4096), INV),
+                     (dict(off=F, ws=F, wsb=4096, B=(1 << 31) - 1, D=8), INV)):
         assert prefill(lib, **kw) == want, kw
 
 
@@ -62,7 +65,8 @@ def test_backward_refusals(lib):
                      (dict(dgate=None), INV), (dict(dx=F), INV), (dict(dgate=F), INV),
                      (dict(dgate=F + 4096), INV), (dict(dhT=F, dh0=F), INV), (dict(dh=F + 2), ALI), (dict(dhT=F + 4), ALI),
                      (dict(dh0=F + 4), ALI), (dict(states=F + 4), ALI), (dict(states=None), WS),
-                     (dict(states=None, ws=F, wsb=16), WS), (dict(off=F), WS)):
+                     (dict(states=None, ws=F, wsb=16), WS), (dict(off=F), WS),
+                     (dict(h0=F + 64, dh0=F + 64), INV)):
         assert backward(lib, **kw) == want, kw
     size = binding.gdn_scan_backward_workspace_size
     assert size(2, 5, 64, False, True) == 0
@@ -76,6 +80,8 @@ def test_backward_refusals(lib):
 
 def test_step_refusals(lib):
     for kw, want in ((dict(h=None), INV), (dict(h_out=None), INV), (dict(y=F), INV),
+                     (dict(y=F + 64), INV), (dict(y=F + 128), INV),
+                     (dict(h_out=F + 64), INV), (dict(h_out=F + 128), INV),
                      (dict(h=F + 4), ALI), (dict(h_out=F + 4), ALI), (dict(y=F + 2), ALI)):
         assert step(lib, **kw) == want, kw
 
