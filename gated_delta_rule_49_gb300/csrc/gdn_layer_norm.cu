@@ -162,12 +162,22 @@ template <typename T, int TENSORS> struct Ring {
         return reinterpret_cast<const T *>(base + (slot * TENSORS + tensor) * bytes) + (long long)i * p.D;
     }
 };
-// A wait with a limit; the first that runs out ends all others of the CTA.
-__device__ __forceinline__ void wait_block(uint64_t *bar, uint32_t parity, int *abort, int *status) {
-    volatile int *const flag = abort;
-    if (sm100::mbar_wait_or_abort(bar, parity, kWaitLimit, flag) || *flag) return;
-    *flag = 1;
+// Waits with a limit; after one that ran out nothing more is fetched.  The threads of a
+// team go on alike all the same, with what the slot holds, so that none is left behind at
+// a barrier of theirs.
+__device__ __forceinline__ void gave_up(int *abort, int *status) {
+    *static_cast<volatile int *>(abort) = 1;
     if (status) atomicOr(status, kStatusTimeout);
+}
+// Where the blocks are dealt out: the first wait that runs out ends all others of the CTA.
+__device__ __forceinline__ void wait_dealt(uint64_t *bar, uint32_t parity, int *abort, int *status) {
+    volatile int *const flag = abort;
+    if (!sm100::mbar_wait_or_abort(bar, parity, kWaitLimit, flag) && !*flag) gave_up(abort, status);
+}
+// Where they are drawn: the team's first thread says which block it is before the barrier
+// completes, or that there is none, once its own waits (of kWaitLimit) have run out.
+__device__ __forceinline__ void wait_drawn(uint64_t *bar, uint32_t parity, int *abort, int *status) {
+    if (!sm100::mbar_wait(bar, parity, 4 * kWaitLimit)) gave_up(abort, status);
 }
 // Copies in flight land before the CTA ends (where nothing went wrong none are).
 __device__ __forceinline__ void drain(uint64_t *full, int slots) {
@@ -198,11 +208,7 @@ __device__ __forceinline__ void ask(Chunks &q, int k, int teams, int *abort, int
     const long long t0 = clock64();
     while (*taken != before) {  // the entry's last answer has been read by all
         if (*flag) return;
-        if (clock64() - t0 > kWaitLimit) {
-            *flag = 1;
-            if (status) atomicOr(status, kStatusTimeout);
-            return;
-        }
+        if (clock64() - t0 > kWaitLimit) return gave_up(abort, status);
     }
     sm100::fence_proxy_async_smem();
     sm100::mbar_arrive_expect_tx(&q.ready[e], 16);
@@ -216,11 +222,15 @@ __device__ __forceinline__ void ask(Chunks &q, int k, int teams, int *abort, int
 // team, which draws no more then: all teams have read the last answer before the CTA
 // ends).  Without taking over, a CTA's chunks lie a grid apart.
 __device__ __forceinline__ long long draw(Chunks &q, int teams, bool more, int *abort, int *status) {
+    volatile int *const flag = abort;
+    if (*flag) return -1;
     const int n = atomicAdd(&q.drawn, 1), k = n / teams;
     if (!more) return ((long long)k * gridDim.x + blockIdx.x) * teams + n % teams;
     const int e = (k - 1) % kAsked;
-    wait_block(&q.ready[e], ((k - 1) / kAsked) & 1, abort, status);
-    if (*static_cast<volatile int *>(abort)) return -1;
+    if (!sm100::mbar_wait_or_abort(&q.ready[e], ((k - 1) / kAsked) & 1, kWaitLimit, flag)) {
+        gave_up(abort, status);
+        return -1;
+    }
     uint32_t ok, chunk;
     asm volatile(
         "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b64 lo, hi;\n\t"
@@ -356,9 +366,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     int slot = 0;
     uint32_t parity = 0;
     for (bool begin = true;; begin = false) {
-        wait_block(&full[team][slot], parity, &abort, p.status);
+        wait_drawn(&full[team][slot], parity, &abort, p.status);
         const long long block = row_of[team][slot];
-        if (block == kEnd || *static_cast<volatile int *>(&abort)) break;
+        if (block == kEnd) break;
         if (begin) {
             // (the first block of the first team has rows; the CTAs of the first round have
             // started by the time that these are here)
@@ -533,7 +543,7 @@ __global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
     uint32_t parity = 0;
     for (long long block = first; block < p.N; block += step) {
         const int n = (int)min((long long)p.rows, p.N - block);
-        wait_block(&full[team][slot], parity, &abort, p.status);
+        wait_dealt(&full[team][slot], parity, &abort, p.status);
         for (int i0 = 0; i0 < n; i0 += BATCH) {
             float2 now[U];
             float t[2 * U];
