@@ -20,11 +20,12 @@ namespace {
 constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
 
 // Threads of a row and pieces of 8 channels of a thread.  A team is a warp, of one
-// row or several, or the threads of a row.
-template <int TPR_, int VPT_> struct RowShape {
+// row or several, or the threads of a row; ALONE: one row at a time.
+template <int TPR_, int VPT_, bool ALONE_ = false> struct RowShape {
     enum {
         TPR = TPR_,
         VPT = VPT_,
+        ALONE = ALONE_,
         kTeam = TPR < 32 ? 32 : TPR,
         kAbreast = kTeam / TPR,  // rows side by side in a team
         // Outputs: one CTA an SM, of up to 20 warps, fewer where the rows are few (24
@@ -38,9 +39,12 @@ template <int TPR_, int VPT_> struct RowShape {
     };
 };
 // Rows of a thread at once: their chains of sums overlap, and one meeting of a
-// team's warps serves them all.
-template <typename T> constexpr int rows_at_once(int tpr, int vpt, bool back) {
-    return !back ? (vpt < 4 ? 4 / vpt : 1) : vpt > 1 ? 1 : tpr > 32 && sizeof(T) == 2 ? 4 : 2;
+// team's warps serves them all.  (Gradients of 5120 bf16 channels: two rows 88 us, one
+// 119.)
+template <typename T, typename S> constexpr int rows_at_once(bool back) {
+    if (S::ALONE) return 1;
+    const int pieces = back && S::TPR > 32 && sizeof(T) == 2 || !back ? 4 : 2;
+    return S::VPT < pieces ? pieces / S::VPT : 1;
 }
 constexpr int kMaxSlots = 4;  // blocks of a team in shared memory
 
@@ -267,12 +271,13 @@ __device__ __forceinline__ void column(Pair (&v)[4], const float *p, float other
         for (int e = 0; e < 4; ++e) v[e] = both(other);
     }
 }
-// Where w and b of a piece come from: a thread's registers, where it has one piece;
-// shared memory, staged once by the CTA, up to 8192 channels; else the L1 cache.
+// Where w and b of a piece come from: a thread's registers, where it has one piece, or
+// where the row has all threads of an SM; shared memory, staged once by the CTA, up to
+// 8192 channels; else (gradients) the L1 cache.
 enum { kRegisters, kStaged, kCached };
 template <typename S> constexpr int weights_in(bool back) {
-    return S::VPT == 1 || (back && S::VPT == 2) ? kRegisters
-           : !back && S::TPR * S::VPT * 8 <= 8192 ? kStaged : kCached;
+    if (back) return S::VPT <= 2 ? kRegisters : kCached;
+    return S::VPT == 1 || S::TPR * S::VPT * 8 > 8192 ? kRegisters : kStaged;
 }
 // Staged: the lower and the upper four channels of every piece apart, so that
 // neighbouring lanes read neighbouring 16 bytes.
@@ -303,7 +308,7 @@ __device__ __forceinline__ float sum2(Pair x) {
 template <typename T, typename S, bool RES>
 __global__ void __launch_bounds__(S::kThreads, 1)
     layer_norm_kernel(const NormArgs p) {
-    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T>(TPR, VPT, false);
+    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T, S>(false);
     constexpr int TENSORS = RES ? 2 : 1, BATCH = U * S::kAbreast;
     constexpr int kWeights = weights_in<S>(false), PIECES = TPR * VPT;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -353,11 +358,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
     RowSum<TPR, U> sum = {red[team], team, 0};
     const float inv = 1.f / p.D;
-    Pair w[4], b[4];
-    if constexpr (kWeights == kRegisters) {
-        column(w, p.w, 1.f, c0, p.D);
-        column(b, p.b, 0.f, c0, p.D);
-    } else if constexpr (kWeights == kStaged) {
+    constexpr bool kHold = kWeights == kRegisters;
+    Pair w[kHold ? VPT : 1][4], b[kHold ? VPT : 1][4];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            column(w[k], p.w, 1.f, c0 + k * TPR * 8, p.D);
+            column(b[k], p.b, 0.f, c0 + k * TPR * 8, p.D);
+        }
+    } else {
         stage_column<PIECES>(weights, p.w, 1.f, p.D);
         stage_column<PIECES>(weights + 2 * PIECES, p.b, 0.f, p.D);
     }
@@ -458,19 +467,17 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                 for (int k = 0; k < VPT; ++k) {
                     if (c0 + k * TPR * 8 < p.D) {
                         if (RES && sums) put8(sr + k * TPR * 8, sv[u][k]);
-                        if constexpr (kWeights == kStaged) {
-                            staged<PIECES>(w, weights, k * TPR + l);
-                            staged<PIECES>(b, weights + 2 * PIECES, k * TPR + l);
-                        } else if constexpr (kWeights == kCached) {
-                            column(w, p.w, 1.f, c0 + k * TPR * 8, p.D);
-                            column(b, p.b, 0.f, c0 + k * TPR * 8, p.D);
+                        const int at_w = kHold ? k : 0;
+                        if constexpr (!kHold) {
+                            staged<PIECES>(w[0], weights, k * TPR + l);
+                            staged<PIECES>(b[0], weights + 2 * PIECES, k * TPR + l);
                         }
                         Pair f[4];
                         repack(sv[u][k]);
                         get4(sv[u][k], f);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            f[e] = fma2(mul2(add2(f[e], minus), scale), w[e], b[e]);
+                            f[e] = fma2(mul2(add2(f[e], minus), scale), w[at_w][e], b[at_w][e]);
                         Vec8<T> out;
                         set4(out, f);
                         put8(yr + k * TPR * 8, out);
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 template <typename T, typename S, bool PAST>
 __global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
     layer_norm_backward_kernel(const NormArgs p) {
-    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T>(TPR, VPT, true);
+    constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T, S>(true);
     constexpr int TENSORS = PAST ? 3 : 2, BATCH = U * S::kAbreast;
     constexpr bool kHold = weights_in<S>(true) == kRegisters;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -706,7 +713,7 @@ struct NormPlan {
 template <typename T, typename S> NormPlan norm_plan(long long N, int D, int tensors, bool back) {
     NormPlan r;
     const int nsm = sm_count() > 0 ? sm_count() : 152, ctas = back ? S::kBackCtas : 1;
-    const int row = D * (int)sizeof(T), batch = rows_at_once<T>(S::TPR, S::VPT, back) * S::kAbreast;
+    const int row = D * (int)sizeof(T), batch = rows_at_once<T, S>(back) * S::kAbreast;
     r.rows = (back && S::TPR > 32 ? 1024 : 4096) * (S::kTeam / 32) / row / batch * batch;
     if (r.rows < batch) r.rows = batch;
     const int fixed = !back && weights_in<S>(back) == kStaged ? 64 * S::TPR * S::VPT : 0;
@@ -731,7 +738,9 @@ template <typename T, typename S> NormPlan norm_plan(long long N, int D, int ten
 }
 
 // f for the shape of D channels.  Outputs: a warp or less a row up to 2048 bf16
-// channels, no barrier; gradients: one piece a thread as far as it goes, for the
+// channels, no barrier; above 8192 all threads of an SM, whose registers hold the weights
+// (12288 and 16384 channels with the sum 85 and 90 us; rows of 256 threads that read the
+// weights from the L1 cache 134 and 126); gradients: one piece a thread as far as it goes, for the
 // sums in registers.
 template <typename T, typename F> auto by_width(int D, F &&f) {
     const int pieces = D / 8;
@@ -744,9 +753,11 @@ template <typename T, typename F> auto by_width(int D, F &&f) {
     if (pieces <= 256) return f(RowShape<W, V>());
     if (pieces <= 512) return f(RowShape<2 * W, V>());
     if (pieces <= 1024) return f(RowShape<4 * W, V>());
-    return f(RowShape<8 * W, V>());
+    return f(RowShape<512, 4>());
 }
-template <typename F> auto by_width_backward(int D, F &&f) {
+// bf16 rows of three tensors that leave room for two blocks of two only go one at a time
+// (8192 channels: two rows 109 us, one 95; without ds, three blocks, 71 and 85).
+template <typename T, typename F> auto by_width_backward(int D, bool past, F &&f) {
     const int pieces = D / 8;
     if (pieces <= 8) return f(RowShape<8, 1>());
     if (pieces <= 16) return f(RowShape<16, 1>());
@@ -755,6 +766,8 @@ template <typename F> auto by_width_backward(int D, F &&f) {
     if (pieces <= 128) return f(RowShape<128, 1>());
     if (pieces <= 256) return f(RowShape<256, 1>());
     if (pieces <= 512) return f(RowShape<256, 2>());
+    if constexpr (sizeof(T) == 2)
+        if (past && pieces > 768 && pieces <= 1024) return f(RowShape<512, 2, true>());
     if (pieces <= 1024) return f(RowShape<512, 2>());
     return f(RowShape<512, 4>());
 }
@@ -787,34 +800,39 @@ template <typename T> cudaError_t forward(const NormArgs &p, cudaStream_t st) {
 }
 
 template <typename T> cudaError_t backward(const NormArgs &p, float *dw, float *db, cudaStream_t st) {
-    return by_width_backward(p.D, [&](auto shape) {
+    return by_width_backward<T>(p.D, p.res != nullptr, [&](auto shape) {
         using S = decltype(shape);
         static uintptr_t set[2][64] = {};
         const NormPlan plan = norm_plan<T, S>(p.N, p.D, p.res ? 3 : 2, true);
-        const cudaError_t e =
-            p.res ? launch(layer_norm_backward_kernel<T, S, true>, set[1], p, plan, st)
-                  : launch(layer_norm_backward_kernel<T, S, false>, set[0], p, plan, st);
+        auto rows = [&] {
+            if constexpr (!S::ALONE)
+                if (!p.res) return launch(layer_norm_backward_kernel<T, S, false>, set[0], p, plan, st);
+            return launch(layer_norm_backward_kernel<T, S, true>, set[1], p, plan, st);
+        };
+        const cudaError_t e = rows();
         if (e != cudaSuccess || !p.parts) return e;
         return launch_pdl(layer_norm_sum_kernel, (2 * p.D + 31) / 32, 1024, 0, st,
                           static_cast<const float *>(p.parts), plan.grid, p.D, dw, db);
     });
 }
 
+template <typename T> int most_parts(long long N, int D) {
+    int most = 0;
+    for (int tensors = 2; tensors <= 3; ++tensors) {
+        const int n = by_width_backward<T>(D, tensors == 3, [&](auto shape) {
+            return norm_plan<T, decltype(shape)>(N, D, tensors, true).grid;
+        });
+        most = most > n ? most : n;
+    }
+    return most;
+}
+
 }  // namespace
 
 int layer_norm_parts(long long N, int D) {
     // the larger of the types' and the forms' grids
-    return by_width_backward(D, [&](auto shape) {
-        using S = decltype(shape);
-        int most = 0;
-        for (int tensors = 2; tensors <= 3; ++tensors) {
-            const int a = norm_plan<__nv_bfloat16, S>(N, D, tensors, true).grid;
-            const int b = norm_plan<float, S>(N, D, tensors, true).grid;
-            most = most > a ? most : a;
-            most = most > b ? most : b;
-        }
-        return most;
-    });
+    const int a = most_parts<__nv_bfloat16>(N, D), b = most_parts<float>(N, D);
+    return a > b ? a : b;
 }
 
 cudaError_t launch_layer_norm(const void *x, const void *res, const float *w, const float *b,
