@@ -144,8 +144,10 @@ int check_scan(const void *x, const void *gate, int B, int T, int D, bool packed
     if (x_stride < D || gate_stride < D || x_stride % unit || gate_stride % gate_unit ||
         x_stride > (1LL << 36) || gate_stride > (1LL << 36))
         return GDN_ERR_INVALID_ARG;
-    const long long most = (1LL << 31) - 1024;  // tokens are 32-bit coordinates of a tile
-    if ((packed ? T : (long long)B * T) > most || B > most || (long long)B * D > (1LL << 36))
+    // tokens and channels are 32-bit coordinates of a tile, rounded up to whole tiles
+    const long long most = (1LL << 31) - 1024;
+    if ((packed ? T : (long long)B * T) > most || B > most || D > most ||
+        (long long)B * D > (1LL << 36))
         return GDN_ERR_INVALID_ARG;
     return aligned16(x) && aligned16(gate) ? GDN_OK : GDN_ERR_ALIGNMENT;
 }

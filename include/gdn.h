@@ -610,7 +610,7 @@ GDN_API int gdn_linear_decode_step(const void *q, const void *k, const void *v,
  *         keep what h held.
  *
  * D a multiple of 8 (else GDN_ERR_UNSUPPORTED); at most 2^31 - 1024 tokens in
- * all, and as many sequences.  Everything is float32 from the load to the one
+ * all, and as many sequences and channels.  Everything is float32 from the load to the one
  * rounding of h.  A value that is not finite reaches what the recurrence carries
  * it to and nothing else.
  * workspace: gdn_scan_prefill_workspace_size bytes (0 unless packed).
