@@ -234,16 +234,17 @@ struct RunMask {
     int seq;
 };
 // The sequence of this lane's token, ahead of the tile that needs it.  tile0: the
-// tile's first token in the stream, r0: the run's in the tile.
+// tile's first token in the stream (unsigned: one ahead of a stream's end may lie past
+// 2^31, one before its start below 0), r0: the run's in the tile.
 template <bool MASKED, int R>
-__device__ __forceinline__ int run_entry(const ScanRun &p, int base, int len, int tile0, int r0) {
+__device__ __forceinline__ int run_entry(const ScanRun &p, int base, int len, unsigned tile0, int r0) {
     if constexpr (!MASKED) return 0;
-    const int lane = threadIdx.x & 31;
-    const int k = r0 + lane - 1, t = tile0 + k;
-    if (lane >= R + 2 || t < 0 || t >= len) return -1;
+    const int lane = threadIdx.x & 31, k = r0 + lane - 1;
+    const unsigned t = tile0 + (unsigned)k;
+    if (lane >= R + 2 || t >= (unsigned)len) return -1;
     if (p.map) return p.map[t];
     // whole sequences in a tile: a neighbour is one of the tile's own tokens
-    return k >= 0 && k < p.step ? (base + t) / p.T : -1;
+    return k >= 0 && k < p.step ? (base + (int)t) / p.T : -1;
 }
 template <bool MASKED, int R>
 __device__ __forceinline__ RunMask run_mask(int seq, int len, int t0) {
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         const int j = n * cluster + rank, buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
         const RunMask m = run_mask<MASKED, R>(entry, len, t0);
-        entry = run_entry<MASKED, R>(p, base, len, tile0 + cluster * p.step, warp * R);
+        entry = run_entry<MASKED, R>(p, base, len, (unsigned)tile0 + (unsigned)(cluster * p.step), warp * R);
         if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
         const T *const xs = reinterpret_cast<const T *>(smem + s * S::kStage) + warp * R * kChannels + 2 * lane;
         const G *const gs = reinterpret_cast<const G *>(smem + s * S::kStage + S::kXBytes) +
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
         RunMask m = {0, 0, 0, -1};
         if (j >= 0) m = run_mask<MASKED, R>(entry, len, t0);
-        entry = run_entry<MASKED, R>(p, base, len, tile0 - cluster * p.step, warp * R);
+        entry = run_entry<MASKED, R>(p, base, len, (unsigned)tile0 - (unsigned)(cluster * p.step), warp * R);
         Pair h = next;
         next = kept(j - cluster);
         if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
