@@ -152,11 +152,52 @@ int check_scan(const void *x, const void *gate, int B, int T, int D, bool packed
     return aligned16(x) && aligned16(gate) ? GDN_OK : GDN_ERR_ALIGNMENT;
 }
 
-// Bytes of the states before every 64th token, rounded up.
-size_t scan_states_bytes(int B, int T, int D, bool packed) {
-    const size_t rows = (size_t)(packed ? 1 : B) * ((T + gdn::kScanBlock - 1) / gdn::kScanBlock);
-    return (rows * D * sizeof(float) + 255) & ~size_t(255);
+// Memory of a call: `rows` rows of `width` bytes, `pitch` bytes apart.  in_place: an output
+// that may take the place of an input, or an input whose place may be taken.
+struct Span {
+    const void *p;
+    long long rows, width, pitch;
+    bool in_place;
+};
+// n * size bytes in one piece.
+Span dense(const void *p, long long n, long long size, bool in_place = false) {
+    const long long most = 1LL << 60;  // no tensor is larger
+    const long long bytes = n > most / size ? most : n * size;
+    return {p, 1, bytes, bytes, in_place};
 }
+// Whether `out`, which is dense, and x share a byte.
+bool meet(const Span &out, const Span &x) {
+    if (!out.p || !x.p || out.width <= 0 || x.width <= 0 || x.rows <= 0) return false;
+    const long long lo =
+        (long long)(reinterpret_cast<uintptr_t>(out.p) - reinterpret_cast<uintptr_t>(x.p));
+    // the first row of x that ends behind the start of out
+    const long long k = lo < x.width ? 0 : (lo - x.width) / x.pitch + 1;
+    return k < x.rows && k * x.pitch < lo + out.width;
+}
+// Whether an output lies over an input or over another output.
+template <int M, int N> bool clash(const Span (&outs)[M], const Span (&ins)[N]) {
+    for (int i = 0; i < M; ++i) {
+        for (const Span &x : ins)
+            if (meet(outs[i], x) && !(outs[i].in_place && x.in_place && outs[i].p == x.p)) return true;
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+// The states before every 64th token, and their bytes rounded up.
+long long scan_states(int B, int T, bool packed) {
+    return (packed ? 1LL : B) * (((long long)T + gdn::kScanBlock - 1) / gdn::kScanBlock);
+}
+size_t scan_states_bytes(int B, int T, int D, bool packed) {
+    return ((size_t)scan_states(B, T, packed) * D * sizeof(float) + 255) & ~size_t(255);
+}
+// Bytes of an element of x (h, y, dh, dx) and of the gates.
+struct ScanSizes {
+    long long x, gate;
+    ScanSizes(int kind, int dtype)
+        : x(dtype == GDN_BF16 ? 2 : 4), gate(kind == GDN_SCAN_DECAY ? 4 : x) {}
+};
 
 int check_layer_norm(long long N, int D, int dtype) {
     if (N < 0 || N > (1LL << 40) || D < 0) return GDN_ERR_INVALID_ARG;
@@ -775,13 +816,22 @@ int gdn_scan_prefill(const void *x, const void *gate, const float *h0, void *h, 
         if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
     if (B == 0 || D == 0) return GDN_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T == 0) return empty_prefill(h0, h_T, B, 1, D, 1, st);
-    if (!x || !gate || (!h && !h_T && !states) || h == x || h == gate) return GDN_ERR_INVALID_ARG;
-    // h0 is read while h and states are written; h_T may take its place
-    if ((h && (h == h0 || h == h_T)) || (states && (states == h0 || states == h_T || states == h)))
-        return GDN_ERR_INVALID_ARG;
+    const long long state = (long long)B * D, tokens = packed ? T : (long long)B * T;
+    if (T == 0) {
+        const Span end[] = {dense(h_T, state, 4, true)}, start[] = {dense(h0, state, 4, true)};
+        if (clash(end, start)) return GDN_ERR_INVALID_ARG;
+        return empty_prefill(h0, h_T, B, 1, D, 1, st);
+    }
+    if (!x || !gate || (!h && !h_T && !states)) return GDN_ERR_INVALID_ARG;
     const size_t need = gdn_scan_prefill_workspace_size(B, T, D, packed);
     if (workspace_bytes < need || (need && !workspace)) return GDN_ERR_WORKSPACE;
+    // every tensor is read while others are written; h_T may take the place of h0
+    const ScanSizes z(kind, dtype);
+    const Span outs[] = {dense(h, tokens * D, z.x), dense(h_T, state, 4, true),
+                         dense(states, scan_states(B, T, packed) * D, 4), dense(workspace, need, 1)};
+    const Span ins[] = {{x, tokens, D * z.x, x_stride * z.x}, {gate, tokens, D * z.gate, gate_stride * z.gate},
+                        dense(h0, state, 4, true), dense(offsets, B + 1LL, 4)};
+    if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
     gdn::ScanArgs a = {};
     a.x = x; a.gate = gate; a.h0 = h0; a.h = h; a.h_T = h_T; a.states = states;
     a.offsets = offsets; a.B = B; a.T = T; a.D = D; a.ldx = x_stride; a.ldg = gate_stride;
@@ -808,15 +858,23 @@ int gdn_scan_backward(const void *x, const void *gate, const void *dh, const flo
         if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
     if (B == 0 || D == 0) return GDN_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T == 0) return empty_prefill(dh_T, dh0, B, 1, D, 1, st);
+    const long long state = (long long)B * D, tokens = packed ? T : (long long)B * T;
+    if (T == 0) {
+        const Span end[] = {dense(dh0, state, 4, true)}, start[] = {dense(dh_T, state, 4, true)};
+        if (clash(end, start)) return GDN_ERR_INVALID_ARG;
+        return empty_prefill(dh_T, dh0, B, 1, D, 1, st);
+    }
     if (!x || !gate || !dh || !dx || !dgate) return GDN_ERR_INVALID_ARG;
-    // every tile's inputs are read while the outputs of others are written
-    const void *ins[] = {x, gate, dh};
-    for (const void *p : ins)
-        if (p == dx || p == dgate) return GDN_ERR_INVALID_ARG;
-    if (dx == dgate || (dh0 && (dh0 == dh_T || dh0 == h0))) return GDN_ERR_INVALID_ARG;
     const size_t need = gdn_scan_backward_workspace_size(B, T, D, packed, states != nullptr);
     if (workspace_bytes < need || (need && !workspace)) return GDN_ERR_WORKSPACE;
+    // every tile's inputs are read while the outputs of others are written
+    const ScanSizes z(kind, dtype);
+    const Span outs[] = {dense(dx, tokens * D, z.x), dense(dgate, tokens * D, z.gate), dense(dh0, state, 4),
+                         dense(workspace, need, 1)};
+    const Span ins[] = {{x, tokens, D * z.x, x_stride * z.x}, {gate, tokens, D * z.gate, gate_stride * z.gate},
+                        dense(dh, tokens * D, z.x), dense(h0, state, 4), dense(dh_T, state, 4),
+                        dense(states, scan_states(B, T, packed) * D, 4), dense(offsets, B + 1LL, 4)};
+    if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
     gdn::ScanArgs a = {};
     a.x = x; a.gate = gate; a.dh = dh; a.h0 = h0; a.dh_T = dh_T; a.states = const_cast<float *>(states);
     a.dx = dx; a.dgate = dgate; a.dh0 = dh0;
@@ -832,11 +890,15 @@ int gdn_scan_decode_step(const void *x, const void *gate, const float *h, float 
     if (e != GDN_OK) return e;
     if (!aligned16(h) || !aligned16(h_out) || !aligned16(y)) return GDN_ERR_ALIGNMENT;
     if (B == 0 || D == 0) return GDN_OK;
-    if (!x || !gate || !h || !h_out || (y && (y == h || y == h_out))) return GDN_ERR_INVALID_ARG;
-    // x and gate have rows and types of their own
-    const void *ins[] = {x, gate};
-    for (const void *p : ins)
-        if (p == y || p == h_out) return GDN_ERR_INVALID_ARG;
+    if (!x || !gate || !h || !h_out) return GDN_ERR_INVALID_ARG;
+    // threads read what others write unless h_out is h; x and gate have rows and types of
+    // their own
+    const ScanSizes z(kind, dtype);
+    const long long n = (long long)B * D;
+    const Span outs[] = {dense(h_out, n, 4, true), dense(y, n, z.x)};
+    const Span ins[] = {{x, B, D * z.x, x_stride * z.x}, {gate, B, D * z.gate, gate_stride * z.gate},
+                        dense(h, n, 4, true)};
+    if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
     return from_cuda(gdn::launch_scan_step(x, gate, h, h_out, y, B, D, x_stride, gate_stride,
                                            kind == GDN_SCAN_SIGMOID, dtype,
                                            static_cast<cudaStream_t>(stream)));

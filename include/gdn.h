@@ -599,16 +599,19 @@ GDN_API int gdn_linear_decode_step(const void *q, const void *k, const void *v,
  *         consecutive tokens lie x_stride / gate_stride elements apart (at least
  *         D, a multiple of 16 bytes), so that they may be parts of one projection
  *   h0    [B, D] float32, or NULL = zero
- *   h     [B, T, D] (dtype), dense, or NULL; no other tensor of the call
+ *   h     [B, T, D] (dtype), dense, or NULL
  *   h_T   [B, D] float32, or NULL; may be h0
  *   states  NULL, or [B, ceil(T / 64), D] float32: the state before every 64th
- *         token, which gdn_scan_backward starts from; no other tensor of the call
+ *         token, which gdn_scan_backward starts from
  *   offsets  NULL, or [B + 1] int32 on the device: the B sequences lie packed
  *         in T tokens as for gdn_linear_prefill (bad offsets as there); states is
  *         then [ceil(T / 64), D], of the T tokens (a row whose token starts a
  *         sequence or belongs to none is undefined), and tokens of no sequence
  *         keep what h held.
  *
+ * Outputs and the workspace share no byte with the inputs or with each other (but
+ * h_T, which may be h0 exactly), else GDN_ERR_INVALID_ARG; so it is for the two
+ * calls below.
  * D a multiple of 8 (else GDN_ERR_UNSUPPORTED); at most 2^31 - 1024 tokens in
  * all, and as many sequences and channels.  Everything is float32 from the load to the one
  * rounding of h.  A value that is not finite reaches what the recurrence carries
@@ -632,8 +635,8 @@ GDN_API int gdn_scan_prefill(const void *x, const void *gate, const float *h0, v
  *     dgate_t = G_t (h_{t-1} - x_t) a_t b_t      (GDN_SCAN_SIGMOID, dtype)
  *     dh0 = a_1 G_1
  *
- * dx, dgate [B, T, D] dense; dh0 [B, D] float32, or NULL; none of them one of
- * the inputs.  Tokens of no sequence keep what dx and dgate held.
+ * dx, dgate [B, T, D] dense; dh0 [B, D] float32, or NULL.  Tokens of no sequence
+ * keep what dx and dgate held.
  * states: as gdn_scan_prefill wrote them for the same inputs, or NULL: they are
  * then formed by a pass over x and gate of the call's own.
  * workspace: gdn_scan_backward_workspace_size bytes (kept: states are given; 0
@@ -650,8 +653,7 @@ GDN_API int gdn_scan_backward(const void *x, const void *gate, const void *dh, c
 /*
  * gdn_scan_decode_step -- one token of gdn_scan_prefill: x, gate [B, D] (rows
  * x_stride / gate_stride elements apart); reads h [B, D] float32 and writes
- * h_out, which may be h, and y [B, D] (dtype, dense), the rounded state, or NULL;
- * neither of them is x or gate.
+ * h_out, which may be h, and y [B, D] (dtype, dense), the rounded state, or NULL.
  */
 GDN_API int gdn_scan_decode_step(const void *x, const void *gate, const float *h, float *h_out,
                                  void *y, int B, int D, long long x_stride, long long gate_stride,
