@@ -165,6 +165,12 @@ Span dense(const void *p, long long n, long long size, bool in_place = false) {
     const long long bytes = n > most / size ? most : n * size;
     return {p, 1, bytes, bytes, in_place};
 }
+// Rows of D elements of `size` bytes, `stride` elements apart.
+Span strided(const void *p, long long rows, int D, long long stride, long long size,
+             bool in_place = false) {
+    const long long most = 1LL << 56;  // further than any two rows lie
+    return {p, rows, D * size, (stride < most ? stride : most) * size, in_place};
+}
 // Whether `out`, which is dense, and x share a byte.
 bool meet(const Span &out, const Span &x) {
     if (!out.p || !x.p || out.width <= 0 || x.width <= 0 || x.rows <= 0) return false;
@@ -829,7 +835,7 @@ int gdn_scan_prefill(const void *x, const void *gate, const float *h0, void *h, 
     const ScanSizes z(kind, dtype);
     const Span outs[] = {dense(h, tokens * D, z.x), dense(h_T, state, 4, true),
                          dense(states, scan_states(B, T, packed) * D, 4), dense(workspace, need, 1)};
-    const Span ins[] = {{x, tokens, D * z.x, x_stride * z.x}, {gate, tokens, D * z.gate, gate_stride * z.gate},
+    const Span ins[] = {strided(x, tokens, D, x_stride, z.x), strided(gate, tokens, D, gate_stride, z.gate),
                         dense(h0, state, 4, true), dense(offsets, B + 1LL, 4)};
     if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
     gdn::ScanArgs a = {};
@@ -871,7 +877,7 @@ int gdn_scan_backward(const void *x, const void *gate, const void *dh, const flo
     const ScanSizes z(kind, dtype);
     const Span outs[] = {dense(dx, tokens * D, z.x), dense(dgate, tokens * D, z.gate), dense(dh0, state, 4),
                          dense(workspace, need, 1)};
-    const Span ins[] = {{x, tokens, D * z.x, x_stride * z.x}, {gate, tokens, D * z.gate, gate_stride * z.gate},
+    const Span ins[] = {strided(x, tokens, D, x_stride, z.x), strided(gate, tokens, D, gate_stride, z.gate),
                         dense(dh, tokens * D, z.x), dense(h0, state, 4), dense(dh_T, state, 4),
                         dense(states, scan_states(B, T, packed) * D, 4), dense(offsets, B + 1LL, 4)};
     if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
@@ -896,7 +902,7 @@ int gdn_scan_decode_step(const void *x, const void *gate, const float *h, float 
     const ScanSizes z(kind, dtype);
     const long long n = (long long)B * D;
     const Span outs[] = {dense(h_out, n, 4, true), dense(y, n, z.x)};
-    const Span ins[] = {{x, B, D * z.x, x_stride * z.x}, {gate, B, D * z.gate, gate_stride * z.gate},
+    const Span ins[] = {strided(x, B, D, x_stride, z.x), strided(gate, B, D, gate_stride, z.gate),
                         dense(h, n, 4, true)};
     if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
     return from_cuda(gdn::launch_scan_step(x, gate, h, h_out, y, B, D, x_stride, gate_stride,
@@ -918,11 +924,14 @@ int gdn_layer_norm(const void *x, const void *residual, const float *w, const fl
     for (const void *p : ptrs)
         if (!aligned16(p)) return GDN_ERR_ALIGNMENT;
     if (N == 0 || D == 0) return GDN_OK;
-    if (!x || !y || (s && !residual) || s == y) return GDN_ERR_INVALID_ARG;
-    // in place only where the rows lie as the outputs do
-    if (((y == x || s == x) && x_stride != D) ||
-        (residual && (y == residual || s == residual) && residual_stride != D))
-        return GDN_ERR_INVALID_ARG;
+    if (!x || !y || (s && !residual)) return GDN_ERR_INVALID_ARG;
+    // rows are read while others are written; in place only where they lie as the outputs do
+    const long long z = dtype == GDN_BF16 ? 2 : 4;
+    const Span outs[] = {dense(y, N * D, z, true), dense(s, N * D, z, true), dense(stats, N * 2, 4)};
+    const Span ins[] = {strided(x, N, D, x_stride, z, x_stride == D),
+                        strided(residual, N, D, residual_stride, z, residual_stride == D),
+                        dense(w, D, 4), dense(b, D, 4)};
+    if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
     return from_cuda(gdn::launch_layer_norm(x, residual, w, b, y, s, stats, N, D, x_stride,
                                             residual_stride, eps, dtype,
                                             static_cast<cudaStream_t>(stream)));
@@ -951,12 +960,17 @@ int gdn_layer_norm_backward(const void *s, const void *dy, const float *stats, c
         if (db && c == cudaSuccess) c = cudaMemsetAsync(db, 0, sizeof(float) * D, st);
         return from_cuda(c);
     }
-    if (!s || !dy || !stats || !dx || (dw && dw == db)) return GDN_ERR_INVALID_ARG;
-    // in place only where the rows lie as the output's do
-    if (dx == s && s_stride != D) return GDN_ERR_INVALID_ARG;
-    if ((dw || db) &&
-        (!workspace || workspace_bytes < gdn_layer_norm_backward_workspace_size(N, D)))
-        return GDN_ERR_WORKSPACE;
+    if (!s || !dy || !stats || !dx) return GDN_ERR_INVALID_ARG;
+    const size_t need = dw || db ? gdn_layer_norm_backward_workspace_size(N, D) : 0;
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    // rows are read while others are written; dx in place only where they lie as its own do;
+    // dw and db are written when all else has been read
+    const long long z = dtype == GDN_BF16 ? 2 : 4;
+    const Span rows[] = {dense(dx, N * D, z, true), dense(workspace, need, 1)};
+    const Span sums[] = {dense(dw, D, 4), dense(db, D, 4)};
+    const Span ins[] = {strided(s, N, D, s_stride, z, s_stride == D), dense(dy, N * D, z, true),
+                        dense(ds, N * D, z, true), dense(stats, N * 2, 4), dense(w, D, 4)};
+    if (clash(rows, ins) || clash(sums, rows)) return GDN_ERR_INVALID_ARG;
     return from_cuda(gdn::launch_layer_norm_backward(s, dy, stats, w, ds, dx, dw, db, N, D, s_stride,
                                                      dtype, static_cast<float *>(workspace), st));
 }

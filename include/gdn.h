@@ -676,8 +676,9 @@ GDN_API int gdn_scan_decode_step(const void *x, const void *gate, const float *h
  *   stats  [N, 2] float32: m and r of each row, for gdn_layer_norm_backward; or
  *          NULL
  *
- * D a multiple of 8 up to 16384 (else GDN_ERR_UNSUPPORTED).  Everything is
- * float32 from the load to the rounding of s and y.
+ * Otherwise outputs share no byte with the inputs or with each other, else
+ * GDN_ERR_INVALID_ARG.  D a multiple of 8 up to 16384 (else GDN_ERR_UNSUPPORTED).
+ * Everything is float32 from the load to the rounding of s and y.
  */
 GDN_API int gdn_layer_norm(const void *x, const void *residual, const float *w, const float *b,
                            void *y, void *s, float *stats, long long N, int D, long long x_stride,
@@ -692,9 +693,9 @@ GDN_API int gdn_layer_norm(const void *x, const void *residual, const float *w, 
  *     dx = r (g - sum g / D - n (sum g n) / D) + ds     (of x and of the residual)
  *     dw = sum over rows of dy .* n,   db = sum over rows of dy
  *
- * dx [N, D] (dtype, dense; may be dy or ds); dw, db [D] float32, each may be
- * NULL.  Where one is wanted: workspace of gdn_layer_norm_backward_workspace_size
- * bytes.  The rows are summed in a fixed order: equal inputs give equal bits.
+ * dx [N, D] (dtype, dense; may be dy, ds or a dense s, and else shares no byte with
+ * the inputs); dw, db [D] float32, each may be NULL.  Where one is wanted: workspace
+ * of gdn_layer_norm_backward_workspace_size bytes, apart from all else.  The rows are summed in a fixed order: equal inputs give equal bits.
  */
 GDN_API size_t gdn_layer_norm_backward_workspace_size(long long N, int D);
 GDN_API int gdn_layer_norm_backward(const void *s, const void *dy, const float *stats,
