@@ -858,6 +858,10 @@ ScanPlan scan_plan(const ScanArgs &a, int tile, int most, const int *map) {
         const int each = (int)((tiles + streams - 1) / streams);
         s.streams = (tiles + each - 1) / each;
         r.stream = each * r.step;
+        // such tiles have nothing to tell each other, so no clusters (with two tiles a stream
+        // clusters of two put them side by side, and cost their start and end and the totals:
+        // 11 sequences of 64 float32 tokens and 2048 channels 13.8 us, one CTA for both 8.8)
+        most = 1;
     } else {
         s.streams = a.B;
         r.stream = a.T;
