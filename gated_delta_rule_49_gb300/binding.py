@@ -47,6 +47,9 @@ GDN_SCAN_SIGMOID = 1
 SCANS = {"decay": GDN_SCAN_DECAY, "sigmoid": GDN_SCAN_SIGMOID}
 GDN_SCAN_BLOCK = 64  # tokens between the states that a scan keeps
 
+GDN_SELFTEST_SCAN = 0
+GDN_SELFTEST_SCAN_BACKWARD = 1
+
 EXPORTS = (
     "gdn_prefill",
     "gdn_prefill_workspace_size",
@@ -57,6 +60,7 @@ EXPORTS = (
     "gdn_status_string",
     "gdn_version",
     "gdn_selftest_wait_timeout",
+    "gdn_selftest_lost_copy",
     "gdn_prefill_noalloc",
     "gdn_prefill_noalloc_max_workspace",
     "gdn_gather_normalize",
@@ -134,6 +138,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gdn_version.restype = i
         lib.gdn_selftest_wait_timeout.argtypes = [ctypes.c_longlong, vp]
         lib.gdn_selftest_wait_timeout.restype = i
+        lib.gdn_selftest_lost_copy.argtypes = [i] + [ctypes.c_longlong] * 2 + [vp, sz, i, i, i, vp]
+        lib.gdn_selftest_lost_copy.restype = i
         lib.gdn_prefill_noalloc.argtypes = [vp] * 8 + [i] * 6 + [vp]
         lib.gdn_prefill_noalloc.restype = i
         lib.gdn_gather_normalize.argtypes = [vp, vp, vp, ctypes.c_longlong, i, i, i, i, vp]
@@ -685,6 +691,12 @@ def gdn_status_string(status: int) -> str:
 def gdn_selftest_wait_timeout(limit_cycles, stream=None) -> int:
     st = load().gdn_selftest_wait_timeout(int(limit_cycles), _stream(stream))
     return _check(st, "gdn_selftest_wait_timeout")
+
+
+def gdn_selftest_lost_copy(call, limit_cycles, lost, buffer, bytes, rows, T, D, stream=None) -> int:
+    st = load().gdn_selftest_lost_copy(call, int(limit_cycles), int(lost), _ptr(buffer), bytes, rows,
+                                       T, D, _stream(stream))
+    return _check(st, "gdn_selftest_lost_copy")
 
 
 def gdn_version() -> int:

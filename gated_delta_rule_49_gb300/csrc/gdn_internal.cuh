@@ -226,6 +226,10 @@ struct ScanArgs {
     int B, T, D;
     long long ldx, ldg;
     bool sigmoid;
+    // self-test: waits end after `limit` SM clocks, and tile `lost` of each stream is not
+    // copied.  0: an ordinary call
+    long long limit;
+    int lost;
 };
 // Bytes of the table of packed tokens' sequences, at the workspace's start.
 size_t scan_map_bytes(int T);

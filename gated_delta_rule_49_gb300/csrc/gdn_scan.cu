@@ -46,6 +46,7 @@ constexpr int kChannels = 64;  // of a CTA
 constexpr int kWarps = 8;      // runs of a tile
 constexpr int kScanThreads = kWarps * 32;
 constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
+constexpr long long kDrainLimit = kWaitLimit / 16;
 
 // a and b of a gate.  b = 1 - a is formed without the difference: a near 1
 // would leave nothing of it.
@@ -126,6 +127,8 @@ struct ScanRun {
     int step;          // tokens of a tile that are its own
     int rows;          // tokens of a box
     int T, blocks;     // dense sequences: tokens, and kept states
+    long long limit;   // of a wait, SM clocks
+    int lost;          // self-test: the tile of each stream that is not copied; or -1
     int *status;
 };
 
@@ -184,20 +187,33 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// A wait with a limit; the first that runs out ends all others of the CTA.
+// A wait with a limit; the first that runs out ends all others of the CTA.  Its threads
+// walk on through their tiles, with what they have, so that all meet at every barrier.  A
+// thread whose wait has run out announces and sends no more (a barrier whose phase is open
+// may not be arrived at again), and nothing is fetched; without its totals the other CTAs of
+// a cluster run out in turn.
 template <bool CLUSTER>
-__device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, int *abort, int *status) {
+__device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity, int *abort, const ScanRun &p) {
     auto ready = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (ready()) return;
+    if (ready()) return true;
     const long long t0 = clock64();
     volatile int *const flag = abort;
     while (!ready()) {
-        if (*flag) return;
-        if (clock64() - t0 > kWaitLimit) {
+        if (*flag) return false;
+        if (clock64() - t0 > p.limit) {
             *flag = 1;
-            if (status) atomicOr(status, kStatusTimeout);
-            return;
+            if (p.status) atomicOr(p.status, kStatusTimeout);
+            return false;
         }
+    }
+    return true;
+}
+// After one that ran out: copies in flight, and totals that other CTAs have sent, land before
+// the CTA ends.
+__device__ __forceinline__ void drain(uint64_t *bar, int n) {
+    for (int i = 0; i < n; ++i) {
+        mbar_wait(&bar[i], 0, kDrainLimit);
+        mbar_wait(&bar[i], 1, kDrainLimit);
     }
 }
 
@@ -324,6 +340,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         const int j = n * cluster + rank, s = n % ST;
         if (j >= tiles) return;
         mbar_arrive_expect_tx(&sh.full[s], bytes);
+        if (j == p.lost) return;
         load_box(smem + s * S::kStage, &mx, &sh.full[s], c0, base + j * p.step);
         load_box(smem + s * S::kStage + S::kXBytes, &mg, &sh.full[s], c0, base + j * p.step);
     };
@@ -343,12 +360,13 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     T *const out = static_cast<T *>(p.h);
     if constexpr (MASKED) pdl_wait();  // for the table
     int entry = run_entry<MASKED, R>(p, base, len, rank * p.step, warp * R);
+    bool gone = false;  // a wait for totals has run out
     for (int n = 0; n < slabs; ++n) {
         const int j = n * cluster + rank, buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
         const RunMask m = run_mask<MASKED, R>(entry, len, t0);
         entry = run_entry<MASKED, R>(p, base, len, (unsigned)tile0 + (unsigned)(cluster * p.step), warp * R);
-        if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
+        if (CLUSTER && threadIdx.x == 0 && !gone) expect_totals(sh.sent, buf, cluster);
         const T *const xs = reinterpret_cast<const T *>(smem + s * S::kStage) + warp * R * kChannels + 2 * lane;
         const G *const gs = reinterpret_cast<const G *>(smem + s * S::kStage + S::kXBytes) +
                             warp * R * kChannels + 2 * lane;
@@ -368,7 +386,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 }
             }
         }
-        if (j < tiles) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p.status);
+        if (j < tiles) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p);
         if (plain) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -419,8 +437,8 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                 }
             });
             auto &to = sh.totals[0];
-            send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
-            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
+            if (!gone) send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
+            if (!wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p)) gone = true;
             h = apply_totals<MASKED>(to, buf, rank, cluster, carry);
             over(h, before, cut);
         } else {
@@ -461,13 +479,11 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     }
     if (!MASKED && p.h_T && rank == 0 && warp == 0 && live)
         store2(p.h_T + (long long)stream * p.D + c, carry);
-    // copies in flight land, and no CTA sends to one that has ended
-    if (sh.abort && threadIdx.x == 0)
-        for (int s = 0; s < ST; ++s) {
-            mbar_wait(&sh.full[s], 0, kWaitLimit / 16);
-            mbar_wait(&sh.full[s], 1, kWaitLimit / 16);
-        }
-    if constexpr (CLUSTER) cluster_sync();
+    if (sh.abort && threadIdx.x == 0) {
+        drain(sh.full, ST);
+        if constexpr (CLUSTER) drain(sh.sent, 2);
+    }
+    if constexpr (CLUSTER) cluster_sync();  // no CTA sends to one that has ended
 }
 
 // ------------------------------------------------------------------ backward
@@ -498,6 +514,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         if (j < 0) return;
         uint8_t *const at = smem + s * S::kStage;
         mbar_arrive_expect_tx(&sh.full[s], bytes);
+        if (j == p.lost) return;
         load_box(at, &mx, &sh.full[s], c0, base + j * p.step);
         load_box(at + S::kXBytes, &mg, &sh.full[s], c0, base + j * p.step);
         load_box(at + S::kXBytes + S::kGBytes, &md, &sh.full[s], c0, base + j * p.step);
@@ -524,6 +541,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     if constexpr (MASKED) pdl_wait();  // for the table
     Pair next = kept(tiles - 1 - rank);
     int entry = run_entry<MASKED, R>(p, base, len, (tiles - 1 - rank) * p.step, warp * R);
+    bool gone = false;  // a wait for totals has run out
     for (int n = 0; n < slabs; ++n) {
         const int j = tiles - 1 - (n * cluster + rank), buf = n & 1, s = n % ST;
         const int tile0 = j * p.step, t0 = tile0 + warp * R;
@@ -532,13 +550,13 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         entry = run_entry<MASKED, R>(p, base, len, (unsigned)tile0 - (unsigned)(cluster * p.step), warp * R);
         Pair h = next;
         next = kept(j - cluster);
-        if (CLUSTER && threadIdx.x == 0) expect_totals(sh.sent, buf, cluster);
+        if (CLUSTER && threadIdx.x == 0 && !gone) expect_totals(sh.sent, buf, cluster);
         const uint8_t *const stage = smem + s * S::kStage;
         const int at0 = warp * R * kChannels + 2 * lane;
         const T *const xs = reinterpret_cast<const T *>(stage) + at0;
         const G *const gs = reinterpret_cast<const G *>(stage + S::kXBytes) + at0;
         const T *const ds = reinterpret_cast<const T *>(stage + S::kXBytes + S::kGBytes) + at0;
-        if (j >= 0) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p.status);
+        if (j >= 0) wait_full<false>(&sh.full[s], (n / ST) & 1, &sh.abort, p);
         Pair a[R] = {}, b[R] = {}, u[R] = {};  // u = b x
         Pair H = zero;
         Piece k = {one, zero};
@@ -614,8 +632,8 @@ __global__ void __launch_bounds__(kScanThreads, 2)
                     over(h, {sh.run[buf][w][lane].p, sh.state[buf][w][lane]}, reset(w, 1));
             });
             auto &to = sh.totals[0];
-            send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
-            wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p.status);
+            if (!gone) send_totals(to, sh.sent, buf, rank, cluster, t, all_cut);
+            if (!wait_full<true>(&sh.sent[buf], (n >> 1) & 1, &sh.abort, p)) gone = true;
             v = apply_totals<MASKED>(to, buf, rank, cluster, carry);
             over(v, after, cut);
         } else {
@@ -678,12 +696,11 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     }
     if (!MASKED && p.dh0 && rank == 0 && warp == 0 && live)
         store2(p.dh0 + (long long)stream * p.D + c, carry);
-    if (sh.abort && threadIdx.x == 0)
-        for (int s = 0; s < ST; ++s) {
-            mbar_wait(&sh.full[s], 0, kWaitLimit / 16);
-            mbar_wait(&sh.full[s], 1, kWaitLimit / 16);
-        }
-    if constexpr (CLUSTER) cluster_sync();
+    if (sh.abort && threadIdx.x == 0) {
+        drain(sh.full, ST);
+        if constexpr (CLUSTER) drain(sh.sent, 2);
+    }
+    if constexpr (CLUSTER) cluster_sync();  // no CTA sends to one that has ended
 }
 
 // ------------------------------------------------------------------ packed tokens
@@ -843,6 +860,8 @@ ScanPlan scan_plan(const ScanArgs &a, int tile, int most, const int *map) {
     r.blocks = (a.T + kScanBlock - 1) / kScanBlock;
     r.total = a.offsets ? a.T : a.B * a.T;
     r.status = device_status_ptr();
+    r.limit = a.limit > 0 ? a.limit : kWaitLimit;
+    r.lost = a.limit > 0 ? a.lost : -1;
     r.step = tile;
     if (a.offsets) {
         s.masked = true;

@@ -1,6 +1,6 @@
-// Self-test of the bounded-wait path used by the tensor-core prefill: a wait
-// on an mbarrier that never completes must give up, record the timeout in the
-// device status word and return (no trap, no hang).
+// Self-tests of the bounded waits: a wait on an mbarrier that never completes must give up,
+// record the timeout in the device status word and return (no trap, no hang); a kernel that
+// lacks one of its copies must end the same way.
 #include "gdn_internal.cuh"
 #include "gdn_sm100.cuh"
 
@@ -25,4 +25,38 @@ extern "C" int gdn_selftest_wait_timeout(long long limit_cycles, void *stream) {
     gdn::wait_timeout_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
         limit_cycles, gdn::device_status_ptr());
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+extern "C" int gdn_selftest_lost_copy(gdn_selftest_call call, long long limit_cycles, long long lost,
+                                      void *buffer, size_t bytes, int rows, int T, int D,
+                                      void *stream) {
+    if (limit_cycles < 1 || limit_cycles > (1LL << 31) || lost < 0 || !buffer || rows < 1 || T < 1 ||
+        D < 8 || D % 8 || (reinterpret_cast<uintptr_t>(buffer) & 15))
+        return GDN_ERR_INVALID_ARG;
+    // each tensor has the room of float32 values (the states before every 64th token are float32)
+    const long long tokens = (long long)rows * T, part = ((tokens * D * 4) + 255) / 256 * 256;
+    if (tokens > (1 << 24) || D > 16384) return GDN_ERR_INVALID_ARG;
+    if (bytes < (size_t)part * 6) return GDN_ERR_WORKSPACE;
+    char *const at = static_cast<char *>(buffer);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaErrorInvalidValue;
+    if (call == GDN_SELFTEST_SCAN || call == GDN_SELFTEST_SCAN_BACKWARD) {
+        gdn::ScanArgs a = {};
+        a.x = at;
+        a.gate = at + part;
+        a.states = reinterpret_cast<float *>(at + 2 * part);
+        a.B = rows; a.T = T; a.D = D;
+        a.ldx = a.ldg = D;
+        a.sigmoid = true;
+        a.limit = limit_cycles;
+        a.lost = (int)(lost < tokens ? lost : tokens);
+        a.h = at + 3 * part;
+        a.dh = at + 3 * part;
+        a.dx = at + 4 * part;
+        a.dgate = at + 5 * part;
+        e = call == GDN_SELFTEST_SCAN ? gdn::launch_scan(a, GDN_BF16, nullptr, st)
+                                      : gdn::launch_scan_backward(a, GDN_BF16, nullptr, st);
+    }
+    if (e == cudaErrorInvalidValue) return GDN_ERR_INVALID_ARG;
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

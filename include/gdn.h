@@ -724,6 +724,19 @@ GDN_API int gdn_get_last_device_status(void *stream);
  */
 GDN_API int gdn_selftest_wait_timeout(long long limit_cycles, void *stream);
 
+/*
+ * gdn_selftest_lost_copy -- run a kernel of the recurrence (bf16, sigmoid gates) with a
+ * copy that never comes: tile `lost` (128 tokens, gradients 64) of each sequence is
+ * announced to its barrier and not fetched.  Every wait ends after limit_cycles SM clock
+ * cycles (1 <= limit_cycles <= 2^31); the kernel sets the timeout bit of the device
+ * status word and returns, with outputs that mean nothing.  rows sequences of T tokens
+ * (2^24 in all at most) of D channels; buffer: 24 rows T D bytes + 1536 of device memory, which
+ * hold the inputs and take the outputs.  Asynchronous on `stream`.
+ */
+typedef enum { GDN_SELFTEST_SCAN = 0, GDN_SELFTEST_SCAN_BACKWARD = 1 } gdn_selftest_call;
+GDN_API int gdn_selftest_lost_copy(gdn_selftest_call call, long long limit_cycles, long long lost,
+                                   void *buffer, size_t bytes, int rows, int T, int D, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 GDN_API const char *gdn_status_string(int status);
 
