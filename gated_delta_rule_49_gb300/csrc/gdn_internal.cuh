@@ -226,16 +226,15 @@ struct ScanArgs {
     int B, T, D;
     long long ldx, ldg;
     bool sigmoid;
-    // self-test: waits end after `limit` SM clocks, and tile `lost` of each stream is not
-    // copied.  0: an ordinary call
-    long long limit;
-    int lost;
 };
 // Bytes of the table of packed tokens' sequences, at the workspace's start.
 size_t scan_map_bytes(int T);
 cudaError_t launch_scan(const ScanArgs &a, gdn_dtype dt, void *workspace, cudaStream_t stream);
 cudaError_t launch_scan_backward(const ScanArgs &a, gdn_dtype dt, void *workspace,
                                  cudaStream_t stream);
+// Self-test (bf16, sigmoid gates, dense; gradients where a.dh is given): waits end after
+// `limit` SM clocks, and tile `lost` of each stream is not copied.
+cudaError_t launch_scan_lost(const ScanArgs &a, long long limit, int lost, cudaStream_t stream);
 cudaError_t launch_scan_step(const void *x, const void *gate, const float *h, float *h_out, void *y,
                              int B, int D, long long ldx, long long ldg, bool sigmoid, gdn_dtype dt,
                              cudaStream_t stream);

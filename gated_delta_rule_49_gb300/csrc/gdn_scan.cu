@@ -127,10 +127,18 @@ struct ScanRun {
     int step;          // tokens of a tile that are its own
     int rows;          // tokens of a box
     int T, blocks;     // dense sequences: tokens, and kept states
-    long long limit;   // of a wait, SM clocks
-    int lost;          // self-test: the tile of each stream that is not copied; or -1
     int *status;
 };
+// Self-test (kernels of their own): the clocks of a wait, and the tile of each stream that is
+// not copied.
+struct LostRun : ScanRun {
+    long long limit;
+    int lost;
+};
+__device__ __forceinline__ long long wait_limit(const ScanRun &) { return kWaitLimit; }
+__device__ __forceinline__ long long wait_limit(const LostRun &p) { return p.limit; }
+__device__ __forceinline__ bool is_lost(const ScanRun &, int) { return false; }
+__device__ __forceinline__ bool is_lost(const LostRun &p, int tile) { return tile == p.lost; }
 
 struct Piece {         // what a run or a tile does to a lane's channels: c -> p c + h
     Pair p, h;
@@ -192,15 +200,15 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
 // thread whose wait has run out announces and sends no more (a barrier whose phase is open
 // may not be arrived at again), and nothing is fetched; without its totals the other CTAs of
 // a cluster run out in turn.
-template <bool CLUSTER>
-__device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity, int *abort, const ScanRun &p) {
+template <bool CLUSTER, typename RUN>
+__device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity, int *abort, const RUN &p) {
     auto ready = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
     if (ready()) return true;
     const long long t0 = clock64();
     volatile int *const flag = abort;
     while (!ready()) {
         if (*flag) return false;
-        if (clock64() - t0 > p.limit) {
+        if (clock64() - t0 > wait_limit(p)) {
             *flag = 1;
             if (p.status) atomicOr(p.status, kStatusTimeout);
             return false;
@@ -317,10 +325,10 @@ __device__ __forceinline__ Pair apply_totals(const Totals<N> &to, int buf, int r
 
 // ------------------------------------------------------------------ forward
 
-template <typename T, bool SIG, bool MASKED, bool CLUSTER>
+template <typename T, bool SIG, bool MASKED, bool CLUSTER, typename RUN>
 __global__ void __launch_bounds__(kScanThreads, 2)
     scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
-                const ScanRun p) {
+                const RUN p) {
     using S = Shape<T, SIG, false>;
     using G = typename S::G;
     constexpr int R = S::kRun, ST = S::kStages;
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         const int j = n * cluster + rank, s = n % ST;
         if (j >= tiles) return;
         mbar_arrive_expect_tx(&sh.full[s], bytes);
-        if (j == p.lost) return;
+        if (is_lost(p, j)) return;
         load_box(smem + s * S::kStage, &mx, &sh.full[s], c0, base + j * p.step);
         load_box(smem + s * S::kStage + S::kXBytes, &mg, &sh.full[s], c0, base + j * p.step);
     };
@@ -489,10 +497,10 @@ __global__ void __launch_bounds__(kScanThreads, 2)
 // ------------------------------------------------------------------ backward
 
 // Tiles last to first: rank 0 of a cluster has the latest.
-template <typename T, bool SIG, bool MASKED, bool CLUSTER>
+template <typename T, bool SIG, bool MASKED, bool CLUSTER, typename RUN>
 __global__ void __launch_bounds__(kScanThreads, 2)
     scan_backward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
-                         const __grid_constant__ CUtensorMap md, const ScanRun p) {
+                         const __grid_constant__ CUtensorMap md, const RUN p) {
     using S = Shape<T, SIG, true>;
     using G = typename S::G;
     constexpr int R = S::kRun, ST = S::kStages;
@@ -514,7 +522,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         if (j < 0) return;
         uint8_t *const at = smem + s * S::kStage;
         mbar_arrive_expect_tx(&sh.full[s], bytes);
-        if (j == p.lost) return;
+        if (is_lost(p, j)) return;
         load_box(at, &mx, &sh.full[s], c0, base + j * p.step);
         load_box(at + S::kXBytes, &mg, &sh.full[s], c0, base + j * p.step);
         load_box(at + S::kXBytes + S::kGBytes, &md, &sh.full[s], c0, base + j * p.step);
@@ -860,8 +868,6 @@ ScanPlan scan_plan(const ScanArgs &a, int tile, int most, const int *map) {
     r.blocks = (a.T + kScanBlock - 1) / kScanBlock;
     r.total = a.offsets ? a.T : a.B * a.T;
     r.status = device_status_ptr();
-    r.limit = a.limit > 0 ? a.limit : kWaitLimit;
-    r.lost = a.limit > 0 ? a.lost : -1;
     r.step = tile;
     if (a.offsets) {
         s.masked = true;
@@ -929,19 +935,19 @@ cudaError_t launch_clustered(K kern, uintptr_t (&set)[64], const ScanPlan &s, si
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <typename T, bool SIG, bool MASKED, bool CLUSTER>
-cudaError_t forward(const ScanArgs &a, const ScanPlan &s, bool after_map, cudaStream_t st) {
+template <typename T, bool SIG, bool MASKED, bool CLUSTER, typename RUN>
+cudaError_t forward(const ScanArgs &a, const ScanPlan &s, const RUN &run, bool after_map, cudaStream_t st) {
     using S = Shape<T, SIG, false>;
     static uintptr_t set[64] = {};
     CUtensorMap mx, mg;
     if (!box_map<T>(&mx, a.x, s.run.total, a.D, a.ldx, s.run.rows) ||
         !box_map<typename S::G>(&mg, a.gate, s.run.total, a.D, a.ldg, s.run.rows))
         return cudaErrorInvalidValue;
-    return launch_clustered(scan_kernel<T, SIG, MASKED, CLUSTER>, set, s, S::kStages * S::kStage, after_map,
-                            st, mx, mg, s.run);
+    return launch_clustered(scan_kernel<T, SIG, MASKED, CLUSTER, RUN>, set, s, S::kStages * S::kStage,
+                            after_map, st, mx, mg, run);
 }
-template <typename T, bool SIG, bool MASKED, bool CLUSTER>
-cudaError_t backward(const ScanArgs &a, const ScanPlan &s, bool after_map, cudaStream_t st) {
+template <typename T, bool SIG, bool MASKED, bool CLUSTER, typename RUN>
+cudaError_t backward(const ScanArgs &a, const ScanPlan &s, const RUN &run, bool after_map, cudaStream_t st) {
     using S = Shape<T, SIG, true>;
     static uintptr_t set[64] = {};
     CUtensorMap mx, mg, md;
@@ -949,23 +955,34 @@ cudaError_t backward(const ScanArgs &a, const ScanPlan &s, bool after_map, cudaS
         !box_map<typename S::G>(&mg, a.gate, s.run.total, a.D, a.ldg, s.run.rows) ||
         !box_map<T>(&md, a.dh, s.run.total, a.D, a.D, s.run.rows))
         return cudaErrorInvalidValue;
-    return launch_clustered(scan_backward_kernel<T, SIG, MASKED, CLUSTER>, set, s, S::kStages * S::kStage,
-                            after_map, st, mx, mg, md, s.run);
+    return launch_clustered(scan_backward_kernel<T, SIG, MASKED, CLUSTER, RUN>, set, s, S::kStages * S::kStage,
+                            after_map, st, mx, mg, md, run);
 }
 
-template <typename T, bool SIG, bool BACK, bool MASKED, bool CLUSTER>
-cudaError_t launch_one(const ScanArgs &a, const ScanPlan &s, bool after_map, cudaStream_t st) {
-    if constexpr (BACK) return backward<T, SIG, MASKED, CLUSTER>(a, s, after_map, st);
-    else return forward<T, SIG, MASKED, CLUSTER>(a, s, after_map, st);
+template <typename T, bool SIG, bool BACK, bool MASKED, bool CLUSTER, typename RUN>
+cudaError_t launch_one(const ScanArgs &a, const ScanPlan &s, const RUN &run, bool after_map, cudaStream_t st) {
+    if constexpr (BACK) return backward<T, SIG, MASKED, CLUSTER>(a, s, run, after_map, st);
+    else return forward<T, SIG, MASKED, CLUSTER>(a, s, run, after_map, st);
 }
 template <typename T, bool SIG, bool BACK>
 cudaError_t launch_any(const ScanArgs &a, const int *map, bool after_map, cudaStream_t st) {
     const ScanPlan s = scan_plan(a, Shape<T, SIG, BACK>::kTokens, Shape<T, SIG, BACK>::kCluster, map);
     if (s.masked)
-        return s.cluster > 1 ? launch_one<T, SIG, BACK, true, true>(a, s, after_map, st)
-                             : launch_one<T, SIG, BACK, true, false>(a, s, after_map, st);
-    return s.cluster > 1 ? launch_one<T, SIG, BACK, false, true>(a, s, after_map, st)
-                         : launch_one<T, SIG, BACK, false, false>(a, s, after_map, st);
+        return s.cluster > 1 ? launch_one<T, SIG, BACK, true, true>(a, s, s.run, after_map, st)
+                             : launch_one<T, SIG, BACK, true, false>(a, s, s.run, after_map, st);
+    return s.cluster > 1 ? launch_one<T, SIG, BACK, false, true>(a, s, s.run, after_map, st)
+                         : launch_one<T, SIG, BACK, false, false>(a, s, s.run, after_map, st);
+}
+template <bool BACK> cudaError_t launch_lost(const ScanArgs &a, long long limit, int lost, cudaStream_t st) {
+    using T = __nv_bfloat16;
+    const ScanPlan s = scan_plan(a, Shape<T, true, BACK>::kTokens, Shape<T, true, BACK>::kCluster, nullptr);
+    LostRun run;
+    static_cast<ScanRun &>(run) = s.run;
+    run.limit = limit;
+    run.lost = lost;
+    if (s.masked) return launch_one<T, true, BACK, true, false>(a, s, run, false, st);
+    return s.cluster > 1 ? launch_one<T, true, BACK, false, true>(a, s, run, false, st)
+                         : launch_one<T, true, BACK, false, false>(a, s, run, false, st);
 }
 // after_map: the launch comes directly after the table's.
 template <bool BACK>
@@ -1023,6 +1040,10 @@ cudaError_t launch_scan_backward(const ScanArgs &a, gdn_dtype dt, void *workspac
         if (e != cudaSuccess) return e;
     }
     return launch_type<true>(b, dt, map, map && a.states, st);
+}
+
+cudaError_t launch_scan_lost(const ScanArgs &a, long long limit, int lost, cudaStream_t st) {
+    return a.dh ? launch_lost<true>(a, limit, lost, st) : launch_lost<false>(a, limit, lost, st);
 }
 
 cudaError_t launch_scan_step(const void *x, const void *gate, const float *h, float *h_out, void *y,

@@ -48,14 +48,14 @@ extern "C" int gdn_selftest_lost_copy(gdn_selftest_call call, long long limit_cy
         a.B = rows; a.T = T; a.D = D;
         a.ldx = a.ldg = D;
         a.sigmoid = true;
-        a.limit = limit_cycles;
-        a.lost = (int)(lost < tokens ? lost : tokens);
-        a.h = at + 3 * part;
-        a.dh = at + 3 * part;
-        a.dx = at + 4 * part;
-        a.dgate = at + 5 * part;
-        e = call == GDN_SELFTEST_SCAN ? gdn::launch_scan(a, GDN_BF16, nullptr, st)
-                                      : gdn::launch_scan_backward(a, GDN_BF16, nullptr, st);
+        if (call == GDN_SELFTEST_SCAN) {
+            a.h = at + 3 * part;
+        } else {
+            a.dh = at + 3 * part;
+            a.dx = at + 4 * part;
+            a.dgate = at + 5 * part;
+        }
+        e = gdn::launch_scan_lost(a, limit_cycles, (int)(lost < tokens ? lost : tokens), st);
     }
     if (e == cudaErrorInvalidValue) return GDN_ERR_INVALID_ARG;
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
