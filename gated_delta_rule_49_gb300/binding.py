@@ -49,6 +49,10 @@ GDN_SCAN_BLOCK = 64  # tokens between the states that a scan keeps
 
 GDN_SELFTEST_SCAN = 0
 GDN_SELFTEST_SCAN_BACKWARD = 1
+GDN_SELFTEST_NORM = 2
+GDN_SELFTEST_NORM_SUM = 3
+GDN_SELFTEST_NORM_ANSWER = 4
+GDN_SELFTEST_NORM_BACKWARD = 5
 
 EXPORTS = (
     "gdn_prefill",

@@ -249,6 +249,14 @@ cudaError_t launch_layer_norm_backward(const void *s, const void *dy, const floa
                                        const float *w, const void *ds, void *dx, float *dw,
                                        float *db, long long N, int D, long long lds, gdn_dtype dt,
                                        float *parts, cudaStream_t stream);
+// Self-test (bf16, D of 64, 2048, 4096 or 16384): waits end after `limit` SM clocks, and the
+// block of row `lost` is not copied (outputs, lost < 0: CTAs to take over are not asked for).
+cudaError_t launch_layer_norm_lost(const void *x, const void *res, void *y, float *stats, long long N,
+                                   int D, long long limit, long long lost, cudaStream_t stream);
+cudaError_t launch_layer_norm_backward_lost(const void *s, const void *dy, const float *stats,
+                                            const void *ds, void *dx, float *dw, float *parts,
+                                            long long N, int D, long long limit, long long lost,
+                                            cudaStream_t stream);
 
 // Programmatic dependent launch: a kernel launched this way may be scheduled
 // while the previous kernel on the stream finishes; it must execute

@@ -11,6 +11,8 @@
 // registers.  (Rows fetched ahead into registers spilled: 124 us for 32768 rows of
 // 2048 bf16 channels with the sum.)  The deviation is taken from the mean, not from
 // the squares' sum: a row about a large mean keeps it.
+#include <type_traits>
+
 #include "gdn_pair.cuh"
 #include "gdn_sm100.cuh"
 
@@ -18,6 +20,8 @@ namespace gdn {
 namespace {
 
 constexpr long long kWaitLimit = 2000000000LL;  // about 1 s of SM clocks
+constexpr long long kDrainLimit = kWaitLimit / 16;
+constexpr long long kLostAnswer = -2;
 
 // Threads of a row and pieces of 8 channels of a thread.  A team is a warp, of one
 // row or several, or the threads of a row; ALONE: one row at a time.
@@ -136,6 +140,19 @@ struct NormArgs {
     bool more;            // outputs: CTAs take over others
     int *status;
 };
+// Self-test (kernels of their own): the clocks of a wait; the row whose block is not copied,
+// or kLostAnswer: CTAs to take over are not asked for.
+struct LostArgs : NormArgs {
+    long long limit, lost;
+};
+__device__ __forceinline__ long long wait_limit(const NormArgs &) { return kWaitLimit; }
+__device__ __forceinline__ long long wait_limit(const LostArgs &p) { return p.limit; }
+__device__ __forceinline__ bool is_lost(const NormArgs &, long long, int) { return false; }
+__device__ __forceinline__ bool is_lost(const LostArgs &p, long long row0, int n) {
+    return p.lost >= row0 && p.lost < row0 + n;
+}
+__device__ __forceinline__ bool unasked(const NormArgs &) { return false; }
+__device__ __forceinline__ bool unasked(const LostArgs &p) { return p.lost == kLostAnswer; }
 
 // A team's ring: block i of the team's is in slot i % slots, its tensors one after
 // another, the rows dense.
@@ -146,11 +163,12 @@ template <typename T, int TENSORS> struct Ring {
     long long ld[TENSORS];
     int bytes;  // of a slot's tensor
     // by one thread
-    __device__ __forceinline__ void fetch(const NormArgs &p, int slot, long long row0) const {
+    template <typename A> __device__ __forceinline__ void fetch(const A &p, int slot, long long row0) const {
         if (row0 >= p.N) return;
         const int n = (int)min((long long)p.rows, p.N - row0), row = p.D * (int)sizeof(T);
         uint8_t *const at = base + slot * TENSORS * bytes;
         sm100::mbar_arrive_expect_tx(&full[slot], TENSORS * n * row);
+        if (is_lost(p, row0, n)) return;
 #pragma unroll
         for (int t = 0; t < TENSORS; ++t) {
             const T *const from = src[t] + row0 * ld[t];
@@ -166,28 +184,32 @@ template <typename T, int TENSORS> struct Ring {
         return reinterpret_cast<const T *>(base + (slot * TENSORS + tensor) * bytes) + (long long)i * p.D;
     }
 };
-// Waits with a limit; after one that ran out nothing more is fetched.  The threads of a
-// team go on alike all the same, with what the slot holds, so that none is left behind at
-// a barrier of theirs.
+// Waits with a limit; after one that ran out nothing more is fetched, and no barrier whose
+// phase is open is arrived at again.  The threads of a team go on alike all the same, with
+// what the slot holds, so that none is left behind at a barrier of theirs.
 __device__ __forceinline__ void gave_up(int *abort, int *status) {
     *static_cast<volatile int *>(abort) = 1;
     if (status) atomicOr(status, kStatusTimeout);
 }
 // Where the blocks are dealt out: the first wait that runs out ends all others of the CTA.
-__device__ __forceinline__ void wait_dealt(uint64_t *bar, uint32_t parity, int *abort, int *status) {
+template <typename A>
+__device__ __forceinline__ void wait_dealt(uint64_t *bar, uint32_t parity, int *abort, const A &p) {
     volatile int *const flag = abort;
-    if (!sm100::mbar_wait_or_abort(bar, parity, kWaitLimit, flag) && !*flag) gave_up(abort, status);
+    if (!sm100::mbar_wait_or_abort(bar, parity, wait_limit(p), flag) && !*flag) gave_up(abort, p.status);
 }
 // Where they are drawn: the team's first thread says which block it is before the barrier
-// completes, or that there is none, once its own waits (of kWaitLimit) have run out.
-__device__ __forceinline__ void wait_drawn(uint64_t *bar, uint32_t parity, int *abort, int *status) {
-    if (!sm100::mbar_wait(bar, parity, 4 * kWaitLimit)) gave_up(abort, status);
+// completes, or that there is none, once its own waits (two of the limit) have run out.
+template <typename A>
+__device__ __forceinline__ bool wait_drawn(uint64_t *bar, uint32_t parity, int *abort, const A &p) {
+    const bool ok = sm100::mbar_wait(bar, parity, 4 * wait_limit(p));
+    if (!ok) gave_up(abort, p.status);
+    return ok;
 }
 // Copies in flight land before the CTA ends (where nothing went wrong none are).
 __device__ __forceinline__ void drain(uint64_t *full, int slots) {
     for (int i = 0; i < slots; ++i) {
-        sm100::mbar_wait(&full[i], 0, kWaitLimit / 16);
-        sm100::mbar_wait(&full[i], 1, kWaitLimit / 16);
+        sm100::mbar_wait(&full[i], 0, kDrainLimit);
+        sm100::mbar_wait(&full[i], 1, kDrainLimit);
     }
 }
 // Outputs: the chunks of a CTA, one block a team each, which the teams draw one by one.
@@ -205,17 +227,21 @@ struct Chunks {
     int taken[kAsked];  // how often the answer has been read
     int drawn;          // blocks drawn from the chunk that the CTA started with on
 };
-// One thread; chunk k >= 1.
-__device__ __forceinline__ void ask(Chunks &q, int k, int teams, int *abort, int *status) {
+// One thread; chunk k >= 1.  (A question that is on its way when another thread gives up is
+// answered long before the CTA's copies and answers have been waited for.)
+template <typename A>
+__device__ __forceinline__ void ask(Chunks &q, int k, int teams, int *abort, const A &p) {
     const int e = (k - 1) % kAsked, before = (k - 1) / kAsked * teams;
     volatile int *const taken = &q.taken[e], *const flag = abort;
     const long long t0 = clock64();
     while (*taken != before) {  // the entry's last answer has been read by all
         if (*flag) return;
-        if (clock64() - t0 > kWaitLimit) return gave_up(abort, status);
+        if (clock64() - t0 > wait_limit(p)) return gave_up(abort, p.status);
     }
+    if (*flag) return;
     sm100::fence_proxy_async_smem();
     sm100::mbar_arrive_expect_tx(&q.ready[e], 16);
+    if (unasked(p)) return;
     asm volatile(
         "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
             sm100::smem_u32(q.answer[e])),
@@ -225,14 +251,15 @@ __device__ __forceinline__ void ask(Chunks &q, int k, int teams, int *abort, int
 // A team's next block, or one past the rows where there is none (by one thread of the
 // team, which draws no more then: all teams have read the last answer before the CTA
 // ends).  Without taking over, a CTA's chunks lie a grid apart.
-__device__ __forceinline__ long long draw(Chunks &q, int teams, bool more, int *abort, int *status) {
+template <typename A>
+__device__ __forceinline__ long long draw(Chunks &q, int teams, int *abort, const A &p) {
     volatile int *const flag = abort;
     if (*flag) return -1;
     const int n = atomicAdd(&q.drawn, 1), k = n / teams;
-    if (!more) return ((long long)k * gridDim.x + blockIdx.x) * teams + n % teams;
+    if (!p.more) return ((long long)k * gridDim.x + blockIdx.x) * teams + n % teams;
     const int e = (k - 1) % kAsked;
-    if (!sm100::mbar_wait_or_abort(&q.ready[e], ((k - 1) / kAsked) & 1, kWaitLimit, flag)) {
-        gave_up(abort, status);
+    if (!sm100::mbar_wait_or_abort(&q.ready[e], ((k - 1) / kAsked) & 1, wait_limit(p), flag)) {
+        gave_up(abort, p.status);
         return -1;
     }
     uint32_t ok, chunk;
@@ -249,7 +276,7 @@ __device__ __forceinline__ long long draw(Chunks &q, int teams, bool more, int *
     atomicAdd(&q.taken[e], 1);
     if (!ok) return -1;
     // (after an answer that there is none no other may be asked for)
-    if (n % teams == 0) ask(q, k + 1, teams, abort, status);
+    if (n % teams == 0) ask(q, k + 1, teams, abort, p);
     return (long long)chunk * teams + n % teams;
 }
 
@@ -305,9 +332,9 @@ __device__ __forceinline__ float sum2(Pair x) {
     return f.x + f.y;
 }
 
-template <typename T, typename S, bool RES>
+template <typename T, typename S, bool RES, typename A>
 __global__ void __launch_bounds__(S::kThreads, 1)
-    layer_norm_kernel(const NormArgs p) {
+    layer_norm_kernel(const A p) {
     constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T, S>(false);
     constexpr int TENSORS = RES ? 2 : 1, BATCH = U * S::kAbreast;
     constexpr int kWeights = weights_in<S>(false), PIECES = TPR * VPT;
@@ -332,17 +359,22 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
     const int teams = blockDim.x / S::kTeam;
     // The team's next block: its rows on the way, or word that it has none (of the last
-    // chunk) or that there is none.
+    // chunk) or that there is none.  open: the slot's last copies have not come.  Then nothing
+    // is drawn any more, and the phase is not arrived at: who waits for the next one goes on at
+    // once, or when its wait runs out, and finds the word, which the team's meeting for the
+    // block's second sum has shown to all.
     constexpr long long kEnd = -1, kEmpty = -2;
     bool ended = false;
-    auto fetch = [&](int slot, long long block) {
+    auto fetch = [&](int slot, long long block, bool open) {
         const long long row0 = block < 0 ? kEnd : block * p.rows < p.N ? block * p.rows : p.more ? kEmpty : kEnd;
         row_of[team][slot] = row0;
         ended = row0 == kEnd;
-        if (row0 < 0) sm100::mbar_arrive(&full[team][slot]);
-        else ring.fetch(p, slot, row0);
+        if (row0 >= 0) ring.fetch(p, slot, row0);
+        else if (!open) sm100::mbar_arrive(&full[team][slot]);
     };
-    auto next = [&](int slot) { fetch(slot, ended ? -1 : draw(chunks, teams, p.more, &abort, p.status)); };
+    auto next = [&](int slot, bool ok) {
+        fetch(slot, ended ? -1 : draw(chunks, teams, &abort, p), !ok);
+    };
     if (threadIdx.x == 0) {
         abort = 0;
         chunks.drawn = teams;
@@ -354,7 +386,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     if (lead) {
         for (int i = 0; i < p.slots; ++i) sm100::mbar_init(&full[team][i], 1);
         sm100::fence_mbar_init();
-        fetch(0, (long long)blockIdx.x * teams + team);
+        fetch(0, (long long)blockIdx.x * teams + team, false);
     }
     RowSum<TPR, U> sum = {red[team], team, 0};
     const float inv = 1.f / p.D;
@@ -375,15 +407,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     int slot = 0;
     uint32_t parity = 0;
     for (bool begin = true;; begin = false) {
-        wait_drawn(&full[team][slot], parity, &abort, p.status);
+        const bool ok = wait_drawn(&full[team][slot], parity, &abort, p);
         const long long block = row_of[team][slot];
         if (block == kEnd) break;
         if (begin) {
             // (the first block of the first team has rows; the CTAs of the first round have
             // started by the time that these are here)
-            if (threadIdx.x == 0 && p.more) ask(chunks, 1, teams, &abort, p.status);
+            if (threadIdx.x == 0 && p.more) ask(chunks, 1, teams, &abort, p);
             if (lead)
-                for (int i = 1; i < p.slots; ++i) next(i);
+                for (int i = 1; i < p.slots; ++i) next(i, true);
         }
         const int at = slot;
         if (++slot == p.slots) {
@@ -393,7 +425,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         if (block == kEmpty) {
             if constexpr (TPR <= 32) __syncwarp();
             else sm100::named_sync(team + 1, TPR);
-            if (lead) next(at);
+            if (lead) next(at, ok);
             continue;
         }
         const int n = (int)min((long long)p.rows, p.N - block);
@@ -431,7 +463,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             sum(m);
             if (i0 + BATCH >= n) {  // the block is in registers
                 if constexpr (TPR <= 32) __syncwarp();
-                if (lead) next(at);
+                if (lead) next(at, ok);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -493,9 +525,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 // A thread's rows leave their sums for dw and db in its registers; the CTA's row
 // groups add theirs up in shared memory, in their order, and the CTA writes one row
 // of `parts`.
-template <typename T, typename S, bool PAST>
+template <typename T, typename S, bool PAST, typename A>
 __global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
-    layer_norm_backward_kernel(const NormArgs p) {
+    layer_norm_backward_kernel(const A p) {
     constexpr int TPR = S::TPR, VPT = S::VPT, U = rows_at_once<T, S>(true);
     constexpr int TENSORS = PAST ? 3 : 2, BATCH = U * S::kAbreast;
     constexpr bool kHold = weights_in<S>(true) == kRegisters;
@@ -550,7 +582,7 @@ __global__ void __launch_bounds__(S::kBackThreads, S::kBackCtas)
     uint32_t parity = 0;
     for (long long block = first; block < p.N; block += step) {
         const int n = (int)min((long long)p.rows, p.N - block);
-        wait_dealt(&full[team][slot], parity, &abort, p.status);
+        wait_dealt(&full[team][slot], parity, &abort, p);
         for (int i0 = 0; i0 < n; i0 += BATCH) {
             float2 now[U];
             float t[2 * U];
@@ -772,8 +804,8 @@ template <typename T, typename F> auto by_width_backward(int D, bool past, F &&f
     return f(RowShape<512, 4>());
 }
 
-template <typename K>
-cudaError_t launch(K kern, uintptr_t (&set)[64], NormArgs p, const NormPlan &plan, cudaStream_t st) {
+template <typename K, typename A>
+cudaError_t launch(K kern, uintptr_t (&set)[64], A p, const NormPlan &plan, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (set[dev] != context_key()) {
@@ -789,31 +821,46 @@ cudaError_t launch(K kern, uintptr_t (&set)[64], NormArgs p, const NormPlan &pla
     return cudaGetLastError();
 }
 
+template <typename T, typename S, typename A> cudaError_t forward_shape(const A &p, cudaStream_t st) {
+    static uintptr_t set[2][64] = {};
+    const NormPlan plan = norm_plan<T, S>(p.N, p.D, p.res ? 2 : 1, false);
+    return p.res ? launch(layer_norm_kernel<T, S, true, A>, set[1], p, plan, st)
+                 : launch(layer_norm_kernel<T, S, false, A>, set[0], p, plan, st);
+}
 template <typename T> cudaError_t forward(const NormArgs &p, cudaStream_t st) {
-    return by_width<T>(p.D, [&](auto shape) {
-        using S = decltype(shape);
-        static uintptr_t set[2][64] = {};
-        const NormPlan plan = norm_plan<T, S>(p.N, p.D, p.res ? 2 : 1, false);
-        return p.res ? launch(layer_norm_kernel<T, S, true>, set[1], p, plan, st)
-                     : launch(layer_norm_kernel<T, S, false>, set[0], p, plan, st);
+    return by_width<T>(p.D, [&](auto shape) { return forward_shape<T, decltype(shape)>(p, st); });
+}
+
+template <typename T, typename S, typename A>
+cudaError_t backward_shape(const A &p, float *dw, float *db, cudaStream_t st) {
+    static uintptr_t set[2][64] = {};
+    const NormPlan plan = norm_plan<T, S>(p.N, p.D, p.res ? 3 : 2, true);
+    auto rows = [&] {
+        if constexpr (!S::ALONE && std::is_same<A, NormArgs>::value)
+            if (!p.res) return launch(layer_norm_backward_kernel<T, S, false, A>, set[0], p, plan, st);
+        return launch(layer_norm_backward_kernel<T, S, true, A>, set[1], p, plan, st);
+    };
+    const cudaError_t e = rows();
+    if (e != cudaSuccess || !p.parts) return e;
+    return launch_pdl(layer_norm_sum_kernel, (2 * p.D + 31) / 32, 1024, 0, st,
+                      static_cast<const float *>(p.parts), plan.grid, p.D, dw, db);
+}
+template <typename T> cudaError_t backward(const NormArgs &p, float *dw, float *db, cudaStream_t st) {
+    return by_width_backward<T>(p.D, p.res != nullptr, [&](auto shape) {
+        return backward_shape<T, decltype(shape)>(p, dw, db, st);
     });
 }
 
-template <typename T> cudaError_t backward(const NormArgs &p, float *dw, float *db, cudaStream_t st) {
-    return by_width_backward<T>(p.D, p.res != nullptr, [&](auto shape) {
-        using S = decltype(shape);
-        static uintptr_t set[2][64] = {};
-        const NormPlan plan = norm_plan<T, S>(p.N, p.D, p.res ? 3 : 2, true);
-        auto rows = [&] {
-            if constexpr (!S::ALONE)
-                if (!p.res) return launch(layer_norm_backward_kernel<T, S, false>, set[0], p, plan, st);
-            return launch(layer_norm_backward_kernel<T, S, true>, set[1], p, plan, st);
-        };
-        const cudaError_t e = rows();
-        if (e != cudaSuccess || !p.parts) return e;
-        return launch_pdl(layer_norm_sum_kernel, (2 * p.D + 31) / 32, 1024, 0, st,
-                          static_cast<const float *>(p.parts), plan.grid, p.D, dw, db);
-    });
+// The shapes that the self-test has: several rows a warp, a row a warp, rows of several
+// warps, rows of all threads of a CTA.
+template <typename F> cudaError_t by_width_tested(int D, F &&f) {
+    switch (D) {
+        case 64: return f(RowShape<8, 1>(), RowShape<8, 1>());
+        case 2048: return f(RowShape<32, 8>(), RowShape<256, 1>());
+        case 4096: return f(RowShape<64, 8>(), RowShape<256, 2>());
+        case 16384: return f(RowShape<512, 4>(), RowShape<512, 4>());
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <typename T> int most_parts(long long N, int D) {
@@ -853,6 +900,30 @@ cudaError_t launch_layer_norm_backward(const void *s, const void *dy, const floa
     p.parts = dw || db ? parts : nullptr;
     p.N = N; p.D = D; p.ldx = lds;
     return dt == GDN_BF16 ? backward<__nv_bfloat16>(p, dw, db, st) : backward<float>(p, dw, db, st);
+}
+
+cudaError_t launch_layer_norm_lost(const void *x, const void *res, void *y, float *stats, long long N,
+                                   int D, long long limit, long long lost, cudaStream_t st) {
+    LostArgs p = {};
+    p.x = x; p.res = res; p.y = y; p.stats = stats; p.N = N; p.D = p.ldx = p.ldr = D; p.eps = 1e-5f;
+    p.limit = limit;
+    p.lost = lost < 0 ? kLostAnswer : lost;
+    return by_width_tested(D, [&](auto shape, auto) {
+        return forward_shape<__nv_bfloat16, decltype(shape)>(p, st);
+    });
+}
+cudaError_t launch_layer_norm_backward_lost(const void *s, const void *dy, const float *stats,
+                                            const void *ds, void *dx, float *dw, float *parts,
+                                            long long N, int D, long long limit, long long lost,
+                                            cudaStream_t st) {
+    LostArgs p = {};
+    p.x = s; p.dy = dy; p.stats = const_cast<float *>(stats); p.res = ds; p.y = dx; p.parts = parts;
+    p.N = N; p.D = p.ldx = D;
+    p.limit = limit;
+    p.lost = lost;
+    return by_width_tested(D, [&](auto, auto shape) {
+        return backward_shape<__nv_bfloat16, decltype(shape)>(p, dw, nullptr, st);
+    });
 }
 
 }  // namespace gdn

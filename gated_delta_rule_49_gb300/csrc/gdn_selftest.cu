@@ -57,6 +57,19 @@ extern "C" int gdn_selftest_lost_copy(gdn_selftest_call call, long long limit_cy
         }
         e = gdn::launch_scan_lost(a, limit_cycles, (int)(lost < tokens ? lost : tokens), st);
     }
+    if (call >= GDN_SELFTEST_NORM && call <= GDN_SELFTEST_NORM_BACKWARD) {
+        const long long half = part / 2;
+        float *const stats = reinterpret_cast<float *>(at + 4 * half);
+        if (call == GDN_SELFTEST_NORM_BACKWARD)
+            e = gdn::launch_layer_norm_backward_lost(
+                at, at + half, stats, at + 2 * half, at + 3 * half,
+                reinterpret_cast<float *>(at + 5 * part), reinterpret_cast<float *>(at + 3 * part),
+                tokens, D, limit_cycles, lost, st);
+        else
+            e = gdn::launch_layer_norm_lost(at, call == GDN_SELFTEST_NORM ? nullptr : at + half,
+                                            at + 2 * half, stats, tokens, D, limit_cycles,
+                                            call == GDN_SELFTEST_NORM_ANSWER ? -1 : lost, st);
+    }
     if (e == cudaErrorInvalidValue) return GDN_ERR_INVALID_ARG;
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -725,15 +725,33 @@ GDN_API int gdn_get_last_device_status(void *stream);
 GDN_API int gdn_selftest_wait_timeout(long long limit_cycles, void *stream);
 
 /*
- * gdn_selftest_lost_copy -- run a kernel of the recurrence (bf16, sigmoid gates) with a
- * copy that never comes: tile `lost` (128 tokens, gradients 64) of each sequence is
- * announced to its barrier and not fetched.  Every wait ends after limit_cycles SM clock
- * cycles (1 <= limit_cycles <= 2^31); the kernel sets the timeout bit of the device
- * status word and returns, with outputs that mean nothing.  rows sequences of T tokens
- * (2^24 in all at most) of D channels; buffer: 24 rows T D bytes + 1536 of device memory, which
- * hold the inputs and take the outputs.  Asynchronous on `stream`.
+ * gdn_selftest_lost_copy -- run a kernel of the recurrence (bf16, sigmoid gates) or of the
+ * layer norm (bf16, without weights) with a copy that never comes: it is announced to its
+ * barrier and not fetched.  Every wait ends after limit_cycles SM clock cycles, four times
+ * them where another comes first (1 <= limit_cycles <= 2^31); the kernel sets the timeout
+ * bit of the device status word and returns, with outputs that mean nothing.
+ *
+ *   GDN_SELFTEST_SCAN, _SCAN_BACKWARD   rows sequences of T tokens; tile `lost` (128 tokens,
+ *                          gradients 64) of each does not come
+ *   GDN_SELFTEST_NORM, _NORM_SUM (with a residual), _NORM_BACKWARD (with ds)   rows x T rows;
+ *                          the block with row `lost` does not come
+ *   GDN_SELFTEST_NORM_ANSWER   as _NORM_SUM with all its rows; the answers about CTAs to
+ *                          take over do not come (with so few rows that none is asked for
+ *                          all is well)
+ *
+ * rows x T at most 2^24, D channels (a multiple of 8 up to 16384; the norm's 64, 2048, 4096
+ * or 16384); buffer: 24 rows T D bytes
+ * + 1536 of device memory, which hold the inputs and take the outputs.  Asynchronous on
+ * `stream`.
  */
-typedef enum { GDN_SELFTEST_SCAN = 0, GDN_SELFTEST_SCAN_BACKWARD = 1 } gdn_selftest_call;
+typedef enum {
+    GDN_SELFTEST_SCAN = 0,
+    GDN_SELFTEST_SCAN_BACKWARD = 1,
+    GDN_SELFTEST_NORM = 2,
+    GDN_SELFTEST_NORM_SUM = 3,
+    GDN_SELFTEST_NORM_ANSWER = 4,
+    GDN_SELFTEST_NORM_BACKWARD = 5
+} gdn_selftest_call;
 GDN_API int gdn_selftest_lost_copy(gdn_selftest_call call, long long limit_cycles, long long lost,
                                    void *buffer, size_t bytes, int rows, int T, int D, void *stream);
 

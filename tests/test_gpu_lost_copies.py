@@ -50,3 +50,39 @@ def test_recurrence(torch, call, rows, T, D, lost):
         again = binding.scan_backward(x, gate, want[0], states=want[2])
         assert again[0].equal(grads[0]) and again[1].equal(grads[1])
     assert binding.gdn_get_last_device_status() == binding.GDN_OK
+
+
+# rows, channels: rows by 8 threads to all 512 of a CTA; one block, and so many rows that CTAs
+# take over others' (a sum's)
+NORMS = [(3, 64), (200_003, 64), (9, 2048), (8193, 2048), (10, 4096), (3000, 4096), (700, 16384)]
+
+
+@pytest.mark.parametrize("call", [binding.GDN_SELFTEST_NORM, binding.GDN_SELFTEST_NORM_SUM,
+                                  binding.GDN_SELFTEST_NORM_BACKWARD], ids=["norm", "sum", "backward"])
+@pytest.mark.parametrize("N,D", NORMS)
+def test_layer_norm(torch, call, N, D):
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, r = (torch.randn(N, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    want = binding.layer_norm(x, residual=r, want_stats=True)
+    grads = binding.layer_norm_backward(want[1], r, want[2], ds=x, want_db=True)
+    for lost in (0, N // 2, N - 1):
+        run(torch, call, N, 1, D, lost)
+        got = binding.layer_norm(x, residual=r, want_stats=True)
+        assert all(p.equal(q) for p, q in zip(got, want))
+        again = binding.layer_norm_backward(want[1], r, want[2], ds=x, want_db=True)
+        assert again[0].equal(grads[0]) and again[2].equal(grads[2])
+    assert binding.gdn_get_last_device_status() == binding.GDN_OK
+
+
+@pytest.mark.parametrize("N,D", [(200_003, 64), (8193, 2048), (3000, 4096), (700, 16384)])
+def test_answers_that_never_come(torch, N, D):
+    """A sum's CTAs ask which others they may take over (fewer rows than CTAs: none asks)."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, r = (torch.randn(N, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    want = binding.layer_norm(x, residual=r)[0]
+    run(torch, binding.GDN_SELFTEST_NORM_ANSWER, N, 1, D, 0)
+    assert binding.layer_norm(x, residual=r)[0].equal(want)
+    size = 24 * 9 * D + 1536
+    buffer = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    binding.gdn_selftest_lost_copy(binding.GDN_SELFTEST_NORM_ANSWER, LIMIT, 0, buffer, size, 9, 1, D)
+    assert binding.gdn_get_last_device_status() == binding.GDN_OK

@@ -23,3 +23,10 @@ def test_refusals(lib):
                dict(D=60), dict(D=32768), dict(rows=1 << 20, T=1 << 20)):
         assert call(**kw) == binding.GDN_ERR_INVALID_ARG, kw
     assert call(bytes=2 * 300 * 64 * 24 - 1) == binding.GDN_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("call", [2, 3, 4, 5])
+def test_norms_of_other_widths(lib, call):
+    for D in (8, 72, 128, 2040, 8192):
+        assert lib.gdn_selftest_lost_copy(call, 1000, 0, F, 1 << 30, 2, 30, D, None) == \
+            binding.GDN_ERR_INVALID_ARG
