@@ -611,11 +611,13 @@ GDN_API int gdn_linear_decode_step(const void *q, const void *k, const void *v,
  *
  * Outputs and the workspace share no byte with the inputs or with each other (but
  * h_T, which may be h0 exactly), else GDN_ERR_INVALID_ARG; so it is for the two
- * calls below.
+ * calls below, each with what it allows.
  * D a multiple of 8 (else GDN_ERR_UNSUPPORTED); at most 2^31 - 1024 tokens in
- * all, and as many sequences and channels.  Everything is float32 from the load to the one
- * rounding of h.  A value that is not finite reaches what the recurrence carries
- * it to and nothing else.
+ * all, and as many sequences and channels.  Everything is float32 from the load to
+ * the one rounding of h.  A value that is not finite reaches what the recurrence
+ * carries it to and nothing else; an infinity may arrive there as a NaN (pieces of
+ * tokens are joined by the products of their decays, and such a product may
+ * underflow to 0).  The same holds for the gradients.
  * workspace: gdn_scan_prefill_workspace_size bytes (0 unless packed).
  */
 typedef enum { GDN_SCAN_DECAY = 0, GDN_SCAN_SIGMOID = 1 } gdn_scan_kind;
