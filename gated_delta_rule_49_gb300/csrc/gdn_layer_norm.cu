@@ -6,10 +6,12 @@
 //
 // Bound by memory: every input read once, every output written once (8 bytes a
 // value with the sum, 4 without; gradients 8 or 6, in bf16).  A team (a warp, or
-// the threads of one wide row) has a ring of blocks of rows in shared memory, which
-// one thread keeps full by bulk copies: what is in flight does not depend on
+// the threads of one wide row) has a ring of one to four blocks of rows in shared memory,
+// which one thread fills by bulk copies: what is in flight does not depend on
 // registers.  (Rows fetched ahead into registers spilled: 124 us for 32768 rows of
-// 2048 bf16 channels with the sum.)  The deviation is taken from the mean, not from
+// 2048 bf16 channels with the sum.)  With one block only, outputs fetch the next as soon as
+// it is in registers; gradients read it twice and fetch after that, so that a team's loads
+// do not overlap its own arithmetic, only the other teams'.  The deviation is taken from the mean, not from
 // the squares' sum: a row about a large mean keeps it.
 #include <type_traits>
 
@@ -33,7 +35,9 @@ template <int TPR_, int VPT_, bool ALONE_ = false> struct RowShape {
         kTeam = TPR < 32 ? 32 : TPR,
         kAbreast = kTeam / TPR,  // rows side by side in a team
         // Outputs: one CTA an SM, of up to 20 warps, fewer where the rows are few (24
-        // warps spilled; two CTAs of 8 would each hold the weights).  Gradients: 16
+        // warps spilled; two CTAs of 8 would each hold the weights).  Of 20 warps float32
+        // rows with the sum of up to 128 channels spill 20 bytes a thread, of 16 warps
+        // float32 rows above 8192 channels 20, with the sum 28.  Gradients: 16
         // warps an SM (24 spilled: 94 -> 116 us for 512 channels).
         kTeams = kTeam < 640 ? 640 / kTeam : 1,
         kThreads = kTeams * kTeam,
@@ -50,7 +54,7 @@ template <typename T, typename S> constexpr int rows_at_once(bool back) {
     const int pieces = back && S::TPR > 32 && sizeof(T) == 2 || !back ? 4 : 2;
     return S::VPT < pieces ? pieces / S::VPT : 1;
 }
-constexpr int kMaxSlots = 4;  // blocks of a team in shared memory
+constexpr int kMaxSlots = 4;  // blocks of a team in shared memory (gradients), at most
 
 // Sums of U values over the threads of a row, the same in all of them and in a
 // fixed order.  Rows of several warps meet at a barrier of their team's; the two
@@ -219,7 +223,7 @@ __device__ __forceinline__ void drain(uint64_t *full, int slots) {
 // (32768 rows of 2048 bf16 channels 92 us, taken over 85).  Without the sum half as much
 // moves, and the questions cost what they bring (512 channels: dealt out 46 us, taken
 // over 48; 2048: 47 and 46).  Who draws a chunk's first block asks for the next chunk.
-constexpr int kOutSlots = 2;
+constexpr int kOutSlots = 2;   // blocks of a team, at most
 constexpr int kAsked = 4;  // chunks asked for and not yet handed out
 struct Chunks {
     alignas(16) unsigned long long answer[kAsked][2];
@@ -734,8 +738,11 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Rows of a block, blocks of a team, CTAs, their threads and shared memory.  A
-// team's block takes about 4 KB a warp and tensor (gradients of wide rows: 1 KB, so
-// that several fit); the rings of an SM's CTAs share its memory.
+// team's block takes about 4 KB a warp and tensor (gradients of rows of several warps: 1
+// KB, so that two to four fit); the rings of an SM's CTAs share its memory.  Many rows leave
+// room for one block a team with the sum to form (but 12288 channels: two) and of 8192 bf16
+// channels without it, in gradients up to 256 channels (1048576 rows of 64 bf16 channels 84
+// us, 71 % of the copy bandwidth, with ds 95, 83 %) and of the widest float32 rows.
 constexpr int kShared = 216 * 1024;  // of an SM
 struct NormPlan {
     int rows, slots, grid, threads;

@@ -26,7 +26,8 @@
 // 176 us).
 //
 // A stream is one sequence, or several: packed ones (a table gives each token's
-// sequence) or dense ones of at most a tile.  There a run knows which of its tokens
+// sequence) or dense ones of up to 64 tokens, whole ones in a tile and without clusters.
+// There a run knows which of its tokens
 // start or end a sequence or belong to none; a start takes h0 in the place of the
 // state that arrives, by selection, never by a factor of 0 (a NaN would pass).
 #include <cudaTypedefs.h>
